@@ -341,6 +341,123 @@ int moe_balance_stats(const moe_config *cfg, const float *logits, const int32_t 
                       void *stream);
 size_t moe_balance_stats_workspace_size(const moe_config *cfg);
 
+/*
+ * MXFP4 — rows of 4-bit floating point with a scale for every 32 elements.
+ *   codes   [rows][d/2] uint8: E2M1 codes (sign, 2 exponent bits with bias 1,
+ *           1 mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and negatives), element
+ *           2i in the low four bits of byte i and element 2i+1 in the high four
+ *   scales  [rows][d/32] uint8: byte B stands for 2^(B - 127), 255 for NaN
+ * Weights are quantised along their reduction axis (the last one of the
+ * nn.Linear layout), so a stack [G][out][in] is G * out rows of d = in.
+ */
+
+/*
+ * moe_quantize_mxfp4 — rows to MXFP4.  The rule is the FP8 dispatch's: per
+ * block of 32 elements the scale is 2^E, E the smallest integer with
+ * max|x| <= 6 * 2^E (0 for a block of zeros, at least -127), and a code is
+ * x / 2^E rounded to the nearest value, ties to the even code; nothing is
+ * clipped.  A block that holds an infinity or a NaN gets scale byte 255 and
+ * codes 0.
+ *   dtype       moe_dtype of x and widened
+ *   x           rows of d elements, x_stride elements apart (x_stride >= d; a
+ *               row starts on a 16-byte boundary, so x_stride is a multiple
+ *               of 8 for MOE_BF16 and of 4 for MOE_F32; ignored for one row)
+ *   widened     [rows][d] dtype output or NULL: the values the codes stand
+ *               for, 2^E times each code's value (exact unless the product
+ *               leaves the type's range: a block whose largest element is
+ *               above 1.75 * 2^127 widens that element to infinity; blocks
+ *               marked NaN widen to NaN)
+ * d is a multiple of 32 (else MOE_ERR_UNSUPPORTED); rows * d < 2^42.
+ */
+int moe_quantize_mxfp4(int32_t dtype, int64_t rows, int32_t d, const void *x, int64_t x_stride,
+                       uint8_t *codes, uint8_t *scales, void *widened, void *stream);
+
+/*
+ * moe_grouped_linear_mxfp4 — one Linear of every group's expert on MXFP4
+ * rows and MXFP4 weights, on the scaled matrix instructions:
+ *   y_rows[r] = act(X[row_index[r]] W_g^T + bias_g),  offsets[g] <= r < offsets[g+1]
+ * with float32 sums, rounded to bf16 once.  A block whose scale byte is 255
+ * makes the outputs it enters NaN.
+ *   x_codes, x_scales   the token rows (k elements each)
+ *   row_index   [max_rows] int32 or NULL: source row of each row (a dispatch's
+ *               row_token, so that a token is quantised once however many
+ *               experts it meets); NULL: row r reads source row r
+ *   offsets     [n_groups+1] int32 DEVICE array, non-decreasing, offsets[0]=0
+ *   max_rows    host-side upper bound on offsets[n_groups], as for
+ *               moe_grouped_ffn; rows at or beyond offsets[n_groups] are
+ *               neither read nor written
+ *   w_codes [G][n_out][k/2], w_scales [G][n_out][k/32]
+ *   bias        [G][n_out] bf16 or NULL;  silu 1: act = SiLU, 0: none
+ *   y_rows      [max_rows][n_out] bf16 output
+ *   ws          optional device scratch of
+ *               moe_grouped_linear_mxfp4_workspace_size bytes (NULL allowed);
+ *               a non-NULL ws smaller than that is MOE_ERR_WORKSPACE.  Calls
+ *               that overlap in time need a scratch of their own each.
+ * k is a multiple of 128 (one step of the matrix instruction) and n_out of 8
+ * (16-byte output rows), n_groups <= 1088; else MOE_ERR_UNSUPPORTED.
+ */
+int moe_grouped_linear_mxfp4(int32_t n_groups, int32_t n_out, int32_t k, const uint8_t *x_codes,
+                             const uint8_t *x_scales, const int32_t *row_index,
+                             const int32_t *offsets, int64_t max_rows, const uint8_t *w_codes,
+                             const uint8_t *w_scales, const void *bias, int32_t silu, void *y_rows,
+                             void *ws, size_t ws_bytes, void *stream);
+size_t moe_grouped_linear_mxfp4_workspace_size(int32_t n_groups, int32_t n_out, int32_t k,
+                                               int64_t max_rows);
+
+/*
+ * moe_layer_forward_few — moe_layer_forward for 1 to MOE_FEW_TOKENS tokens (a
+ * decode step) in two kernels instead of one per stage.  Arguments, shapes,
+ * capacity rule and optional outputs as moe_layer_forward, with these
+ * differences:
+ *   - T > MOE_FEW_TOKENS and cfg->dispatch == MOE_DISPATCH_FP8 return
+ *     MOE_ERR_UNSUPPORTED;
+ *   - the logits are float32 sums in a fixed tree order, not moe_route's
+ *     chain, so two experts whose logits differ by no more than their rounding
+ *     may be ordered differently than there; ties still go to the lower id;
+ *   - hidden activations keep 16 significant bits (bf16 layers; float32
+ *     otherwise) and expert outputs are not rounded before the sum over
+ *     experts: y is rounded once.  Routed experts are summed in ascending
+ *     expert id, the shared experts after them;
+ *   - ws holds moe_few_workspace_size(cfg) bytes, all scratch.  Nothing in it
+ *     needs to be initialised.  Calls that overlap in time (other streams,
+ *     parallel branches of a graph) need a workspace of their own each.
+ * Results do not depend on timing.
+ */
+#define MOE_FEW_TOKENS 16
+int moe_layer_forward_few(const moe_config *cfg, const moe_weights *w, const void *x, void *y,
+                          int32_t *topk_idx, float *topk_gate, int32_t *counts, void *ws,
+                          size_t ws_bytes, void *stream);
+
+/* Device workspace of the two few-token calls (0 when cfg is invalid or
+ * unsupported there). */
+size_t moe_few_workspace_size(const moe_config *cfg);
+
+/* moe_weights with the expert matrices in MXFP4 (codes and scale bytes);
+ * biases are bf16. */
+typedef struct {
+    const float *w_router;      /* [N][d] float32                               */
+    const float *router_bias;   /* [N] float32 or NULL                          */
+    const uint8_t *w1;          /* [N][f][d/2] codes                            */
+    const uint8_t *w1_scales;   /* [N][f][d/32]                                 */
+    const void *b1;             /* [N][f] bf16 or NULL                          */
+    const uint8_t *w2;          /* [N][d][f/2] codes                            */
+    const uint8_t *w2_scales;   /* [N][d][f/32]                                 */
+    const void *b2;             /* [N][d] bf16 or NULL                          */
+    const uint8_t *ws1;         /* [K_s][f][d/2] (NULL when K_s == 0)           */
+    const uint8_t *ws1_scales;  /* [K_s][f][d/32]                               */
+    const void *bs1;            /* [K_s][f] bf16 or NULL                        */
+    const uint8_t *ws2;         /* [K_s][d][f/2] (NULL when K_s == 0)           */
+    const uint8_t *ws2_scales;  /* [K_s][d][f/32]                               */
+    const void *bs2;            /* [K_s][d] bf16 or NULL                        */
+} moe_weights_mxfp4;
+
+/* moe_layer_forward_few on MXFP4 expert weights (widened exactly to bf16 in
+ * registers; activations stay bf16).  cfg->dtype is MOE_BF16 and d_model and
+ * d_ff are multiples of 128, else MOE_ERR_UNSUPPORTED. */
+int moe_layer_forward_few_mxfp4(const moe_config *cfg, const moe_weights_mxfp4 *w, const void *x,
+                                void *y, int32_t *topk_idx, float *topk_gate, int32_t *counts,
+                                void *ws, size_t ws_bytes, void *stream);
+
 /* Per-expert capacity the library applies for cfg (-1 = unlimited). */
 int64_t moe_capacity(const moe_config *cfg);
 

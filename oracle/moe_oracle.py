@@ -80,6 +80,8 @@ __all__ = [
     "balance_statistics", "fmaf_array",
     "e4m3_values", "round_e4m3", "fp8_scale_exponent", "quantize_fp8_rows",
     "dequantize_fp8_rows",
+    "e2m1_values", "round_e2m1", "mx_scale_exponent", "quantize_mxfp4", "pack_mxfp4",
+    "unpack_mxfp4", "dequantize_mxfp4",
 ]
 
 _LIB = None
@@ -500,3 +502,78 @@ def balance_statistics(logits: np.ndarray, idx: np.ndarray, alpha: float = 0.01)
     f = np.bincount(np.asarray(idx).ravel(), minlength=N).astype(np.float64) / (T * K)
     P = s.mean(axis=0)
     return f, P, float(alpha * N * np.sum(f * P))
+
+
+# ---------------------------------------------------------------------------
+# MXFP4: E2M1 codes with one power-of-two scale per 32 elements
+# ---------------------------------------------------------------------------
+
+MX_BLOCK = 32
+
+
+def e2m1_values() -> np.ndarray:
+    """Values of the 16 codes: sign, two exponent bits (bias 1), one mantissa bit."""
+    v = np.empty(16)
+    for c in range(16):
+        e, m = (c >> 1) & 3, c & 1
+        v[c] = (m * 0.5 if e == 0 else (1.0 + 0.5 * m) * 2.0 ** (e - 1)) * (-1.0 if c & 8 else 1.0)
+    return v
+
+
+def round_e2m1(v) -> np.ndarray:
+    """Codes of |v| <= 6 (float64), nearest, ties to the even code; -0 keeps its sign."""
+    v = np.asarray(v, dtype=np.float64)
+    mags = e2m1_values()[:8]
+    a = np.abs(v)[..., None]
+    d = np.abs(a - mags)
+    near = d == d.min(axis=-1, keepdims=True)
+    # of two equally near codes exactly one is even
+    even = (np.arange(8) % 2 == 0)
+    pick = np.where(near & even, 2, 0) + near
+    code = np.argmax(pick, axis=-1)
+    return (code + 8 * np.signbit(v)).astype(np.uint8)
+
+
+def mx_scale_exponent(block) -> int:
+    """Smallest E in [-127, 127] with max|block| <= 6 * 2^E; 0 for a block of zeros."""
+    a = float(np.max(np.abs(np.asarray(block, dtype=np.float64))))
+    if a == 0.0:
+        return 0
+    m, e = math.frexp(a)                       # a = m * 2^e, 6 = 0.75 * 2^3
+    return max(-127, e - 3 if m <= 0.75 else e - 2)
+
+
+def quantize_mxfp4(x):
+    """Codes [rows, d] (one per element, 0..15) and scale bytes [rows, d/32]."""
+    x = np.asarray(x, dtype=np.float64)
+    rows, d = x.shape
+    v = x.reshape(rows, d // MX_BLOCK, MX_BLOCK)
+    scales = np.empty((rows, d // MX_BLOCK), dtype=np.uint8)
+    codes = np.zeros(v.shape, dtype=np.uint8)
+    for r in range(rows):
+        for b in range(d // MX_BLOCK):
+            if not np.isfinite(v[r, b]).all():
+                scales[r, b] = 255
+                continue
+            E = mx_scale_exponent(v[r, b])
+            scales[r, b] = E + 127
+            codes[r, b] = round_e2m1(v[r, b] * 2.0 ** -E)
+    return codes.reshape(rows, d), scales
+
+
+def pack_mxfp4(codes) -> np.ndarray:
+    """Bytes [..., d/2]: the even element in the low four bits."""
+    c = np.asarray(codes, dtype=np.uint8)
+    return c[..., 0::2] | (c[..., 1::2] << 4)
+
+
+def unpack_mxfp4(packed) -> np.ndarray:
+    p = np.asarray(packed, dtype=np.uint8)
+    return np.stack([p & 15, p >> 4], axis=-1).reshape(*p.shape[:-1], 2 * p.shape[-1])
+
+
+def dequantize_mxfp4(codes, scales) -> np.ndarray:
+    """The values (float64) of codes [..., d] with scale bytes [..., d/32]."""
+    s = np.asarray(scales, dtype=np.float64)
+    f = np.where(s == 255, np.nan, np.exp2(s - 127.0))
+    return e2m1_values()[np.asarray(codes)] * np.repeat(f, MX_BLOCK, axis=-1)

@@ -28,7 +28,9 @@ EXPORTS = ("moe_route", "moe_permute", "moe_permute_workspace_size", "moe_groupe
            "moe_grouped_ffn_workspace_size", "moe_combine", "moe_balance_stats",
            "moe_balance_stats_workspace_size", "moe_layer_forward", "moe_layer_forward_events",
            "moe_layer_forward_noalloc", "moe_workspace_size", "moe_workspace_layout",
-           "moe_capacity", "moe_status_string", "moe_version")
+           "moe_quantize_mxfp4", "moe_grouped_linear_mxfp4",
+           "moe_grouped_linear_mxfp4_workspace_size", "moe_layer_forward_few",
+           "moe_layer_forward_few_mxfp4", "moe_few_workspace_size", "moe_capacity", "moe_status_string", "moe_version")
 STAGES = ("router", "topk", "dispatch", "up", "down", "combine")
 # moe_version() of the interface these ctypes declarations mirror (the structs
 # below must match the header's field for field)
@@ -63,6 +65,13 @@ class Weights(ctypes.Structure):
                 ("w_router", "router_bias", "w1", "b1", "w2", "b2", "ws1", "bs1", "ws2", "bs2")]
 
 
+class WeightsMxfp4(ctypes.Structure):
+    """Mirror of moe_weights_mxfp4."""
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("w_router", "router_bias", "w1", "w1_scales", "b1", "w2", "w2_scales", "b2",
+                 "ws1", "ws1_scales", "bs1", "ws2", "ws2_scales", "bs2")]
+
+
 _LIB = None
 
 
@@ -89,6 +98,15 @@ def lib():
             "moe_layer_forward_events": (I, [C, ctypes.POINTER(Weights), P, P, P, P, P, P, Z,
                                              ctypes.POINTER(ctypes.c_void_p), P]),
             "moe_layer_forward_noalloc": (I, [C, ctypes.POINTER(Weights), P, P, P, P, P, P]),
+            "moe_quantize_mxfp4": (I, [ctypes.c_int32, I64, ctypes.c_int32, P, I64, P, P, P, P]),
+            "moe_grouped_linear_mxfp4": (I, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, P, P,
+                                             P, P, I64, P, P, P, ctypes.c_int32, P, P, Z, P]),
+            "moe_grouped_linear_mxfp4_workspace_size": (Z, [ctypes.c_int32, ctypes.c_int32,
+                                                            ctypes.c_int32, I64]),
+            "moe_layer_forward_few": (I, [C, ctypes.POINTER(Weights), P, P, P, P, P, P, Z, P]),
+            "moe_layer_forward_few_mxfp4": (I, [C, ctypes.POINTER(WeightsMxfp4), P, P, P, P, P, P,
+                                                Z, P]),
+            "moe_few_workspace_size": (Z, [C]),
             "moe_workspace_size": (Z, [C]),
             "moe_workspace_layout": (I, [C, ctypes.POINTER(WsLayout)]),
             "moe_capacity": (I64, [C]),
@@ -234,6 +252,111 @@ def layer_forward_events(cfg: Config, w: Weights, x, y, events, topk_idx=None, t
            lib().moe_layer_forward_events(ctypes.byref(cfg), ctypes.byref(w), _ptr(x), _ptr(y),
                                           _ptr(topk_idx), _ptr(topk_gate), _ptr(counts), _ptr(ws),
                                           nbytes, arr, _stream(stream)))
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _on_device(**tensors):
+    """The tensors given (None allowed) live on the current GPU, whose streams
+    the calls use."""
+    for name, t in tensors.items():
+        if t is not None:
+            _need(t.is_cuda and t.device.index == torch.cuda.current_device(),
+                  f"{name} must be on the current GPU")
+
+
+def quantize_mxfp4(x, codes, scales, widened=None, stream=None):
+    """x [rows, d] (bf16 or f32; rows may be strided) to codes [rows, d/2] and
+    scale bytes [rows, d/32] (uint8), and the values they stand for (widened
+    [rows, d], x's type)."""
+    _on_device(x=x, codes=codes, scales=scales, widened=widened)
+    _need(x.dim() == 2 and x.dtype in (torch.bfloat16, torch.float32), "x must be [rows, d] bf16 or f32")
+    rows, d = x.shape
+    _need(x.stride(1) == 1 or d <= 1, "elements of a row of x must be contiguous")
+    _need(codes.dtype == scales.dtype == torch.uint8, "codes and scales must be uint8")
+    _need(tuple(codes.shape) == (rows, d // 2) and tuple(scales.shape) == (rows, d // 32),
+          "codes must be [rows, d/2] and scales [rows, d/32]")
+    _need(widened is None or (widened.shape == x.shape and widened.dtype == x.dtype),
+          "widened must have x's shape and type")
+    _check("moe_quantize_mxfp4", lib().moe_quantize_mxfp4(
+        MOE_BF16 if x.dtype == torch.bfloat16 else MOE_F32, rows, d, x.data_ptr(), x.stride(0),
+        _ptr(codes), _ptr(scales), _ptr(widened), _stream(stream)))
+
+
+def grouped_linear_mxfp4_workspace_size(n_groups, n_out, k, max_rows) -> int:
+    return int(lib().moe_grouped_linear_mxfp4_workspace_size(int(n_groups), int(n_out), int(k),
+                                                             int(max_rows)))
+
+
+def grouped_linear_mxfp4(x_codes, x_scales, offsets, w_codes, w_scales, y_rows, row_index=None,
+                         bias=None, silu=False, ws=None, stream=None):
+    """y_rows [max_rows, n_out] (bf16) of x rows [., k/2] and weights
+    [n_groups, n_out, k/2]; the sizes come from the tensors."""
+    _on_device(x_codes=x_codes, x_scales=x_scales, offsets=offsets, w_codes=w_codes,
+               w_scales=w_scales, y_rows=y_rows, row_index=row_index, bias=bias, ws=ws)
+    _need(w_codes.dim() == 3 and y_rows.dim() == 2, "w_codes must be [G, n_out, k/2], y_rows [rows, n_out]")
+    g, n_out, k = w_codes.shape[0], w_codes.shape[1], 2 * w_codes.shape[2]
+    max_rows = y_rows.shape[0]
+    _need(all(t.dtype == torch.uint8 for t in (x_codes, x_scales, w_codes, w_scales)),
+          "codes and scales must be uint8")
+    _need(tuple(w_scales.shape) == (g, n_out, k // 32), "w_scales must be [G, n_out, k/32]")
+    _need(x_codes.dim() == 2 and x_codes.shape[1] * 2 == k and
+          tuple(x_scales.shape) == (x_codes.shape[0], k // 32), "x_codes must be [., k/2], x_scales [., k/32]")
+    _need(y_rows.dtype == torch.bfloat16 and y_rows.shape[1] == n_out, "y_rows must be [rows, n_out] bf16")
+    _need(offsets.dtype == torch.int32 and offsets.numel() == g + 1, "offsets must be [G + 1] int32")
+    if row_index is None:
+        _need(x_codes.shape[0] >= max_rows, "x has fewer rows than y_rows (and no row_index)")
+    else:
+        _need(row_index.dtype == torch.int32 and row_index.numel() >= max_rows,
+              "row_index must be [max_rows] int32")
+    _need(bias is None or (bias.dtype == torch.bfloat16 and tuple(bias.shape) == (g, n_out)),
+          "bias must be [G, n_out] bf16")
+    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check("moe_grouped_linear_mxfp4", lib().moe_grouped_linear_mxfp4(
+        g, n_out, k, _ptr(x_codes), _ptr(x_scales), _ptr(row_index), _ptr(offsets), max_rows,
+        _ptr(w_codes), _ptr(w_scales), _ptr(bias), int(bool(silu)), _ptr(y_rows), _ptr(ws), nbytes,
+        _stream(stream)))
+
+
+def few_workspace_size(cfg: Config) -> int:
+    return int(lib().moe_few_workspace_size(ctypes.byref(cfg)))
+
+
+def weights_mxfp4(w_router, router_bias, w1, w1_scales, b1, w2, w2_scales, b2, ws1=None,
+                  ws1_scales=None, bs1=None, ws2=None, ws2_scales=None, bs2=None) -> WeightsMxfp4:
+    return WeightsMxfp4(*[_ptr(t) for t in (w_router, router_bias, w1, w1_scales, b1, w2, w2_scales,
+                                            b2, ws1, ws1_scales, bs1, ws2, ws2_scales, bs2)])
+
+
+def _layer_forward_few(fn: str, cfg, w, x, y, topk_idx, topk_gate, counts, ws, stream):
+    _on_device(x=x, y=y, topk_idx=topk_idx, topk_gate=topk_gate, counts=counts, ws=ws)
+    T, K = cfg.T, cfg.top_k
+    act = torch.bfloat16 if cfg.dtype == MOE_BF16 else torch.float32
+    _need(x.dtype == y.dtype == act and x.numel() == y.numel() == T * cfg.d_model,
+          "x and y must be [T, d_model] of the layer's type")
+    for t, dt, n in ((topk_idx, torch.int32, T * K), (topk_gate, torch.float32, T * K),
+                     (counts, torch.int32, cfg.n_routed)):
+        _need(t is None or (t.dtype == dt and t.numel() == n), "a routing output has another size or type")
+    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(fn, getattr(lib(), fn)(ctypes.byref(cfg), ctypes.byref(w), _ptr(x), _ptr(y),
+                                  _ptr(topk_idx), _ptr(topk_gate), _ptr(counts), _ptr(ws), nbytes,
+                                  _stream(stream)))
+
+
+def layer_forward_few(cfg: Config, w: Weights, x, y, topk_idx=None, topk_gate=None, counts=None,
+                      ws=None, stream=None):
+    """The layer for 1 to 16 tokens (workspace: few_workspace_size)."""
+    _layer_forward_few("moe_layer_forward_few", cfg, w, x, y, topk_idx, topk_gate, counts, ws, stream)
+
+
+def layer_forward_few_mxfp4(cfg: Config, w: WeightsMxfp4, x, y, topk_idx=None, topk_gate=None,
+                            counts=None, ws=None, stream=None):
+    """layer_forward_few on MXFP4 expert weights."""
+    _layer_forward_few("moe_layer_forward_few_mxfp4", cfg, w, x, y, topk_idx, topk_gate, counts, ws,
+                       stream)
 
 
 class HipEvents:

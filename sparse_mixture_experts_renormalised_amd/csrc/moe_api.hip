@@ -429,6 +429,162 @@ int moe_layer_forward_noalloc(const moe_config *cfg, const moe_weights *w, const
                    static_cast<hipStream_t>(stream));
 }
 
+int moe_quantize_mxfp4(int32_t dtype, int64_t rows, int32_t d, const void *x, int64_t x_stride,
+                       uint8_t *codes, uint8_t *scales, void *widened, void *stream) {
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (rows < 0 || d <= 0) return MOE_ERR_INVALID_ARG;
+  if (d % 32 != 0) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!x || !codes || !scales) return MOE_ERR_INVALID_ARG;
+  if (!all_aligned16({x, codes, scales, widened})) return MOE_ERR_INVALID_ARG;
+  const int64_t lanes = dtype == MOE_BF16 ? 8 : 4;    // elements of a 16-byte load
+  if (rows > 1 && (x_stride < d || x_stride % lanes != 0)) return MOE_ERR_INVALID_ARG;
+  // one lane takes 8 elements, 256 lanes a workgroup, at most 2^31 - 1 workgroups
+  if (rows > (int64_t(1) << 39) / (d / 8)) return MOE_ERR_UNSUPPORTED;
+  return hip_status(moe::launch_quantize_mxfp4(dtype == MOE_BF16, x, rows, d, x_stride, codes,
+                                               scales, widened, static_cast<hipStream_t>(stream)));
+}
+
+static int check_linear_mxfp4(int32_t n_groups, int32_t n_out, int32_t k, int64_t max_rows) {
+  if (n_groups <= 0 || n_out <= 0 || k <= 0 || max_rows < 0) return MOE_ERR_INVALID_ARG;
+  if (n_groups > moe::kMaxRouted + moe::kMaxShared) return MOE_ERR_UNSUPPORTED;
+  if (n_out % 8 != 0 || k % 128 != 0) return MOE_ERR_UNSUPPORTED;
+  if (max_rows >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+size_t moe_grouped_linear_mxfp4_workspace_size(int32_t n_groups, int32_t n_out, int32_t k,
+                                               int64_t max_rows) {
+  if (check_linear_mxfp4(n_groups, n_out, k, max_rows) != MOE_OK) return 0;
+  return moe::linear_mxfp4_workspace_bytes(n_groups, n_out, k, max_rows);
+}
+
+int moe_grouped_linear_mxfp4(int32_t n_groups, int32_t n_out, int32_t k, const uint8_t *x_codes,
+                             const uint8_t *x_scales, const int32_t *row_index,
+                             const int32_t *offsets, int64_t max_rows, const uint8_t *w_codes,
+                             const uint8_t *w_scales, const void *bias, int32_t silu, void *y_rows,
+                             void *ws, size_t ws_bytes, void *stream) {
+  const int st = check_linear_mxfp4(n_groups, n_out, k, max_rows);
+  if (st != MOE_OK) return st;
+  if (silu != 0 && silu != 1) return MOE_ERR_INVALID_ARG;
+  if (max_rows == 0) return MOE_OK;
+  if (!x_codes || !x_scales || !offsets || !w_codes || !w_scales || !y_rows)
+    return MOE_ERR_INVALID_ARG;
+  if (!all_aligned16({x_codes, x_scales, row_index, offsets, w_codes, w_scales, bias, y_rows, ws}))
+    return MOE_ERR_INVALID_ARG;
+  const size_t need = moe::linear_mxfp4_workspace_bytes(n_groups, n_out, k, max_rows);
+  if (ws && ws_bytes < need) return MOE_ERR_WORKSPACE;
+  moe::MxLinear p{};
+  p.x = x_codes;
+  p.xs = x_scales;
+  p.index = row_index;
+  p.offsets = offsets;
+  p.w = w_codes;
+  p.ws = w_scales;
+  p.bias = bias;
+  p.y = y_rows;
+  p.groups = n_groups;
+  p.n_out = n_out;
+  p.k = k;
+  p.max_rows = max_rows;
+  p.silu = silu != 0;
+  p.scratch = need ? ws : nullptr;
+  p.scratch_bytes = p.scratch ? need : 0;
+  return hip_status(moe::launch_linear_mxfp4(p, static_cast<hipStream_t>(stream)));
+}
+
+// Shape checks of the few-token layer.
+static int check_few(const moe_config *cfg) {
+  const int st = check_config(cfg, true, true);
+  if (st != MOE_OK) return st;
+  if (cfg->T > moe::kFewTokens || cfg->dispatch != MOE_DISPATCH_BF16) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+size_t moe_few_workspace_size(const moe_config *cfg) {
+  if (check_few(cfg) != MOE_OK) return 0;
+  return moe::few_workspace_bytes(static_cast<int>(cfg->T), cfg->d_model, cfg->n_routed,
+                                  cfg->top_k, cfg->n_shared, cfg->d_ff);
+}
+
+static int run_few(const moe_config *cfg, moe::FewLayer &p, const void *x, void *y,
+                   int32_t *topk_idx, float *topk_gate, int32_t *counts, void *ws,
+                   size_t ws_bytes, void *stream) {
+  if (!x || !y || !p.w_router || !p.w1 || !p.w2) return MOE_ERR_INVALID_ARG;
+  if (cfg->n_shared > 0 && (!p.ws1 || !p.ws2)) return MOE_ERR_INVALID_ARG;
+  if (!all_aligned16({x, y, p.w_router, p.router_bias, p.w1, p.b1, p.w2, p.b2, p.ws1, p.bs1, p.ws2,
+                      p.bs2, p.c1, p.c2, p.cs1, p.cs2, topk_idx, topk_gate, counts, ws}))
+    return MOE_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < moe_few_workspace_size(cfg)) return MOE_ERR_WORKSPACE;
+  const int64_t C = capacity_of(cfg);
+  p.x = x;
+  p.select_only = cfg->bias_mode == MOE_BIAS_SELECTION_ONLY;
+  p.y = y;
+  p.idx = topk_idx;
+  p.gate = topk_gate;
+  p.counts = counts;
+  p.T = static_cast<int>(cfg->T);
+  p.d = cfg->d_model;
+  p.N = cfg->n_routed;
+  p.K = cfg->top_k;
+  p.Ks = cfg->n_shared;
+  p.f = cfg->d_ff;
+  p.cap = static_cast<int>(C >= 0 && C < cfg->T ? C : cfg->T);
+  return hip_status(moe::launch_few_layer(p, ws, static_cast<hipStream_t>(stream)));
+}
+
+int moe_layer_forward_few(const moe_config *cfg, const moe_weights *w, const void *x, void *y,
+                          int32_t *topk_idx, float *topk_gate, int32_t *counts, void *ws,
+                          size_t ws_bytes, void *stream) {
+  const int st = check_few(cfg);
+  if (st != MOE_OK) return st;
+  if (!w) return MOE_ERR_INVALID_ARG;
+  if (cfg->T == 0) return MOE_OK;
+  moe::FewLayer p{};
+  p.kind = cfg->dtype == MOE_BF16 ? moe::kFewBf16 : moe::kFewF32;
+  p.w_router = w->w_router;
+  p.router_bias = w->router_bias;
+  p.w1 = w->w1;
+  p.b1 = w->b1;
+  p.w2 = w->w2;
+  p.b2 = w->b2;
+  p.ws1 = w->ws1;
+  p.bs1 = w->bs1;
+  p.ws2 = w->ws2;
+  p.bs2 = w->bs2;
+  return run_few(cfg, p, x, y, topk_idx, topk_gate, counts, ws, ws_bytes, stream);
+}
+
+int moe_layer_forward_few_mxfp4(const moe_config *cfg, const moe_weights_mxfp4 *w, const void *x,
+                                void *y, int32_t *topk_idx, float *topk_gate, int32_t *counts,
+                                void *ws, size_t ws_bytes, void *stream) {
+  const int st = check_few(cfg);
+  if (st != MOE_OK) return st;
+  if (cfg->dtype != MOE_BF16 || cfg->d_model % 128 != 0 || cfg->d_ff % 128 != 0)
+    return MOE_ERR_UNSUPPORTED;
+  if (!w) return MOE_ERR_INVALID_ARG;
+  if (cfg->T == 0) return MOE_OK;
+  if (!w->w1_scales || !w->w2_scales) return MOE_ERR_INVALID_ARG;
+  if (cfg->n_shared > 0 && (!w->ws1_scales || !w->ws2_scales)) return MOE_ERR_INVALID_ARG;
+  moe::FewLayer p{};
+  p.kind = moe::kFewMxfp4;
+  p.w_router = w->w_router;
+  p.router_bias = w->router_bias;
+  p.w1 = w->w1;
+  p.c1 = w->w1_scales;
+  p.b1 = w->b1;
+  p.w2 = w->w2;
+  p.c2 = w->w2_scales;
+  p.b2 = w->b2;
+  p.ws1 = w->ws1;
+  p.cs1 = w->ws1_scales;
+  p.bs1 = w->bs1;
+  p.ws2 = w->ws2;
+  p.cs2 = w->ws2_scales;
+  p.bs2 = w->bs2;
+  return run_few(cfg, p, x, y, topk_idx, topk_gate, counts, ws, ws_bytes, stream);
+}
+
 }  // extern "C"
 
 namespace {

@@ -124,6 +124,46 @@ hipError_t launch_grouped_gemm(bool bf16, const GemmGroups &g, Epilogue epi, hip
 // when xw is not null, the codes widened back to bf16 rows xw [T][d].
 hipError_t launch_quantize_fp8(const void *x, int64_t T, int d, uint8_t *q, int32_t *exps,
                                void *xw, hipStream_t s);
+// MXFP4 codes [rows][d/2] and scale bytes [rows][d/32] of x (rows `stride`
+// elements apart), and, when wide is not null, the values they stand for.
+hipError_t launch_quantize_mxfp4(bool bf16, const void *x, int64_t rows, int d, int64_t stride,
+                                 uint8_t *codes, uint8_t *scales, void *wide, hipStream_t s);
+
+struct MxLinear {
+  const uint8_t *x, *xs;        // codes and scale bytes of the rows
+  const int32_t *index;         // row r reads source row index[r] (null: r)
+  const int32_t *offsets;       // [groups + 1], device
+  const uint8_t *w, *ws;        // codes and scale bytes of the weights
+  const void *bias;             // bf16 [groups][n_out] or null
+  void *y;                      // bf16 [max_rows][n_out]
+  int groups, n_out, k;
+  int64_t max_rows;
+  bool silu;
+  void *scratch;
+  size_t scratch_bytes;
+};
+size_t linear_mxfp4_workspace_bytes(int groups, int n_out, int k, int64_t max_rows);
+hipError_t launch_linear_mxfp4(const MxLinear &p, hipStream_t s);
+
+// The whole layer for at most kFewTokens tokens.
+constexpr int kFewTokens = 16;
+enum FewKind { kFewF32, kFewBf16, kFewMxfp4 };
+struct FewLayer {
+  FewKind kind;
+  const void *x;
+  const float *w_router, *router_bias;
+  bool select_only;             // the bias enters the selection only
+  const void *w1, *b1, *w2, *b2, *ws1, *bs1, *ws2, *bs2;
+  const uint8_t *c1, *c2, *cs1, *cs2;   // scale bytes (MXFP4)
+  void *y;
+  int32_t *idx;
+  float *gate;
+  int32_t *counts;
+  int T, d, N, K, Ks, f, cap;
+};
+size_t few_workspace_bytes(int T, int d, int N, int K, int Ks, int f);
+hipError_t launch_few_layer(const FewLayer &p, void *ws, hipStream_t s);
+
 hipError_t launch_combine(bool bf16, const void *y_rows, const int32_t *slot_row,
                           const float *gates, const void *shared_out, int n_shared, int64_t T,
                           int K, int d, void *y, hipStream_t s);
