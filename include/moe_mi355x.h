@@ -378,10 +378,11 @@ int moe_quantize_mxfp4(int32_t dtype, int64_t rows, int32_t d, const void *x, in
  *   y_rows[r] = act(X[row_index[r]] W_g^T + bias_g),  offsets[g] <= r < offsets[g+1]
  * with float32 sums, rounded to bf16 once.  A block whose scale byte is 255
  * makes the outputs it enters NaN.
- *   x_codes, x_scales   the token rows (k elements each)
+ *   x_rows      rows of x_codes and x_scales, the token rows (k elements each)
  *   row_index   [max_rows] int32 or NULL: source row of each row (a dispatch's
  *               row_token, so that a token is quantised once however many
- *               experts it meets); NULL: row r reads source row r
+ *               experts it meets), values in [0, x_rows); NULL: row r reads
+ *               source row r, and x_rows >= max_rows
  *   offsets     [n_groups+1] int32 DEVICE array, non-decreasing, offsets[0]=0
  *   max_rows    host-side upper bound on offsets[n_groups], as for
  *               moe_grouped_ffn; rows at or beyond offsets[n_groups] are
@@ -394,10 +395,13 @@ int moe_quantize_mxfp4(int32_t dtype, int64_t rows, int32_t d, const void *x, in
  *               a non-NULL ws smaller than that is MOE_ERR_WORKSPACE.  Calls
  *               that overlap in time need a scratch of their own each.
  * k is a multiple of 128 (one step of the matrix instruction) and n_out of 8
- * (16-byte output rows), n_groups <= 1088; else MOE_ERR_UNSUPPORTED.
+ * (16-byte output rows), n_groups <= 1088, and the codes of all token rows
+ * and those of one group's matrix take less than 4 GiB each (32-bit offsets);
+ * else MOE_ERR_UNSUPPORTED.
  */
-int moe_grouped_linear_mxfp4(int32_t n_groups, int32_t n_out, int32_t k, const uint8_t *x_codes,
-                             const uint8_t *x_scales, const int32_t *row_index,
+int moe_grouped_linear_mxfp4(int32_t n_groups, int32_t n_out, int32_t k, int64_t x_rows,
+                             const uint8_t *x_codes, const uint8_t *x_scales,
+                             const int32_t *row_index,
                              const int32_t *offsets, int64_t max_rows, const uint8_t *w_codes,
                              const uint8_t *w_scales, const void *bias, int32_t silu, void *y_rows,
                              void *ws, size_t ws_bytes, void *stream);

@@ -99,8 +99,9 @@ def lib():
                                              ctypes.POINTER(ctypes.c_void_p), P]),
             "moe_layer_forward_noalloc": (I, [C, ctypes.POINTER(Weights), P, P, P, P, P, P]),
             "moe_quantize_mxfp4": (I, [ctypes.c_int32, I64, ctypes.c_int32, P, I64, P, P, P, P]),
-            "moe_grouped_linear_mxfp4": (I, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, P, P,
-                                             P, P, I64, P, P, P, ctypes.c_int32, P, P, Z, P]),
+            "moe_grouped_linear_mxfp4": (I, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, I64,
+                                             P, P, P, P, I64, P, P, P, ctypes.c_int32, P, P, Z,
+                                             P]),
             "moe_grouped_linear_mxfp4_workspace_size": (Z, [ctypes.c_int32, ctypes.c_int32,
                                                             ctypes.c_int32, I64]),
             "moe_layer_forward_few": (I, [C, ctypes.POINTER(Weights), P, P, P, P, P, P, Z, P]),
@@ -316,7 +317,7 @@ def grouped_linear_mxfp4(x_codes, x_scales, offsets, w_codes, w_scales, y_rows, 
           "bias must be [G, n_out] bf16")
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     _check("moe_grouped_linear_mxfp4", lib().moe_grouped_linear_mxfp4(
-        g, n_out, k, _ptr(x_codes), _ptr(x_scales), _ptr(row_index), _ptr(offsets), max_rows,
+        g, n_out, k, x_codes.shape[0], _ptr(x_codes), _ptr(x_scales), _ptr(row_index), _ptr(offsets), max_rows,
         _ptr(w_codes), _ptr(w_scales), _ptr(bias), int(bool(silu)), _ptr(y_rows), _ptr(ws), nbytes,
         _stream(stream)))
 

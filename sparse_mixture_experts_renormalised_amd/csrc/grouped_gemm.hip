@@ -38,6 +38,7 @@
 // The weight tile is the MFMA's first operand, so each lane ends up holding
 // four consecutive output features of one row and the epilogues store packed
 // bf16 pairs.
+#include "lds_dma.h"
 #include "moe_common.h"
 
 namespace moe {
@@ -209,47 +210,6 @@ __device__ __forceinline__ void decode_tile(int L, int total_m, int n_nt, int *m
   *mt = first + r % gm;
   *nt = r / gm;
 }
-
-// ---------------------------------------------------------------------------
-// Global-to-LDS copies shared by the MFMA kernels.
-// ---------------------------------------------------------------------------
-namespace dma {
-// LDS byte address of a __shared__ object (wave-uniform).
-__device__ __forceinline__ uint32_t lds_addr(const void *p) {
-  return static_cast<uint32_t>(
-      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void *)p));
-}
-
-// One wave-wide LDS DMA (64 lanes x 16 B into the 1 KB block at LDS byte
-// address m0), written as inline assembly so the compiler does not drain
-// every load in flight before later LDS reads; the explicit waits cover it.
-// The s_nop separates the compiler's write of M0 from the copy that reads it.
-__device__ __forceinline__ void dma16(const uint16_t *src, uint32_t m0) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(src), "{m0}"(m0) : "memory");
-}
-// The same copy with the non-temporal policy, for data read exactly once (a
-// weight block used by a single row block): streaming it past the caches
-// raises the sustained read rate from about 6.1 to 7.2 TB/s on MI355X.
-__device__ __forceinline__ void dma16_nt(const uint16_t *src, uint32_t m0) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt" : : "v"(src), "{m0}"(m0) : "memory");
-}
-
-// The same copy addressed as a wave-uniform 64-bit base in SGPRs plus a 32-bit
-// per-lane byte offset (the instruction's SGPR-base form): advancing along K
-// then costs one scalar add per base instead of a 64-bit vector add per copy.
-__device__ __forceinline__ void dma16s(uint32_t voff, const uint16_t *sbase, uint32_t m0) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(voff), "s"(sbase), "{m0}"(m0) : "memory");
-}
-
-// Wait until at most N of this wave's copies are in flight and its LDS reads
-// are done, then meet the other waves.
-template <int N>
-__device__ __forceinline__ void wait_and_barrier() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-}  // namespace dma
 
 // ---------------------------------------------------------------------------
 // bf16 MFMA kernel: 256x256 tiles, four 128x128 wave tiles, two LDS buffers

@@ -449,6 +449,7 @@ static int check_linear_mxfp4(int32_t n_groups, int32_t n_out, int32_t k, int64_
   if (n_groups <= 0 || n_out <= 0 || k <= 0 || max_rows < 0) return MOE_ERR_INVALID_ARG;
   if (n_groups > moe::kMaxRouted + moe::kMaxShared) return MOE_ERR_UNSUPPORTED;
   if (n_out % 8 != 0 || k % 128 != 0) return MOE_ERR_UNSUPPORTED;
+  if (n_out >= (int64_t(1) << 32) / (k / 2)) return MOE_ERR_UNSUPPORTED;
   if (max_rows >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
@@ -459,15 +460,17 @@ size_t moe_grouped_linear_mxfp4_workspace_size(int32_t n_groups, int32_t n_out, 
   return moe::linear_mxfp4_workspace_bytes(n_groups, n_out, k, max_rows);
 }
 
-int moe_grouped_linear_mxfp4(int32_t n_groups, int32_t n_out, int32_t k, const uint8_t *x_codes,
-                             const uint8_t *x_scales, const int32_t *row_index,
-                             const int32_t *offsets, int64_t max_rows, const uint8_t *w_codes,
+int moe_grouped_linear_mxfp4(int32_t n_groups, int32_t n_out, int32_t k, int64_t x_rows,
+                             const uint8_t *x_codes, const uint8_t *x_scales,
+                             const int32_t *row_index, const int32_t *offsets, int64_t max_rows, const uint8_t *w_codes,
                              const uint8_t *w_scales, const void *bias, int32_t silu, void *y_rows,
                              void *ws, size_t ws_bytes, void *stream) {
   const int st = check_linear_mxfp4(n_groups, n_out, k, max_rows);
   if (st != MOE_OK) return st;
-  if (silu != 0 && silu != 1) return MOE_ERR_INVALID_ARG;
+  if (x_rows < 0 || (silu != 0 && silu != 1)) return MOE_ERR_INVALID_ARG;
+  if (x_rows >= (int64_t(1) << 32) / (k / 2)) return MOE_ERR_UNSUPPORTED;
   if (max_rows == 0) return MOE_OK;
+  if (x_rows < (row_index ? 1 : max_rows)) return MOE_ERR_INVALID_ARG;
   if (!x_codes || !x_scales || !offsets || !w_codes || !w_scales || !y_rows)
     return MOE_ERR_INVALID_ARG;
   if (!all_aligned16({x_codes, x_scales, row_index, offsets, w_codes, w_scales, bias, y_rows, ws}))

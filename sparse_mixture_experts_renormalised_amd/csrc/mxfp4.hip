@@ -12,6 +12,7 @@
 // outside float32's subnormal range, rounded to nearest with ties to the even
 // code.  A block that holds an infinity or a NaN has no such scale: its byte
 // is 255 and its codes 0.
+#include "lds_dma.h"
 #include "moe_common.h"
 
 namespace moe {
@@ -20,6 +21,7 @@ namespace {
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 // ---------------------------------------------------------------------------
 // Quantisation
@@ -142,9 +144,22 @@ hipError_t quantize(const void *x, int64_t rows, int d, int64_t stride, uint8_t 
 }
 
 // ---------------------------------------------------------------------------
-// Grouped product
+// Grouped product: y[r, n] = act(sum_k X[r, k] W_g[n, k] + bias_g[n]).
+//
+// Both operands enter the scaled matrix instructions as they lie in memory:
+// v_mfma_scale_f32_*_f8f6f4 multiplies 4-bit codes, applies each block's two
+// scale bytes and adds in float32, so nothing is widened.  Weights are the
+// first operand, so a lane ends up with four consecutive features of a row.
+//
+// Two kernels, by the rows of a group:
+//   * up to kStreamRows rows: bound by the bytes of the weights; operands go
+//     straight from memory to registers, eight waves share the reduction;
+//   * more: 256 x 256 tiles (128 x 256 and 64 x 256 for a group's last rows),
+//     operands through LDS.
 // ---------------------------------------------------------------------------
 constexpr int kMaxGroups = kMaxRouted + kMaxShared;
+constexpr int kXcds = 8;
+constexpr int kStreamRows = 32;
 
 struct MxArgs {
   const uint8_t *x, *xs;         // rows of codes, rows of scale bytes
@@ -156,88 +171,510 @@ struct MxArgs {
   int groups, n_out, k;
 };
 
-// Group of tile mt from the tile prefix: largest g with pref[g] <= mt.
-__device__ __forceinline__ int mx_find_group(const int *pref, int n, int mt) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (pref[mid] <= mt) lo = mid; else hi = mid;
-  }
-  return lo;
+__device__ __forceinline__ int64_t source_row(const MxArgs &a, int64_t r) {
+  return a.index ? static_cast<int64_t>(a.index[r]) : r;
 }
 
-// 16 rows x 64 features per wave, operands straight from memory: the 64 lanes
-// of v_mfma_scale_f32_16x16x128_f8f6f4 hold 16 rows x four blocks of 32
-// elements, each lane one block (16 bytes) and that block's scale byte.
+__device__ __forceinline__ i32x8_t codes32(u32x4_t v) {
+  return i32x8_t{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
+}
+
+// ---- few rows ----
+namespace stream {
+constexpr int WAVES = 8, NT = WAVES * 64, R = 4, BN = 16 * R;
+
+// One item: 64 features of a group with at most 16 C rows.  A lane holds one
+// block (16 bytes of codes and its scale byte) of one row per 128 elements;
+// wave w takes the 128-element chunks w, w + 8, ...
+template <int C, bool SILU>
+__device__ __forceinline__ void item(const MxArgs &a, int g, int64_t first, int rows, int n0,
+                                     float (*s_red)[R * 2][256]) {
+  constexpr int U = C == 1 ? 2 : 1;      // chunks in flight per wave
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int r16 = lane & 15, q = lane >> 4;
+  const int64_t kb = a.k / 2, ksb = a.k / 32;
+  const uint8_t *xp[C], *xsp[C], *wp[R], *wsp[R];
+  bool live[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    live[c] = c * 16 + r16 < rows;
+    const int64_t src = source_row(a, first + (live[c] ? c * 16 + r16 : 0));
+    xp[c] = a.x + src * kb + q * 16;
+    xsp[c] = a.xs + src * ksb + q;
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int64_t n = static_cast<int64_t>(g) * a.n_out + min(n0 + i * 16 + r16, a.n_out - 1);
+    wp[i] = a.w + n * kb + q * 16;
+    wsp[i] = a.ws + n * ksb + q;
+  }
+  f32x4_t acc[R][C];
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[i][c] = f32x4_t{0, 0, 0, 0};
+  const int nch = a.k / 128;
+  for (int c0 = wave; c0 < nch; c0 += WAVES * U) {
+    u32x4_t xv[U][C], wv[U][R];
+    int sx[U][C], sw[U][R];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + u * WAVES;
+      const bool in = c < nch;
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        xv[u][j] = u32x4_t{0, 0, 0, 0};
+        sx[u][j] = 127;
+        if (in && live[j]) {
+          xv[u][j] = *reinterpret_cast<const u32x4_t *>(xp[j] + c * 64);
+          sx[u][j] = xsp[j][c * 4];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        wv[u][i] = u32x4_t{0, 0, 0, 0};
+        sw[u][i] = 127;
+        if (in) {
+          wv[u][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t *>(wp[i] + c * 64));
+          sw[u][i] = wsp[i][c * 4];
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              codes32(wv[u][i]), codes32(xv[u][j]), acc[i][j], 4, 4, 0, sw[u][i], 0, sx[u][j]);
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+      *reinterpret_cast<f32x4_t *>(&s_red[wave][i * C + j][lane * 4]) = acc[i][j];
+  __syncthreads();
+  for (int o = tid; o < rows * BN; o += NT) {
+    const int t = o / BN, nl = o % BN, n = n0 + nl;
+    if (n >= a.n_out) continue;
+    const int f16 = nl & 15, at = ((f16 >> 2) * 16 + (t & 15)) * 4 + (f16 & 3);
+    float z = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) z += s_red[w][(nl >> 4) * C + (t >> 4)][at];
+    if (a.bias) z += bf16_to_f32(a.bias[static_cast<int64_t>(g) * a.n_out + n]);
+    if (SILU) z = silu_fast(z);
+    a.y[(first + t) * a.n_out + n] = f32_to_bf16(z);
+  }
+  __syncthreads();
+}
+}  // namespace stream
+
 template <bool SILU>
-__global__ __launch_bounds__(256) void mx_linear_kernel(MxArgs a) {
-  __shared__ int s_pref[kMaxGroups + 1];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+__global__ __launch_bounds__(stream::NT, 4) void mx_stream_kernel(MxArgs a) {
+  using namespace stream;
+  __shared__ float s_red[WAVES][R * 2][256];
+  __shared__ int16_t s_list[kMaxGroups];
+  __shared__ int s_n;
+  const int tid = threadIdx.x, lane = tid & 63;
   if (tid < 64) {
-    int run = 0;
+    int n = 0;
+    for (int g0 = 0; g0 < a.groups; g0 += 64) {
+      const int g = g0 + lane;
+      const int rows = g < a.groups ? a.offsets[g + 1] - a.offsets[g] : 0;
+      const bool in = rows > 0 && rows <= kStreamRows;
+      const uint64_t m = __ballot(in);
+      if (in) s_list[n + __popcll(m & ((1ull << lane) - 1))] = static_cast<int16_t>(g);
+      n += __popcll(m);
+    }
+    if (tid == 0) s_n = n;
+  }
+  __syncthreads();
+  const int nblk = (a.n_out + BN - 1) / BN, items = uniform(s_n) * nblk;
+  for (int it = blockIdx.x; it < items; it += gridDim.x) {
+    const int i = it / nblk, g = uniform(s_list[i]), n0 = (it - i * nblk) * BN;
+    const int64_t first = a.offsets[g];
+    const int rows = static_cast<int>(a.offsets[g + 1] - first);
+    if (rows <= 16) item<1, SILU>(a, g, first, rows, n0, s_red);
+    else item<2, SILU>(a, g, first, rows, n0, s_red);
+  }
+}
+
+// ---- many rows ----
+// Tiles of BM rows x 256 features, four waves of BM/2 x 128 (TM x 4 blocks of
+// 32 x 32).  A step of 256 elements is 128 bytes per row; two LDS buffers hold
+// the steps' codes, filled two steps ahead by global-to-LDS copies that are
+// spread among the matrix instructions, and every step's fragments sit in
+// registers before its first instruction.  The scale bytes come in pairs of
+// steps (16 bytes per row), in two LDS buffers of their own.
+//
+// 16-byte chunk c of tile row r lies at position c ^ ((r / 2) % 8) of its
+// 128-byte row, so that the 16 rows read together cover all banks once.
+namespace tile {
+constexpr int NT = 256, BN = 256, NS = 4, TN = 4, BUF = 2 * 512 * 128, SBUF = 512 * 16;
+
+__device__ __forceinline__ int swz(int r, int c) { return c ^ ((r >> 1) & 7); }
+
+// Workgroup barrier that waits for this wave's LDS reads; matrix instructions
+// may move across it.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+template <int BM>
+struct Tile {
+  static constexpr int TM = BM / 64, AC = BM / 32, BC = 8, NCP = AC + BC;   // code copies per wave
+  static constexpr int SC = 4, N = NCP + SC;                                // scale, all copies
+  static constexpr int STEP = (BM + BN) * 128, SPAIR = 512 * 16;            // LDS bytes
+  static constexpr int MF = NS * TN * TM;
+
+  // Byte offsets of this lane's part of each copy, from wave-uniform bases (the
+  // host refuses operands of 4 GiB or more), at step 0.
+  struct Src {
+    uint32_t a[AC], b[BC];     // 16-byte chunks of X and W rows
+    uint32_t sa[SC], sb[SC];   // their scale rows
+    const uint8_t *abase, *bbase, *sabase, *sbbase;
+    int tadj;                  // byte correction of this lane in a half last step
+    int nk, nd;                // steps, 128-element units
+  };
+  struct Frags {
+    u32x4_t a[NS][TM], b[NS][TN];
+    uint32_t sa[TM], sb[TN];   // byte ks: scale of this lane's block of slice ks
+  };
+  using Acc = f32x16_t[TN][TM];
+
+  static __device__ __forceinline__ void source(const MxArgs &a, int g, int64_t first, int64_t row0,
+                                                int64_t rows, int n0, int tid, Src &s) {
+    const int64_t kb = a.k / 2, ksb = a.k / 32;
+    const int c = (tid & 7) ^ ((tid >> 4) & 7);       // row = tid/8 + 32i
+    // scale copy j of wave w: rows 16 (w + 4 j) .. +15, four lanes of 4 bytes a
+    // row (rows past the tile repeat the last one, here and for the codes)
+    const int sr = (tid >> 6) * 16 + ((tid & 63) >> 2);
+    int64_t ra[AC], rs[SC];
+#pragma unroll
+    for (int i = 0; i < AC; ++i) ra[i] = first + min(row0 + (tid >> 3) + i * 32, rows - 1);
+#pragma unroll
+    for (int j = 0; j < SC; ++j) rs[j] = first + min(row0 + sr + j * 64, rows - 1);
+    if (a.index) {
+#pragma unroll
+      for (int i = 0; i < AC; ++i) ra[i] = a.index[ra[i]];
+#pragma unroll
+      for (int j = 0; j < SC; ++j) rs[j] = a.index[rs[j]];
+    }
+#pragma unroll
+    for (int i = 0; i < AC; ++i) s.a[i] = static_cast<uint32_t>(ra[i] * kb) + c * 16;
+    s.abase = a.x;
+    s.sabase = a.xs;
+    s.sbbase = a.ws + static_cast<int64_t>(g) * a.n_out * ksb;
+    s.bbase = a.w + static_cast<int64_t>(g) * a.n_out * kb;
+#pragma unroll
+    for (int i = 0; i < BC; ++i)
+      s.b[i] = static_cast<uint32_t>(min(n0 + (tid >> 3) + i * 32, a.n_out - 1)) *
+                   static_cast<uint32_t>(kb) + c * 16;
+#pragma unroll
+    for (int j = 0; j < SC; ++j) {
+      s.sa[j] = static_cast<uint32_t>(rs[j] * ksb);
+      s.sb[j] = static_cast<uint32_t>(min(n0 + sr + j * 64, a.n_out - 1)) * static_cast<uint32_t>(ksb);
+    }
+    s.nd = a.k / 128;
+    s.nk = (s.nd + 1) / 2;
+    s.tadj = (s.nd & 1) && c >= 4 ? -64 : 0;
+  }
+
+  // Byte offset of step kb for this lane; a half last step reads its first
+  // half twice (the second is not multiplied).
+  static __device__ __forceinline__ int step_off(const Src &s, int kb) {
+    return kb * 128 + (kb == s.nk - 1 ? s.tadj : 0);
+  }
+  static __device__ __forceinline__ void copy(const Src &s, int i, int off, uint32_t base, int wave) {
+    if (i < AC) dma::dma16s(s.a[i] + off, s.abase, base + (4 * i + wave) * 1024);
+    else dma::dma16s(s.b[i - AC] + off, s.bbase, base + BM * 128 + (4 * (i - AC) + wave) * 1024);
+  }
+  // Scale copies: the rows of X (which 0) or W (1) for the steps 2p and 2p + 1.
+  static __device__ __forceinline__ int pair_off(const Src &s, int p, int lane) {
+    return min(4 * p + (lane & 3), s.nd - 1) * 4;
+  }
+  static __device__ __forceinline__ void scale_copy(const Src &s, int j, bool of_w, int off,
+                                                    uint32_t base, int wave) {
+    dma::dma4s((of_w ? s.sb[j] : s.sa[j]) + off, of_w ? s.sbbase : s.sabase,
+               base + (of_w ? 256 * 16 : 0) + (4 * j + wave) * 256);
+  }
+
+  // Fragments and scales of a step: lane half h takes block 2 ks + h in slice
+  // ks, so of the row's eight scale bytes it keeps the even or the odd four.
+  static __device__ __forceinline__ void read(const uint8_t *buf, const uint8_t *sbuf, int half,
+                                              Frags &f, int wm, int wn, int lane) {
+    const int h = lane >> 5, r32 = lane & 31;
+    const uint32_t pick = h ? 0x07050301u : 0x06040200u;
+#pragma unroll
+    for (int mi = 0; mi < TM; ++mi) {
+      const int row = wm * (BM / 2) + mi * 32 + r32;
+      const uint2 sv = *reinterpret_cast<const uint2 *>(sbuf + row * 16 + half * 8);
+      f.sa[mi] = __builtin_amdgcn_perm(sv.y, sv.x, pick);
+    }
+#pragma unroll
+    for (int ni = 0; ni < TN; ++ni) {
+      const int row = 256 + wn * 128 + ni * 32 + r32;
+      const uint2 sv = *reinterpret_cast<const uint2 *>(sbuf + row * 16 + half * 8);
+      f.sb[ni] = __builtin_amdgcn_perm(sv.y, sv.x, pick);
+    }
+#pragma unroll
+    for (int ks = 0; ks < NS; ++ks) {
+      const int c = ks * 2 + h;
+#pragma unroll
+      for (int mi = 0; mi < TM; ++mi) {
+        const int row = wm * (BM / 2) + mi * 32 + r32;
+        f.a[ks][mi] = *reinterpret_cast<const u32x4_t *>(buf + row * 128 + swz(row, c) * 16);
+      }
+#pragma unroll
+      for (int ni = 0; ni < TN; ++ni) {
+        const int row = wn * 128 + ni * 32 + r32;
+        f.b[ks][ni] =
+            *reinterpret_cast<const u32x4_t *>(buf + BM * 128 + row * 128 + swz(row, c) * 16);
+      }
+    }
+  }
+
+  // Matrix instructions M0 .. M1-1 of a step, in (slice, ni, mi) order.
+  template <int M0, int M1>
+  static __device__ __forceinline__ void mfma(const Frags &f, Acc &acc) {
+    if constexpr (M0 < M1) {
+      constexpr int ks = M0 / (TN * TM), ni = (M0 / TM) % TN, mi = M0 % TM;
+      acc[ni][mi] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+          codes32(f.b[ks][ni]), codes32(f.a[ks][mi]), acc[ni][mi], 4, 4, ks, f.sb[ni], ks,
+          f.sa[mi]);
+      mfma<M0 + 1, M1>(f, acc);
+    }
+  }
+
+  // Copies I.. of a step spread over the first three slices.
+  template <int I>
+  static __device__ __forceinline__ void copies_mfmas(const Src &s, int off, bool of_w, int soff,
+                                                      uint32_t base, uint32_t sbase, int wave,
+                                                      const Frags &f, Acc &acc) {
+    if constexpr (I < N) {
+      constexpr int M3 = MF / 4 * 3;
+      if constexpr (I < NCP) copy(s, I, off, base, wave);
+      else scale_copy(s, I - NCP, of_w, soff, sbase, wave);
+      mfma<I * M3 / N, (I + 1) * M3 / N>(f, acc);
+      __builtin_amdgcn_sched_barrier(0);
+      copies_mfmas<I + 1>(s, off, of_w, soff, base, sbase, wave, f, acc);
+    }
+  }
+
+  static __device__ __forceinline__ void body(const Src &s, uint8_t *buf, uint8_t *sbuf, Acc &acc,
+                                              int wave, int wm, int wn, int lane) {
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int j = 0; j < TM; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+    const uint32_t b0 = uniform(static_cast<int>(dma::lds_addr(buf))), b1 = b0 + STEP;
+    const uint32_t sb0 = uniform(static_cast<int>(dma::lds_addr(sbuf)));
+    Frags f;
+    const int soff0 = pair_off(s, 0, lane), soff1 = pair_off(s, 1, lane);
+#pragma unroll
+    for (int j = 0; j < SC; ++j) {
+      scale_copy(s, j, false, soff0, sb0, wave);
+      scale_copy(s, j, true, soff0, sb0, wave);
+      scale_copy(s, j, false, soff1, sb0 + SPAIR, wave);
+    }
+    const int off0 = step_off(s, 0);
+#pragma unroll
+    for (int i = 0; i < NCP; ++i) copy(s, i, off0, b0, wave);
+    if (s.nk > 1) {
+      const int off1 = step_off(s, 1);
+#pragma unroll
+      for (int i = 0; i < NCP; ++i) copy(s, i, off1, b1, wave);
+      dma::wait_and_barrier<NCP>();
+    } else {
+      dma::wait_and_barrier<0>();
+    }
+    read(buf, sbuf, 0, f, wm, wn, lane);
+    __builtin_amdgcn_sched_barrier(0);
+    // Step kb, with the copies of step kb + 2 into the buffer that its
+    // fragments have left.  Scales of the pair p of steps 2p, 2p + 1: those of
+    // X during step 2p - 3, when the second step of pair p - 2, the buffer's
+    // last user, is in registers; those of W during step 2p - 2.
+    int kb = 0;
+    for (; kb + 2 < s.nk; ++kb) {
+      const int cur = kb & 1;
+      lds_barrier();                       // every wave holds its fragments of step kb
+      __builtin_amdgcn_sched_barrier(0);
+      const int p = (kb + 3) >> 1;
+      copies_mfmas<0>(s, step_off(s, kb + 2), cur == 0, pair_off(s, p, lane), cur ? b1 : b0,
+                      sb0 + (p & 1) * SPAIR, wave, f, acc);
+      dma::wait_and_barrier<N>();          // step kb + 1 has landed for every wave
+      mfma<MF / 4 * 3, MF>(f, acc);
+      read(buf + (cur ? 0 : STEP), sbuf + (((kb + 1) >> 1) & 1) * SPAIR, 1 - cur, f, wm, wn, lane);
+      constexpr int READS = NS * (TM + TN) + TM + TN, LAST = MF / 4;
+#pragma unroll
+      for (int i = 0; i < LAST; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x100, (READS + LAST - 1) / LAST, 0);   // LDS reads
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                           // matrix
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (kb + 1 < s.nk) {
+      mfma<0, MF>(f, acc);
+      dma::wait_and_barrier<0>();
+      ++kb;
+      read(buf + (kb & 1) * STEP, sbuf + ((kb >> 1) & 1) * SPAIR, kb & 1, f, wm, wn, lane);
+    }
+    mfma<0, MF / 2>(f, acc);
+    if (!(s.nd & 1)) mfma<MF / 2, MF>(f, acc);
+    lds_barrier();                       // buffers are free
+  }
+
+  // Bias, SiLU and bf16 rounding into LDS rows of 256 features (16-byte chunks
+  // swizzled by the row), then whole-row stores.
+  template <bool SILU, bool BIAS>
+  static __device__ __forceinline__ void epilogue(const Acc &acc, const MxArgs &a, int g,
+                                                  int64_t first, int64_t row0, int64_t rows, int n0,
+                                                  uint8_t *buf, int wm, int wn, int lane, int tid) {
+    uint16_t *st = reinterpret_cast<uint16_t *>(buf);
+#pragma unroll
+    for (int ni = 0; ni < TN; ++ni)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int nl = wn * 128 + ni * 32 + q * 8 + (lane >> 5) * 4, n = n0 + nl;
+        float bv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (BIAS && n < a.n_out) {
+          const uint2 b = *reinterpret_cast<const uint2 *>(a.bias + static_cast<int64_t>(g) * a.n_out + n);
+          bv[0] = __uint_as_float(b.x << 16);
+          bv[1] = __uint_as_float(b.x & 0xFFFF0000u);
+          bv[2] = __uint_as_float(b.y << 16);
+          bv[3] = __uint_as_float(b.y & 0xFFFF0000u);
+        }
+#pragma unroll
+        for (int mi = 0; mi < TM; ++mi) {
+          const int ml = wm * (BM / 2) + mi * 32 + (lane & 31);
+          float o[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            o[j] = acc[ni][mi][q * 4 + j];
+            if (BIAS) o[j] += bv[j];
+            if (SILU) o[j] = silu_fast(o[j]);
+          }
+          uint2 p;
+          p.x = pack_bf16x2(o[0], o[1]);
+          p.y = pack_bf16x2(o[2], o[3]);
+          *reinterpret_cast<uint2 *>(st + ml * BN + ((nl >> 3) ^ (ml & 31)) * 8 + ((nl >> 2) & 1) * 4) = p;
+        }
+      }
+    lds_barrier();
+    const int c = tid & 31, r0 = tid >> 5, n = n0 + c * 8;
+    if (n < a.n_out) {
+      uint16_t *out = a.y + (first + row0 + r0) * a.n_out + n;
+      const int64_t lim = rows - row0 - r0;
+#pragma unroll 8
+      for (int j = 0; j < BM / 8; ++j) {
+        const int r = r0 + 8 * j;
+        const u32x4_t v = *reinterpret_cast<const u32x4_t *>(st + r * BN + ((c ^ (r & 31)) << 3));
+        if (8 * j < lim) store_nt(out + static_cast<int64_t>(8 * j) * a.n_out, v);
+      }
+    }
+    lds_barrier();
+  }
+
+  template <bool SILU>
+  static __device__ __forceinline__ void run(const MxArgs &a, int g, int64_t row0, int n0, uint8_t *buf,
+                                             uint8_t *sbuf) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int wm = wave & 1, wn = wave >> 1;
+    const int64_t first = a.offsets[g], rows = a.offsets[g + 1] - first;
+    Src s;
+    source(a, g, first, row0, rows, n0, tid, s);
+    Acc acc;
+    body(s, buf, sbuf, acc, wave, wm, wn, lane);
+    if (a.bias) epilogue<SILU, true>(acc, a, g, first, row0, rows, n0, buf, wm, wn, lane, tid);
+    else epilogue<SILU, false>(acc, a, g, first, row0, rows, n0, buf, wm, wn, lane, tid);
+  }
+};
+}  // namespace tile
+
+// Full tiles of a group and the height of the tile that takes what is left:
+// 0, 64 or 128 (a remainder above 128 rows is a full tile).
+__device__ __forceinline__ int mx_full_tiles(int rows, int *tail) {
+  const int r = rows % 256;
+  *tail = rows <= kStreamRows || r == 0 || r > 128 ? 0 : r <= 64 ? 64 : 128;
+  if (rows <= kStreamRows) return 0;
+  return rows / 256 + (r > 128 ? 1 : 0);
+}
+
+// Persistent workgroups, one per CU.  The full tiles, in bands of four row
+// tiles, then the 128- and the 64-row tiles are each split into eight
+// contiguous shares, one per XCD (workgroups are dealt to the XCDs round-robin
+// by number), so that tiles running together on an XCD share operands in its L2.
+template <bool SILU>
+__global__ __launch_bounds__(tile::NT, 1) void mx_tile_kernel(MxArgs a) {
+  using namespace tile;
+  __shared__ __attribute__((aligned(16))) uint8_t s_buf[BUF];
+  __shared__ __attribute__((aligned(16))) uint8_t s_sc[2 * SBUF];
+  __shared__ int s_pref[kMaxGroups + 1];
+  __shared__ int16_t s_t128[kMaxGroups], s_t64[kMaxGroups];
+  __shared__ int s_cnt[2];
+  const int tid = threadIdx.x;
+  if (tid < 64) {
+    int full = 0, n128 = 0, n64 = 0;
+    const uint64_t below = (1ull << tid) - 1;
     for (int g0 = 0; g0 < a.groups; g0 += 64) {
       const int g = g0 + tid;
-      const int n = g < a.groups ? (a.offsets[g + 1] - a.offsets[g] + 15) / 16 : 0;
+      int t = 0;
+      const int n = g < a.groups ? mx_full_tiles(a.offsets[g + 1] - a.offsets[g], &t) : 0;
       int incl = n;
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) {
         const int o = __shfl_up(incl, off);
-        if (lane >= off) incl += o;
+        if (tid >= off) incl += o;
       }
-      if (g < a.groups) s_pref[g] = run + incl - n;
-      run += __shfl(incl, 63);
+      if (g < a.groups) s_pref[g] = full + incl - n;
+      full += __shfl(incl, 63);
+      const uint64_t m128 = __ballot(t == 128), m64 = __ballot(t == 64);
+      if (t == 128) s_t128[n128 + __popcll(m128 & below)] = static_cast<int16_t>(g);
+      if (t == 64) s_t64[n64 + __popcll(m64 & below)] = static_cast<int16_t>(g);
+      n128 += __popcll(m128);
+      n64 += __popcll(m64);
     }
-    if (tid == 0) s_pref[a.groups] = run;
+    if (tid == 0) {
+      s_pref[a.groups] = full;
+      s_cnt[0] = n128;
+      s_cnt[1] = n64;
+    }
   }
   __syncthreads();
-  const int tiles = s_pref[a.groups];
-  const int r16 = lane & 15, q = lane >> 4;
-  const int64_t kb = a.k / 2, ksb = a.k / 32;
-  for (int mt = blockIdx.y; mt < tiles; mt += gridDim.y) {
-    const int g = mx_find_group(s_pref, a.groups, mt);
-    const int64_t first = a.offsets[g];
-    const int64_t rows = a.offsets[g + 1] - first;
-    const int64_t r0 = static_cast<int64_t>(mt - s_pref[g]) * 16;
-    const int64_t rr = first + min(r0 + r16, rows - 1);
-    const int64_t src = a.index ? static_cast<int64_t>(a.index[rr]) : rr;
-    const uint8_t *xp = a.x + src * kb + q * 16, *xsp = a.xs + src * ksb + q;
-    const int n0 = blockIdx.x * 256 + wave * 64;
-    const uint8_t *wp[4], *wsp[4];
-    f32x4_t acc[4] = {};
+  const int nt = (a.n_out + BN - 1) / BN;
+  const int total[3] = {uniform(s_pref[a.groups]) * nt, uniform(s_cnt[0]) * nt, uniform(s_cnt[1]) * nt};
+  const int xcd = blockIdx.x % kXcds, slot = blockIdx.x / kXcds, slots = gridDim.x / kXcds;
+  int begin[3], cnt[3];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t n = static_cast<int64_t>(g) * a.n_out + min(n0 + i * 16 + r16, a.n_out - 1);
-      wp[i] = a.w + n * kb + q * 16;
-      wsp[i] = a.ws + n * ksb + q;
-    }
-    for (int k = 0; k < a.k / 128; ++k) {
-      const u32x4_t xv = *reinterpret_cast<const u32x4_t *>(xp + k * 64);
-      const int sx = xsp[k * 4];
-      const i32x8_t b = {(int)xv[0], (int)xv[1], (int)xv[2], (int)xv[3], 0, 0, 0, 0};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const u32x4_t wv = *reinterpret_cast<const u32x4_t *>(wp[i] + k * 64);
-        const int sw = wsp[i][k * 4];
-        const i32x8_t w = {(int)wv[0], (int)wv[1], (int)wv[2], (int)wv[3], 0, 0, 0, 0};
-        acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, b, acc[i], 4, 4, 0, sw, 0, sx);
+  for (int l = 0; l < 3; ++l) {
+    const int part = (total[l] + kXcds - 1) / kXcds;
+    begin[l] = min(xcd * part, total[l]);
+    cnt[l] = min(begin[l] + part, total[l]) - begin[l];
+  }
+  for (int it = slot; it < cnt[0] + cnt[1] + cnt[2]; it += slots) {
+    if (it < cnt[0]) {
+      constexpr int GM = 4;
+      const int L = begin[0] + it, tm = s_pref[a.groups];
+      const int band = L / (GM * nt), m0 = band * GM, gm = min(GM, tm - m0), r = L - band * GM * nt;
+      const int mt = m0 + r % gm, n = r / gm;
+      int lo = 0, hi = a.groups;         // s_pref[lo] <= mt < s_pref[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_pref[mid] <= mt) lo = mid; else hi = mid;
       }
-    }
-    if (r0 + r16 >= rows) continue;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = n0 + i * 16 + q * 4;
-      if (n >= a.n_out) continue;
-      float o[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        o[j] = acc[i][j];
-        if (a.bias) o[j] += bf16_to_f32(a.bias[static_cast<int64_t>(g) * a.n_out + n + j]);
-        if (SILU) o[j] = silu_fast(o[j]);
-      }
-      uint2 p;
-      p.x = pack_bf16x2(o[0], o[1]);
-      p.y = pack_bf16x2(o[2], o[3]);
-      *reinterpret_cast<uint2 *>(a.y + (first + r0 + r16) * a.n_out + n) = p;
+      const int g = uniform(lo);
+      Tile<256>::run<SILU>(a, g, static_cast<int64_t>(mt - s_pref[g]) * 256, n * BN, s_buf, s_sc);
+    } else {
+      const int i = it - cnt[0];
+      const bool wide = i < cnt[1];
+      const int q = wide ? begin[1] + i : begin[2] + i - cnt[1];
+      const int g = uniform(wide ? s_t128[q / nt] : s_t64[q / nt]), n0 = (q % nt) * BN;
+      const int64_t row0 = (a.offsets[g + 1] - a.offsets[g]) / 256 * 256;
+      if (wide) Tile<128>::run<SILU>(a, g, row0, n0, s_buf, s_sc);
+      else Tile<64>::run<SILU>(a, g, row0, n0, s_buf, s_sc);
     }
   }
 }
@@ -253,12 +690,18 @@ hipError_t launch_quantize_mxfp4(bool bf16, const void *x, int64_t rows, int d, 
 hipError_t launch_linear_mxfp4(const MxLinear &p, hipStream_t s) {
   MxArgs a{p.x, p.xs, p.index, p.offsets, p.w, p.ws, static_cast<const uint16_t *>(p.bias),
            static_cast<uint16_t *>(p.y), p.groups, p.n_out, p.k};
-  const int64_t tiles = p.max_rows / 16 + (p.max_rows < p.groups ? p.max_rows : p.groups) + 1;
-  const dim3 grid((p.n_out + 255) / 256, static_cast<unsigned>(tiles < 2048 ? tiles : 2048));
-  if (p.silu)
-    hipLaunchKernelGGL(mx_linear_kernel<true>, grid, dim3(256), 0, s, a);
-  else
-    hipLaunchKernelGGL(mx_linear_kernel<false>, grid, dim3(256), 0, s, a);
+  // the groups' row counts are on the device: both kernels look, each takes
+  // the groups of its size
+  const int64_t met = p.max_rows < p.groups ? p.max_rows : p.groups;
+  const int64_t items = met * ((p.n_out + stream::BN - 1) / stream::BN);
+  const dim3 sgrid(static_cast<unsigned>(items < 512 ? items : 512));
+  if (p.silu) hipLaunchKernelGGL(mx_stream_kernel<true>, sgrid, dim3(stream::NT), 0, s, a);
+  else hipLaunchKernelGGL(mx_stream_kernel<false>, sgrid, dim3(stream::NT), 0, s, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.max_rows <= kStreamRows) return e;
+  const dim3 tgrid(256);
+  if (p.silu) hipLaunchKernelGGL(mx_tile_kernel<true>, tgrid, dim3(tile::NT), 0, s, a);
+  else hipLaunchKernelGGL(mx_tile_kernel<false>, tgrid, dim3(tile::NT), 0, s, a);
   return hipGetLastError();
 }
 

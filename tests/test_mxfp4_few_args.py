@@ -33,9 +33,9 @@ def test_quantize_refusals(B):
         assert quant(B, **bad) == -2, bad
 
 
-def linear(B, g=3, n=64, k=128, xc=4096, xs=4096, idx=None, off=4096, rows=8, wc=4096, ws_=4096,
+def linear(B, g=3, n=64, k=128, xr=8, xc=4096, xs=4096, idx=None, off=4096, rows=8, wc=4096, ws_=4096,
            bias=None, silu=0, y=4096, ws=None, nbytes=0):
-    return B.lib().moe_grouped_linear_mxfp4(g, n, k, P(xc), P(xs), P(idx), P(off), rows, P(wc),
+    return B.lib().moe_grouped_linear_mxfp4(g, n, k, xr, P(xc), P(xs), P(idx), P(off), rows, P(wc),
                                             P(ws_), P(bias), silu, P(y), P(ws), nbytes, None)
 
 
@@ -44,9 +44,10 @@ def test_linear_refusals(B):
     for bad in ({"g": 0}, {"n": 0}, {"k": 0}, {"rows": -1}, {"silu": 2}, {"xc": None}, {"xs": None},
                 {"off": None}, {"wc": None}, {"ws_": None}, {"y": None}, {"xc": 4104}, {"xs": 4100},
                 {"idx": 4100}, {"off": 4100}, {"wc": 4104}, {"ws_": 4100}, {"bias": 4104}, {"y": 4104},
-                {"ws": 4100, "nbytes": 1 << 40}):
+                {"ws": 4100, "nbytes": 1 << 40}, {"xr": -1}, {"xr": 7}, {"xr": 0, "idx": 4096}):
         assert linear(B, **bad) == -1, bad
-    for bad in ({"n": 60}, {"k": 64}, {"k": 192}, {"g": 1089}, {"rows": 1 << 31}):
+    for bad in ({"n": 60}, {"k": 64}, {"k": 192}, {"g": 1089}, {"rows": 1 << 31, "xr": 1 << 31},
+                {"xr": 1 << 26}, {"k": 1 << 20, "n": 1 << 13}):
         assert linear(B, **bad) == -2, bad
     need = B.grouped_linear_mxfp4_workspace_size(3, 64, 128, 8)
     if need:
