@@ -6,12 +6,11 @@
 // more kernels and keeps per-expert row lists in memory; here
 //
 //   kernel 1 (few_logits_kernel) computes the router's logits, one workgroup
-//     per expert, and clears the counters that kernel 2 uses;
+//     per expert, and clears the shares' states and the counts of kernel 2;
 //   kernel 2 (few_layer_kernel) does the rest.  Every workgroup repeats the
 //     top-K selection, gates and capacity from the logits (T * N numbers)
-//     into LDS, and then takes work items in order from one counter: first
-//     the hidden rows of every met or shared expert (up items), then the
-//     output rows (down items).
+//     into LDS.  Then come the hidden rows of every met or shared expert (up
+//     items), and after them the output rows (down items).
 //
 // The 16 tokens are the 16 columns of one matrix instruction, and the rows of
 // a weight matrix are its rows: a wave multiplies 16 R weight rows by a share
@@ -26,15 +25,20 @@
 // significant bits, for the price of a second matrix instruction on a
 // bandwidth-bound path); float32 layers keep float32.
 //
-// Waiting.  A down item needs every hidden row, so it waits until the count of
-// finished up items is complete.  Items are taken in counter order, so an up
-// item belongs to a workgroup that is already running, and no workgroup waits
-// while it holds an unfinished up item (the item fetched ahead has a higher
-// number than the one in work): every wait ends, whatever the number of
-// resident workgroups and whatever else runs on the device.
+// Waiting.  A down item needs every hidden row.  The up items are dealt to as
+// many shares as there are workgroups, and a share has a state: free, taken,
+// done.  A workgroup takes its own share first, and where it then waits for all
+// shares to be done, it takes any that is still free (its workgroup has not
+// started yet).  So a share that is waited for is either taken, by a workgroup
+// that runs and does not wait before it is done, or will be taken by one that
+// waits: every wait ends, whatever the number of resident workgroups and
+// whatever else runs on the device.  One counter that deals the items out would
+// be simpler, but atomics on one address cost about 80 ns each here.
 //
 // Results do not depend on timing: sums are split in a way fixed by the sizes
 // and joined in a fixed order.
+#include <type_traits>
+
 #include "moe_common.h"
 
 namespace moe {
@@ -45,6 +49,7 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
+enum : uint32_t { kFree = 0, kTaken = 1, kDone = 2 };   // states of an up share
 constexpr int kTok = 16;            // columns of the matrix instruction
 constexpr int kWaves = 8;
 constexpr int kThreads = kWaves * 64;
@@ -65,48 +70,56 @@ __device__ __forceinline__ float4 load4<uint16_t>(const uint16_t *p) {
                      __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
 }
 
-// One workgroup per expert: thread i sums elements 4i, 4i + 1024, ... of
-// W_e . x_t for each token, then the wave and the four waves are added in a
-// fixed tree.
-template <typename T>
-__global__ __launch_bounds__(256) void few_logits_kernel(const T *__restrict__ x,
-                                                         const float *__restrict__ w,
-                                                         const float *__restrict__ bias,
-                                                         float *__restrict__ logits, int tokens,
-                                                         int d, int N, uint32_t *ctr, int n_ctr) {
-  __shared__ float s_part[4][kTok];
+// One workgroup per expert: thread i sums elements 4i, 4i + 4096, ... of
+// W_e . x_t for each token, then the wave and the sixteen waves are added in a
+// fixed tree.  TT is T rounded up to a power of two (the loads of a step are
+// issued together); columns past T repeat the last token and are not stored.
+constexpr int kLogitThreads = 1024;
+template <typename T, int TT>
+__global__ __launch_bounds__(kLogitThreads) void few_logits_kernel(
+    const T *__restrict__ x, const float *__restrict__ w, const float *__restrict__ bias,
+    float *__restrict__ logits, int tokens, int d, int N, uint32_t *zero, int n_zero) {
+  constexpr int NW = kLogitThreads / 64;
+  __shared__ float s_part[NW][TT];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int e = blockIdx.x;
   if (e == 0)
-    for (int i = tid; i < n_ctr; i += 256) ctr[i] = 0;
+    for (int i = tid; i < n_zero; i += kLogitThreads) zero[i] = 0;
   const float *wr = w + static_cast<int64_t>(e) * d;
-  float acc[kTok];
+  float acc[TT];
 #pragma unroll
-  for (int t = 0; t < kTok; ++t) acc[t] = 0.0f;
-  for (int k = tid * 4; k < d; k += 1024) {
+  for (int t = 0; t < TT; ++t) acc[t] = 0.0f;
+  for (int k = tid * 4; k < d; k += kLogitThreads * 4) {
     const float4 wv = load4<float>(wr + k);
+    float4 xv[TT];
 #pragma unroll
-    for (int t = 0; t < kTok; ++t) {
-      if (t >= tokens) break;
-      const float4 xv = load4<T>(x + static_cast<int64_t>(t) * d + k);
-      acc[t] = __builtin_fmaf(wv.x, xv.x, acc[t]);
-      acc[t] = __builtin_fmaf(wv.y, xv.y, acc[t]);
-      acc[t] = __builtin_fmaf(wv.z, xv.z, acc[t]);
-      acc[t] = __builtin_fmaf(wv.w, xv.w, acc[t]);
+    for (int t = 0; t < TT; ++t)
+      xv[t] = load4<T>(x + static_cast<int64_t>(min(t, tokens - 1)) * d + k);
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      acc[t] = __builtin_fmaf(wv.x, xv[t].x, acc[t]);
+      acc[t] = __builtin_fmaf(wv.y, xv[t].y, acc[t]);
+      acc[t] = __builtin_fmaf(wv.z, xv[t].z, acc[t]);
+      acc[t] = __builtin_fmaf(wv.w, xv[t].w, acc[t]);
     }
   }
 #pragma unroll
-  for (int t = 0; t < kTok; ++t) {
-    if (t >= tokens) break;
+  for (int off = 32; off >= 1; off >>= 1)
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) acc[t] += __shfl_xor(acc[t], off);
-    if (lane == 0) s_part[wave][t] = acc[t];
-  }
+    for (int t = 0; t < TT; ++t) acc[t] += __shfl_xor(acc[t], off);
+  if (lane == 0)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) s_part[wave][t] = acc[t];
   __syncthreads();
   if (tid < tokens) {
-    float v = (s_part[0][tid] + s_part[1][tid]) + (s_part[2][tid] + s_part[3][tid]);
-    if (bias) v += bias[e];
-    logits[static_cast<int64_t>(tid) * N + e] = v;
+    float v[NW];
+#pragma unroll
+    for (int i = 0; i < NW; ++i) v[i] = s_part[i][tid];
+#pragma unroll
+    for (int n = NW / 2; n >= 1; n /= 2)
+#pragma unroll
+      for (int i = 0; i < n; ++i) v[i] += v[i + n];
+    logits[static_cast<int64_t>(tid) * N + e] = bias ? v[0] + bias[e] : v[0];
   }
 }
 
@@ -120,7 +133,8 @@ struct FewArgs {
   const uint8_t *c1, *c2, *cs1, *cs2;   // scale bytes of MXFP4 weights
   void *h;                               // hidden rows: float, or bf16 parts [2][rows][f]
   float *part;                           // [S][T][d] parts of split outputs
-  uint32_t *ctr;                         // ticket, finished up items, arrivals per row block
+  uint32_t *state;                       // [grid] of the up shares
+  uint32_t *arrived;                     // [row blocks] finished parts of split outputs
   void *y;
   int32_t *idx;
   float *gate;
@@ -156,21 +170,24 @@ template <int W> struct BFrag {
   u32x4_t v[Kind<W>::NB];
 };
 
+// Part of chunk c of this lane's row: row is the row's (and the lane's) byte
+// offset from the matrix, which lies at a wave-uniform address.
 template <int W>
-__device__ __forceinline__ void load_a(AFrag<W> &a, const uint8_t *p, const uint8_t *sp, int c) {
+__device__ __forceinline__ void load_a(AFrag<W> &a, const uint8_t *base, uint32_t row, int c) {
 #pragma unroll
   for (int j = 0; j < Kind<W>::NA; ++j)
-    a.v[j] = __builtin_nontemporal_load(
-        reinterpret_cast<const u32x4_t *>(p + static_cast<int64_t>(c) * Kind<W>::ABYTES) + j);
-  if constexpr (W == kWMx) a.s = sp[c * 4];
+    a.v[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t *>(
+        base + (row + static_cast<uint32_t>(c) * Kind<W>::ABYTES + j * 16)));
 }
 template <int W>
-__device__ __forceinline__ void load_b(BFrag<W> &b, const uint8_t *p, bool live, int c) {
+__device__ __forceinline__ void load_b(BFrag<W> &b, const uint8_t *base, uint32_t row, bool live,
+                                       int c) {
 #pragma unroll
   for (int j = 0; j < Kind<W>::NB; ++j) {
     b.v[j] = u32x4_t{0, 0, 0, 0};
     if (live)
-      b.v[j] = *(reinterpret_cast<const u32x4_t *>(p + static_cast<int64_t>(c) * Kind<W>::BBYTES) + j);
+      b.v[j] = *reinterpret_cast<const u32x4_t *>(
+          base + (row + static_cast<uint32_t>(c) * Kind<W>::BBYTES + j * 16));
   }
 }
 
@@ -182,6 +199,9 @@ __device__ __forceinline__ bf16x8_t widen_mx(uint32_t c, float scale) {
   const bf16x2_t e = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 3);
   return bf16x8_t{a[0], a[1], b[0], b[1], d[0], d[1], e[0], e[1]};
 }
+
+// Chunks in flight per wave.
+template <int W> constexpr int kDepth = 2;
 
 // acc += A (B0 + B1), 16 weight rows x 16 columns.
 template <int W, bool TWO>
@@ -223,6 +243,33 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
+// Largest value of the wave: within each row of 16 lanes by lane permutations,
+// then the four rows.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0xB1, 0xF, 0xF, true)));
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0x4E, 0xF, 0xF, true)));
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0x141, 0xF, 0xF, true)));
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0x140, 0xF, 0xF, true)));
+  const uint32_t a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
+  const uint32_t c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
+  return max(max(a, b), max(c, d));
+}
+
+// Stores and loads of data that other workgroups of the same launch read or
+// wrote: at device scope, so they pass the L2 caches of the eight XCDs, which
+// are not coherent with each other.  A fence in their place would write back a
+// whole L2 for every item (measured: 121 us for the layer that takes 116 MB of
+// weights, against REPLACED us this way).
+__device__ __forceinline__ void put_shared(uint32_t *p, uint32_t v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float get_shared(const float *p) {
+  return __uint_as_float(__hip_atomic_load(reinterpret_cast<const uint32_t *>(p), __ATOMIC_RELAXED,
+                                           __HIP_MEMORY_SCOPE_AGENT));
+}
+// This wave's device-scope stores have arrived.
+__device__ __forceinline__ void wait_stores() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
 __device__ __forceinline__ float act_f32(const void *p, int64_t i, float) {
   return static_cast<const float *>(p)[i];
 }
@@ -242,18 +289,29 @@ __global__ __launch_bounds__(kThreads, 4) void few_layer_kernel(FewArgs a) {
   __shared__ float s_gate[kTok * 64];
   __shared__ int16_t s_idx[kTok * 64];
   __shared__ float s_red[kWaves][R][256];
-  __shared__ uint32_t s_ticket, s_last;
+  __shared__ uint32_t s_last;
+  __shared__ int s_free, s_claim;
   __shared__ int s_ne;
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int T = a.T, K = a.K, N = a.N, Ks = a.Ks, d = a.d, f = a.f;
 
   // ---- routing ----
-  if (tid == 0) s_ticket = atomicAdd(a.ctr, 1u);
+  auto claim = [&](int w) {
+    uint32_t was = kFree;
+    __hip_atomic_compare_exchange_strong(a.state + w, &was, kTaken, __ATOMIC_RELAXED, __ATOMIC_RELAXED,
+                                         __HIP_MEMORY_SCOPE_AGENT);
+    return was == kFree;
+  };
+  if (tid == 0) {
+    s_claim = claim(blockIdx.x);
+    s_free = kThreads;
+  }
   for (int e = tid; e < N; e += kThreads) s_mask[e] = 0;
   for (int t = wave; t < T; t += kWaves) {
     uint32_t key[kMaxRouted / 64];
 #pragma unroll
     for (int j = 0; j < kMaxRouted / 64; ++j) {
+      if (j * 64 >= N) break;
       const int e = j * 64 + lane;
       key[j] = 0;
       if (e < N) {
@@ -265,21 +323,26 @@ __global__ __launch_bounds__(kThreads, 4) void few_layer_kernel(FewArgs a) {
     float mine = 0.0f;
     int mine_e = 0;
     for (int k = 0; k < K; ++k) {
-      uint64_t best = 0;
+      // this lane's best, the wave's, and the lowest id among equals
+      uint32_t best = 0;
+      int at = lane;
 #pragma unroll
       for (int j = 0; j < kMaxRouted / 64; ++j) {
-        const uint64_t c = (static_cast<uint64_t>(key[j]) << 32) | (0xFFFFFFFFu - (j * 64 + lane));
-        if (key[j] != 0 && c > best) best = c;
+        if (j * 64 >= N) break;
+        if (key[j] > best) {
+          best = key[j];
+          at = j * 64 + lane;
+        }
       }
+      const uint32_t top = wave_max(best);
+      uint64_t who = __ballot(best == top);
+      int e = __builtin_amdgcn_readlane(at, __builtin_ctzll(who));
+      while (who &= who - 1) e = min(e, __builtin_amdgcn_readlane(at, __builtin_ctzll(who)));
 #pragma unroll
-      for (int off = 32; off >= 1; off >>= 1) {
-        const uint64_t o = __shfl_xor(static_cast<unsigned long long>(best), off);
-        if (o > best) best = o;
-      }
-      const int e = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(best));
-#pragma unroll
-      for (int j = 0; j < kMaxRouted / 64; ++j)
+      for (int j = 0; j < kMaxRouted / 64; ++j) {
+        if (j * 64 >= N) break;
         if (e == j * 64 + lane) key[j] = 0;
+      }
       if (lane == k) mine_e = e;
     }
     if (lane < K) mine = a.logits[static_cast<int64_t>(t) * N + mine_e];
@@ -343,8 +406,7 @@ __global__ __launch_bounds__(kThreads, 4) void few_layer_kernel(FewArgs a) {
 
   // ---- items ----
   const int fblk = (f + RB - 1) / RB, dblk = (d + RB - 1) / RB;
-  const uint32_t n_up = static_cast<uint32_t>(entries) * fblk;
-  const uint32_t n_all = n_up + static_cast<uint32_t>(dblk) * a.S;
+  const int n_up = entries * fblk, n_down = dblk * a.S;
   const int col = lane & 15, q = lane >> 4;
   const int64_t pairs = static_cast<int64_t>(T) * K + static_cast<int64_t>(Ks) * T;
   // hidden row of (entry, token): routed pairs first, then the shared experts
@@ -352,161 +414,212 @@ __global__ __launch_bounds__(kThreads, 4) void few_layer_kernel(FewArgs a) {
     if (i < ne) return s_pair[i * kTok + t];
     return t < T ? T * K + (i - ne) * T + t : -1;
   };
-  bool waited = false;
-  uint32_t item = s_ticket;
-  while (item < n_all) {
-    uint32_t next = 0;
-    if (tid == 0) next = atomicAdd(a.ctr, 1u);
+
+  // Sum over n chunks from chunk cc of entry i on, running on into the next
+  // entries: 16 R rows from r0 of the Linear `up`, against x or the hidden rows.
+  auto walk = [&](auto is_up, int i, int cc, int n, int r0, f32x4_t (&acc)[R]) {
+    constexpr bool UP = decltype(is_up)::value;
+    constexpr bool B2 = TWO && !UP;
+    constexpr int D = kDepth<W>;
+    const int rows = UP ? f : d, nch = (UP ? d : f) / KD::CH;
+    const uint8_t *rw = static_cast<const uint8_t *>(UP ? a.w1 : a.w2);
+    const uint8_t *sw = static_cast<const uint8_t *>(UP ? a.ws1 : a.ws2);
+    const uint8_t *rc = UP ? a.c1 : a.c2, *sc = UP ? a.cs1 : a.cs2;
+    const uint8_t *bb = static_cast<const uint8_t *>(UP ? a.x : a.h);
+    const int64_t msize = static_cast<int64_t>(rows) * nch;       // chunks of a matrix
+    uint32_t row[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) row[r] = static_cast<uint32_t>(min(r0 + r * 16 + col, rows - 1)) * nch;
+    const uint8_t *wb = nullptr, *cb = nullptr;
+    uint32_t bo = 0;
+    bool live = false;
+    auto enter = [&]() {
+      const bool routed = i < ne;
+      const int64_t e = routed ? uniform(s_list[i]) : i - ne;
+      wb = (routed ? rw : sw) + e * msize * KD::ABYTES;
+      if constexpr (W == kWMx) cb = (routed ? rc : sc) + e * msize * 4;
+      const int hr = hidden_row(i, col);
+      live = hr >= 0;
+      bo = static_cast<uint32_t>(UP ? col : max(hr, 0)) * nch * KD::BBYTES + q * (KD::NB * 16);
+    };
+    enter();
+    struct Stage {
+      AFrag<W> a[R];
+      BFrag<W> b0, b1;
+    } st[D];
+    auto fetch = [&](Stage &s) {
+      load_b<W>(s.b0, bb, bo, live, cc);
+      if constexpr (B2) load_b<W>(s.b1, bb + pairs * f * 2, bo, live, cc);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        load_a<W>(s.a[r], wb, row[r] * KD::ABYTES + q * (KD::NA * 16), cc);
+        if constexpr (W == kWMx) s.a[r].s = cb[row[r] * 4 + q + cc * 4];
+      }
+      if (++cc == nch) {
+        cc = 0;
+        if (++i < entries) enter();
+      }
+    };
+    auto use = [&](Stage &s) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) mma<W, B2>(acc[r], s.a[r], s.b0, s.b1);
+    };
+#pragma unroll
+    for (int k = 0; k < D; ++k)
+      if (k < n) fetch(st[k]);
+    int c = 0;
+    for (; c + 2 * D <= n; c += D) {
+#pragma unroll
+      for (int k = 0; k < D; ++k) {
+        use(st[k]);
+        fetch(st[k]);
+      }
+    }
+    for (; c < n; c += D) {
+#pragma unroll
+      for (int k = 0; k < D; ++k) {
+        if (c + k < n) use(st[k]);
+        if (c + k + D < n) fetch(st[k]);
+      }
+    }
+  };
+  // sum of the eight waves' parts of (row rl, token t)
+  auto sum_waves = [&](int rl, int t) {
+    const int r16 = rl & 15, at = ((r16 >> 2) * 16 + t) * 4 + (r16 & 3);
+    float z = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) z += s_red[w][rl >> 4][at];
+    return z;
+  };
+
+  // ---- hidden rows: the share of workgroup w ----
+  const int grid = gridDim.x;
+  auto up_share = [&](int w) {
+    for (int item = w; item < n_up; item += grid) {
+      f32x4_t acc[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) acc[r] = f32x4_t{0, 0, 0, 0};
+      // hidden rows r0 .. r0+RB-1 of entry i, for its tokens
+      const int i = item / fblk, r0 = (item - i * fblk) * RB, nch = d / KD::CH;
+      const int c0 = nch * wave / kWaves, c1 = nch * (wave + 1) / kWaves;
+      if (c0 < c1) walk(std::true_type{}, i, c0, c1 - c0, r0, acc);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        *reinterpret_cast<f32x4_t *>(&s_red[wave][r][lane * 4]) = acc[r];
+      __syncthreads();
+      const bool routed = i < ne;
+      const int64_t e = routed ? s_list[i] : i - ne;
+      const void *bias = routed ? a.b1 : a.bs1;
+      // thread: token t, two neighbouring rows
+      for (int o = tid; o < kTok * RB / 2; o += kThreads) {
+        const int t = o / (RB / 2), rl = o % (RB / 2) * 2, row = r0 + rl;
+        const int hr = hidden_row(i, t);
+        if (hr < 0 || row >= f) continue;
+        const float g = routed ? s_gate[t * 64 + (hr - t * K)] : 1.0f;
+        float v[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float z = sum_waves(rl + j, t);
+          if (bias) z += act_f32(bias, e * f + row + j, Act{});
+          v[j] = g * silu(z);
+        }
+        const int64_t at_h = static_cast<int64_t>(hr) * f + row;
+        if constexpr (TWO) {
+          uint32_t *hp = static_cast<uint32_t *>(a.h);
+          const uint32_t hi = pack_bf16x2(v[0], v[1]);
+          put_shared(hp + at_h / 2, hi);
+          put_shared(hp + (pairs * f + at_h) / 2,
+                     pack_bf16x2(v[0] - __uint_as_float(hi << 16),
+                                 v[1] - __uint_as_float(hi & 0xFFFF0000u)));
+        } else {
+          put_shared(static_cast<uint32_t *>(a.h) + at_h, __float_as_uint(v[0]));
+          put_shared(static_cast<uint32_t *>(a.h) + at_h + 1, __float_as_uint(v[1]));
+        }
+      }
+      __syncthreads();
+    }
+    wait_stores();
+    __syncthreads();
+    if (tid == 0) put_shared(a.state + w, kDone);
+  };
+  if (s_claim) up_share(blockIdx.x);
+  for (;;) {
+    uint32_t v = kDone;
+    if (tid < grid) v = __hip_atomic_load(a.state + tid, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (v == kFree) atomicMin(&s_free, tid);
+    if (__syncthreads_and(v == kDone)) break;
+    const int w = s_free;
+    __syncthreads();
+    if (w < kThreads) {
+      if (tid == 0) {
+        s_claim = claim(w);
+        s_free = kThreads;
+      }
+      __syncthreads();
+      if (s_claim) up_share(w);
+    } else {
+      __builtin_amdgcn_s_sleep(4);
+    }
+  }
+  if (tid == 0) __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+  __syncthreads();
+
+  // ---- output rows ----
+  for (int item = blockIdx.x; item < n_down; item += grid) {
     f32x4_t acc[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) acc[r] = f32x4_t{0, 0, 0, 0};
-    if (item < n_up) {
-      // hidden rows r0 .. r0+RB-1 of entry i, for its tokens
-      const int i = item / fblk, r0 = (item - i * fblk) * RB;
-      const bool routed = i < ne;
-      const int64_t e = routed ? s_list[i] : i - ne;
-      const uint8_t *wb = static_cast<const uint8_t *>(routed ? a.w1 : a.ws1);
-      const uint8_t *sb = routed ? a.c1 : a.cs1;
-      const int nch = d / KD::CH;
-      const uint8_t *wp[R], *sp[R];
+    // output rows r0 .. r0+RB-1: part s of the (entry, hidden) chunks
+    const int blk = item / a.S, s = item - blk * a.S, r0 = blk * RB;
+    const int nch = f / KD::CH, total = entries * nch, parts = a.S * kWaves;
+    const int p = s * kWaves + wave;
+    const int c0 = static_cast<int>(static_cast<int64_t>(total) * p / parts);
+    const int c1 = static_cast<int>(static_cast<int64_t>(total) * (p + 1) / parts);
+    if (c0 < c1) {
+      const int i = uniform(c0 / nch);
+      walk(std::false_type{}, i, c0 - i * nch, c1 - c0, r0, acc);
+    }
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int64_t row = e * f + min(r0 + r * 16 + col, f - 1);
-        wp[r] = wb + row * nch * KD::ABYTES + q * (KD::NA * 16);
-        sp[r] = W == kWMx ? sb + row * nch * 4 + q : nullptr;
+    for (int r = 0; r < R; ++r)
+      *reinterpret_cast<f32x4_t *>(&s_red[wave][r][lane * 4]) = acc[r];
+    __syncthreads();
+    bool finish = a.S == 1;
+    if (a.S > 1) {
+      for (int o = tid; o < T * RB; o += kThreads) {
+        const int t = o / RB, rl = o % RB;
+        if (r0 + rl < d)
+          put_shared(reinterpret_cast<uint32_t *>(a.part) + (static_cast<int64_t>(s) * T + t) * d + r0 + rl,
+                     __float_as_uint(sum_waves(rl, t)));
       }
-      const bool live = hidden_row(i, col) >= 0;
-      const uint8_t *xp = static_cast<const uint8_t *>(a.x) +
-                          static_cast<int64_t>(live ? col : 0) * nch * KD::BBYTES + q * (KD::NB * 16);
-      for (int c = wave; c < nch; c += kWaves) {
-        AFrag<W> fa[R];
-        BFrag<W> fb;
-        load_b<W>(fb, xp, live, c);
-#pragma unroll
-        for (int r = 0; r < R; ++r) load_a<W>(fa[r], wp[r], sp[r], c);
-#pragma unroll
-        for (int r = 0; r < R; ++r) mma<W, false>(acc[r], fa[r], fb, fb);
-      }
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-        *reinterpret_cast<f32x4_t *>(&s_red[wave][r][lane * 4]) = acc[r];
-      __syncthreads();
-      // thread: token t, row rl of the item
-      for (int o = tid; o < kTok * RB; o += kThreads) {
-        const int t = o / RB, rl = o % RB, r16 = rl & 15;
-        const int at = ((r16 >> 2) * 16 + t) * 4 + (r16 & 3);
-        float z = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) z += s_red[w][rl >> 4][at];
-        const int hr = hidden_row(i, t), row = r0 + rl;
-        if (hr >= 0 && row < f) {
-          const void *b = routed ? a.b1 : a.bs1;
-          if (b) z += act_f32(b, e * f + row, Act{});
-          float g = 1.0f;
-          if (routed) g = s_gate[t * 64 + (hr - t * K)];
-          const float v = g * silu(z);
-          const int64_t at_h = static_cast<int64_t>(hr) * f + row;
-          if constexpr (TWO) {
-            uint16_t *hp = static_cast<uint16_t *>(a.h);
-            const uint16_t hi = f32_to_bf16(v);
-            hp[at_h] = hi;
-            hp[pairs * f + at_h] = f32_to_bf16(v - bf16_to_f32(hi));
-          } else {
-            static_cast<float *>(a.h)[at_h] = v;
-          }
-        }
-      }
+      wait_stores();
       __syncthreads();
       if (tid == 0)
-        __hip_atomic_fetch_add(a.ctr + 1, 1u, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_AGENT);
-    } else {
-      // output rows r0 .. r0+RB-1: part s of the (entry, hidden) chunks
-      const int j = item - n_up, blk = j / a.S, s = j - blk * a.S, r0 = blk * RB;
-      const int nch = f / KD::CH;
-      const int total = entries * nch;
-      const int c_end = static_cast<int>(static_cast<int64_t>(total) * (s + 1) / a.S);
-      int c = static_cast<int>(static_cast<int64_t>(total) * s / a.S) + wave;
-      if (!waited) {
-        if (tid == 0) {
-          while (__hip_atomic_load(a.ctr + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < n_up)
-            __builtin_amdgcn_s_sleep(2);
-          __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-        }
-        __syncthreads();
-        waited = true;
-      }
-      for (; c < c_end; c += kWaves) {
-        const int i = c / nch, cc = c - i * nch;
-        const bool routed = i < ne;
-        const int64_t e = routed ? s_list[i] : i - ne;
-        const uint8_t *wb = static_cast<const uint8_t *>(routed ? a.w2 : a.ws2);
-        const uint8_t *sb = routed ? a.c2 : a.cs2;
-        const int hr = hidden_row(i, col);
-        const uint8_t *hp = static_cast<const uint8_t *>(a.h) +
-                            static_cast<int64_t>(max(hr, 0)) * nch * KD::BBYTES + q * (KD::NB * 16);
-        AFrag<W> fa[R];
-        BFrag<W> b0, b1;
-        load_b<W>(b0, hp, hr >= 0, cc);
-        if constexpr (TWO) load_b<W>(b1, hp + pairs * f * 2, hr >= 0, cc);
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const int64_t row = e * d + min(r0 + r * 16 + col, d - 1);
-          load_a<W>(fa[r], wb + row * nch * KD::ABYTES + q * (KD::NA * 16),
-                    W == kWMx ? sb + row * nch * 4 + q : nullptr, cc);
-        }
-#pragma unroll
-        for (int r = 0; r < R; ++r) mma<W, TWO>(acc[r], fa[r], b0, b1);
-      }
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-        *reinterpret_cast<f32x4_t *>(&s_red[wave][r][lane * 4]) = acc[r];
+        s_last = __hip_atomic_fetch_add(a.arrived + blk, 1u, __ATOMIC_RELAXED,
+                                        __HIP_MEMORY_SCOPE_AGENT);
       __syncthreads();
-      bool finish = a.S == 1;
-      if (a.S > 1) {
-        for (int o = tid; o < T * RB; o += kThreads) {
-          const int t = o / RB, rl = o % RB, r16 = rl & 15;
-          const int at = ((r16 >> 2) * 16 + t) * 4 + (r16 & 3);
-          float z = 0.0f;
-#pragma unroll
-          for (int w = 0; w < kWaves; ++w) z += s_red[w][rl >> 4][at];
-          if (r0 + rl < d) a.part[(static_cast<int64_t>(s) * T + t) * d + r0 + rl] = z;
-        }
-        __syncthreads();
-        if (tid == 0)
-          s_last = __hip_atomic_fetch_add(a.ctr + 2 + blk, 1u, __ATOMIC_ACQ_REL,
-                                          __HIP_MEMORY_SCOPE_AGENT);
-        __syncthreads();
-        finish = s_last == static_cast<uint32_t>(a.S - 1);
-      }
-      if (finish) {
-        for (int o = tid; o < T * RB; o += kThreads) {
-          const int t = o / RB, rl = o % RB, r16 = rl & 15, row = r0 + rl;
-          if (row >= d) continue;
-          float z = 0.0f;
-          if (a.S == 1) {
-            const int at = ((r16 >> 2) * 16 + t) * 4 + (r16 & 3);
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) z += s_red[w][rl >> 4][at];
-          } else {
-            for (int p = 0; p < a.S; ++p) z += a.part[(static_cast<int64_t>(p) * T + t) * d + row];
+      finish = s_last == static_cast<uint32_t>(a.S - 1);
+    }
+    if (finish) {
+      for (int o = tid; o < T * RB; o += kThreads) {
+        const int t = o / RB, rl = o % RB, row = r0 + rl;
+        if (row >= d) continue;
+        float z = 0.0f;
+        if (a.S == 1) z = sum_waves(rl, t);
+        else
+          for (int k = 0; k < a.S; ++k) z += get_shared(a.part + (static_cast<int64_t>(k) * T + t) * d + row);
+        if (a.bs2)
+          for (int i = 0; i < Ks; ++i) z += act_f32(a.bs2, static_cast<int64_t>(i) * d + row, Act{});
+        if (a.b2)
+          for (int k = 0; k < K; ++k) {
+            const int e = s_idx[t * 64 + k];
+            if ((s_mask[e] >> t) & 1)
+              z += s_gate[t * 64 + k] * act_f32(a.b2, static_cast<int64_t>(e) * d + row, Act{});
           }
-          if (a.bs2)
-            for (int i = 0; i < Ks; ++i) z += act_f32(a.bs2, static_cast<int64_t>(i) * d + row, Act{});
-          if (a.b2)
-            for (int k = 0; k < K; ++k) {
-              const int e = s_idx[t * 64 + k];
-              if ((s_mask[e] >> t) & 1)
-                z += s_gate[t * 64 + k] * act_f32(a.b2, static_cast<int64_t>(e) * d + row, Act{});
-            }
-          const int64_t at_y = static_cast<int64_t>(t) * d + row;
-          if constexpr (TWO) static_cast<uint16_t *>(a.y)[at_y] = f32_to_bf16(z);
-          else static_cast<float *>(a.y)[at_y] = z;
-        }
+        const int64_t at_y = static_cast<int64_t>(t) * d + row;
+        if constexpr (TWO) static_cast<uint16_t *>(a.y)[at_y] = f32_to_bf16(z);
+        else static_cast<float *>(a.y)[at_y] = z;
       }
     }
-    if (tid == 0) s_ticket = next;
-    __syncthreads();
-    item = s_ticket;
     __syncthreads();
   }
 }
@@ -521,6 +634,8 @@ int down_parts(int d, int rb) {
 }
 
 constexpr int kRows = 2;   // 16-row tiles of an item
+constexpr int kGrid = 512;   // most workgroups: two per CU
+static_assert(kGrid <= kThreads, "one state per thread where they are looked through");
 
 struct FewWs {
   size_t logits, ctr, h, part, bytes;
@@ -531,7 +646,7 @@ FewWs few_ws(int T, int d, int N, int K, int Ks, int f) {
   auto up = [](size_t b) { return (b + 255) & ~size_t(255); };
   FewWs w;
   w.parts = down_parts(d, 16 * kRows);
-  w.n_ctr = 2 + (d + 16 * kRows - 1) / (16 * kRows);
+  w.n_ctr = kGrid + (d + 16 * kRows - 1) / (16 * kRows);
   size_t at = 0;
   w.logits = at;
   at += up(sizeof(float) * T * N);
@@ -557,14 +672,21 @@ hipError_t launch_few_layer(const FewLayer &p, void *ws, hipStream_t s) {
   float *logits = reinterpret_cast<float *>(base + L.logits);
   uint32_t *ctr = reinterpret_cast<uint32_t *>(base + L.ctr);
   const float *in_logit = p.select_only ? nullptr : p.router_bias;
-  if (p.kind == kFewF32)
-    hipLaunchKernelGGL(few_logits_kernel<float>, dim3(p.N), dim3(256), 0, s,
-                       static_cast<const float *>(p.x), p.w_router, in_logit, logits, p.T, p.d, p.N,
-                       ctr, L.n_ctr);
-  else
-    hipLaunchKernelGGL(few_logits_kernel<uint16_t>, dim3(p.N), dim3(256), 0, s,
-                       static_cast<const uint16_t *>(p.x), p.w_router, in_logit, logits, p.T, p.d,
-                       p.N, ctr, L.n_ctr);
+  auto route = [&](auto zero, auto kernel) {
+    using X = decltype(zero);
+    hipLaunchKernelGGL(kernel, dim3(p.N), dim3(kLogitThreads), 0, s, static_cast<const X *>(p.x),
+                       p.w_router, in_logit, logits, p.T, p.d, p.N, ctr, L.n_ctr);
+  };
+  auto route_t = [&](auto zero) {
+    using X = decltype(zero);
+    if (p.T <= 1) route(zero, few_logits_kernel<X, 1>);
+    else if (p.T <= 2) route(zero, few_logits_kernel<X, 2>);
+    else if (p.T <= 4) route(zero, few_logits_kernel<X, 4>);
+    else if (p.T <= 8) route(zero, few_logits_kernel<X, 8>);
+    else route(zero, few_logits_kernel<X, 16>);
+  };
+  if (p.kind == kFewF32) route_t(0.0f);
+  else route_t(uint16_t{0});
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   FewArgs a;
@@ -576,15 +698,17 @@ hipError_t launch_few_layer(const FewLayer &p, void *ws, hipStream_t s) {
   a.c1 = p.c1; a.c2 = p.c2; a.cs1 = p.cs1; a.cs2 = p.cs2;
   a.h = base + L.h;
   a.part = reinterpret_cast<float *>(base + L.part);
-  a.ctr = ctr;
+  a.state = ctr;
+  a.arrived = ctr + kGrid;
   a.y = p.y; a.idx = p.idx; a.gate = p.gate; a.counts = p.counts;
   a.T = p.T; a.d = p.d; a.N = p.N; a.K = p.K; a.Ks = p.Ks; a.f = p.f;
   a.S = L.parts;
   a.cap = p.cap;
-  const int met = p.T * p.K < p.N ? p.T * p.K : p.N;
-  const int64_t items = static_cast<int64_t>(met + p.Ks) * ((p.f + 16 * kRows - 1) / (16 * kRows)) +
-                        static_cast<int64_t>((p.d + 16 * kRows - 1) / (16 * kRows)) * L.parts;
-  const dim3 grid(static_cast<unsigned>(items < 512 ? items : 512));
+  const int rb = 16 * kRows;
+  const int64_t met = (p.T * p.K < p.N ? p.T * p.K : p.N) + p.Ks;
+  const int64_t up = met * ((p.f + rb - 1) / rb), down = static_cast<int64_t>((p.d + rb - 1) / rb) * L.parts;
+  const int64_t items = up > down ? up : down;
+  const dim3 grid(static_cast<unsigned>(items < kGrid ? items : kGrid));
   if (p.kind == kFewF32)
     hipLaunchKernelGGL((few_layer_kernel<kWF32, kRows>), grid, dim3(kThreads), 0, s, a);
   else if (p.kind == kFewBf16)

@@ -501,6 +501,11 @@ static int check_few(const moe_config *cfg) {
   const int st = check_config(cfg, true, true);
   if (st != MOE_OK) return st;
   if (cfg->T > moe::kFewTokens || cfg->dispatch != MOE_DISPATCH_BF16) return MOE_ERR_UNSUPPORTED;
+  // 32-bit byte offsets into one expert's matrix and into the hidden rows
+  const int64_t slots = cfg->T * (static_cast<int64_t>(cfg->top_k) + cfg->n_shared);
+  const int64_t lim = int64_t(1) << 32;
+  if (cfg->d_ff >= lim / static_cast<int64_t>(act_bytes(cfg)) / cfg->d_model) return MOE_ERR_UNSUPPORTED;
+  if (slots * cfg->d_ff >= lim / 4) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
