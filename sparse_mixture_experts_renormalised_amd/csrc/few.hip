@@ -6,7 +6,7 @@
 // more kernels and keeps per-expert row lists in memory; here
 //
 //   kernel 1 (few_logits_kernel) computes the router's logits, one workgroup
-//     per expert, and clears the shares' states and the counts of kernel 2;
+//     per expert, and clears the states, counts and row of zeros of kernel 2;
 //   kernel 2 (few_layer_kernel) does the rest.  Every workgroup repeats the
 //     top-K selection, gates and capacity from the logits (T * N numbers)
 //     into LDS.  Then come the hidden rows of every met or shared expert (up
@@ -75,16 +75,21 @@ __device__ __forceinline__ float4 load4<uint16_t>(const uint16_t *p) {
 // fixed tree.  TT is T rounded up to a power of two (the loads of a step are
 // issued together); columns past T repeat the last token and are not stored.
 constexpr int kLogitThreads = 1024;
+struct FewZero {   // words to clear for kernel 2
+  uint32_t *p[3];
+  int n[3];
+};
 template <typename T, int TT>
 __global__ __launch_bounds__(kLogitThreads) void few_logits_kernel(
     const T *__restrict__ x, const float *__restrict__ w, const float *__restrict__ bias,
-    float *__restrict__ logits, int tokens, int d, int N, uint32_t *zero, int n_zero) {
+    float *__restrict__ logits, int tokens, int d, int N, FewZero zero) {
   constexpr int NW = kLogitThreads / 64;
   __shared__ float s_part[NW][TT];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int e = blockIdx.x;
-  if (e == 0)
-    for (int i = tid; i < n_zero; i += kLogitThreads) zero[i] = 0;
+#pragma unroll
+  for (int r = 0; r < 3; ++r)
+    for (int i = e * kLogitThreads + tid; i < zero.n[r]; i += N * kLogitThreads) zero.p[r][i] = 0;
   const float *wr = w + static_cast<int64_t>(e) * d;
   float acc[TT];
 #pragma unroll
@@ -131,7 +136,7 @@ struct FewArgs {
   const float *logits, *sel_bias;
   const void *w1, *b1, *w2, *b2, *ws1, *bs1, *ws2, *bs2;
   const uint8_t *c1, *c2, *cs1, *cs2;   // scale bytes of MXFP4 weights
-  void *h;                               // hidden rows: float, or bf16 parts [2][rows][f]
+  void *h;                               // hidden rows and one of zeros: float, or bf16 parts [2][rows + 1][f]
   float *part;                           // [S][T][d] parts of split outputs
   uint32_t *state;                       // [grid] of the up shares
   uint32_t *arrived;                     // [row blocks] finished parts of split outputs
@@ -144,22 +149,22 @@ struct FewArgs {
 };
 
 // The three kinds of weights.  CH elements of the reduction axis make a chunk:
-// what the four lanes of a row load together.  A lane's A part lies at byte
-// lane_a() of the row's chunk, and the activations that belong to it
-// at byte lane_b() of theirs.
+// what the four lanes of a row load together.  A row's chunk is read in NA
+// pieces of 64 neighbouring bytes, 16 to a lane; lane q finds the activations
+// that belong to its piece j at byte q * BLANE + j * BSTEP of theirs.
 enum { kWF32, kWBf16, kWMx };
 template <int W> struct Kind;
 template <> struct Kind<kWF32> {
   using Act = float;
-  static constexpr int CH = 16, NA = 1, NB = 1, ABYTES = 64, BBYTES = 64;
+  static constexpr int CH = 16, NA = 1, NB = 1, ABYTES = 64, BBYTES = 64, BLANE = 16, BSTEP = 64;
 };
 template <> struct Kind<kWBf16> {
   using Act = uint16_t;
-  static constexpr int CH = 64, NA = 2, NB = 2, ABYTES = 128, BBYTES = 128;
+  static constexpr int CH = 64, NA = 2, NB = 2, ABYTES = 128, BBYTES = 128, BLANE = 16, BSTEP = 64;
 };
 template <> struct Kind<kWMx> {
   using Act = uint16_t;
-  static constexpr int CH = 128, NA = 1, NB = 4, ABYTES = 64, BBYTES = 256;
+  static constexpr int CH = 128, NA = 1, NB = 4, ABYTES = 64, BBYTES = 256, BLANE = 64, BSTEP = 16;
 };
 
 template <int W> struct AFrag {
@@ -176,19 +181,15 @@ template <int W>
 __device__ __forceinline__ void load_a(AFrag<W> &a, const uint8_t *base, uint32_t row, int c) {
 #pragma unroll
   for (int j = 0; j < Kind<W>::NA; ++j)
-    a.v[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t *>(
-        base + (row + static_cast<uint32_t>(c) * Kind<W>::ABYTES + j * 16)));
+    a.v[j] = *reinterpret_cast<const u32x4_t *>(
+        base + (row + static_cast<uint32_t>(c) * Kind<W>::ABYTES + j * 64));
 }
 template <int W>
-__device__ __forceinline__ void load_b(BFrag<W> &b, const uint8_t *base, uint32_t row, bool live,
-                                       int c) {
+__device__ __forceinline__ void load_b(BFrag<W> &b, const uint8_t *base, uint32_t row, int c) {
 #pragma unroll
-  for (int j = 0; j < Kind<W>::NB; ++j) {
-    b.v[j] = u32x4_t{0, 0, 0, 0};
-    if (live)
-      b.v[j] = *reinterpret_cast<const u32x4_t *>(
-          base + (row + static_cast<uint32_t>(c) * Kind<W>::BBYTES + j * 16));
-  }
+  for (int j = 0; j < Kind<W>::NB; ++j)
+    b.v[j] = *reinterpret_cast<const u32x4_t *>(
+        base + (row + static_cast<uint32_t>(c) * Kind<W>::BBYTES + j * Kind<W>::BSTEP));
 }
 
 // Eight E2M1 codes times the block's power of two, as bf16 (exact).
@@ -415,8 +416,8 @@ __global__ __launch_bounds__(kThreads, 4) void few_layer_kernel(FewArgs a) {
     return t < T ? T * K + (i - ne) * T + t : -1;
   };
 
-  // Sum over n chunks from chunk cc of entry i on, running on into the next
-  // entries: 16 R rows from r0 of the Linear `up`, against x or the hidden rows.
+  // Sum over every kWaves-th of the chunks from chunk cc of entry i on, n of
+  // them, running on into the next entries: 16 R rows from r0 of the Linear `up`, against x or the hidden rows.
   auto walk = [&](auto is_up, int i, int cc, int n, int r0, f32x4_t (&acc)[R]) {
     constexpr bool UP = decltype(is_up)::value;
     constexpr bool B2 = TWO && !UP;
@@ -432,15 +433,18 @@ __global__ __launch_bounds__(kThreads, 4) void few_layer_kernel(FewArgs a) {
     for (int r = 0; r < R; ++r) row[r] = static_cast<uint32_t>(min(r0 + r * 16 + col, rows - 1)) * nch;
     const uint8_t *wb = nullptr, *cb = nullptr;
     uint32_t bo = 0;
-    bool live = false;
     auto enter = [&]() {
       const bool routed = i < ne;
       const int64_t e = routed ? uniform(s_list[i]) : i - ne;
       wb = (routed ? rw : sw) + e * msize * KD::ABYTES;
       if constexpr (W == kWMx) cb = (routed ? rc : sc) + e * msize * 4;
-      const int hr = hidden_row(i, col);
-      live = hr >= 0;
-      bo = static_cast<uint32_t>(UP ? col : max(hr, 0)) * nch * KD::BBYTES + q * (KD::NB * 16);
+      // Every lane loads (loads under a condition cannot be counted, and each
+      // wait would be for all of them).  An up item's column without a token
+      // repeats some token: columns do not mix, and it is not stored.  In a
+      // down item it takes the row of zeros, since the sum runs over entries.
+      int br = UP ? min(col, T - 1) : hidden_row(i, col);
+      if (br < 0) br = static_cast<int>(pairs);
+      bo = static_cast<uint32_t>(br) * nch * KD::BBYTES + q * KD::BLANE;
     };
     enter();
     struct Stage {
@@ -448,40 +452,51 @@ __global__ __launch_bounds__(kThreads, 4) void few_layer_kernel(FewArgs a) {
       BFrag<W> b0, b1;
     } st[D];
     auto fetch = [&](Stage &s) {
-      load_b<W>(s.b0, bb, bo, live, cc);
-      if constexpr (B2) load_b<W>(s.b1, bb + pairs * f * 2, bo, live, cc);
+      load_b<W>(s.b0, bb, bo, cc);
+      if constexpr (B2) load_b<W>(s.b1, bb + (pairs + 1) * f * 2, bo, cc);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        load_a<W>(s.a[r], wb, row[r] * KD::ABYTES + q * (KD::NA * 16), cc);
+        load_a<W>(s.a[r], wb, row[r] * KD::ABYTES + q * 16, cc);
         if constexpr (W == kWMx) s.a[r].s = cb[row[r] * 4 + q + cc * 4];
       }
-      if (++cc == nch) {
-        cc = 0;
-        if (++i < entries) enter();
+      cc += kWaves;
+      if (cc >= nch) {
+        do {
+          cc -= nch;
+          ++i;
+        } while (cc >= nch);
+        if (i < entries) enter();
       }
     };
     auto use = [&](Stage &s) {
 #pragma unroll
       for (int r = 0; r < R; ++r) mma<W, B2>(acc[r], s.a[r], s.b0, s.b1);
     };
+    if (n < D) {
+      for (int c = 0; c < n; ++c) {
+        fetch(st[0]);
+        use(st[0]);
+      }
+      return;
+    }
 #pragma unroll
-    for (int k = 0; k < D; ++k)
-      if (k < n) fetch(st[k]);
-    int c = 0;
-    for (; c + 2 * D <= n; c += D) {
+    for (int k = 0; k < D; ++k) fetch(st[k]);
+    int left = n - D;
+    for (; left >= D; left -= D) {
 #pragma unroll
       for (int k = 0; k < D; ++k) {
         use(st[k]);
         fetch(st[k]);
       }
     }
-    for (; c < n; c += D) {
 #pragma unroll
-      for (int k = 0; k < D; ++k) {
-        if (c + k < n) use(st[k]);
-        if (c + k + D < n) fetch(st[k]);
-      }
+    for (int k = 0; k < D; ++k) {
+      use(st[k]);
+      if (k < left) fetch(st[k]);
     }
+#pragma unroll
+    for (int k = 0; k < D; ++k)
+      if (k < left) use(st[k]);
   };
   // sum of the eight waves' parts of (row rl, token t)
   auto sum_waves = [&](int rl, int t) {
@@ -501,8 +516,8 @@ __global__ __launch_bounds__(kThreads, 4) void few_layer_kernel(FewArgs a) {
       for (int r = 0; r < R; ++r) acc[r] = f32x4_t{0, 0, 0, 0};
       // hidden rows r0 .. r0+RB-1 of entry i, for its tokens
       const int i = item / fblk, r0 = (item - i * fblk) * RB, nch = d / KD::CH;
-      const int c0 = nch * wave / kWaves, c1 = nch * (wave + 1) / kWaves;
-      if (c0 < c1) walk(std::true_type{}, i, c0, c1 - c0, r0, acc);
+      // the waves take neighbouring chunks, so that a row is read in long pieces
+      if (wave < nch) walk(std::true_type{}, i, wave, (nch - wave + kWaves - 1) / kWaves, r0, acc);
 #pragma unroll
       for (int r = 0; r < R; ++r)
         *reinterpret_cast<f32x4_t *>(&s_red[wave][r][lane * 4]) = acc[r];
@@ -528,7 +543,7 @@ __global__ __launch_bounds__(kThreads, 4) void few_layer_kernel(FewArgs a) {
           uint32_t *hp = static_cast<uint32_t *>(a.h);
           const uint32_t hi = pack_bf16x2(v[0], v[1]);
           put_shared(hp + at_h / 2, hi);
-          put_shared(hp + (pairs * f + at_h) / 2,
+          put_shared(hp + ((pairs + 1) * f + at_h) / 2,
                      pack_bf16x2(v[0] - __uint_as_float(hi << 16),
                                  v[1] - __uint_as_float(hi & 0xFFFF0000u)));
         } else {
@@ -571,13 +586,12 @@ __global__ __launch_bounds__(kThreads, 4) void few_layer_kernel(FewArgs a) {
     for (int r = 0; r < R; ++r) acc[r] = f32x4_t{0, 0, 0, 0};
     // output rows r0 .. r0+RB-1: part s of the (entry, hidden) chunks
     const int blk = item / a.S, s = item - blk * a.S, r0 = blk * RB;
-    const int nch = f / KD::CH, total = entries * nch, parts = a.S * kWaves;
-    const int p = s * kWaves + wave;
-    const int c0 = static_cast<int>(static_cast<int64_t>(total) * p / parts);
-    const int c1 = static_cast<int>(static_cast<int64_t>(total) * (p + 1) / parts);
+    const int nch = f / KD::CH, total = entries * nch;
+    const int c0 = static_cast<int>(static_cast<int64_t>(total) * s / a.S) + wave;
+    const int c1 = static_cast<int>(static_cast<int64_t>(total) * (s + 1) / a.S);
     if (c0 < c1) {
       const int i = uniform(c0 / nch);
-      walk(std::false_type{}, i, c0 - i * nch, c1 - c0, r0, acc);
+      walk(std::false_type{}, i, c0 - i * nch, (c1 - c0 + kWaves - 1) / kWaves, r0, acc);
     }
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -653,7 +667,7 @@ FewWs few_ws(int T, int d, int N, int K, int Ks, int f) {
   w.ctr = at;
   at += up(sizeof(uint32_t) * w.n_ctr);
   w.h = at;
-  at += up(sizeof(float) * (static_cast<size_t>(T) * K + static_cast<size_t>(Ks) * T) * f);
+  at += up(sizeof(float) * (static_cast<size_t>(T) * K + static_cast<size_t>(Ks) * T + 1) * f);
   w.part = at;
   at += w.parts > 1 ? up(sizeof(float) * w.parts * T * d) : 0;
   w.bytes = at;
@@ -671,19 +685,31 @@ hipError_t launch_few_layer(const FewLayer &p, void *ws, hipStream_t s) {
   char *base = static_cast<char *>(ws);
   float *logits = reinterpret_cast<float *>(base + L.logits);
   uint32_t *ctr = reinterpret_cast<uint32_t *>(base + L.ctr);
+  // the row of zeros behind the hidden rows, of both parts where there are two
+  const int64_t pairs = static_cast<int64_t>(p.T) * (p.K + p.Ks);
+  uint32_t *h = reinterpret_cast<uint32_t *>(base + L.h);
+  FewZero zero{{ctr, nullptr, nullptr}, {L.n_ctr, 0, 0}};
+  if (p.kind == kFewF32) {
+    zero.p[1] = h + pairs * p.f;
+    zero.n[1] = p.f;
+  } else {
+    zero.p[1] = h + pairs * p.f / 2;
+    zero.p[2] = h + (2 * pairs + 1) * p.f / 2;
+    zero.n[1] = zero.n[2] = p.f / 2;
+  }
   const float *in_logit = p.select_only ? nullptr : p.router_bias;
-  auto route = [&](auto zero, auto kernel) {
-    using X = decltype(zero);
+  auto route = [&](auto x0, auto kernel) {
+    using X = decltype(x0);
     hipLaunchKernelGGL(kernel, dim3(p.N), dim3(kLogitThreads), 0, s, static_cast<const X *>(p.x),
-                       p.w_router, in_logit, logits, p.T, p.d, p.N, ctr, L.n_ctr);
+                       p.w_router, in_logit, logits, p.T, p.d, p.N, zero);
   };
-  auto route_t = [&](auto zero) {
-    using X = decltype(zero);
-    if (p.T <= 1) route(zero, few_logits_kernel<X, 1>);
-    else if (p.T <= 2) route(zero, few_logits_kernel<X, 2>);
-    else if (p.T <= 4) route(zero, few_logits_kernel<X, 4>);
-    else if (p.T <= 8) route(zero, few_logits_kernel<X, 8>);
-    else route(zero, few_logits_kernel<X, 16>);
+  auto route_t = [&](auto x0) {
+    using X = decltype(x0);
+    if (p.T <= 1) route(x0, few_logits_kernel<X, 1>);
+    else if (p.T <= 2) route(x0, few_logits_kernel<X, 2>);
+    else if (p.T <= 4) route(x0, few_logits_kernel<X, 4>);
+    else if (p.T <= 8) route(x0, few_logits_kernel<X, 8>);
+    else route(x0, few_logits_kernel<X, 16>);
   };
   if (p.kind == kFewF32) route_t(0.0f);
   else route_t(uint16_t{0});

@@ -505,7 +505,7 @@ static int check_few(const moe_config *cfg) {
   const int64_t slots = cfg->T * (static_cast<int64_t>(cfg->top_k) + cfg->n_shared);
   const int64_t lim = int64_t(1) << 32;
   if (cfg->d_ff >= lim / static_cast<int64_t>(act_bytes(cfg)) / cfg->d_model) return MOE_ERR_UNSUPPORTED;
-  if (slots * cfg->d_ff >= lim / 4) return MOE_ERR_UNSUPPORTED;
+  if ((slots + 1) * cfg->d_ff >= lim / 4) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
