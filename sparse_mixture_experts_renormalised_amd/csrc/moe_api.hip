@@ -511,7 +511,7 @@ static int check_few(const moe_config *cfg) {
 
 size_t moe_few_workspace_size(const moe_config *cfg) {
   if (check_few(cfg) != MOE_OK) return 0;
-  return moe::few_workspace_bytes(static_cast<int>(cfg->T), cfg->d_model, cfg->n_routed,
+  return moe::few_workspace_bytes(cfg->dtype == MOE_BF16, static_cast<int>(cfg->T), cfg->d_model, cfg->n_routed,
                                   cfg->top_k, cfg->n_shared, cfg->d_ff);
 }
 

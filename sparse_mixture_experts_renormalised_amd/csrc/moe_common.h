@@ -161,7 +161,7 @@ struct FewLayer {
   int32_t *counts;
   int T, d, N, K, Ks, f, cap;
 };
-size_t few_workspace_bytes(int T, int d, int N, int K, int Ks, int f);
+size_t few_workspace_bytes(bool bf16, int T, int d, int N, int K, int Ks, int f);
 hipError_t launch_few_layer(const FewLayer &p, void *ws, hipStream_t s);
 
 hipError_t launch_combine(bool bf16, const void *y_rows, const int32_t *slot_row,
