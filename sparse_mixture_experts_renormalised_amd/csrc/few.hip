@@ -6,26 +6,34 @@
 // more kernels and keeps per-expert row lists in memory; here
 //
 //   kernel 1 (few_logits_kernel) computes the router's logits, one workgroup
-//     per expert, and clears the states, counts and row of zeros of kernel 2;
+//     per expert, lays the tokens out for kernel 2 and clears its counters;
 //   kernel 2 (few_layer_kernel) does the rest.  Every workgroup repeats the
 //     top-K selection, gates and capacity from the logits (T * N numbers)
-//     into LDS.  Then come the hidden rows of every met or shared expert (up
-//     items), and after them the output rows (down items).
+//     into LDS.  Then come the hidden rows of every met or shared expert, and
+//     after them the output rows.
 //
-// The 16 tokens are the 16 columns of one matrix instruction, and the rows of
-// a weight matrix are its rows: a wave multiplies 16 R weight rows by a share
-// of the reduction axis, every lane loading its weights straight from memory
-// in the instruction's own layout (each lane of a row takes 16 or 32
-// neighbouring bytes, so a row is read in whole 64- or 128-byte pieces).  A token that
-// is not routed to the expert is a column of zeros that is never loaded.
+// Layout of the products.  A wave reads weights straight from memory into
+// the operand registers of 16 x 16 matrix instructions, 16 bytes a lane.  In
+// the instruction's own order neighbouring lanes belong to different rows,
+// and the 64 lanes' addresses are then looked up one by one (measured: 64
+// clocks a load instead of 16, which bound the kernel at a third of the
+// memory's rate).  So its 16 rows are taken as 4 weight rows x 4 pieces b of a
+// chunk of the reduction axis, and its 16 columns as 4 tokens x 4 pieces b':
 //
-// Hidden values carry the gate (g * SiLU(.)), so a down item sums over all
-// (expert, hidden) pairs in one accumulator and no per-expert output exists.
-// They are kept in two bf16 parts (value, and what its rounding left: 16
-// significant bits, for the price of a second matrix instruction on a
-// bandwidth-bound path); float32 layers keep float32.
+//   A[(row, b)][q] = W[row][piece 4q + b],  B[q][(token, b')] = x[token][piece 4q + b']
 //
-// Waiting.  A down item needs every hidden row.  The up items are dealt to as
+// (q: the four lanes that share a row), so four neighbouring lanes read 64
+// neighbouring bytes, on both sides.  Entry ((row, b), (token, b')) of the
+// result is of use where b = b', and the four of them add up to the product
+// of the row with the token.  Each instruction still takes 1 KB of new weights;
+// five to sixteen tokens take two or four of them.
+//
+// Hidden values carry the gate (g * SiLU(.)), so an output row is one sum over
+// all (expert, hidden) pairs and no per-expert output exists.  bf16 layers keep
+// them in two bf16 parts (value, and what its rounding left: 16 significant
+// bits), MXFP4 layers in three E4M3 parts (below), float32 layers in float32.
+//
+// Waiting.  Output rows need every hidden row.  The hidden rows are dealt to as
 // many shares as there are workgroups, and a share has a state: free, taken,
 // done.  A workgroup takes its own share first, and where it then waits for all
 // shares to be done, it takes any that is still free (its workgroup has not
@@ -37,6 +45,8 @@
 //
 // Results do not depend on timing: sums are split in a way fixed by the sizes
 // and joined in a fixed order.
+#include <math.h>
+
 #include <type_traits>
 
 #include "moe_common.h"
@@ -71,12 +81,6 @@ __device__ __forceinline__ float4 load4<uint16_t>(const uint16_t *p) {
                      __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
 }
 
-// Words to clear for kernel 2: the states and counts, and the row of zeros.
-struct FewZero {
-  uint32_t *p[5];
-  int n[5];
-};
-
 // Activations of MXFP4 layers enter the scaled matrix instructions as sums of
 // E4M3 numbers: per block of 32 a scale 2^E, E the smallest integer with
 // max|v| <= 448 * 2^E, and parts v / 2^E = p0 + p1 / 16 + p2 / 256 + ..., each
@@ -106,46 +110,97 @@ __device__ __forceinline__ uint32_t take_part(float (&v)[4]) {
   return static_cast<uint32_t>(w);
 }
 
-// Token rows as two parts: eight lanes a block, four elements each.
-__device__ __forceinline__ void split_tokens(const uint16_t *x, int64_t unit, int64_t units,
-                                             uint32_t *xq, uint8_t *xs) {
-  if (unit >= units) return;                // units is a multiple of 8: whole blocks leave
-  const float4 q = load4<uint16_t>(x + unit * 4);
-  float v[4] = {q.x, q.y, q.z, q.w};
-  uint32_t amax = 0;
+// The three kinds of layers.  A chunk is what the 16 lanes of a weight row load
+// together: 16 pieces of 16 bytes.
+//   CH        elements of a chunk;  EB: element bytes times 8
+//   CB        bytes of a chunk of one part of the activations, in NB loads
+//   PUP, PDN  parts of the activations of the first and of the second Linear
+// The activations are kept in the workspace, padded with zeros to whole chunks.
+// A chunk of E4M3 parts is stored in the order in which its 16-byte pieces are
+// loaded: the instruction's 8-bit operand holds elements 16 q .. +15 (first
+// load) and 64 + 16 q .. +15 (second) of the 128 it multiplies, while the lane
+// with 4-bit codes holds 32 q .. +31.
+enum { kWF32, kWBf16, kWMx };
+template <int W> struct Kind;
+template <> struct Kind<kWF32> {
+  using Act = float;
+  static constexpr int CH = 64, CB = 256, NB = 1, PUP = 1, PDN = 1;
+};
+template <> struct Kind<kWBf16> {
+  using Act = uint16_t;
+  static constexpr int CH = 128, CB = 256, NB = 1, PUP = 1, PDN = 2;
+};
+template <> struct Kind<kWMx> {
+  using Act = uint16_t;
+  static constexpr int CH = 512, CB = 512, NB = 2, PUP = 2, PDN = 3;
+};
+// Byte of element k (of a chunk of E4M3 parts) within the chunk.
+__device__ __forceinline__ int part_byte(int k) {
+  const int blk = k >> 5, q = blk >> 2, b = blk & 3, e = k & 31;
+  return (q >> 1) * 256 + ((q & 1) * 2 + (e >> 4)) * 64 + b * 16 + (e & 15);
+}
+
+// What kernel 1 does beside the logits.
+struct FewPrep {
+  int kind;
+  void *x;                    // tokens [parts][T][chunks of d]
+  uint8_t *xs;                // scale bytes of their blocks [T][16 a chunk]
+  uint32_t *ctr, *h, *hs;     // to clear: counters, hidden rows' padding and zeros
+  int n_ctr, h_rows, h_parts, h_chunks, h_words, hs_words;   // h_words: of a chunk
+  bool h_pad;                 // the last chunk of a hidden row has padding
+};
+
+// Four elements of a token row: copied, or split into parts (eight lanes a block).
+template <typename T>
+__device__ __forceinline__ void prepare_tokens(const FewPrep &p, const T *x, int64_t i, int tokens, int d) {
+  const int ch = p.kind == kWMx ? Kind<kWMx>::CH : sizeof(T) == 4 ? Kind<kWF32>::CH : Kind<kWBf16>::CH;
+  const int nch = (d + ch - 1) / ch, row4 = nch * ch / 4;
+  const int t = static_cast<int>(i / row4), k = static_cast<int>(i - static_cast<int64_t>(t) * row4) * 4;
+  if (t >= tokens) return;                  // rows are whole blocks: eight lanes leave together
+  float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (k < d) q = load4<T>(x + static_cast<int64_t>(t) * d + k);
+  if constexpr (sizeof(T) == 4) {
+    reinterpret_cast<float4 *>(p.x)[i] = q;
+  } else if (p.kind == kWBf16) {
+    reinterpret_cast<uint2 *>(p.x)[i] = make_uint2(pack_bf16x2(q.x, q.y), pack_bf16x2(q.z, q.w));
+  } else {
+    float v[4] = {q.x, q.y, q.z, q.w};
+    uint32_t amax = 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    for (int j = 0; j < 4; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7FFFFFFFu);
 #pragma unroll
-  for (int off = 1; off < 8; off <<= 1)
-    amax = max(amax, static_cast<uint32_t>(__shfl_xor(static_cast<int>(amax), off)));
-  const int E = part_exponent(amax);
+    for (int off = 1; off < 8; off <<= 1)
+      amax = max(amax, static_cast<uint32_t>(__shfl_xor(static_cast<int>(amax), off)));
+    const int E = part_exponent(amax);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] = __builtin_ldexpf(v[j], -E);
-  xq[unit] = take_part(v);
-  xq[units + unit] = take_part(v);
-  if ((unit & 7) == 0) xs[unit >> 3] = static_cast<uint8_t>(amax >= 0x7F800000u ? 255 : E + 127);
+    for (int j = 0; j < 4; ++j) v[j] = __builtin_ldexpf(v[j], -E);
+    uint8_t *to = static_cast<uint8_t *>(p.x) + (static_cast<int64_t>(t) * nch + k / ch) * ch + part_byte(k % ch);
+    *reinterpret_cast<uint32_t *>(to) = take_part(v);
+    *reinterpret_cast<uint32_t *>(to + static_cast<int64_t>(tokens) * nch * ch) = take_part(v);
+    if (k % 32 == 0)
+      p.xs[static_cast<int64_t>(t) * nch * 16 + k / 32] =
+          static_cast<uint8_t>(amax >= 0x7F800000u ? 255 : E + 127);
+  }
 }
 
 // One workgroup per expert: thread i sums elements 4i, 4i + 4096, ... of
 // W_e . x_t for each token, then the wave and the sixteen waves are added in a
 // fixed tree.  TT is T rounded up to a power of two (the loads of a step are
 // issued together); columns past T repeat the last token and are not stored.
-// Workgroups past the experts split the token rows into parts (xq not null).
+// The workgroups past the experts lay out the tokens.
 constexpr int kLogitThreads = 1024;
 template <typename T, int TT>
 __global__ __launch_bounds__(kLogitThreads) void few_logits_kernel(
     const T *__restrict__ x, const float *__restrict__ w, const float *__restrict__ bias,
-    float *__restrict__ logits, int tokens, int d, int N, FewZero zero, uint32_t *xq, uint8_t *xs) {
+    float *__restrict__ logits, int tokens, int d, int N, FewPrep prep) {
   constexpr int NW = kLogitThreads / 64;
   __shared__ float s_part[NW][TT];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int e = blockIdx.x;
-  if constexpr (sizeof(T) == 2)
-    if (e >= N) {
-      split_tokens(x, static_cast<int64_t>(e - N) * kLogitThreads + tid,
-                   static_cast<int64_t>(tokens) * d / 4, xq, xs);
-      return;
-    }
+  if (e >= N) {
+    prepare_tokens<T>(prep, x, static_cast<int64_t>(e - N) * kLogitThreads + tid, tokens, d);
+    return;
+  }
   const float *wr = w + static_cast<int64_t>(e) * d;
   float acc[TT];
 #pragma unroll
@@ -164,9 +219,23 @@ __global__ __launch_bounds__(kLogitThreads) void few_logits_kernel(
       acc[t] = __builtin_fmaf(wv.w, xv[t].w, acc[t]);
     }
   }
-#pragma unroll
-  for (int r = 0; r < 5; ++r)
-    for (int i = e * kLogitThreads + tid; i < zero.n[r]; i += N * kLogitThreads) zero.p[r][i] = 0;
+  // counters, scale bytes, the row of zeros of each part, and the last chunk
+  // of every hidden row where that has padding
+  {
+    const int at = e * kLogitThreads + tid, step = N * kLogitThreads;
+    const int row = prep.h_chunks * prep.h_words, rows = prep.h_rows * prep.h_parts;
+    for (int i = at; i < prep.n_ctr; i += step) prep.ctr[i] = 0;
+    for (int i = at; i < prep.hs_words; i += step) prep.hs[i] = 0;
+    for (int i = at; i < prep.h_parts * row; i += step) {
+      const int p = i / row;
+      prep.h[(static_cast<int64_t>(p + 1) * prep.h_rows - 1) * row + (i - p * row)] = 0;
+    }
+    if (prep.h_pad)
+      for (int64_t i = at; i < static_cast<int64_t>(rows) * prep.h_words; i += step) {
+        const int64_t r = i / prep.h_words;
+        prep.h[(r + 1) * row - prep.h_words + (i - r * prep.h_words)] = 0;
+      }
+  }
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1)
 #pragma unroll
@@ -191,17 +260,15 @@ __global__ __launch_bounds__(kLogitThreads) void few_logits_kernel(
 // Kernel 2
 // ---------------------------------------------------------------------------
 struct FewArgs {
-  const void *x;                         // token rows (MXFP4 layers: their parts [2][T][d])
-  const uint8_t *xs;                     // scale bytes of the parts
+  const void *x;                         // tokens as kernel 1 laid them out
+  const uint8_t *xs;                     // scale bytes of their parts
   const float *logits, *sel_bias;
   const void *w1, *b1, *w2, *b2, *ws1, *bs1, *ws2, *bs2;
   const uint8_t *c1, *c2, *cs1, *cs2;   // scale bytes of MXFP4 weights
-  // hidden rows and one of zeros: float [rows + 1][f], bf16 parts [2][rows + 1][f]
-  // or E4M3 parts [3][rows + 1][f] with scale bytes hs
-  void *h;
-  uint8_t *hs;
+  void *h;                               // hidden rows and one of zeros [parts][rows + 1][chunks of f]
+  uint8_t *hs;                           // scale bytes of their parts [rows + 1][16 a chunk]
   float *part;                           // [S][T][d] parts of split outputs
-  uint32_t *state;                       // [grid] of the up shares
+  uint32_t *state;                       // [grid] of the shares of hidden rows
   uint32_t *arrived;                     // [row blocks] finished parts of split outputs
   void *y;
   int32_t *idx;
@@ -211,88 +278,48 @@ struct FewArgs {
   int cap;                               // rows an expert keeps (T or more: no limit)
 };
 
-// The three kinds of weights.
-//   CH      elements of the reduction axis in a chunk, what the four lanes of a
-//           row load together
-//   ABYTES  bytes of a row's chunk, in pieces of 64 neighbouring bytes, 16 a lane
-//   BBYTES  bytes of a chunk of one part of the activations, in such pieces too
-//   PUP, PDN  parts of the activations of the first and of the second Linear
-//   UNIT    16-row tiles that hidden rows are dealt out in (a block of hidden
-//           values has 32 rows)
-enum { kWF32, kWBf16, kWMx };
-template <int W> struct Kind;
-template <> struct Kind<kWF32> {
-  using Act = float;
-  static constexpr int CH = 16, ABYTES = 64, BBYTES = 64, PUP = 1, PDN = 1, UNIT = 1;
-};
-template <> struct Kind<kWBf16> {
-  using Act = uint16_t;
-  static constexpr int CH = 64, ABYTES = 128, BBYTES = 128, PUP = 1, PDN = 2, UNIT = 1;
-};
-template <> struct Kind<kWMx> {
-  using Act = uint16_t;
-  static constexpr int CH = 128, ABYTES = 64, BBYTES = 128, PUP = 2, PDN = 3, UNIT = 2;
-};
-constexpr int kMaxTiles = 4;        // 16-row tiles of a wave
-constexpr int kDepth = 2;           // chunks in flight per wave
+constexpr int kMaxTiles = 4;             // 4-row tiles of a wave
+constexpr int kDownRows = 4 * kMaxTiles;   // output rows of an item
+// Chunks in flight per wave, by what the activations leave of 256 registers.
+template <int W, int TB> constexpr int kDepth = W == kWMx ? (TB == 1 ? 3 : 2) : TB == 4 ? 2 : 3;
+// The parts of sixteen tokens' chunk would fill the registers: there the four
+// waves walk the same chunks of rows of their own and share it through LDS.
+template <int W, int TB> constexpr bool kShare = W == kWMx && TB == 4;
 
-template <int W> struct AFrag {
-  u32x4_t v[Kind<W>::ABYTES / 64];
+struct AFrag {
+  u32x4_t v;
   int s;
 };
-template <int W, int P> struct BFrag {
-  u32x4_t v[P][Kind<W>::BBYTES / 64];
-  int s;
+template <int W, int TB, int P> struct BFrag {
+  u32x4_t v[TB][P][Kind<W>::NB];
+  int s[TB];
 };
 
-// Chunk c of the row whose first byte for this lane is base + row (base is
-// wave-uniform), and of a row of activations.
-template <int W>
-__device__ __forceinline__ void load_a(AFrag<W> &a, const uint8_t *base, uint32_t row, int c) {
+// acc += A (B_0 + B_1 + ...), one 16-byte piece a lane.
+template <int W, int TB, int P>
+__device__ __forceinline__ void mma(f32x4_t (&acc)[TB], const AFrag &a, const BFrag<W, TB, P> &b) {
 #pragma unroll
-  for (int j = 0; j < Kind<W>::ABYTES / 64; ++j)
-    a.v[j] = *reinterpret_cast<const u32x4_t *>(
-        base + (row + static_cast<uint32_t>(c) * Kind<W>::ABYTES + j * 64));
-}
-template <int W, int P>
-__device__ __forceinline__ void load_b(BFrag<W, P> &b, const uint8_t *base, int64_t part, uint32_t row,
-                                       int c) {
-#pragma unroll
-  for (int p = 0; p < P; ++p)
-#pragma unroll
-    for (int j = 0; j < Kind<W>::BBYTES / 64; ++j)
-      b.v[p][j] = *reinterpret_cast<const u32x4_t *>(
-          base + p * part + (row + static_cast<uint32_t>(c) * Kind<W>::BBYTES + j * 64));
-}
-
-// acc += A (B_0 + B_1 + ...), 16 weight rows x 16 columns.  For MXFP4 weights
-// a lane's 16 bytes of codes are one block; its E4M3 operand holds elements
-// 16 q .. +15 and 64 + 16 q .. +15 of the chunk's 128.
-template <int W, int P>
-__device__ __forceinline__ void mma(f32x4_t &acc, const AFrag<W> &a, const BFrag<W, P> &b) {
-  if constexpr (W == kWF32) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.v[0][j]),
-                                                 __uint_as_float(b.v[0][0][j]), acc, 0, 0, 0);
-  } else if constexpr (W == kWBf16) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a.v[j]),
-                                                      __builtin_bit_cast(bf16x8_t, b.v[p][j]), acc, 0,
-                                                      0, 0);
-  } else {
-    const i32x8_t av = {(int)a.v[0][0], (int)a.v[0][1], (int)a.v[0][2], (int)a.v[0][3], 0, 0, 0, 0};
+  for (int t = 0; t < TB; ++t)
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const i32x8_t bv = {(int)b.v[p][0][0], (int)b.v[p][0][1], (int)b.v[p][0][2], (int)b.v[p][0][3],
-                          (int)b.v[p][1][0], (int)b.v[p][1][1], (int)b.v[p][1][2], (int)b.v[p][1][3]};
-      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, acc, 4, 0, 0, a.s, 0,
-                                                             b.s - 4 * p);
+      if constexpr (W == kWF32) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.v[j]),
+                                                        __uint_as_float(b.v[t][p][0][j]), acc[t], 0, 0, 0);
+      } else if constexpr (W == kWBf16) {
+        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a.v),
+                                                         __builtin_bit_cast(bf16x8_t, b.v[t][p][0]),
+                                                         acc[t], 0, 0, 0);
+      } else {
+        const i32x8_t av = {(int)a.v[0], (int)a.v[1], (int)a.v[2], (int)a.v[3], 0, 0, 0, 0};
+        const u32x4_t l = b.v[t][p][0], h = b.v[t][p][Kind<W>::NB - 1];
+        const i32x8_t bv = {(int)l[0], (int)l[1], (int)l[2], (int)l[3],
+                            (int)h[0], (int)h[1], (int)h[2], (int)h[3]};
+        acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, acc[t], 4, 0, 0, a.s, 0,
+                                                                  b.s[t] - 4 * p);
+      }
     }
-  }
 }
 
 // Larger float, larger key; NaN sorts somewhere, so that a selection always
@@ -337,16 +364,22 @@ __device__ __forceinline__ float act_f32(const void *p, int64_t i, uint16_t) {
   return bf16_to_f32(static_cast<const uint16_t *>(p)[i]);
 }
 
-template <int W>
+// TB: tokens in fours (1, 2 or 4).
+template <int W, int TB>
 __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
   using KD = Kind<W>;
   using Act = typename KD::Act;
-  __shared__ int16_t s_pair[kMaxRouted * kTok];    // hidden row of (entry, token), or -1
+  __shared__ uint8_t s_slot[kTok][kMaxRouted];     // slot k of (token, expert), where the mask has it
   __shared__ int16_t s_list[kMaxRouted];           // expert of each entry
   __shared__ alignas(4) uint16_t s_mask[kMaxRouted];   // tokens of each expert
   __shared__ float s_gate[kTok * 64];
   __shared__ int16_t s_idx[kTok * 64];
-  __shared__ float s_red[kWaves][kMaxTiles][256];
+  __shared__ float s_red[kWaves][TB][64];
+  constexpr bool SHARE = kShare<W, TB>;
+  // two chunks of the sixteen tokens' parts, and their scale bytes
+  __shared__ __attribute__((aligned(16))) uint8_t s_b[SHARE ? 2 : 1][SHARE ? KD::PDN * kTok * 512 : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t s_bs[SHARE ? 2 : 1][SHARE ? kTok * 16 : 16];
+  __shared__ uint32_t s_amax[kWaves][kTok];
   __shared__ uint32_t s_last;
   __shared__ int s_free, s_claim;
   __shared__ int s_ne;
@@ -435,6 +468,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
   for (int i = tid; i < T * 64; i += kThreads)
     if ((i & 63) < K) {
       const int e = s_idx[i];
+      s_slot[i >> 6][e] = static_cast<uint8_t>(i & 63);
       atomicOr(reinterpret_cast<uint32_t *>(s_mask) + (e >> 1), (1u << (i >> 6)) << ((e & 1) * 16));
     }
   __syncthreads();
@@ -465,48 +499,73 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
   }
   __syncthreads();
   const int ne = uniform(s_ne), entries = ne + Ks;
-  for (int i = tid; i < ne * kTok; i += kThreads) {
-    const int e = s_list[i >> 4], t = i & 15;
-    int row = -1;
-    if ((s_mask[e] >> t) & 1)
-      for (int k = 0; k < K; ++k)
-        if (s_idx[t * 64 + k] == e) row = t * K + k;
-    s_pair[i] = static_cast<int16_t>(row);
-  }
-  __syncthreads();
 
   // ---- the sums ----
-  const int col = lane & 15, q = lane >> 4;
+  // lane: column (token tl of four, piece b), q; as a row of A: (row ar of a tile, b)
+  const int b = lane & 3, tl = (lane >> 2) & 3, ar = tl, q = lane >> 4, piece = q * 4 + b;
   const int pairs = T * (K + Ks);
   // hidden row of (entry, token): routed pairs first, then the shared experts
   auto hidden_row = [&](int i, int t) -> int {
-    if (i < ne) return s_pair[i * kTok + t];
-    return t < T ? T * K + (i - ne) * T + t : -1;
+    if (i >= ne) return t < T ? T * K + (i - ne) * T + t : -1;
+    const int e = s_list[i];
+    return (s_mask[e] >> t) & 1 ? t * K + s_slot[t][e] : -1;
   };
-
-  // Sums of R tiles of 16 weight rows over every `step`-th chunk from chunk cc
-  // of entry i on, n of them.  row[r] is the byte offset of the lane's row, at
-  // the first chunk, from the matrix at wb[r] (scale bytes: row / 16 from
-  // cb[r]); `next` moves those and the activations' row br to entry i.
-  auto walk = [&](auto parts, auto &acc, const uint8_t *bb, const uint8_t *bs, int64_t part, int nch,
-                  const uint8_t *(&wb)[kMaxTiles], const uint8_t *(&cb)[kMaxTiles],
-                  const uint32_t (&row)[kMaxTiles], uint32_t &br, int i, int cc, int n, int step,
-                  auto next) {
+  // z of walk() from its sums: register i of a lane is entry ((row q, piece i),
+  // (token tl, piece b)) of tile r: take i = b, add the four lanes b, and let
+  // lane b keep tile b.
+  auto gather = [&](auto &acc, f32x4_t &z) {
     constexpr int R = std::extent_v<std::remove_reference_t<decltype(acc)>>;
-    constexpr int P = decltype(parts)::value, D = kDepth;
 #pragma unroll
-    for (int r = 0; r < R; ++r) acc[r] = f32x4_t{0, 0, 0, 0};
-    struct Stage {
-      AFrag<W> a[R];
-      BFrag<W, P> b;
-    } st[D];
-    auto fetch = [&](Stage &s) {
-      load_b<W, P>(s.b, bb, part, br * KD::BBYTES + q * 16, cc);
-      if constexpr (W == kWMx) s.b.s = bs[br * 4 + cc * 4 + q];
+    for (int t = 0; t < TB; ++t) {
+      float keep = 0.0f;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        load_a<W>(s.a[r], wb[r], row[r] * KD::ABYTES + q * 16, cc);
-        if constexpr (W == kWMx) s.a[r].s = cb[r][row[r] * 4 + cc * 4 + q];
+        const f32x4_t v = acc[r][t];
+        float x = b == 0 ? v[0] : b == 1 ? v[1] : b == 2 ? v[2] : v[3];
+        x += __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(x), 0xB1, 0xF, 0xF, true));
+        x += __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(x), 0x4E, 0xF, 0xF, true));
+        keep = b == r ? x : keep;
+      }
+      z[t] = keep;
+    }
+  };
+  // Sums of R tiles of four weight rows with the tokens over every `step`-th
+  // chunk from chunk cc of entry i on, n of them.  row[r]: pieces before the
+  // lane's row in the matrix wb[r] (its scale bytes cb[r]) of `pieces` a row;
+  // `next` moves those and the activations' rows br to entry i.  On return
+  // each lane holds z[t]: row 4 b + q of the 4 R, token 4 t + tl (b < R).
+  auto walk = [&](auto tiles, auto parts, f32x4_t &z, const uint8_t *bb, const uint8_t *bs,
+                  int64_t part, int pieces, const uint8_t *(&wb)[kMaxTiles],
+                  const uint8_t *(&cb)[kMaxTiles], const uint32_t (&row)[kMaxTiles],
+                  uint32_t (&br)[TB], int i, int cc, int n, int step, auto next) {
+    constexpr int R = decltype(tiles)::value, P = decltype(parts)::value, D = kDepth<W, TB>;
+    const int nch = (pieces + 15) >> 4;
+    f32x4_t acc[R][TB];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int t = 0; t < TB; ++t) acc[r][t] = f32x4_t{0, 0, 0, 0};
+    struct Stage {
+      AFrag a[R];
+      BFrag<W, TB, P> b;
+    } st[D];
+    auto fetch = [&](Stage &s) {
+#pragma unroll
+      for (int t = 0; t < TB; ++t) {
+        const uint32_t at = (br[t] * nch + cc) * KD::CB + piece * 16;
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int j = 0; j < KD::NB; ++j)
+            s.b.v[t][p][j] = *reinterpret_cast<const u32x4_t *>(bb + p * part + (at + j * 256));
+        if constexpr (W == kWMx) s.b.s[t] = bs[(br[t] * nch + cc) * 16 + piece];
+      }
+      // past the end of a row: its last piece again, times the padding's zeros
+      const uint32_t at = min(cc * 16 + piece, pieces - 1);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        s.a[r].v = *reinterpret_cast<const u32x4_t *>(wb[r] + (row[r] + at) * 16);
+        if constexpr (W == kWMx) s.a[r].s = cb[r][row[r] + at];
       }
       cc += step;
       if (cc >= nch) {
@@ -519,173 +578,281 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
     };
     auto use = [&](Stage &s) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) mma<W, P>(acc[r], s.a[r], s.b);
+      for (int r = 0; r < R; ++r) mma<W, TB, P>(acc[r], s.a[r], s.b);
+      // done here, not later, or the operands outlive the next loads
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int t = 0; t < TB; ++t) asm volatile("" : "+v"(acc[r][t]));
     };
     if (n < D) {
       for (int c = 0; c < n; ++c) {
         fetch(st[0]);
         use(st[0]);
       }
-      return;
-    }
+    } else {
 #pragma unroll
-    for (int k = 0; k < D; ++k) fetch(st[k]);
-    int left = n - D;
-    for (; left >= D; left -= D) {
+      for (int k = 0; k < D; ++k) fetch(st[k]);
+      int left = n - D;
+      for (; left >= D; left -= D) {
+#pragma unroll
+        for (int k = 0; k < D; ++k) {
+          use(st[k]);
+          fetch(st[k]);
+        }
+      }
 #pragma unroll
       for (int k = 0; k < D; ++k) {
         use(st[k]);
-        fetch(st[k]);
+        if (k < left) fetch(st[k]);
       }
-    }
 #pragma unroll
-    for (int k = 0; k < D; ++k) {
-      use(st[k]);
-      if (k < left) fetch(st[k]);
+      for (int k = 0; k < D; ++k)
+        if (k < left) use(st[k]);
     }
+    gather(acc, z);
+  };
+
+  // The same for waves that share the activations: n chunks from chunk cc of
+  // entry i on, the same for all four waves, each for tiles of its own.  A chunk
+  // of the sixteen rows br goes from memory through registers into LDS one step
+  // ahead, 2 P pieces of 16 bytes a thread (rows tid / 32 and 8 more); piece u of
+  // a row lies at u ^ 4 (row % 4), so that the rows read together use all banks.
+  auto walk_shared = [&](auto tiles, auto parts, f32x4_t &z, const uint8_t *bb, const uint8_t *bs,
+                         int64_t part, int pieces, const uint8_t *(&wb)[kMaxTiles],
+                         const uint8_t *(&cb)[kMaxTiles], const uint32_t (&row)[kMaxTiles],
+                         uint32_t (&br)[2], uint32_t &bsr, int i, int cc, int n, auto next) {
+    constexpr int R = decltype(tiles)::value, P = decltype(parts)::value;
+    const int nch = (pieces + 15) >> 4;
+    f32x4_t acc[R][TB];
 #pragma unroll
-    for (int k = 0; k < D; ++k)
-      if (k < left) use(st[k]);
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int t = 0; t < TB; ++t) acc[r][t] = f32x4_t{0, 0, 0, 0};
+    if (n > 0) {
+      struct Stage {
+        AFrag a[R];
+      } st[2];
+      u32x4_t bv[P][2];
+      uint32_t bsv;
+      int bi = i, bc = cc;                 // entry and chunk of the next activations
+      auto fetch_b = [&]() {
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            bv[p][j] = *reinterpret_cast<const u32x4_t *>(
+                bb + p * part + ((br[j] * nch + bc) * 512 + (tid & 31) * 16));
+        bsv = *reinterpret_cast<const uint32_t *>(bs + ((bsr * nch + bc) * 16 + (lane & 3) * 4));
+        if (++bc == nch) {
+          bc = 0;
+          next(++bi, true);
+        }
+      };
+      auto store_b = [&](int buf) {
+        const int tok = tid >> 5, at = tok * 512 + ((tid & 31) ^ ((tok & 3) << 2)) * 16;
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            *reinterpret_cast<u32x4_t *>(&s_b[SHARE ? buf : 0][p * 8192 + j * 4096 + at]) = bv[p][j];
+        if (wave == 0) *reinterpret_cast<uint32_t *>(&s_bs[SHARE ? buf : 0][lane * 4]) = bsv;
+      };
+      auto fetch_a = [&](Stage &s) {
+        const uint32_t at = min(cc * 16 + piece, pieces - 1);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          s.a[r].v = *reinterpret_cast<const u32x4_t *>(wb[r] + (row[r] + at) * 16);
+          s.a[r].s = cb[r][row[r] + at];
+        }
+        if (++cc == nch) {
+          cc = 0;
+          next(++i, false);
+        }
+      };
+      auto use = [&](Stage &s, int buf) {
+#pragma unroll
+        for (int t = 0; t < TB; ++t) {
+          const int sc = s_bs[SHARE ? buf : 0][(t * 4 + tl) * 16 + piece];
+#pragma unroll
+          for (int p = 0; p < P; ++p) {
+            const uint8_t *at = &s_b[SHARE ? buf : 0][p * 8192 + (t * 4 + tl) * 512];
+            const u32x4_t l = *reinterpret_cast<const u32x4_t *>(at + (piece ^ (tl << 2)) * 16);
+            const u32x4_t h = *reinterpret_cast<const u32x4_t *>(at + 256 + (piece ^ (tl << 2)) * 16);
+            const i32x8_t b8 = {(int)l[0], (int)l[1], (int)l[2], (int)l[3],
+                                (int)h[0], (int)h[1], (int)h[2], (int)h[3]};
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              const u32x4_t v = s.a[r].v;
+              const i32x8_t a8 = {(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
+              acc[r][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, acc[r][t], 4, 0, 0,
+                                                                           s.a[r].s, 0, sc - 4 * p);
+            }
+          }
+          // holds the products and the next reads in their places; left to itself
+          // the compiler reads everything first and spills
+#pragma unroll
+          for (int r = 0; r < R; ++r) asm volatile("" : "+v"(acc[r][t])::"memory");
+        }
+      };
+      // LDS operations are done, and every wave is here
+      auto meet = [&]() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+      fetch_b();
+      fetch_a(st[0]);
+      store_b(0);
+      meet();
+      int left = n - 1;                    // chunks whose loads have not been issued
+      while (left >= 2) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          fetch_b();
+          fetch_a(st[1 - k]);
+          use(st[k], k);
+          store_b(1 - k);
+          meet();
+        }
+        left -= 2;
+      }
+      if (left) {
+        fetch_b();
+        fetch_a(st[1]);
+        use(st[0], 0);
+        store_b(1);
+        meet();
+        use(st[1], 1);
+      } else {
+        use(st[0], 0);
+      }
+      meet();                              // the buffers are free
+    }
+    gather(acc, z);
   };
 
   // ---- hidden rows ----
-  // All tiles of all entries form one row; share w is a range of it.  A wave
-  // sums up to kMaxTiles tiles, over the whole reduction axis when the range
-  // is long enough to keep the four waves busy that way, else over half or a
-  // quarter of it (`ks` waves a tile), joined through LDS.
+  // All 4-row tiles of all entries form one row.  A share is a range of it,
+  // dealt to the waves, each over the whole reduction axis.  MXFP4 layers deal
+  // in blocks of 32 rows (the hidden values' scale blocks), which the
+  // workgroup's waves share.
   const int grid = gridDim.x;
-  constexpr int U = KD::UNIT;
-  const int per_entry = (f / 16 + U - 1) / U;              // units of an entry (f is a multiple of 16)
-  const int units = entries * per_entry;
-  const int ks = units * U > 8 * grid ? 1 : units * U > 4 * grid ? 2 : 4;
-  const int64_t hsize = static_cast<int64_t>(pairs + 1) * f;
-  // Hidden values of the sums z[0 .. U-1][4]: tiles u*U .., rows 4q .. 4q+3,
-  // for token `col`.
-  auto hidden_out = [&](int u, f32x4_t (&z)[U]) {
-    const int i = u / per_entry, r0 = (u - i * per_entry) * U * 16 + q * 4;
-    const bool routed = i < ne;
-    const int64_t e = routed ? s_list[i] : i - ne;
-    const void *bias = routed ? a.b1 : a.bs1;
-    const int hr = hidden_row(i, col);
-    const float g = routed && hr >= 0 ? s_gate[col * 64 + (hr - col * K)] : 1.0f;
-#pragma unroll
-    for (int x = 0; x < U; ++x)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (bias) z[x][j] += act_f32(bias, e * f + r0 + x * 16 + j, Act{});
-        z[x][j] = g * silu(z[x][j]);
-      }
-    const int64_t at = static_cast<int64_t>(hr) * f + r0;
-    if constexpr (W == kWF32) {
-      uint64_t *hp = static_cast<uint64_t *>(a.h);
-      if (hr < 0) return;
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        put_shared(hp + at / 2 + j, __float_as_uint(z[0][2 * j]) |
-                                        static_cast<uint64_t>(__float_as_uint(z[0][2 * j + 1])) << 32);
-    } else if constexpr (W == kWBf16) {
-      uint64_t *hp = static_cast<uint64_t *>(a.h);
-      if (hr < 0) return;
-      uint32_t hi[2], lo[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        hi[j] = pack_bf16x2(z[0][2 * j], z[0][2 * j + 1]);
-        lo[j] = pack_bf16x2(z[0][2 * j] - __uint_as_float(hi[j] << 16),
-                            z[0][2 * j + 1] - __uint_as_float(hi[j] & 0xFFFF0000u));
-      }
-      put_shared(hp + at / 4, hi[0] | static_cast<uint64_t>(hi[1]) << 32);
-      put_shared(hp + (hsize + at) / 4, lo[0] | static_cast<uint64_t>(lo[1]) << 32);
-    } else {
-      // the four lanes of a token hold its block of 32
-      uint32_t amax = 0;
-#pragma unroll
-      for (int x = 0; x < U; ++x)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) amax = max(amax, __float_as_uint(z[x][j]) & 0x7FFFFFFFu);
-      amax = max(amax, static_cast<uint32_t>(__shfl_xor(static_cast<int>(amax), 16)));
-      amax = max(amax, static_cast<uint32_t>(__shfl_xor(static_cast<int>(amax), 32)));
-      const int E = part_exponent(amax);
-      if (hr < 0) return;
-      uint32_t *hp = static_cast<uint32_t *>(a.h);
-#pragma unroll
-      for (int x = 0; x < U; ++x) {
-        float v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = __builtin_ldexpf(z[x][j], -E);
-#pragma unroll
-        for (int p = 0; p < KD::PDN; ++p) put_shared(hp + (p * hsize + at + x * 16) / 4, take_part(v));
-      }
-      if (q == 0)
-        put_shared(a.hs + at / 32, static_cast<uint8_t>(amax >= 0x7F800000u ? 255 : E + 127));
-    }
-  };
-  // Units u0 .. u0+m-1; a wave group takes RU = ceil(m / groups) of them.
-  auto up_pass = [&](auto units_each, int u0, int m) {
-    constexpr int RU = decltype(units_each)::value, R = RU * U;
-    const int group = wave / ks, kw = wave - group * ks, nch = d / KD::CH;
+  const int h_chunks = (f + KD::CH - 1) / KD::CH;
+  const int64_t h_part = static_cast<int64_t>(pairs + 1) * h_chunks * KD::CB;
+  // Tiles u0 .. u0+m-1 of the row of tiles (m <= R; past them the last again, not stored).
+  auto up_pass = [&](auto tiles, int u0, int m) {
+    constexpr int R = decltype(tiles)::value;
+    const int per_entry = f / 4, pieces = W == kWMx ? d / 32 : d * static_cast<int>(sizeof(Act)) / 16;
     const uint8_t *wb[kMaxTiles], *cb[kMaxTiles];
-    uint32_t row[kMaxTiles];
+    uint32_t row[kMaxTiles], br[TB];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      // past the range: its last unit again, not stored
-      const int u = u0 + min(group * RU + r / U, m - 1), i = u / per_entry;
+      const int u = u0 + min(r, m - 1), i = u / per_entry;
       const bool routed = i < ne;
       const int64_t e = routed ? uniform(s_list[i]) : i - ne;
-      const int r0 = (u - i * per_entry) * U * 16 + r % U * 16 + col;
-      wb[r] = static_cast<const uint8_t *>(routed ? a.w1 : a.ws1) + e * f * nch * KD::ABYTES;
-      cb[r] = W == kWMx ? (routed ? a.c1 : a.cs1) + e * f * nch * 4 : nullptr;
-      row[r] = static_cast<uint32_t>(r0) * nch;
+      wb[r] = static_cast<const uint8_t *>(routed ? a.w1 : a.ws1) + e * f * pieces * 16;
+      cb[r] = W == kWMx ? (routed ? a.c1 : a.cs1) + e * f * pieces : nullptr;
+      row[r] = static_cast<uint32_t>((u - i * per_entry) * 4 + ar) * pieces;
     }
     // A column without a token repeats one: columns do not mix, and it is not
     // stored.  Loads under a condition could not be counted, and each wait
     // would be for all of them.
-    uint32_t br = static_cast<uint32_t>(min(col, T - 1)) * nch;
-    f32x4_t acc[R];
-    walk(std::integral_constant<int, KD::PUP>{}, acc, static_cast<const uint8_t *>(a.x), a.xs,
-         static_cast<int64_t>(T) * nch * KD::BBYTES, nch, wb, cb, row, br, 0, kw,
-         max(0, (nch - kw + ks - 1) / ks), ks, [](int) {});
-    if (ks == 1) {
 #pragma unroll
-      for (int x = 0; x < RU; ++x)
-        if (group * RU + x < m) {
-          f32x4_t z[U];
+    for (int t = 0; t < TB; ++t) br[t] = min(t * 4 + tl, T - 1);
+    const int nch = (pieces + 15) >> 4;
+    f32x4_t z = {0, 0, 0, 0};
+    const uint8_t *xb = static_cast<const uint8_t *>(a.x);
+    const int64_t part = static_cast<int64_t>(T) * nch * KD::CB;
+    if constexpr (SHARE) {
+      uint32_t rows[2] = {static_cast<uint32_t>(min(tid >> 5, T - 1)),
+                          static_cast<uint32_t>(min((tid >> 5) + 8, T - 1))};
+      uint32_t srow = min(lane >> 2, T - 1);
+      walk_shared(tiles, std::integral_constant<int, KD::PUP>{}, z, xb, a.xs, part, pieces, wb, cb, row,
+                  rows, srow, 0, 0, nch, [](int, bool) {});
+    } else {
+      walk(tiles, std::integral_constant<int, KD::PUP>{}, z, xb, a.xs, part, pieces, wb, cb, row, br, 0,
+           0, nch, 1, [](int) {});
+    }
+    // lane: row 4 b + q of the pass, that is row q of tile u0 + b
+    const int u = u0 + min(b, m - 1), i = u / per_entry, hidden = (u - i * per_entry) * 4 + q;
+    const bool routed = i < ne, in_pass = b < m;
+    const int64_t e = routed ? s_list[i] : i - ne;
+    const void *bias = routed ? a.b1 : a.bs1;
+    const float bv = bias ? act_f32(bias, e * f + hidden, Act{}) : 0.0f;
+    const int chunk = hidden / KD::CH, in_chunk = hidden % KD::CH;
 #pragma unroll
-          for (int y = 0; y < U; ++y) z[y] = acc[x * U + y];
-          hidden_out(u0 + group * RU + x, z);
+    for (int t = 0; t < TB; ++t) {
+      const int token = t * 4 + tl, hr = in_pass ? hidden_row(i, token) : -1;
+      const float g = routed && hr >= 0 ? s_gate[token * 64 + (hr - token * K)] : 1.0f;
+      const float v = g * silu(z[t] + bv);
+      uint8_t *hp = static_cast<uint8_t *>(a.h) + (static_cast<int64_t>(hr) * h_chunks + chunk) * KD::CB;
+      if constexpr (W == kWF32) {
+        if (hr >= 0) put_shared(reinterpret_cast<uint32_t *>(hp) + in_chunk, __float_as_uint(v));
+      } else if constexpr (W == kWBf16) {
+        const uint16_t hi = f32_to_bf16(v);
+        if (hr >= 0) {
+          put_shared(reinterpret_cast<uint16_t *>(hp) + in_chunk, hi);
+          put_shared(reinterpret_cast<uint16_t *>(hp + h_part) + in_chunk, f32_to_bf16(v - bf16_to_f32(hi)));
         }
-      return;
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) *reinterpret_cast<f32x4_t *>(&s_red[wave][r][lane * 4]) = acc[r];
-    __syncthreads();
-    for (int x = wave; x < m; x += kWaves) {
-      const int gr = x / RU, rr = (x - gr * RU) * U;
-      f32x4_t z[U];
-#pragma unroll
-      for (int y = 0; y < U; ++y) {
-        z[y] = *reinterpret_cast<const f32x4_t *>(&s_red[gr * ks][rr + y][lane * 4]);
-        for (int w = 1; w < ks; ++w)
-          z[y] += *reinterpret_cast<const f32x4_t *>(&s_red[gr * ks + w][rr + y][lane * 4]);
+      } else {
+        z[t] = v;
       }
-      hidden_out(u0 + x, z);
     }
-    __syncthreads();
+    if constexpr (W == kWMx) {
+      // largest of each token's values in the wave (lanes q and b), then in the
+      // waves that share the block: all four, or two and two
+#pragma unroll
+      for (int t = 0; t < TB; ++t) {
+        uint32_t m = __float_as_uint(z[t]) & 0x7FFFFFFFu;
+#pragma unroll
+        for (int off = 1; off < 64; off = off == 2 ? 16 : off * 2)
+          m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), off)));
+        if ((lane & 0x33) == 0) s_amax[wave][t * 4 + tl] = m;
+      }
+      __syncthreads();
+      const int w0 = R == 2 ? 0 : wave & 2, w1 = R == 2 ? kWaves : w0 + 2;
+#pragma unroll
+      for (int t = 0; t < TB; ++t) {
+        const int token = t * 4 + tl, hr = in_pass ? hidden_row(i, token) : -1;
+        uint32_t amax = 0;
+        for (int w = w0; w < w1; ++w) amax = max(amax, s_amax[w][token]);
+        const int E = part_exponent(amax);
+        float v[4] = {__builtin_ldexpf(z[t], -E), 0.0f, 0.0f, 0.0f};
+        uint8_t *hp = static_cast<uint8_t *>(a.h) + (static_cast<int64_t>(hr) * h_chunks + chunk) * KD::CB +
+                      part_byte(in_chunk);
+#pragma unroll
+        for (int p = 0; p < KD::PDN; ++p) {
+          const uint32_t c = take_part(v);
+          if (hr >= 0) put_shared(hp + p * h_part, static_cast<uint8_t>(c));
+        }
+        if (hr >= 0 && hidden % 32 == 0)
+          put_shared(a.hs + (static_cast<int64_t>(hr) * h_chunks + chunk) * 16 + in_chunk / 32,
+                     static_cast<uint8_t>(amax >= 0x7F800000u ? 255 : E + 127));
+      }
+      __syncthreads();
+    }
   };
   auto up_share = [&](int w) {
-    int u = static_cast<int>(static_cast<int64_t>(units) * w / grid);
-    const int end = static_cast<int>(static_cast<int64_t>(units) * (w + 1) / grid);
-    const int groups = kWaves / ks, most = groups * (kMaxTiles / U);
-    while (u < end) {
-      // passes of equal length
-      const int passes = (end - u + most - 1) / most, m = (end - u + passes - 1) / passes;
-      const int each = (m + groups - 1) / groups;
-      if (each == 1) up_pass(std::integral_constant<int, 1>{}, u, m);
-      else if (each == 2) up_pass(std::integral_constant<int, 2>{}, u, m);
-      if constexpr (U == 1) {
-        if (each == 3) up_pass(std::integral_constant<int, 3>{}, u, m);
-        else if (each == 4) up_pass(std::integral_constant<int, 4>{}, u, m);
+    if constexpr (W == kWMx) {
+      const int units = entries * (f / 32), end = static_cast<int>(static_cast<int64_t>(units) * (w + 1) / grid);
+      for (int u = static_cast<int>(static_cast<int64_t>(units) * w / grid); u < end;) {
+        if (u + 1 < end) {
+          up_pass(std::integral_constant<int, 4>{}, u * 8 + wave * 4, 4);
+          u += 2;
+        } else {
+          up_pass(std::integral_constant<int, 2>{}, u * 8 + wave * 2, 2);
+          u += 1;
+        }
       }
-      u += m;
+    } else {
+      const int units = entries * (f / 4), waves = grid * kWaves, v = w * kWaves + wave;
+      int u = static_cast<int>(static_cast<int64_t>(units) * v / waves);
+      const int end = static_cast<int>(static_cast<int64_t>(units) * (v + 1) / waves);
+      while (u < end) {
+        // passes of equal length
+        const int passes = (end - u + kMaxTiles - 1) / kMaxTiles, m = (end - u + passes - 1) / passes;
+        if (m == 1) up_pass(std::integral_constant<int, 1>{}, u, m);
+        else if (m == 2) up_pass(std::integral_constant<int, 2>{}, u, m);
+        else up_pass(std::integral_constant<int, 4>{}, u, m);
+        u += m;
+      }
     }
     wait_stores();
     __syncthreads();
@@ -718,61 +885,100 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
   if (tid == 0) __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
   __syncthreads();
 
-  // ---- output rows ----
-  constexpr int RB = 16 * kMaxTiles;
-  const int n_down = (d + RB - 1) / RB * a.S;
+  // ---- output rows: an item's chunks are split over S items and, where the
+  // waves do not have rows of their own, over the waves ----
+  constexpr int DROWS = SHARE ? kDownRows * kWaves : kDownRows;
+  const int n_down = d / DROWS * a.S;
   for (int item = blockIdx.x; item < n_down; item += grid) {
-    // rows r0 .. r0+RB-1: part s of the (entry, hidden) chunks
-    const int blk = item / a.S, s = item - blk * a.S, r0 = blk * RB;
-    const int nch = f / KD::CH, total = entries * nch;
-    const int c0 = static_cast<int>(static_cast<int64_t>(total) * s / a.S) + wave;
+    const int blk = item / a.S, s = item - blk * a.S, r0 = blk * DROWS + (SHARE ? wave * kDownRows : 0);
+    const int pieces = W == kWMx ? f / 32 : f * static_cast<int>(sizeof(Act)) / 16;
+    const int total = entries * h_chunks;
+    const int c0 = static_cast<int>(static_cast<int64_t>(total) * s / a.S) + (SHARE ? 0 : wave);
     const int c1 = static_cast<int>(static_cast<int64_t>(total) * (s + 1) / a.S);
-    const int i0 = uniform(c0 / nch), n = max(0, (c1 - c0 + kWaves - 1) / kWaves);
+    const int i0 = uniform(c0 / h_chunks);
     const uint8_t *wb[kMaxTiles], *cb[kMaxTiles];
-    uint32_t row[kMaxTiles], br = 0;
+    uint32_t row[kMaxTiles];
 #pragma unroll
-    for (int r = 0; r < kMaxTiles; ++r) row[r] = static_cast<uint32_t>(min(r0 + r * 16 + col, d - 1)) * nch;
-    // the entry's matrix, and the hidden row of each column: the row of zeros
-    // for one without a token there
-    auto enter = [&](int i) {
-      if (i >= entries) return;
+    for (int r = 0; r < kMaxTiles; ++r) row[r] = static_cast<uint32_t>(r0 + r * 4 + ar) * pieces;
+    auto enter_w = [&](int i) {              // the entry's matrix
       const bool routed = i < ne;
       const int64_t e = routed ? uniform(s_list[i]) : i - ne;
-      const uint8_t *w = static_cast<const uint8_t *>(routed ? a.w2 : a.ws2) + e * d * nch * KD::ABYTES;
-      const uint8_t *c = W == kWMx ? (routed ? a.c2 : a.cs2) + e * d * nch * 4 : nullptr;
+      const uint8_t *w = static_cast<const uint8_t *>(routed ? a.w2 : a.ws2) + e * d * pieces * 16;
+      const uint8_t *c = W == kWMx ? (routed ? a.c2 : a.cs2) + e * d * pieces : nullptr;
 #pragma unroll
       for (int r = 0; r < kMaxTiles; ++r) {
         wb[r] = w;
         cb[r] = c;
       }
-      const int hr = hidden_row(i, col);
-      br = static_cast<uint32_t>(hr < 0 ? pairs : hr) * nch;
     };
-    enter(i0);
-    f32x4_t acc[kMaxTiles];
-    walk(std::integral_constant<int, KD::PDN>{}, acc, static_cast<const uint8_t *>(a.h), a.hs,
-         static_cast<int64_t>(pairs + 1) * nch * KD::BBYTES, nch, wb, cb, row, br, i0, c0 - i0 * nch, n,
-         kWaves, enter);
+    // the hidden row of a token: the row of zeros where it has none in the entry
+    auto hidden_or_zeros = [&](int i, int t) -> uint32_t {
+      const int hr = hidden_row(i, t);
+      return hr < 0 ? pairs : hr;
+    };
+    f32x4_t z = {0, 0, 0, 0};
+    const uint8_t *hb = static_cast<const uint8_t *>(a.h);
+    if constexpr (SHARE) {
+      uint32_t rows[2], srow = 0;
+      auto enter_b = [&](int i) {
+        rows[0] = hidden_or_zeros(i, tid >> 5);
+        rows[1] = hidden_or_zeros(i, (tid >> 5) + 8);
+        srow = hidden_or_zeros(i, lane >> 2);
+      };
+      const int n = max(0, c1 - c0);
+      if (n > 0) {
+        enter_w(i0);
+        enter_b(i0);
+      }
+      walk_shared(std::integral_constant<int, kMaxTiles>{}, std::integral_constant<int, KD::PDN>{}, z, hb,
+                  a.hs, h_part, pieces, wb, cb, row, rows, srow, i0, c0 - i0 * h_chunks, n,
+                  [&](int i, bool of_b) {
+                    if (i >= entries) return;
+                    if (of_b) enter_b(i);
+                    else enter_w(i);
+                  });
+    } else {
+      uint32_t br[TB];
+      auto enter = [&](int i) {
+        if (i >= entries) return;
+        enter_w(i);
 #pragma unroll
-    for (int r = 0; r < kMaxTiles; ++r)
-      *reinterpret_cast<f32x4_t *>(&s_red[wave][r][lane * 4]) = acc[r];
-    __syncthreads();
-    // wave: tile r, as many as there are waves; lane: token col, rows 4q .. 4q+3
-    static_assert(kMaxTiles == kWaves, "one tile per wave");
-    const int orow = r0 + wave * 16 + q * 4;
-    const bool out = col < T && orow < d;
-    f32x4_t z = *reinterpret_cast<const f32x4_t *>(&s_red[0][wave][lane * 4]);
+        for (int t = 0; t < TB; ++t) br[t] = hidden_or_zeros(i, t * 4 + tl);
+      };
+      enter(i0);
+      walk(std::integral_constant<int, kMaxTiles>{}, std::integral_constant<int, KD::PDN>{}, z, hb, a.hs,
+           h_part, pieces, wb, cb, row, br, i0, c0 - i0 * h_chunks,
+           max(0, (c1 - c0 + kWaves - 1) / kWaves), kWaves, enter);
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) z += *reinterpret_cast<const f32x4_t *>(&s_red[w][wave][lane * 4]);
+      for (int t = 0; t < TB; ++t) s_red[wave][t][lane] = z[t];
+      __syncthreads();
+    }
+    // Outputs of this lane: row 4 b + q, and token 4 t + tl for each t where the
+    // wave has rows of its own, else for t = wave alone (waves past TB: none).
+    const int orow = r0 + b * 4 + q;
+    constexpr int OUT = SHARE ? TB : 1;
+    float v[OUT];
+    bool out[OUT];
+#pragma unroll
+    for (int t = 0; t < OUT; ++t) {
+      if constexpr (SHARE) {
+        v[t] = z[t];
+        out[t] = t * 4 + tl < T;
+      } else {
+        v[t] = 0.0f;
+        out[t] = wave < TB && wave * 4 + tl < T;
+        if (out[t])
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) v[t] += s_red[w][wave][lane];
+      }
+    }
+    auto token_of = [&](int t) { return (SHARE ? t : wave) * 4 + tl; };
     bool finish = true;
     if (a.S > 1) {
-      const int64_t at = static_cast<int64_t>(col) * d + orow, size = static_cast<int64_t>(T) * d;
-      uint64_t *pp = reinterpret_cast<uint64_t *>(a.part);
-      if (out)
+      const int64_t size = static_cast<int64_t>(T) * d;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          put_shared(pp + (s * size + at) / 2 + j,
-                     __float_as_uint(z[2 * j]) | static_cast<uint64_t>(__float_as_uint(z[2 * j + 1])) << 32);
+      for (int t = 0; t < OUT; ++t)
+        if (out[t]) put_shared(a.part + s * size + static_cast<int64_t>(token_of(t)) * d + orow, v[t]);
       wait_stores();
       __syncthreads();
       if (tid == 0)
@@ -780,67 +986,73 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
                                         __HIP_MEMORY_SCOPE_AGENT);
       __syncthreads();
       finish = s_last == static_cast<uint32_t>(a.S - 1);
-      if (finish && out) {
-        z = f32x4_t{0, 0, 0, 0};
-        for (int k = 0; k < a.S; ++k)
+      if (finish)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint64_t v = get_shared(pp + (k * size + at) / 2 + j);
-            z[2 * j] += __uint_as_float(static_cast<uint32_t>(v));
-            z[2 * j + 1] += __uint_as_float(static_cast<uint32_t>(v >> 32));
+        for (int t = 0; t < OUT; ++t)
+          if (out[t]) {
+            v[t] = 0.0f;
+            for (int k = 0; k < a.S; ++k)
+              v[t] += get_shared(a.part + k * size + static_cast<int64_t>(token_of(t)) * d + orow);
           }
-      }
     }
-    if (finish && out) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+    for (int t = 0; t < OUT; ++t)
+      if (finish && out[t]) {
+        const int token = token_of(t);
         if (a.bs2)
-          for (int i = 0; i < Ks; ++i)
-            z[j] += act_f32(a.bs2, static_cast<int64_t>(i) * d + orow + j, Act{});
+          for (int i = 0; i < Ks; ++i) v[t] += act_f32(a.bs2, static_cast<int64_t>(i) * d + orow, Act{});
         if (a.b2)
           for (int k = 0; k < K; ++k) {
-            const int e = s_idx[col * 64 + k];
-            if ((s_mask[e] >> col) & 1)
-              z[j] += s_gate[col * 64 + k] * act_f32(a.b2, static_cast<int64_t>(e) * d + orow + j, Act{});
+            const int e = s_idx[token * 64 + k];
+            if ((s_mask[e] >> token) & 1)
+              v[t] += s_gate[token * 64 + k] * act_f32(a.b2, static_cast<int64_t>(e) * d + orow, Act{});
           }
+        const int64_t at = static_cast<int64_t>(token) * d + orow;
+        if constexpr (W == kWF32) static_cast<float *>(a.y)[at] = v[t];
+        else static_cast<uint16_t *>(a.y)[at] = f32_to_bf16(v[t]);
       }
-      const int64_t at = static_cast<int64_t>(col) * d + orow;
-      if constexpr (W == kWF32) {
-        *reinterpret_cast<f32x4_t *>(static_cast<float *>(a.y) + at) = z;
-      } else {
-        uint2 o;
-        o.x = pack_bf16x2(z[0], z[1]);
-        o.y = pack_bf16x2(z[2], z[3]);
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.y) + at) = o;
-      }
-    }
     __syncthreads();
   }
 }
 
-// Parts that a row block of the second Linear is cut into along its reduction
-// axis: as many as leave the least of the last round of items empty, a few
-// percent of which a smaller number is worth.
-int down_parts(int blocks) {
-  int best = 1;
-  double least = 1e30;
+// How the output rows are dealt out: rows of an item, and the parts S its
+// chunks are cut into.  More parts fill the chip and shorten the last round, but
+// an item costs about as much as six chunks beside its own; the cost of a round
+// is that and the chunks that a wave sums, for as many experts as tokens that
+// are routed evenly would meet.
+struct DownPlan {
+  int rows, parts;
+};
+DownPlan down_plan(FewKind kind, int T, int d, int N, int K, int Ks, int f) {
+  const bool share = kind == kFewMxfp4 && T > 8;
+  const int ch = kind == kFewF32 ? Kind<kWF32>::CH : kind == kFewBf16 ? Kind<kWBf16>::CH : Kind<kWMx>::CH;
+  DownPlan p{share ? kDownRows * kWaves : kDownRows, 1};
+  const double met = N * (1.0 - pow(1.0 - static_cast<double>(K) / N, T)) + Ks;
+  const double chunks = met * ((f + ch - 1) / ch) / (share ? 1 : kWaves);
+  const int blocks = d / p.rows;
+  double least = 1e300;
   for (int s = 1; s <= 16; ++s) {
-    const int n = blocks * s, rounds = (n + kGrid - 1) / kGrid;
-    const double cost = static_cast<double>(rounds) * kGrid / n * (1.0 + 0.005 * s);
+    const int rounds = (blocks * s + kGrid - 1) / kGrid;
+    const double cost = rounds * (6.0 + chunks / s);
     if (cost < least) {
       least = cost;
-      best = s;
+      p.parts = s;
     }
   }
-  return best;
+  return p;
 }
-
-constexpr int kDownRows = 16 * kMaxTiles;
 
 struct FewWs {
   size_t logits, ctr, h, hs, x, xs, part, bytes;
-  int parts, n_ctr;
+  int parts, blocks, n_ctr;
 };
+
+// Bytes of a row of n activations in one part.
+size_t few_row_bytes(FewKind k, int n) {
+  const int ch = k == kFewF32 ? Kind<kWF32>::CH : k == kFewBf16 ? Kind<kWBf16>::CH : Kind<kWMx>::CH;
+  const int cb = k == kFewMxfp4 ? Kind<kWMx>::CB : 256;
+  return static_cast<size_t>((n + ch - 1) / ch) * cb;
+}
 
 FewWs few_ws(FewKind kind, int T, int d, int N, int K, int Ks, int f) {
   FewWs w;
@@ -850,19 +1062,30 @@ FewWs few_ws(FewKind kind, int T, int d, int N, int K, int Ks, int f) {
     at += (b + 255) & ~size_t(255);
     return o;
   };
-  const int blocks = (d + kDownRows - 1) / kDownRows;
+  const bool mx = kind == kFewMxfp4;
   const size_t rows = static_cast<size_t>(T) * (K + Ks) + 1;
-  w.parts = down_parts(blocks);
-  w.n_ctr = kGrid + blocks;
+  const int x_parts = mx ? Kind<kWMx>::PUP : 1, h_parts = mx ? Kind<kWMx>::PDN : kind == kFewBf16 ? 2 : 1;
+  const DownPlan plan = down_plan(kind, T, d, N, K, Ks, f);
+  w.parts = plan.parts;
+  w.blocks = d / plan.rows;
+  w.n_ctr = kGrid + w.blocks;
   w.logits = take(sizeof(float) * T * N);
   w.ctr = take(sizeof(uint32_t) * w.n_ctr);
-  w.h = take((kind == kFewMxfp4 ? 3 : 4) * rows * f);
-  w.hs = take(kind == kFewMxfp4 ? rows * (f / 32) : 0);
-  w.x = take(kind == kFewMxfp4 ? static_cast<size_t>(2) * T * d : 0);
-  w.xs = take(kind == kFewMxfp4 ? static_cast<size_t>(T) * (d / 32) : 0);
+  w.h = take(h_parts * rows * few_row_bytes(kind, f));
+  w.hs = take(mx ? rows * (few_row_bytes(kind, f) / 32) : 0);
+  w.x = take(x_parts * T * few_row_bytes(kind, d));
+  w.xs = take(mx ? T * (few_row_bytes(kind, d) / 32) : 0);
   w.part = take(w.parts > 1 ? sizeof(float) * w.parts * T * d : 0);
   w.bytes = at;
   return w;
+}
+
+template <int TB>
+hipError_t launch_layer(FewKind kind, dim3 grid, const FewArgs &a, hipStream_t s) {
+  if (kind == kFewF32) hipLaunchKernelGGL((few_layer_kernel<kWF32, TB>), grid, dim3(kThreads), 0, s, a);
+  else if (kind == kFewBf16) hipLaunchKernelGGL((few_layer_kernel<kWBf16, TB>), grid, dim3(kThreads), 0, s, a);
+  else hipLaunchKernelGGL((few_layer_kernel<kWMx, TB>), grid, dim3(kThreads), 0, s, a);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -881,27 +1104,28 @@ hipError_t launch_few_layer(const FewLayer &p, void *ws, hipStream_t s) {
   char *base = static_cast<char *>(ws);
   float *logits = reinterpret_cast<float *>(base + L.logits);
   uint32_t *ctr = reinterpret_cast<uint32_t *>(base + L.ctr);
-  uint32_t *xq = mx ? reinterpret_cast<uint32_t *>(base + L.x) : nullptr;
-  uint8_t *xs = reinterpret_cast<uint8_t *>(base + L.xs), *hs = reinterpret_cast<uint8_t *>(base + L.hs);
-  // the row of zeros behind the hidden rows, in each part
-  const size_t rows = static_cast<size_t>(p.T) * (p.K + p.Ks);
-  FewZero zero{{ctr}, {L.n_ctr}};
-  const int n_parts = mx ? 3 : p.kind == kFewBf16 ? 2 : 1, bytes = mx ? 1 : p.kind == kFewBf16 ? 2 : 4;
-  for (int i = 0; i < n_parts; ++i) {
-    zero.p[1 + i] = reinterpret_cast<uint32_t *>(base + L.h + ((i * (rows + 1) + rows) * p.f) * bytes);
-    zero.n[1 + i] = p.f * bytes / 4;
-  }
-  if (mx) {
-    zero.p[4] = reinterpret_cast<uint32_t *>(hs + rows * (p.f / 32));
-    zero.n[4] = p.f / 128;
-  }
+  FewPrep prep;
+  prep.kind = mx ? kWMx : p.kind == kFewBf16 ? kWBf16 : kWF32;
+  prep.x = base + L.x;
+  prep.xs = reinterpret_cast<uint8_t *>(base + L.xs);
+  prep.ctr = ctr;
+  prep.h = reinterpret_cast<uint32_t *>(base + L.h);
+  prep.hs = reinterpret_cast<uint32_t *>(base + L.hs);
+  prep.n_ctr = L.n_ctr;
+  prep.h_rows = p.T * (p.K + p.Ks) + 1;
+  prep.h_parts = mx ? Kind<kWMx>::PDN : p.kind == kFewBf16 ? 2 : 1;
+  const int ch = mx ? Kind<kWMx>::CH : p.kind == kFewBf16 ? Kind<kWBf16>::CH : Kind<kWF32>::CH;
+  prep.h_words = (mx ? Kind<kWMx>::CB : 256) / 4;
+  prep.h_chunks = (p.f + ch - 1) / ch;
+  prep.hs_words = mx ? prep.h_rows * prep.h_chunks * 4 : 0;
+  prep.h_pad = p.f % ch != 0;
   const float *in_logit = p.select_only ? nullptr : p.router_bias;
-  const int split = mx ? (p.T * (p.d / 4) + kLogitThreads - 1) / kLogitThreads : 0;
+  const int64_t quads = static_cast<int64_t>(p.T) * ((p.d + ch - 1) / ch) * (ch / 4);
+  const int blocks = static_cast<int>((quads + kLogitThreads - 1) / kLogitThreads);
   auto route = [&](auto x0, auto kernel) {
     using X = decltype(x0);
-    hipLaunchKernelGGL(kernel, dim3(p.N + split), dim3(kLogitThreads), 0, s,
-                       static_cast<const X *>(p.x), p.w_router, in_logit, logits, p.T, p.d, p.N, zero,
-                       xq, xs);
+    hipLaunchKernelGGL(kernel, dim3(p.N + blocks), dim3(kLogitThreads), 0, s,
+                       static_cast<const X *>(p.x), p.w_router, in_logit, logits, p.T, p.d, p.N, prep);
   };
   auto route_t = [&](auto x0) {
     using X = decltype(x0);
@@ -916,15 +1140,15 @@ hipError_t launch_few_layer(const FewLayer &p, void *ws, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   FewArgs a;
-  a.x = mx ? static_cast<const void *>(xq) : p.x;
-  a.xs = xs;
+  a.x = base + L.x;
+  a.xs = prep.xs;
   a.logits = logits;
   a.sel_bias = p.select_only ? p.router_bias : nullptr;
   a.w1 = p.w1; a.b1 = p.b1; a.w2 = p.w2; a.b2 = p.b2;
   a.ws1 = p.ws1; a.bs1 = p.bs1; a.ws2 = p.ws2; a.bs2 = p.bs2;
   a.c1 = p.c1; a.c2 = p.c2; a.cs1 = p.cs1; a.cs2 = p.cs2;
   a.h = base + L.h;
-  a.hs = hs;
+  a.hs = reinterpret_cast<uint8_t *>(base + L.hs);
   a.part = reinterpret_cast<float *>(base + L.part);
   a.state = ctr;
   a.arrived = ctr + kGrid;
@@ -932,15 +1156,14 @@ hipError_t launch_few_layer(const FewLayer &p, void *ws, hipStream_t s) {
   a.T = p.T; a.d = p.d; a.N = p.N; a.K = p.K; a.Ks = p.Ks; a.f = p.f;
   a.S = L.parts;
   a.cap = p.cap;
-  const int urows = mx ? 16 * Kind<kWMx>::UNIT : 16;
+  // a workgroup for every share that can have rows, and for every output item
   const int64_t met = (p.T * p.K < p.N ? p.T * p.K : p.N) + p.Ks;
-  const int64_t up = met * ((p.f + urows - 1) / urows), down = static_cast<int64_t>((p.d + kDownRows - 1) / kDownRows) * L.parts;
+  const int64_t up = met * (mx ? p.f / 32 : (p.f / 4 + kWaves - 1) / kWaves);
+  const int64_t down = static_cast<int64_t>(L.blocks) * L.parts;
   const int64_t items = up > down ? up : down;
   const dim3 grid(static_cast<unsigned>(items < kGrid ? items : kGrid));
-  if (p.kind == kFewF32) hipLaunchKernelGGL(few_layer_kernel<kWF32>, grid, dim3(kThreads), 0, s, a);
-  else if (p.kind == kFewBf16) hipLaunchKernelGGL(few_layer_kernel<kWBf16>, grid, dim3(kThreads), 0, s, a);
-  else hipLaunchKernelGGL(few_layer_kernel<kWMx>, grid, dim3(kThreads), 0, s, a);
-  return hipGetLastError();
+  return p.T <= 4 ? launch_layer<1>(p.kind, grid, a, s)
+                  : p.T <= 8 ? launch_layer<2>(p.kind, grid, a, s) : launch_layer<4>(p.kind, grid, a, s);
 }
 
 }  // namespace moe
