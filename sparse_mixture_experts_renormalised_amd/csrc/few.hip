@@ -282,9 +282,12 @@ constexpr int kMaxTiles = 4;             // 4-row tiles of a wave
 constexpr int kDownRows = 4 * kMaxTiles;   // output rows of an item
 // Chunks in flight per wave, by what the activations leave of 256 registers.
 template <int W, int TB> constexpr int kDepth = W == kWMx ? (TB == 1 ? 3 : 2) : TB == 4 ? 2 : 3;
-// The parts of sixteen tokens' chunk would fill the registers: there the four
-// waves walk the same chunks of rows of their own and share it through LDS.
+// The parts of sixteen tokens' chunk would fill the registers, and four times
+// the matrix instructions would take longer than the weights: there the four
+// waves walk the same chunks of rows of their own, share the tokens through
+// LDS, and turn the weights in registers into 16 whole rows.
 template <int W, int TB> constexpr bool kShare = W == kWMx && TB == 4;
+constexpr int kShareDepth = 4;
 
 struct AFrag {
   u32x4_t v;
@@ -320,6 +323,23 @@ __device__ __forceinline__ void mma(f32x4_t (&acc)[TB], const AFrag &a, const BF
                                                                   b.s[t] - 4 * p);
       }
     }
+}
+
+// 4 x 4 transpose between the four registers and four neighbouring lanes:
+// v[j] of lane b becomes what v[b] of lane j was.
+__device__ __forceinline__ void transpose4(uint32_t (&v)[4], bool odd, bool high) {
+#pragma unroll
+  for (int k = 0; k < 4; k += 2) {
+    const uint32_t other = __builtin_amdgcn_mov_dpp(odd ? v[k] : v[k + 1], 0xB1, 0xF, 0xF, true);
+    v[k] = odd ? other : v[k];
+    v[k + 1] = odd ? v[k + 1] : other;
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t other = __builtin_amdgcn_mov_dpp(high ? v[k] : v[k + 2], 0x4E, 0xF, 0xF, true);
+    v[k] = high ? other : v[k];
+    v[k + 2] = high ? v[k + 2] : other;
+  }
 }
 
 // Larger float, larger key; NaN sorts somewhere, so that a selection always
@@ -613,119 +633,151 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
     gather(acc, z);
   };
 
-  // The same for waves that share the activations: n chunks from chunk cc of
-  // entry i on, the same for all four waves, each for tiles of its own.  A chunk
-  // of the sixteen rows br goes from memory through registers into LDS one step
-  // ahead, 2 P pieces of 16 bytes a thread (rows tid / 32 and 8 more); piece u of
-  // a row lies at u ^ 4 (row % 4), so that the rows read together use all banks.
-  auto walk_shared = [&](auto tiles, auto parts, f32x4_t &z, const uint8_t *bb, const uint8_t *bs,
-                         int64_t part, int pieces, const uint8_t *(&wb)[kMaxTiles],
-                         const uint8_t *(&cb)[kMaxTiles], const uint32_t (&row)[kMaxTiles],
-                         uint32_t (&br)[2], uint32_t &bsr, int i, int cc, int n, auto next) {
-    constexpr int R = decltype(tiles)::value, P = decltype(parts)::value;
+  // The same for waves that share the activations (kShare): n chunks from chunk
+  // cc of entry i on, the same for all four waves, each for four tiles of its
+  // own.  The four lanes b and the registers of the four tiles are transposed:
+  // operand j then holds piece 4 q + j of row q' of tile b, sixteen rows in all,
+  // and is multiplied by piece 4 q + j of sixteen tokens (column lane % 16).
+  // srow: pieces before the row of tile b of this lane, for the scale bytes.
+  // A chunk of the sixteen rows br goes from memory through registers into LDS one
+  // step ahead, 2 P pieces of 16 bytes a thread (rows tid / 32 and 8 more); piece
+  // u of row t lies at u ^ t, so that the rows read together use all banks.
+  // On return z[r] is row r of tile q, token lane % 16.
+  auto walk_shared = [&](auto parts, f32x4_t &z, const uint8_t *bb, const uint8_t *bs, int64_t part,
+                         int pieces, const uint8_t *(&wb)[kMaxTiles], const uint8_t *(&cb)[kMaxTiles],
+                         const uint32_t (&row)[kMaxTiles], uint32_t srow, uint32_t (&br)[2],
+                         uint32_t &bsr, int i, int cc, int n,
+                         auto next) __attribute__((always_inline)) {
+    constexpr int P = decltype(parts)::value, R = kMaxTiles, D = kShareDepth;
     const int nch = (pieces + 15) >> 4;
-    f32x4_t acc[R][TB];
+    f32x4_t acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+    z = acc[0];
+    if (n <= 0) return;
+    struct Stage {
+      u32x4_t a[R];
+      int s;
+    } st[D];
+    u32x4_t bv[P][2];
+    uint32_t bsv;
+    int bi = i, bc = cc;                   // entry and chunk of the next activations
+    auto fetch_b = [&]() {
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+      for (int p = 0; p < P; ++p)
 #pragma unroll
-      for (int t = 0; t < TB; ++t) acc[r][t] = f32x4_t{0, 0, 0, 0};
-    if (n > 0) {
-      struct Stage {
-        AFrag a[R];
-      } st[2];
-      u32x4_t bv[P][2];
-      uint32_t bsv;
-      int bi = i, bc = cc;                 // entry and chunk of the next activations
-      auto fetch_b = [&]() {
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            bv[p][j] = *reinterpret_cast<const u32x4_t *>(
-                bb + p * part + ((br[j] * nch + bc) * 512 + (tid & 31) * 16));
-        bsv = *reinterpret_cast<const uint32_t *>(bs + ((bsr * nch + bc) * 16 + (lane & 3) * 4));
-        if (++bc == nch) {
-          bc = 0;
-          next(++bi, true);
-        }
-      };
-      auto store_b = [&](int buf) {
-        const int tok = tid >> 5, at = tok * 512 + ((tid & 31) ^ ((tok & 3) << 2)) * 16;
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            *reinterpret_cast<u32x4_t *>(&s_b[SHARE ? buf : 0][p * 8192 + j * 4096 + at]) = bv[p][j];
-        if (wave == 0) *reinterpret_cast<uint32_t *>(&s_bs[SHARE ? buf : 0][lane * 4]) = bsv;
-      };
-      auto fetch_a = [&](Stage &s) {
-        const uint32_t at = min(cc * 16 + piece, pieces - 1);
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          s.a[r].v = *reinterpret_cast<const u32x4_t *>(wb[r] + (row[r] + at) * 16);
-          s.a[r].s = cb[r][row[r] + at];
-        }
-        if (++cc == nch) {
-          cc = 0;
-          next(++i, false);
-        }
-      };
-      auto use = [&](Stage &s, int buf) {
-#pragma unroll
-        for (int t = 0; t < TB; ++t) {
-          const int sc = s_bs[SHARE ? buf : 0][(t * 4 + tl) * 16 + piece];
-#pragma unroll
-          for (int p = 0; p < P; ++p) {
-            const uint8_t *at = &s_b[SHARE ? buf : 0][p * 8192 + (t * 4 + tl) * 512];
-            const u32x4_t l = *reinterpret_cast<const u32x4_t *>(at + (piece ^ (tl << 2)) * 16);
-            const u32x4_t h = *reinterpret_cast<const u32x4_t *>(at + 256 + (piece ^ (tl << 2)) * 16);
-            const i32x8_t b8 = {(int)l[0], (int)l[1], (int)l[2], (int)l[3],
-                                (int)h[0], (int)h[1], (int)h[2], (int)h[3]};
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-              const u32x4_t v = s.a[r].v;
-              const i32x8_t a8 = {(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
-              acc[r][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, acc[r][t], 4, 0, 0,
-                                                                           s.a[r].s, 0, sc - 4 * p);
-            }
-          }
-          // holds the products and the next reads in their places; left to itself
-          // the compiler reads everything first and spills
-#pragma unroll
-          for (int r = 0; r < R; ++r) asm volatile("" : "+v"(acc[r][t])::"memory");
-        }
-      };
-      // LDS operations are done, and every wave is here
-      auto meet = [&]() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
-      fetch_b();
-      fetch_a(st[0]);
-      store_b(0);
-      meet();
-      int left = n - 1;                    // chunks whose loads have not been issued
-      while (left >= 2) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          fetch_b();
-          fetch_a(st[1 - k]);
-          use(st[k], k);
-          store_b(1 - k);
-          meet();
-        }
-        left -= 2;
+        for (int j = 0; j < 2; ++j)
+          bv[p][j] = *reinterpret_cast<const u32x4_t *>(
+              bb + p * part + ((br[j] * nch + bc) * 512 + (tid & 31) * 16));
+      bsv = *reinterpret_cast<const uint32_t *>(bs + ((bsr * nch + bc) * 16 + (lane & 3) * 4));
+      if (++bc == nch) {
+        bc = 0;
+        next(++bi, true);
       }
-      if (left) {
+    };
+    auto store_b = [&](int buf) {
+      const int tok = tid >> 5, u = tid & 31;
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          *reinterpret_cast<u32x4_t *>(
+              &s_b[SHARE ? buf : 0][p * 8192 + (tok + 8 * j) * 512 + (u ^ (tok + 8 * j)) * 16]) = bv[p][j];
+      if (wave == 0) *reinterpret_cast<uint32_t *>(&s_bs[SHARE ? buf : 0][lane * 4]) = bsv;
+    };
+    auto fetch_a = [&](Stage &s) {
+      const uint32_t at = min(cc * 16 + piece, pieces - 1);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        s.a[r] = *reinterpret_cast<const u32x4_t *>(wb[r] + (row[r] + at) * 16);
+      s.s = *reinterpret_cast<const int *>(cb[0] + (srow + min(cc * 16 + q * 4, pieces - 4)));
+      if (++cc == nch) {
+        cc = 0;
+        next(++i, false);
+      }
+    };
+    auto use = [&](Stage &s, int buf) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t v[4] = {s.a[0][w], s.a[1][w], s.a[2][w], s.a[3][w]};
+        transpose4(v, b & 1, b & 2);
+#pragma unroll
+        for (int r = 0; r < R; ++r) s.a[r][w] = v[r];
+      }
+      const int col = lane & 15;
+      const uint32_t sc = *reinterpret_cast<const uint32_t *>(&s_bs[SHARE ? buf : 0][col * 16 + q * 4]);
+      auto product = [&](auto jj) {
+        constexpr int j = decltype(jj)::value;
+        const i32x8_t a8 = {(int)s.a[j][0], (int)s.a[j][1], (int)s.a[j][2], (int)s.a[j][3], 0, 0, 0, 0};
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const uint8_t *at = &s_b[SHARE ? buf : 0][p * 8192 + col * 512 + ((q * 4 + j) ^ col) * 16];
+          const u32x4_t l = *reinterpret_cast<const u32x4_t *>(at);
+          const u32x4_t h = *reinterpret_cast<const u32x4_t *>(at + 256);
+          const i32x8_t b8 = {(int)l[0], (int)l[1], (int)l[2], (int)l[3],
+                              (int)h[0], (int)h[1], (int)h[2], (int)h[3]};
+          // the scale bytes of piece j, those of the activations 4 p lower (the
+          // zeros of padding may borrow from each other: they multiply zeros)
+          acc[p & 1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              a8, b8, acc[p & 1], 4, 0, j, s.s, j, static_cast<int>(sc - 0x04040404u * p));
+        }
+      };
+      product(std::integral_constant<int, 0>{});
+      product(std::integral_constant<int, 1>{});
+      product(std::integral_constant<int, 2>{});
+      product(std::integral_constant<int, 3>{});
+      // holds the products in their place
+      asm volatile("" : "+v"(acc[0]), "+v"(acc[1])::"memory");
+    };
+    // LDS operations are done, and every wave is here
+    auto meet = [&]() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+    // step k of n: stage k % D, buffer k % 2; weights D - 1 chunks ahead
+    fetch_b();
+#pragma unroll
+    for (int k = 0; k < D - 1; ++k)
+      if (k < n) fetch_a(st[k]);
+    store_b(0);
+    meet();
+    int k = 0;
+    constexpr int STEP = D;
+    static_assert(D % 2 == 0, "stage and buffer of a step");
+    for (; k + STEP + D - 1 <= n; k += STEP) {
+#pragma unroll
+      for (int x = 0; x < STEP; ++x) {
         fetch_b();
-        fetch_a(st[1]);
-        use(st[0], 0);
-        store_b(1);
+        fetch_a(st[(x + D - 1) % D]);
+        use(st[x % D], x & 1);
+        store_b(1 - (x & 1));
         meet();
-        use(st[1], 1);
-      } else {
-        use(st[0], 0);
       }
-      meet();                              // the buffers are free
     }
-    gather(acc, z);
+#pragma unroll
+    for (int x = 0; x < STEP + D - 1; ++x) {
+      if (k + x < n) {
+        const bool more = k + x + 1 < n;
+        if (more) fetch_b();
+        if (k + x + D - 1 < n) fetch_a(st[(x + D - 1) % D]);
+        use(st[x % D], x & 1);
+        if (more) store_b(1 - (x & 1));
+        meet();
+      }
+    }
+    // registers: tiles, lanes q: rows of a tile; the other way round
+    const f32x4_t sum = acc[0] + acc[1];
+    uint32_t v[4] = {__float_as_uint(sum[0]), __float_as_uint(sum[1]), __float_as_uint(sum[2]),
+                     __float_as_uint(sum[3])};
+#pragma unroll
+    for (int x = 0; x < 4; x += 2) {
+      const uint32_t other = __shfl_xor(q & 1 ? v[x] : v[x + 1], 16);
+      v[x] = q & 1 ? other : v[x];
+      v[x + 1] = q & 1 ? v[x + 1] : other;
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const uint32_t other = __shfl_xor(q & 2 ? v[x] : v[x + 2], 32);
+      v[x] = q & 2 ? other : v[x];
+      v[x + 2] = q & 2 ? v[x + 2] : other;
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) z[x] = __uint_as_float(v[x]);
   };
 
   // ---- hidden rows ----
@@ -737,7 +789,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
   const int h_chunks = (f + KD::CH - 1) / KD::CH;
   const int64_t h_part = static_cast<int64_t>(pairs + 1) * h_chunks * KD::CB;
   // Tiles u0 .. u0+m-1 of the row of tiles (m <= R; past them the last again, not stored).
-  auto up_pass = [&](auto tiles, int u0, int m) {
+  auto up_pass = [&](auto tiles, int u0, int m) __attribute__((always_inline)) {
     constexpr int R = decltype(tiles)::value;
     const int per_entry = f / 4, pieces = W == kWMx ? d / 32 : d * static_cast<int>(sizeof(Act)) / 16;
     const uint8_t *wb[kMaxTiles], *cb[kMaxTiles];
@@ -763,68 +815,85 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
     if constexpr (SHARE) {
       uint32_t rows[2] = {static_cast<uint32_t>(min(tid >> 5, T - 1)),
                           static_cast<uint32_t>(min((tid >> 5) + 8, T - 1))};
-      uint32_t srow = min(lane >> 2, T - 1);
-      walk_shared(tiles, std::integral_constant<int, KD::PUP>{}, z, xb, a.xs, part, pieces, wb, cb, row,
-                  rows, srow, 0, 0, nch, [](int, bool) {});
+      uint32_t brow = min(lane >> 2, T - 1);
+      // the tiles of a pass are of one entry
+      const int us = u0 + min(b, m - 1);
+      const uint32_t srow = static_cast<uint32_t>((us - us / per_entry * per_entry) * 4 + ar) * pieces;
+      walk_shared(std::integral_constant<int, KD::PUP>{}, z, xb, a.xs, part, pieces, wb, cb, row, srow,
+                  rows, brow, 0, 0, nch, [](int, bool) {});
     } else {
       walk(tiles, std::integral_constant<int, KD::PUP>{}, z, xb, a.xs, part, pieces, wb, cb, row, br, 0,
            0, nch, 1, [](int) {});
     }
-    // lane: row 4 b + q of the pass, that is row q of tile u0 + b
-    const int u = u0 + min(b, m - 1), i = u / per_entry, hidden = (u - i * per_entry) * 4 + q;
-    const bool routed = i < ne, in_pass = b < m;
+    // The lane's values: row q of tile b for up to 4 TB tokens, or the four rows of
+    // tile q for one.
+    constexpr int NV = SHARE ? 4 : TB;
+    const int tile = SHARE ? q : b, u = u0 + min(tile, m - 1), i = u / per_entry;
+    const bool routed = i < ne;
     const int64_t e = routed ? s_list[i] : i - ne;
     const void *bias = routed ? a.b1 : a.bs1;
-    const float bv = bias ? act_f32(bias, e * f + hidden, Act{}) : 0.0f;
-    const int chunk = hidden / KD::CH, in_chunk = hidden % KD::CH;
+    auto hidden_of = [&](int v) { return (u - i * per_entry) * 4 + (SHARE ? v : q); };
+    auto token_of = [&](int v) { return SHARE ? lane & 15 : v * 4 + tl; };
+    uint32_t amax[TB] = {};
 #pragma unroll
-    for (int t = 0; t < TB; ++t) {
-      const int token = t * 4 + tl, hr = in_pass ? hidden_row(i, token) : -1;
+    for (int v = 0; v < NV; ++v) {
+      const int hidden = hidden_of(v), token = token_of(v), hr = tile < m ? hidden_row(i, token) : -1;
+      if (bias) z[v] += act_f32(bias, e * f + hidden, Act{});
       const float g = routed && hr >= 0 ? s_gate[token * 64 + (hr - token * K)] : 1.0f;
-      const float v = g * silu(z[t] + bv);
-      uint8_t *hp = static_cast<uint8_t *>(a.h) + (static_cast<int64_t>(hr) * h_chunks + chunk) * KD::CB;
+      z[v] = g * silu(z[v]);
+      uint8_t *hp = static_cast<uint8_t *>(a.h) + (static_cast<int64_t>(hr) * h_chunks + hidden / KD::CH) * KD::CB;
       if constexpr (W == kWF32) {
-        if (hr >= 0) put_shared(reinterpret_cast<uint32_t *>(hp) + in_chunk, __float_as_uint(v));
+        if (hr >= 0) put_shared(reinterpret_cast<uint32_t *>(hp) + hidden % KD::CH, __float_as_uint(z[v]));
       } else if constexpr (W == kWBf16) {
-        const uint16_t hi = f32_to_bf16(v);
+        const uint16_t hi = f32_to_bf16(z[v]);
         if (hr >= 0) {
-          put_shared(reinterpret_cast<uint16_t *>(hp) + in_chunk, hi);
-          put_shared(reinterpret_cast<uint16_t *>(hp + h_part) + in_chunk, f32_to_bf16(v - bf16_to_f32(hi)));
+          put_shared(reinterpret_cast<uint16_t *>(hp) + hidden % KD::CH, hi);
+          put_shared(reinterpret_cast<uint16_t *>(hp + h_part) + hidden % KD::CH,
+                     f32_to_bf16(z[v] - bf16_to_f32(hi)));
         }
-      } else {
-        z[t] = v;
       }
+      uint32_t &most = amax[SHARE ? 0 : v];
+      most = max(most, __float_as_uint(z[v]) & 0x7FFFFFFFu);
     }
     if constexpr (W == kWMx) {
-      // largest of each token's values in the wave (lanes q and b), then in the
-      // waves that share the block: all four, or two and two
+      // largest of each token's values in the wave (lanes q, and b where those are
+      // tiles), then in the waves that share the block: all four, or two and two
+      constexpr int NT = SHARE ? 1 : TB;
 #pragma unroll
-      for (int t = 0; t < TB; ++t) {
-        uint32_t m = __float_as_uint(z[t]) & 0x7FFFFFFFu;
-#pragma unroll
-        for (int off = 1; off < 64; off = off == 2 ? 16 : off * 2)
-          m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), off)));
-        if ((lane & 0x33) == 0) s_amax[wave][t * 4 + tl] = m;
+      for (int t = 0; t < NT; ++t) {
+        if constexpr (!SHARE) {
+          amax[t] = max(amax[t], static_cast<uint32_t>(__shfl_xor(static_cast<int>(amax[t]), 1)));
+          amax[t] = max(amax[t], static_cast<uint32_t>(__shfl_xor(static_cast<int>(amax[t]), 2)));
+        }
+        amax[t] = max(amax[t], static_cast<uint32_t>(__shfl_xor(static_cast<int>(amax[t]), 16)));
+        amax[t] = max(amax[t], static_cast<uint32_t>(__shfl_xor(static_cast<int>(amax[t]), 32)));
+        if (q == 0 && (SHARE || b == 0)) s_amax[wave][token_of(t)] = amax[t];
       }
       __syncthreads();
-      const int w0 = R == 2 ? 0 : wave & 2, w1 = R == 2 ? kWaves : w0 + 2;
+      const int w0 = m == 2 ? 0 : wave & 2, w1 = m == 2 ? kWaves : w0 + 2;
 #pragma unroll
-      for (int t = 0; t < TB; ++t) {
-        const int token = t * 4 + tl, hr = in_pass ? hidden_row(i, token) : -1;
-        uint32_t amax = 0;
-        for (int w = w0; w < w1; ++w) amax = max(amax, s_amax[w][token]);
-        const int E = part_exponent(amax);
-        float v[4] = {__builtin_ldexpf(z[t], -E), 0.0f, 0.0f, 0.0f};
+      for (int t = 0; t < NT; ++t) {
+        const int hidden = hidden_of(0), token = token_of(t), hr = tile < m ? hidden_row(i, token) : -1;
+        uint32_t most = 0;
+        for (int w = w0; w < w1; ++w) most = max(most, s_amax[w][token]);
+        const int E = part_exponent(most), chunk = hidden / KD::CH, in_chunk = hidden % KD::CH;
+        float x[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) x[v] = SHARE ? __builtin_ldexpf(z[v], -E) : 0.0f;
+        if (!SHARE) x[0] = __builtin_ldexpf(z[t], -E);
         uint8_t *hp = static_cast<uint8_t *>(a.h) + (static_cast<int64_t>(hr) * h_chunks + chunk) * KD::CB +
                       part_byte(in_chunk);
 #pragma unroll
         for (int p = 0; p < KD::PDN; ++p) {
-          const uint32_t c = take_part(v);
-          if (hr >= 0) put_shared(hp + p * h_part, static_cast<uint8_t>(c));
+          const uint32_t c = take_part(x);
+          if (hr >= 0) {
+            if constexpr (SHARE) put_shared(reinterpret_cast<uint32_t *>(hp + p * h_part), c);
+            else put_shared(hp + p * h_part, static_cast<uint8_t>(c));
+          }
         }
         if (hr >= 0 && hidden % 32 == 0)
           put_shared(a.hs + (static_cast<int64_t>(hr) * h_chunks + chunk) * 16 + in_chunk / 32,
-                     static_cast<uint8_t>(amax >= 0x7F800000u ? 255 : E + 127));
+                     static_cast<uint8_t>(most >= 0x7F800000u ? 255 : E + 127));
       }
       __syncthreads();
     }
@@ -833,13 +902,10 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
     if constexpr (W == kWMx) {
       const int units = entries * (f / 32), end = static_cast<int>(static_cast<int64_t>(units) * (w + 1) / grid);
       for (int u = static_cast<int>(static_cast<int64_t>(units) * w / grid); u < end;) {
-        if (u + 1 < end) {
-          up_pass(std::integral_constant<int, 4>{}, u * 8 + wave * 4, 4);
-          u += 2;
-        } else {
-          up_pass(std::integral_constant<int, 2>{}, u * 8 + wave * 2, 2);
-          u += 1;
-        }
+        const int m = u + 1 < end ? 4 : 2;       // two units, or the last one
+        if (SHARE || m == 4) up_pass(std::integral_constant<int, 4>{}, u * 8 + wave * m, m);
+        else up_pass(std::integral_constant<int, 2>{}, u * 8 + wave * m, m);
+        u += m / 2;
       }
     } else {
       const int units = entries * (f / 4), waves = grid * kWaves, v = w * kWaves + wave;
@@ -919,19 +985,19 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
     f32x4_t z = {0, 0, 0, 0};
     const uint8_t *hb = static_cast<const uint8_t *>(a.h);
     if constexpr (SHARE) {
-      uint32_t rows[2], srow = 0;
+      uint32_t rows[2], brow = 0;
       auto enter_b = [&](int i) {
         rows[0] = hidden_or_zeros(i, tid >> 5);
         rows[1] = hidden_or_zeros(i, (tid >> 5) + 8);
-        srow = hidden_or_zeros(i, lane >> 2);
+        brow = hidden_or_zeros(i, lane >> 2);
       };
       const int n = max(0, c1 - c0);
       if (n > 0) {
         enter_w(i0);
         enter_b(i0);
       }
-      walk_shared(std::integral_constant<int, kMaxTiles>{}, std::integral_constant<int, KD::PDN>{}, z, hb,
-                  a.hs, h_part, pieces, wb, cb, row, rows, srow, i0, c0 - i0 * h_chunks, n,
+      walk_shared(std::integral_constant<int, KD::PDN>{}, z, hb, a.hs, h_part, pieces, wb, cb, row,
+                  static_cast<uint32_t>(r0 + b * 4 + ar) * pieces, rows, brow, i0, c0 - i0 * h_chunks, n,
                   [&](int i, bool of_b) {
                     if (i >= entries) return;
                     if (of_b) enter_b(i);
@@ -953,32 +1019,28 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
       for (int t = 0; t < TB; ++t) s_red[wave][t][lane] = z[t];
       __syncthreads();
     }
-    // Outputs of this lane: row 4 b + q, and token 4 t + tl for each t where the
-    // wave has rows of its own, else for t = wave alone (waves past TB: none).
-    const int orow = r0 + b * 4 + q;
-    constexpr int OUT = SHARE ? TB : 1;
+    // Outputs of this lane: where the wave has rows of its own, the four rows of
+    // tile q for token lane % 16, else row q of tile b for token 4 wave + tl
+    // (waves past TB: none).
+    constexpr int OUT = SHARE ? 4 : 1;
+    const int token = SHARE ? lane & 15 : wave * 4 + tl;
+    const bool out = token < T && (SHARE || wave < TB);
+    auto row_of = [&](int t) { return r0 + (SHARE ? q * 4 + t : b * 4 + q); };
     float v[OUT];
-    bool out[OUT];
 #pragma unroll
     for (int t = 0; t < OUT; ++t) {
-      if constexpr (SHARE) {
-        v[t] = z[t];
-        out[t] = t * 4 + tl < T;
-      } else {
-        v[t] = 0.0f;
-        out[t] = wave < TB && wave * 4 + tl < T;
-        if (out[t])
+      v[t] = SHARE ? z[t] : 0.0f;
+      if (!SHARE && out)
 #pragma unroll
-          for (int w = 0; w < kWaves; ++w) v[t] += s_red[w][wave][lane];
-      }
+        for (int w = 0; w < kWaves; ++w) v[t] += s_red[w][min(wave, TB - 1)][lane];
     }
-    auto token_of = [&](int t) { return (SHARE ? t : wave) * 4 + tl; };
     bool finish = true;
     if (a.S > 1) {
       const int64_t size = static_cast<int64_t>(T) * d;
+      if (out)
 #pragma unroll
-      for (int t = 0; t < OUT; ++t)
-        if (out[t]) put_shared(a.part + s * size + static_cast<int64_t>(token_of(t)) * d + orow, v[t]);
+        for (int t = 0; t < OUT; ++t)
+          put_shared(a.part + s * size + static_cast<int64_t>(token) * d + row_of(t), v[t]);
       wait_stores();
       __syncthreads();
       if (tid == 0)
@@ -986,19 +1048,18 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
                                         __HIP_MEMORY_SCOPE_AGENT);
       __syncthreads();
       finish = s_last == static_cast<uint32_t>(a.S - 1);
-      if (finish)
+      if (finish && out)
 #pragma unroll
-        for (int t = 0; t < OUT; ++t)
-          if (out[t]) {
-            v[t] = 0.0f;
-            for (int k = 0; k < a.S; ++k)
-              v[t] += get_shared(a.part + k * size + static_cast<int64_t>(token_of(t)) * d + orow);
-          }
+        for (int t = 0; t < OUT; ++t) {
+          v[t] = 0.0f;
+          for (int k = 0; k < a.S; ++k)
+            v[t] += get_shared(a.part + k * size + static_cast<int64_t>(token) * d + row_of(t));
+        }
     }
+    if (finish && out)
 #pragma unroll
-    for (int t = 0; t < OUT; ++t)
-      if (finish && out[t]) {
-        const int token = token_of(t);
+      for (int t = 0; t < OUT; ++t) {
+        const int orow = row_of(t);
         if (a.bs2)
           for (int i = 0; i < Ks; ++i) v[t] += act_f32(a.bs2, static_cast<int64_t>(i) * d + orow, Act{});
         if (a.b2)
