@@ -132,8 +132,14 @@ def _ptr(t: Optional[torch.Tensor]):
     return t.data_ptr()
 
 
+# the current stream's handle without building a Stream object (about 2.5 us)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
@@ -260,31 +266,34 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _on_device(**tensors):
+def _on_device(*tensors):
     """The tensors given (None allowed) live on the current GPU, whose streams
     the calls use."""
-    for name, t in tensors.items():
-        if t is not None:
-            _need(t.is_cuda and t.device.index == torch.cuda.current_device(),
-                  f"{name} must be on the current GPU")
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors must be on the current GPU")
 
 
 def quantize_mxfp4(x, codes, scales, widened=None, stream=None):
     """x [rows, d] (bf16 or f32; rows may be strided) to codes [rows, d/2] and
     scale bytes [rows, d/32] (uint8), and the values they stand for (widened
     [rows, d], x's type)."""
-    _on_device(x=x, codes=codes, scales=scales, widened=widened)
-    _need(x.dim() == 2 and x.dtype in (torch.bfloat16, torch.float32), "x must be [rows, d] bf16 or f32")
+    _on_device(x, codes, scales, widened)
+    dt = x.dtype
+    _need(x.dim() == 2 and (dt is torch.bfloat16 or dt is torch.float32),
+          "x must be [rows, d] bf16 or f32")
     rows, d = x.shape
-    _need(x.stride(1) == 1 or d <= 1, "elements of a row of x must be contiguous")
-    _need(codes.dtype == scales.dtype == torch.uint8, "codes and scales must be uint8")
-    _need(tuple(codes.shape) == (rows, d // 2) and tuple(scales.shape) == (rows, d // 32),
+    ldx, inner = x.stride()
+    _need(inner == 1 or d <= 1, "elements of a row of x must be contiguous")
+    _need(codes.dtype is torch.uint8 and scales.dtype is torch.uint8, "codes and scales must be uint8")
+    _need(codes.shape == (rows, d // 2) and scales.shape == (rows, d // 32),
           "codes must be [rows, d/2] and scales [rows, d/32]")
-    _need(widened is None or (widened.shape == x.shape and widened.dtype == x.dtype),
+    _need(widened is None or (widened.shape == (rows, d) and widened.dtype is dt),
           "widened must have x's shape and type")
     _check("moe_quantize_mxfp4", lib().moe_quantize_mxfp4(
-        MOE_BF16 if x.dtype == torch.bfloat16 else MOE_F32, rows, d, x.data_ptr(), x.stride(0),
-        _ptr(codes), _ptr(scales), _ptr(widened), _stream(stream)))
+        MOE_BF16 if dt is torch.bfloat16 else MOE_F32, rows, d, x.data_ptr(), ldx, _ptr(codes),
+        _ptr(scales), _ptr(widened), _stream(stream)))
 
 
 def grouped_linear_mxfp4_workspace_size(n_groups, n_out, k, max_rows) -> int:
@@ -296,28 +305,30 @@ def grouped_linear_mxfp4(x_codes, x_scales, offsets, w_codes, w_scales, y_rows, 
                          bias=None, silu=False, ws=None, stream=None):
     """y_rows [max_rows, n_out] (bf16) of x rows [., k/2] and weights
     [n_groups, n_out, k/2]; the sizes come from the tensors."""
-    _on_device(x_codes=x_codes, x_scales=x_scales, offsets=offsets, w_codes=w_codes,
-               w_scales=w_scales, y_rows=y_rows, row_index=row_index, bias=bias, ws=ws)
-    _need(w_codes.dim() == 3 and y_rows.dim() == 2, "w_codes must be [G, n_out, k/2], y_rows [rows, n_out]")
-    g, n_out, k = w_codes.shape[0], w_codes.shape[1], 2 * w_codes.shape[2]
-    max_rows = y_rows.shape[0]
-    _need(all(t.dtype == torch.uint8 for t in (x_codes, x_scales, w_codes, w_scales)),
+    _on_device(x_codes, x_scales, offsets, w_codes, w_scales, y_rows, row_index, bias, ws)
+    _need(w_codes.dim() == 3 and y_rows.dim() == 2 and x_codes.dim() == 2,
+          "w_codes must be [G, n_out, k/2], y_rows [rows, n_out], x_codes [., k/2]")
+    u8 = torch.uint8
+    _need(x_codes.dtype is u8 and x_scales.dtype is u8 and w_codes.dtype is u8 and w_scales.dtype is u8,
           "codes and scales must be uint8")
-    _need(tuple(w_scales.shape) == (g, n_out, k // 32), "w_scales must be [G, n_out, k/32]")
-    _need(x_codes.dim() == 2 and x_codes.shape[1] * 2 == k and
-          tuple(x_scales.shape) == (x_codes.shape[0], k // 32), "x_codes must be [., k/2], x_scales [., k/32]")
-    _need(y_rows.dtype == torch.bfloat16 and y_rows.shape[1] == n_out, "y_rows must be [rows, n_out] bf16")
-    _need(offsets.dtype == torch.int32 and offsets.numel() == g + 1, "offsets must be [G + 1] int32")
+    g, n_out, kb = w_codes.shape
+    max_rows, cols = y_rows.shape
+    x_rows, xb = x_codes.shape
+    k = 2 * kb
+    _need(w_scales.shape == (g, n_out, k // 32), "w_scales must be [G, n_out, k/32]")
+    _need(xb == kb and x_scales.shape == (x_rows, k // 32), "x_codes must be [., k/2], x_scales [., k/32]")
+    _need(y_rows.dtype is torch.bfloat16 and cols == n_out, "y_rows must be [rows, n_out] bf16")
+    _need(offsets.dtype is torch.int32 and offsets.numel() == g + 1, "offsets must be [G + 1] int32")
     if row_index is None:
-        _need(x_codes.shape[0] >= max_rows, "x has fewer rows than y_rows (and no row_index)")
+        _need(x_rows >= max_rows, "x has fewer rows than y_rows (and no row_index)")
     else:
-        _need(row_index.dtype == torch.int32 and row_index.numel() >= max_rows,
+        _need(row_index.dtype is torch.int32 and row_index.numel() >= max_rows,
               "row_index must be [max_rows] int32")
-    _need(bias is None or (bias.dtype == torch.bfloat16 and tuple(bias.shape) == (g, n_out)),
+    _need(bias is None or (bias.dtype is torch.bfloat16 and bias.shape == (g, n_out)),
           "bias must be [G, n_out] bf16")
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     _check("moe_grouped_linear_mxfp4", lib().moe_grouped_linear_mxfp4(
-        g, n_out, k, x_codes.shape[0], _ptr(x_codes), _ptr(x_scales), _ptr(row_index), _ptr(offsets), max_rows,
+        g, n_out, k, x_rows, _ptr(x_codes), _ptr(x_scales), _ptr(row_index), _ptr(offsets), max_rows,
         _ptr(w_codes), _ptr(w_scales), _ptr(bias), int(bool(silu)), _ptr(y_rows), _ptr(ws), nbytes,
         _stream(stream)))
 
@@ -333,14 +344,15 @@ def weights_mxfp4(w_router, router_bias, w1, w1_scales, b1, w2, w2_scales, b2, w
 
 
 def _layer_forward_few(fn: str, cfg, w, x, y, topk_idx, topk_gate, counts, ws, stream):
-    _on_device(x=x, y=y, topk_idx=topk_idx, topk_gate=topk_gate, counts=counts, ws=ws)
+    _on_device(x, y, topk_idx, topk_gate, counts, ws)
     T, K = cfg.T, cfg.top_k
     act = torch.bfloat16 if cfg.dtype == MOE_BF16 else torch.float32
-    _need(x.dtype == y.dtype == act and x.numel() == y.numel() == T * cfg.d_model,
+    _need(x.dtype is act and y.dtype is act and x.numel() == y.numel() == T * cfg.d_model,
           "x and y must be [T, d_model] of the layer's type")
-    for t, dt, n in ((topk_idx, torch.int32, T * K), (topk_gate, torch.float32, T * K),
-                     (counts, torch.int32, cfg.n_routed)):
-        _need(t is None or (t.dtype == dt and t.numel() == n), "a routing output has another size or type")
+    _need((topk_idx is None or (topk_idx.dtype is torch.int32 and topk_idx.numel() == T * K)) and
+          (topk_gate is None or (topk_gate.dtype is torch.float32 and topk_gate.numel() == T * K)) and
+          (counts is None or (counts.dtype is torch.int32 and counts.numel() == cfg.n_routed)),
+          "a routing output has another size or type")
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     _check(fn, getattr(lib(), fn)(ctypes.byref(cfg), ctypes.byref(w), _ptr(x), _ptr(y),
                                   _ptr(topk_idx), _ptr(topk_gate), _ptr(counts), _ptr(ws), nbytes,
