@@ -153,13 +153,13 @@ hipError_t quantize(const void *x, int64_t rows, int d, int64_t stride, uint8_t 
 //
 // Two kernels, by the rows of a group:
 //   * up to kStreamRows rows: bound by the bytes of the weights; operands go
-//     straight from memory to registers, eight waves share the reduction;
+//     straight from memory to registers;
 //   * more: 256 x 256 tiles (128 x 256 and 64 x 256 for a group's last rows),
 //     operands through LDS.
 // ---------------------------------------------------------------------------
 constexpr int kMaxGroups = kMaxRouted + kMaxShared;
 constexpr int kXcds = 8;
-constexpr int kStreamRows = 32;
+constexpr int kStreamRows = 64;
 
 struct MxArgs {
   const uint8_t *x, *xs;         // rows of codes, rows of scale bytes
@@ -180,123 +180,295 @@ __device__ __forceinline__ i32x8_t codes32(u32x4_t v) {
 }
 
 // ---- few rows ----
+// A wave takes units of 16 features over the whole reduction axis, reading the
+// weights straight into the operand registers of 16x16x128 instructions, 16
+// bytes (one block) a lane and several chunks ahead.  A chunk is what the 16
+// lanes of a row read together: 16 blocks, 512 elements.  So that neighbouring
+// lanes read neighbouring bytes (in the instruction's own order they belong to
+// different rows, and the addresses of a load are then looked up one by one, 64
+// clocks instead of 16), load r of a lane (a, b, q) is block 4 q + b of row
+// 4 r + a, four rows a load.  From there
+//   * up to 16 rows of X: rows (a, b) x columns (row t of four, b') with
+//       A[(a, b)][q] = W[4 r + a][block 4 q + b],  B[q][(t, b')] = X[t][block 4 q + b'],
+//     of whose 16 x 16 results those with b = b' are of use and the four of
+//     them add up: no data moves, and one, two or four instructions a load;
+//   * up to 64: the loads r and lanes b are transposed, which gives sixteen
+//     whole rows for four instructions, W's and X's alike.
 namespace stream {
-constexpr int WAVES = 8, NT = WAVES * 64, R = 4, BN = 16 * R;
+constexpr int WAVES = 4, NT = WAVES * 64, R = 4, UN = 4 * R;
 
-// One item: 64 features of a group with at most 16 C rows.  A lane holds one
-// block (16 bytes of codes and its scale byte) of one row per 128 elements;
-// wave w takes the 128-element chunks w, w + 8, ...
-template <int C, bool SILU>
-__device__ __forceinline__ void item(const MxArgs &a, int g, int64_t first, int rows, int n0,
-                                     float (*s_red)[R * 2][256]) {
-  constexpr int U = C == 1 ? 2 : 1;      // chunks in flight per wave
-  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-  const int r16 = lane & 15, q = lane >> 4;
-  const int64_t kb = a.k / 2, ksb = a.k / 32;
-  const uint8_t *xp[C], *xsp[C], *wp[R], *wsp[R];
-  bool live[C];
+// Operands that MODE columns take: MODE 1, 2, 4 fours of rows (diagonal), or 8
+// and 16: two and four tiles of 16 (transposed).
+template <int MODE> constexpr bool kTurn = MODE >= 8;
+template <int MODE> constexpr int kLoadsB = MODE;                           // 16-byte loads of X
+template <int MODE> constexpr int kScalesB = kTurn<MODE> ? MODE / 4 : MODE;  // and of its scales
+template <int MODE> constexpr int kDepth = MODE == 1 ? 6 : MODE == 2 ? 5 : MODE == 16 ? 2 : 3;
+
+// 4 x 4 transpose between four registers and four neighbouring lanes.
+__device__ __forceinline__ void transpose4(uint32_t (&v)[4], bool odd, bool high) {
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    live[c] = c * 16 + r16 < rows;
-    const int64_t src = source_row(a, first + (live[c] ? c * 16 + r16 : 0));
-    xp[c] = a.x + src * kb + q * 16;
-    xsp[c] = a.xs + src * ksb + q;
+  for (int k = 0; k < 4; k += 2) {
+    const uint32_t other = __builtin_amdgcn_mov_dpp(odd ? v[k] : v[k + 1], 0xB1, 0xF, 0xF, true);
+    v[k] = odd ? other : v[k];
+    v[k + 1] = odd ? v[k + 1] : other;
   }
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int64_t n = static_cast<int64_t>(g) * a.n_out + min(n0 + i * 16 + r16, a.n_out - 1);
-    wp[i] = a.w + n * kb + q * 16;
-    wsp[i] = a.ws + n * ksb + q;
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t other = __builtin_amdgcn_mov_dpp(high ? v[k] : v[k + 2], 0x4E, 0xF, 0xF, true);
+    v[k] = high ? other : v[k];
+    v[k + 2] = high ? v[k + 2] : other;
   }
-  f32x4_t acc[R][C];
+}
+__device__ __forceinline__ void transpose4(u32x4_t *v, bool odd, bool high) {
 #pragma unroll
-  for (int i = 0; i < R; ++i)
+  for (int w = 0; w < 4; ++w) {
+    uint32_t x[4] = {v[0][w], v[1][w], v[2][w], v[3][w]};
+    transpose4(x, odd, high);
 #pragma unroll
-    for (int c = 0; c < C; ++c) acc[i][c] = f32x4_t{0, 0, 0, 0};
-  const int nch = a.k / 128;
-  for (int c0 = wave; c0 < nch; c0 += WAVES * U) {
-    u32x4_t xv[U][C], wv[U][R];
-    int sx[U][C], sw[U][R];
+    for (int r = 0; r < 4; ++r) v[r][w] = x[r];
+  }
+}
+
+// acc += A B with the scale bytes J of both.
+template <int J>
+__device__ __forceinline__ void product(f32x4_t &acc, u32x4_t a, u32x4_t b, int sa, int sb) {
+  acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(codes32(a), codes32(b), acc, 4, 4, J, sa, J, sb);
+}
+
+// Units u0 .. u0 + count - 1 of a group whose rows first .. first + rows - 1 fit MODE.
+template <int MODE, bool SILU>
+__device__ __forceinline__ void run(const MxArgs &a, int g, int64_t first, int rows, int u0, int count) {
+  constexpr int D = kDepth<MODE>, NB = kLoadsB<MODE>, NS = kScalesB<MODE>, NA = kTurn<MODE> ? MODE / 4 : R * MODE;
+  const int lane = threadIdx.x & 63;
+  const int b = lane & 3, ar = (lane >> 2) & 3, q = lane >> 4, piece = q * 4 + b;
+  const int pieces = a.k / 32, nch = (pieces + 15) >> 4, tail = pieces & 15;
+  const uint8_t *w = a.w + static_cast<int64_t>(g) * a.n_out * pieces * 16;
+  const uint8_t *ws = a.ws + static_cast<int64_t>(g) * a.n_out * pieces;
+  // blocks before this lane's row of X in each load, and its scale row
+  uint32_t bo[NB], bso[NS];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int c = c0 + u * WAVES;
-      const bool in = c < nch;
+  for (int i = 0; i < NB; ++i) {
+    // columns 4 i + ar (diagonal), or row 4 r + ar of tile i / 4
+    const int r = min(i * 4 + ar, rows - 1);
+    bo[i] = static_cast<uint32_t>(source_row(a, first + r)) * pieces;
+  }
 #pragma unroll
-      for (int j = 0; j < C; ++j) {
-        xv[u][j] = u32x4_t{0, 0, 0, 0};
-        sx[u][j] = 127;
-        if (in && live[j]) {
-          xv[u][j] = *reinterpret_cast<const u32x4_t *>(xp[j] + c * 64);
-          sx[u][j] = xsp[j][c * 4];
+  for (int i = 0; i < NS; ++i) {
+    if (!kTurn<MODE>) {
+      bso[i] = bo[i];
+    } else {
+      const int r = min(i * 16 + b * 4 + ar, rows - 1);     // row of the turned column
+      bso[i] = static_cast<uint32_t>(source_row(a, first + r)) * pieces;
+    }
+  }
+  f32x4_t acc[NA];
+#pragma unroll
+  for (int i = 0; i < NA; ++i) acc[i] = f32x4_t{0, 0, 0, 0};
+  struct Stage {
+    u32x4_t a[R], b[NB];
+    int sa[kTurn<MODE> ? 1 : R], sb[NS];
+  } st[D];
+  int fu = u0, fc = 0, uu = u0, uc = 0;         // unit and chunk of the next fetch, of the next use
+  auto fetch = [&](Stage &s) {
+    const uint32_t at = min(fc * 16 + piece, pieces - 1), at4 = min(fc * 16 + q * 4, pieces - 4);
+#pragma unroll
+    for (int i = 0; i < NB; ++i) s.b[i] = *reinterpret_cast<const u32x4_t *>(a.x + (bo[i] + at) * 16);
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+      s.sb[i] = kTurn<MODE> ? *reinterpret_cast<const int *>(a.xs + (bso[i] + at4)) : a.xs[bso[i] + at];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const uint32_t row = min(fu * UN + r * 4 + ar, a.n_out - 1) * pieces;
+      s.a[r] = *reinterpret_cast<const u32x4_t *>(w + (row + at) * 16);
+      if (!kTurn<MODE>) s.sa[r] = ws[row + at];
+    }
+    if (kTurn<MODE>)
+      s.sa[0] = *reinterpret_cast<const int *>(
+          ws + (static_cast<uint32_t>(min(fu * UN + b * 4 + ar, a.n_out - 1)) * pieces + at4));
+    if (++fc == nch) {
+      fc = 0;
+      ++fu;
+    }
+  };
+  auto finish = [&]() {
+    const int64_t gn = static_cast<int64_t>(g) * a.n_out;
+    if constexpr (!kTurn<MODE>) {
+      // register i of a lane: entry ((row q, block i), (column ar, block b)) of load
+      // r; take i = b, add the four lanes b, and let lane b keep load b
+#pragma unroll
+      for (int t = 0; t < MODE; ++t) {
+        float z = 0.0f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const f32x4_t v = acc[r * MODE + t];
+          float x = b == 0 ? v[0] : b == 1 ? v[1] : b == 2 ? v[2] : v[3];
+          x += __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(x), 0xB1, 0xF, 0xF, true));
+          x += __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(x), 0x4E, 0xF, 0xF, true));
+          z = b == r ? x : z;
+        }
+        const int n = uu * UN + b * 4 + q, row = t * 4 + ar;
+        if (row < rows && n < a.n_out) {
+          if (a.bias) z += bf16_to_f32(a.bias[gn + n]);
+          if (SILU) z = silu_fast(z);
+          a.y[(first + row) * a.n_out + n] = f32_to_bf16(z);
         }
       }
+    } else {
+      // register i of a lane: feature 4 i + q, column lane % 16, which is row
+      // 4 b + ar; turned so that a lane holds features 4 q .. 4 q + 3
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        wv[u][i] = u32x4_t{0, 0, 0, 0};
-        sw[u][i] = 127;
-        if (in) {
-          wv[u][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t *>(wp[i] + c * 64));
-          sw[u][i] = wsp[i][c * 4];
+      for (int c = 0; c < NA; ++c) {
+        uint32_t v[4] = {__float_as_uint(acc[c][0]), __float_as_uint(acc[c][1]),
+                         __float_as_uint(acc[c][2]), __float_as_uint(acc[c][3])};
+#pragma unroll
+        for (int x = 0; x < 4; x += 2) {
+          const uint32_t other = __shfl_xor(q & 1 ? v[x] : v[x + 1], 16);
+          v[x] = q & 1 ? other : v[x];
+          v[x + 1] = q & 1 ? v[x + 1] : other;
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t other = __shfl_xor(q & 2 ? v[x] : v[x + 2], 32);
+          v[x] = q & 2 ? other : v[x];
+          v[x + 2] = q & 2 ? v[x + 2] : other;
+        }
+        const int n = uu * UN + q * 4, row = c * 16 + b * 4 + ar;
+        if (row < rows && n < a.n_out) {
+          float z[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            z[x] = __uint_as_float(v[x]);
+            if (a.bias) z[x] += bf16_to_f32(a.bias[gn + n + x]);
+            if (SILU) z[x] = silu_fast(z[x]);
+          }
+          uint2 o;
+          o.x = pack_bf16x2(z[0], z[1]);
+          o.y = pack_bf16x2(z[2], z[3]);
+          *reinterpret_cast<uint2 *>(a.y + (first + row) * a.n_out + n) = o;
         }
       }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int i = 0; i < NA; ++i) acc[i] = f32x4_t{0, 0, 0, 0};
+  };
+  auto use = [&](Stage &s) {
+    if (tail && uc == nch - 1) {
+      // past the end of a row both sides hold its last block: X's count as zeros
+      const bool past = piece >= tail;
 #pragma unroll
-      for (int i = 0; i < R; ++i)
+      for (int i = 0; i < NB; ++i)
 #pragma unroll
-        for (int j = 0; j < C; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              codes32(wv[u][i]), codes32(xv[u][j]), acc[i][j], 4, 4, 0, sw[u][i], 0, sx[u][j]);
+        for (int x = 0; x < 4; ++x) s.b[i][x] = past ? 0u : s.b[i][x];
+    }
+    if constexpr (!kTurn<MODE>) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int t = 0; t < MODE; ++t) product<0>(acc[r * MODE + t], s.a[r], s.b[t], s.sa[r], s.sb[t]);
+    } else {
+      transpose4(s.a, b & 1, b & 2);
+#pragma unroll
+      for (int c = 0; c < NA; ++c) {
+        transpose4(s.b + c * 4, b & 1, b & 2);
+        product<0>(acc[c], s.a[0], s.b[c * 4 + 0], s.sa[0], s.sb[c]);
+        product<1>(acc[c], s.a[1], s.b[c * 4 + 1], s.sa[0], s.sb[c]);
+        product<2>(acc[c], s.a[2], s.b[c * 4 + 2], s.sa[0], s.sb[c]);
+        product<3>(acc[c], s.a[3], s.b[c * 4 + 3], s.sa[0], s.sb[c]);
+      }
+    }
+    // done here, not later, or the operands outlive the next loads
+#pragma unroll
+    for (int i = 0; i < NA; ++i) asm volatile("" : "+v"(acc[i]));
+    if (++uc == nch) {
+      finish();
+      uc = 0;
+      ++uu;
+    }
+  };
+  const int n = count * nch;
+  if (n < D) {
+    for (int k = 0; k < n; ++k) {
+      fetch(st[0]);
+      use(st[0]);
+    }
+    return;
   }
 #pragma unroll
-  for (int i = 0; i < R; ++i)
+  for (int k = 0; k < D; ++k) fetch(st[k]);
+  int left = n - D;
+  for (; left >= D; left -= D) {
 #pragma unroll
-    for (int j = 0; j < C; ++j)
-      *reinterpret_cast<f32x4_t *>(&s_red[wave][i * C + j][lane * 4]) = acc[i][j];
-  __syncthreads();
-  for (int o = tid; o < rows * BN; o += NT) {
-    const int t = o / BN, nl = o % BN, n = n0 + nl;
-    if (n >= a.n_out) continue;
-    const int f16 = nl & 15, at = ((f16 >> 2) * 16 + (t & 15)) * 4 + (f16 & 3);
-    float z = 0.0f;
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) z += s_red[w][(nl >> 4) * C + (t >> 4)][at];
-    if (a.bias) z += bf16_to_f32(a.bias[static_cast<int64_t>(g) * a.n_out + n]);
-    if (SILU) z = silu_fast(z);
-    a.y[(first + t) * a.n_out + n] = f32_to_bf16(z);
+    for (int k = 0; k < D; ++k) {
+      use(st[k]);
+      fetch(st[k]);
+    }
   }
-  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < D; ++k) {
+    use(st[k]);
+    if (k < left) fetch(st[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < D; ++k)
+    if (k < left) use(st[k]);
 }
 }  // namespace stream
 
+// What a unit of a group of `rows` rows takes, in quarters of one of a few rows
+// (0: not this kernel's): with more rows X takes more registers and fewer chunks
+// are in flight.
+__device__ __forceinline__ int mx_unit_cost(int rows) {
+  return rows <= 0 || rows > kStreamRows ? 0 : rows <= 8 ? 4 : rows <= 16 ? 5 : rows <= 32 ? 7 : 10;
+}
+
+// Every wave takes a range of equal cost of all groups' units: those whose first
+// quarter lies in it.
 template <bool SILU>
-__global__ __launch_bounds__(stream::NT, 4) void mx_stream_kernel(MxArgs a) {
+__global__ __launch_bounds__(stream::NT, 2) void mx_stream_kernel(MxArgs a) {
   using namespace stream;
-  __shared__ float s_red[WAVES][R * 2][256];
-  __shared__ int16_t s_list[kMaxGroups];
-  __shared__ int s_n;
+  __shared__ int64_t s_pref[kMaxGroups + 1];
   const int tid = threadIdx.x, lane = tid & 63;
+  const int per = (a.n_out + UN - 1) / UN;
   if (tid < 64) {
-    int n = 0;
+    int64_t base = 0;
     for (int g0 = 0; g0 < a.groups; g0 += 64) {
       const int g = g0 + lane;
-      const int rows = g < a.groups ? a.offsets[g + 1] - a.offsets[g] : 0;
-      const bool in = rows > 0 && rows <= kStreamRows;
-      const uint64_t m = __ballot(in);
-      if (in) s_list[n + __popcll(m & ((1ull << lane) - 1))] = static_cast<int16_t>(g);
-      n += __popcll(m);
+      const int c = g < a.groups ? mx_unit_cost(a.offsets[g + 1] - a.offsets[g]) : 0;
+      int incl = c;
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const int o = __shfl_up(incl, off);
+        if (lane >= off) incl += o;
+      }
+      if (g < a.groups) s_pref[g] = base + static_cast<int64_t>(incl - c) * per;
+      base += static_cast<int64_t>(__shfl(incl, 63)) * per;
     }
-    if (tid == 0) s_n = n;
+    if (tid == 0) s_pref[a.groups] = base;
   }
   __syncthreads();
-  const int nblk = (a.n_out + BN - 1) / BN, items = uniform(s_n) * nblk;
-  for (int it = blockIdx.x; it < items; it += gridDim.x) {
-    const int i = it / nblk, g = uniform(s_list[i]), n0 = (it - i * nblk) * BN;
-    const int64_t first = a.offsets[g];
-    const int rows = static_cast<int>(a.offsets[g + 1] - first);
-    if (rows <= 16) item<1, SILU>(a, g, first, rows, n0, s_red);
-    else item<2, SILU>(a, g, first, rows, n0, s_red);
+  const int64_t total = s_pref[a.groups];
+  const int v = blockIdx.x * WAVES + uniform(tid >> 6), waves = gridDim.x * WAVES;
+  const int64_t lo = total * v / waves, hi = total * (v + 1) / waves;
+  if (lo >= hi) return;
+  int g = 0, up = a.groups;                // s_pref[g] <= lo < s_pref[up]
+  while (up - g > 1) {
+    const int mid = (g + up) >> 1;
+    if (s_pref[mid] <= lo) g = mid; else up = mid;
+  }
+  for (; g < a.groups && s_pref[g] < hi; ++g) {
+    const int ug = uniform(g);
+    const int first = uniform(a.offsets[ug]), rows = uniform(a.offsets[ug + 1]) - first;
+    const int cost = mx_unit_cost(rows);
+    if (cost == 0) continue;
+    const int64_t base = s_pref[ug];
+    const int u0 = uniform(static_cast<int>(max(int64_t(0), (lo - base + cost - 1) / cost)));
+    const int u1 = uniform(static_cast<int>(min(static_cast<int64_t>(per), (hi - base + cost - 1) / cost)));
+    if (u0 >= u1) continue;
+    if (rows <= 4) run<1, SILU>(a, ug, first, rows, u0, u1 - u0);
+    else if (rows <= 8) run<2, SILU>(a, ug, first, rows, u0, u1 - u0);
+    else if (rows <= 16) run<4, SILU>(a, ug, first, rows, u0, u1 - u0);
+    else if (rows <= 32) run<8, SILU>(a, ug, first, rows, u0, u1 - u0);
+    else run<16, SILU>(a, ug, first, rows, u0, u1 - u0);
   }
 }
 
@@ -693,8 +865,9 @@ hipError_t launch_linear_mxfp4(const MxLinear &p, hipStream_t s) {
   // the groups' row counts are on the device: both kernels look, each takes
   // the groups of its size
   const int64_t met = p.max_rows < p.groups ? p.max_rows : p.groups;
-  const int64_t items = met * ((p.n_out + stream::BN - 1) / stream::BN);
-  const dim3 sgrid(static_cast<unsigned>(items < 512 ? items : 512));
+  const int64_t units = met * ((p.n_out + stream::UN - 1) / stream::UN);
+  const int64_t blocks = (units + stream::WAVES - 1) / stream::WAVES;
+  const dim3 sgrid(static_cast<unsigned>(blocks < 512 ? blocks : 512));
   if (p.silu) hipLaunchKernelGGL(mx_stream_kernel<true>, sgrid, dim3(stream::NT), 0, s, a);
   else hipLaunchKernelGGL(mx_stream_kernel<false>, sgrid, dim3(stream::NT), 0, s, a);
   const hipError_t e = hipGetLastError();
