@@ -279,7 +279,8 @@ __device__ __forceinline__ void run(const MxArgs &a, int g, int64_t first, int r
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const uint32_t row = min(fu * UN + r * 4 + ar, a.n_out - 1) * pieces;
-      s.a[r] = *reinterpret_cast<const u32x4_t *>(w + (row + at) * 16);
+      s.a[r] = __builtin_nontemporal_load(     // read once
+          reinterpret_cast<const u32x4_t *>(w + (row + at) * 16));
       if (!kTurn<MODE>) s.sa[r] = ws[row + at];
     }
     if (kTurn<MODE>)
@@ -560,7 +561,7 @@ struct Tile {
   }
   static __device__ __forceinline__ void copy(const Src &s, int i, int off, uint32_t base, int wave) {
     if (i < AC) dma::dma16s(s.a[i] + off, s.abase, base + (4 * i + wave) * 1024);
-    else dma::dma16s(s.b[i - AC] + off, s.bbase, base + BM * 128 + (4 * (i - AC) + wave) * 1024);
+    else dma::dma16s_nt(s.b[i - AC] + off, s.bbase, base + BM * 128 + (4 * (i - AC) + wave) * 1024);
   }
   // Scale copies: the rows of X (which 0) or W (1) for the steps 2p and 2p + 1.
   static __device__ __forceinline__ int pair_off(const Src &s, int p, int lane) {
