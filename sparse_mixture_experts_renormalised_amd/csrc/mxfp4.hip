@@ -484,7 +484,7 @@ __global__ __launch_bounds__(stream::NT, 2) void mx_stream_kernel(MxArgs a) {
 // 16-byte chunk c of tile row r lies at position c ^ ((r / 2) % 8) of its
 // 128-byte row, so that the 16 rows read together cover all banks once.
 namespace tile {
-constexpr int NT = 256, BN = 256, NS = 4, TN = 4, BUF = 2 * 512 * 128, SBUF = 512 * 16;
+constexpr int NT = 512, BN = 256, NS = 2, TN = 2, BUF = 2 * 512 * 128, SBUF = 512 * 16;
 
 __device__ __forceinline__ int swz(int r, int c) { return c ^ ((r >> 1) & 7); }
 
@@ -496,8 +496,8 @@ __device__ __forceinline__ void lds_barrier() {
 
 template <int BM>
 struct Tile {
-  static constexpr int TM = BM / 64, AC = BM / 32, BC = 8, NCP = AC + BC;   // code copies per wave
-  static constexpr int SC = 4, N = NCP + SC;                                // scale, all copies
+  static constexpr int TM = BM / 64, AC = BM / 64, BC = 4, NCP = AC + BC;   // code copies per wave
+  static constexpr int SC = 2, N = NCP + SC;                                // scale, all copies
   static constexpr int STEP = (BM + BN) * 128, SPAIR = 512 * 16;            // LDS bytes
   static constexpr int MF = NS * TN * TM;
 
@@ -512,7 +512,9 @@ struct Tile {
   };
   struct Frags {
     u32x4_t a[NS][TM], b[NS][TN];
-    uint32_t sa[TM], sb[TN];   // byte ks: scale of this lane's block of slice ks
+  };
+  struct Scales {
+    uint32_t a[TM], b[TN];     // byte ks: scale of this lane's block of slice ks
   };
   using Acc = f32x16_t[TN][TM];
 
@@ -525,9 +527,9 @@ struct Tile {
     const int sr = (tid >> 6) * 16 + ((tid & 63) >> 2);
     int64_t ra[AC], rs[SC];
 #pragma unroll
-    for (int i = 0; i < AC; ++i) ra[i] = first + min(row0 + (tid >> 3) + i * 32, rows - 1);
+    for (int i = 0; i < AC; ++i) ra[i] = first + min(row0 + (tid >> 3) + i * 64, rows - 1);
 #pragma unroll
-    for (int j = 0; j < SC; ++j) rs[j] = first + min(row0 + sr + j * 64, rows - 1);
+    for (int j = 0; j < SC; ++j) rs[j] = first + min(row0 + sr + j * 128, rows - 1);
     if (a.index) {
 #pragma unroll
       for (int i = 0; i < AC; ++i) ra[i] = a.index[ra[i]];
@@ -542,12 +544,12 @@ struct Tile {
     s.bbase = a.w + static_cast<int64_t>(g) * a.n_out * kb;
 #pragma unroll
     for (int i = 0; i < BC; ++i)
-      s.b[i] = static_cast<uint32_t>(min(n0 + (tid >> 3) + i * 32, a.n_out - 1)) *
+      s.b[i] = static_cast<uint32_t>(min(n0 + (tid >> 3) + i * 64, a.n_out - 1)) *
                    static_cast<uint32_t>(kb) + c * 16;
 #pragma unroll
     for (int j = 0; j < SC; ++j) {
       s.sa[j] = static_cast<uint32_t>(rs[j] * ksb);
-      s.sb[j] = static_cast<uint32_t>(min(n0 + sr + j * 64, a.n_out - 1)) * static_cast<uint32_t>(ksb);
+      s.sb[j] = static_cast<uint32_t>(min(n0 + sr + j * 128, a.n_out - 1)) * static_cast<uint32_t>(ksb);
     }
     s.nd = a.k / 128;
     s.nk = (s.nd + 1) / 2;
@@ -560,8 +562,8 @@ struct Tile {
     return kb * 128 + (kb == s.nk - 1 ? s.tadj : 0);
   }
   static __device__ __forceinline__ void copy(const Src &s, int i, int off, uint32_t base, int wave) {
-    if (i < AC) dma::dma16s(s.a[i] + off, s.abase, base + (4 * i + wave) * 1024);
-    else dma::dma16s_nt(s.b[i - AC] + off, s.bbase, base + BM * 128 + (4 * (i - AC) + wave) * 1024);
+    if (i < AC) dma::dma16s(s.a[i] + off, s.abase, base + (8 * i + wave) * 1024);
+    else dma::dma16s_nt(s.b[i - AC] + off, s.bbase, base + BM * 128 + (8 * (i - AC) + wave) * 1024);
   }
   // Scale copies: the rows of X (which 0) or W (1) for the steps 2p and 2p + 1.
   static __device__ __forceinline__ int pair_off(const Src &s, int p, int lane) {
@@ -570,30 +572,35 @@ struct Tile {
   static __device__ __forceinline__ void scale_copy(const Src &s, int j, bool of_w, int off,
                                                     uint32_t base, int wave) {
     dma::dma4s((of_w ? s.sb[j] : s.sa[j]) + off, of_w ? s.sbbase : s.sabase,
-               base + (of_w ? 256 * 16 : 0) + (4 * j + wave) * 256);
+               base + (of_w ? 256 * 16 : 0) + (8 * j + wave) * 256);
   }
 
-  // Fragments and scales of a step: lane half h takes block 2 ks + h in slice
-  // ks, so of the row's eight scale bytes it keeps the even or the odd four.
-  static __device__ __forceinline__ void read(const uint8_t *buf, const uint8_t *sbuf, int half,
-                                              Frags &f, int wm, int wn, int lane) {
+  // Scales of a step: lane half h takes block 2 ks + h in slice ks, so of the
+  // row's eight scale bytes it keeps the even or the odd four.
+  static __device__ __forceinline__ void scales(const uint8_t *sbuf, int half, Scales &f, int wm, int wn,
+                                                int lane) {
     const int h = lane >> 5, r32 = lane & 31;
     const uint32_t pick = h ? 0x07050301u : 0x06040200u;
 #pragma unroll
     for (int mi = 0; mi < TM; ++mi) {
       const int row = wm * (BM / 2) + mi * 32 + r32;
       const uint2 sv = *reinterpret_cast<const uint2 *>(sbuf + row * 16 + half * 8);
-      f.sa[mi] = __builtin_amdgcn_perm(sv.y, sv.x, pick);
+      f.a[mi] = __builtin_amdgcn_perm(sv.y, sv.x, pick);
     }
 #pragma unroll
     for (int ni = 0; ni < TN; ++ni) {
-      const int row = 256 + wn * 128 + ni * 32 + r32;
+      const int row = 256 + wn * 64 + ni * 32 + r32;
       const uint2 sv = *reinterpret_cast<const uint2 *>(sbuf + row * 16 + half * 8);
-      f.sb[ni] = __builtin_amdgcn_perm(sv.y, sv.x, pick);
+      f.b[ni] = __builtin_amdgcn_perm(sv.y, sv.x, pick);
     }
+  }
+  // Fragments of the slices 2 H and 2 H + 1 of a step.
+  template <int H>
+  static __device__ __forceinline__ void read(const uint8_t *buf, Frags &f, int wm, int wn, int lane) {
+    const int h = lane >> 5, r32 = lane & 31;
 #pragma unroll
     for (int ks = 0; ks < NS; ++ks) {
-      const int c = ks * 2 + h;
+      const int c = (2 * H + ks) * 2 + h;
 #pragma unroll
       for (int mi = 0; mi < TM; ++mi) {
         const int row = wm * (BM / 2) + mi * 32 + r32;
@@ -601,37 +608,37 @@ struct Tile {
       }
 #pragma unroll
       for (int ni = 0; ni < TN; ++ni) {
-        const int row = wn * 128 + ni * 32 + r32;
+        const int row = wn * 64 + ni * 32 + r32;
         f.b[ks][ni] =
             *reinterpret_cast<const u32x4_t *>(buf + BM * 128 + row * 128 + swz(row, c) * 16);
       }
     }
   }
 
-  // Matrix instructions M0 .. M1-1 of a step, in (slice, ni, mi) order.
-  template <int M0, int M1>
-  static __device__ __forceinline__ void mfma(const Frags &f, Acc &acc) {
+  // Matrix instructions M0 .. M1-1 of half a step, in (slice, ni, mi) order.
+  template <int H, int M0, int M1>
+  static __device__ __forceinline__ void mfma(const Frags &f, const Scales &c, Acc &acc) {
     if constexpr (M0 < M1) {
       constexpr int ks = M0 / (TN * TM), ni = (M0 / TM) % TN, mi = M0 % TM;
       acc[ni][mi] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-          codes32(f.b[ks][ni]), codes32(f.a[ks][mi]), acc[ni][mi], 4, 4, ks, f.sb[ni], ks,
-          f.sa[mi]);
-      mfma<M0 + 1, M1>(f, acc);
+          codes32(f.b[ks][ni]), codes32(f.a[ks][mi]), acc[ni][mi], 4, 4, 2 * H + ks, c.b[ni], 2 * H + ks,
+          c.a[mi]);
+      mfma<H, M0 + 1, M1>(f, c, acc);
     }
   }
 
-  // Copies I.. of a step spread over the first three slices.
+  // Copies I.. of a step spread over three quarters of its second half.
   template <int I>
   static __device__ __forceinline__ void copies_mfmas(const Src &s, int off, bool of_w, int soff,
                                                       uint32_t base, uint32_t sbase, int wave,
-                                                      const Frags &f, Acc &acc) {
+                                                      const Frags &f, const Scales &c, Acc &acc) {
     if constexpr (I < N) {
       constexpr int M3 = MF / 4 * 3;
       if constexpr (I < NCP) copy(s, I, off, base, wave);
       else scale_copy(s, I - NCP, of_w, soff, sbase, wave);
-      mfma<I * M3 / N, (I + 1) * M3 / N>(f, acc);
+      mfma<1, I * M3 / N, (I + 1) * M3 / N>(f, c, acc);
       __builtin_amdgcn_sched_barrier(0);
-      copies_mfmas<I + 1>(s, off, of_w, soff, base, sbase, wave, f, acc);
+      copies_mfmas<I + 1>(s, off, of_w, soff, base, sbase, wave, f, c, acc);
     }
   }
 
@@ -645,7 +652,8 @@ struct Tile {
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
     const uint32_t b0 = uniform(static_cast<int>(dma::lds_addr(buf))), b1 = b0 + STEP;
     const uint32_t sb0 = uniform(static_cast<int>(dma::lds_addr(sbuf)));
-    Frags f;
+    Frags f0, f1;
+    Scales c;
     const int soff0 = pair_off(s, 0, lane), soff1 = pair_off(s, 1, lane);
 #pragma unroll
     for (int j = 0; j < SC; ++j) {
@@ -664,7 +672,8 @@ struct Tile {
     } else {
       dma::wait_and_barrier<0>();
     }
-    read(buf, sbuf, 0, f, wm, wn, lane);
+    scales(sbuf, 0, c, wm, wn, lane);
+    read<0>(buf, f0, wm, wn, lane);
     __builtin_amdgcn_sched_barrier(0);
     // Step kb, with the copies of step kb + 2 into the buffer that its
     // fragments have left.  Scales of the pair p of steps 2p, 2p + 1: those of
@@ -673,30 +682,33 @@ struct Tile {
     int kb = 0;
     for (; kb + 2 < s.nk; ++kb) {
       const int cur = kb & 1;
+      read<1>(buf + (cur ? STEP : 0), f1, wm, wn, lane);
+      mfma<0, 0, MF>(f0, c, acc);
       lds_barrier();                       // every wave holds its fragments of step kb
       __builtin_amdgcn_sched_barrier(0);
       const int p = (kb + 3) >> 1;
       copies_mfmas<0>(s, step_off(s, kb + 2), cur == 0, pair_off(s, p, lane), cur ? b1 : b0,
-                      sb0 + (p & 1) * SPAIR, wave, f, acc);
+                      sb0 + (p & 1) * SPAIR, wave, f1, c, acc);
       dma::wait_and_barrier<N>();          // step kb + 1 has landed for every wave
-      mfma<MF / 4 * 3, MF>(f, acc);
-      read(buf + (cur ? 0 : STEP), sbuf + (((kb + 1) >> 1) & 1) * SPAIR, 1 - cur, f, wm, wn, lane);
-      constexpr int READS = NS * (TM + TN) + TM + TN, LAST = MF / 4;
-#pragma unroll
-      for (int i = 0; i < LAST; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x100, (READS + LAST - 1) / LAST, 0);   // LDS reads
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                           // matrix
-      }
+      mfma<1, MF / 4 * 3, MF>(f1, c, acc);
+      read<0>(buf + (cur ? 0 : STEP), f0, wm, wn, lane);
+      scales(sbuf + (((kb + 1) >> 1) & 1) * SPAIR, 1 - cur, c, wm, wn, lane);
       __builtin_amdgcn_sched_barrier(0);
     }
     if (kb + 1 < s.nk) {
-      mfma<0, MF>(f, acc);
+      read<1>(buf + (kb & 1) * STEP, f1, wm, wn, lane);
+      mfma<0, 0, MF>(f0, c, acc);
+      mfma<1, 0, MF>(f1, c, acc);
       dma::wait_and_barrier<0>();
       ++kb;
-      read(buf + (kb & 1) * STEP, sbuf + ((kb >> 1) & 1) * SPAIR, kb & 1, f, wm, wn, lane);
+      scales(sbuf + ((kb >> 1) & 1) * SPAIR, kb & 1, c, wm, wn, lane);
+      read<0>(buf + (kb & 1) * STEP, f0, wm, wn, lane);
     }
-    mfma<0, MF / 2>(f, acc);
-    if (!(s.nd & 1)) mfma<MF / 2, MF>(f, acc);
+    mfma<0, 0, MF>(f0, c, acc);
+    if (!(s.nd & 1)) {
+      read<1>(buf + (kb & 1) * STEP, f1, wm, wn, lane);
+      mfma<1, 0, MF>(f1, c, acc);
+    }
     lds_barrier();                       // buffers are free
   }
 
@@ -711,7 +723,7 @@ struct Tile {
     for (int ni = 0; ni < TN; ++ni)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int nl = wn * 128 + ni * 32 + q * 8 + (lane >> 5) * 4, n = n0 + nl;
+        const int nl = wn * 64 + ni * 32 + q * 8 + (lane >> 5) * 4, n = n0 + nl;
         float bv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         if (BIAS && n < a.n_out) {
           const uint2 b = *reinterpret_cast<const uint2 *>(a.bias + static_cast<int64_t>(g) * a.n_out + n);
@@ -742,10 +754,10 @@ struct Tile {
       uint16_t *out = a.y + (first + row0 + r0) * a.n_out + n;
       const int64_t lim = rows - row0 - r0;
 #pragma unroll 8
-      for (int j = 0; j < BM / 8; ++j) {
-        const int r = r0 + 8 * j;
+      for (int j = 0; j < BM / 16; ++j) {
+        const int r = r0 + 16 * j;
         const u32x4_t v = *reinterpret_cast<const u32x4_t *>(st + r * BN + ((c ^ (r & 31)) << 3));
-        if (8 * j < lim) store_nt(out + static_cast<int64_t>(8 * j) * a.n_out, v);
+        if (16 * j < lim) store_nt(out + static_cast<int64_t>(16 * j) * a.n_out, v);
       }
     }
     lds_barrier();
@@ -781,7 +793,7 @@ __device__ __forceinline__ int mx_full_tiles(int rows, int *tail) {
 // contiguous shares, one per XCD (workgroups are dealt to the XCDs round-robin
 // by number), so that tiles running together on an XCD share operands in its L2.
 template <bool SILU>
-__global__ __launch_bounds__(tile::NT, 1) void mx_tile_kernel(MxArgs a) {
+__global__ __launch_bounds__(tile::NT, 2) void mx_tile_kernel(MxArgs a) {
   using namespace tile;
   __shared__ __attribute__((aligned(16))) uint8_t s_buf[BUF];
   __shared__ __attribute__((aligned(16))) uint8_t s_sc[2 * SBUF];
