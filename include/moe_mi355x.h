@@ -377,7 +377,8 @@ int moe_quantize_mxfp4(int32_t dtype, int64_t rows, int32_t d, const void *x, in
  * rows and MXFP4 weights, on the scaled matrix instructions:
  *   y_rows[r] = act(X[row_index[r]] W_g^T + bias_g),  offsets[g] <= r < offsets[g+1]
  * with float32 sums, rounded to bf16 once.  A block whose scale byte is 255
- * makes the outputs it enters NaN.
+ * makes the outputs it enters NaN.  Equal calls give equal bits; the order of a
+ * row's sums depends on how many rows all groups have.
  *   x_rows      rows of x_codes and x_scales, the token rows (k elements each)
  *   row_index   [max_rows] int32 or NULL: source row of each row (a dispatch's
  *               row_token, so that a token is quantised once however many
@@ -418,10 +419,10 @@ size_t moe_grouped_linear_mxfp4_workspace_size(int32_t n_groups, int32_t n_out, 
  *   - the logits are float32 sums in a fixed tree order, not moe_route's
  *     chain, so two experts whose logits differ by no more than their rounding
  *     may be ordered differently than there; ties still go to the lower id;
- *   - hidden activations keep 16 significant bits (bf16 layers; float32
- *     otherwise) and expert outputs are not rounded before the sum over
- *     experts: y is rounded once.  Routed experts are summed in ascending
- *     expert id, the shared experts after them;
+ *   - hidden activations keep at least 16 significant bits (float32 layers:
+ *     all) and expert outputs are not rounded before the sum over experts: y
+ *     is rounded once.  Routed experts are summed in ascending expert id, the
+ *     shared experts after them;
  *   - ws holds moe_few_workspace_size(cfg) bytes, all scratch.  Nothing in it
  *     needs to be initialised.  Calls that overlap in time (other streams,
  *     parallel branches of a graph) need a workspace of their own each.
@@ -455,9 +456,15 @@ typedef struct {
     const void *bs2;            /* [K_s][d] bf16 or NULL                        */
 } moe_weights_mxfp4;
 
-/* moe_layer_forward_few on MXFP4 expert weights (widened exactly to bf16 in
- * registers; activations stay bf16).  cfg->dtype is MOE_BF16 and d_model and
- * d_ff are multiples of 128, else MOE_ERR_UNSUPPORTED. */
+/* moe_layer_forward_few on MXFP4 expert weights.  The codes go into the scaled
+ * matrix instructions as they are, against tokens and hidden rows as sums of
+ * E4M3 parts with a power-of-two scale for every 32 elements:
+ *   tokens  two parts, exact for a bf16 element down to 2^-13 of the largest of
+ *           its 32, and within 2^-21 of that largest below;
+ *   hidden  three parts, the rest at most 2^-12 of the element or 2^-25 of the
+ *           largest of its 32.
+ * cfg->dtype is MOE_BF16 and d_model and d_ff are multiples of 128, else
+ * MOE_ERR_UNSUPPORTED. */
 int moe_layer_forward_few_mxfp4(const moe_config *cfg, const moe_weights_mxfp4 *w, const void *x,
                                 void *y, int32_t *topk_idx, float *topk_gate, int32_t *counts,
                                 void *ws, size_t ws_bytes, void *stream);

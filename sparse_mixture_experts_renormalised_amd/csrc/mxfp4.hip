@@ -151,15 +151,24 @@ hipError_t quantize(const void *x, int64_t rows, int d, int64_t stride, uint8_t 
 // scale bytes and adds in float32, so nothing is widened.  Weights are the
 // first operand, so a lane ends up with four consecutive features of a row.
 //
-// Two kernels, by the rows of a group:
-//   * up to kStreamRows rows: bound by the bytes of the weights; operands go
-//     straight from memory to registers;
-//   * more: 256 x 256 tiles (128 x 256 and 64 x 256 for a group's last rows),
-//     operands through LDS.
+// Two kernels:
+//   * tiles of 256 x 256 (128 x 256 and 64 x 256 for a group's last rows),
+//     operands through LDS, one workgroup a CU: every group, where there are
+//     tiles for most of the CUs, and else the groups of more than kStreamRows
+//     rows;
+//   * else the groups of up to kStreamRows rows: units of 16 features, operands
+//     straight from memory to registers, which a few groups have enough of.
+// Measured on MI355X: 256 groups, 207 rows in about 110 of them, 7168 -> 2048:
+// 118 us, 5.6 TB/s (134 us straight from memory); 64 groups, 32768 rows, 2048 ->
+// 1408 with SiLU: 102 us; 256 groups, 32768 rows, 2048 -> 7168: 572 us, 4.4 TB/s;
+// 8 groups, 8192 rows, 4096 -> 14336 with bias and SiLU: 334 us, 2.9 PFLOP/s.
 // ---------------------------------------------------------------------------
 constexpr int kMaxGroups = kMaxRouted + kMaxShared;
 constexpr int kXcds = 8;
 constexpr int kStreamRows = 64;
+namespace tile {
+constexpr int BN = 256;                // features of a tile
+}
 
 struct MxArgs {
   const uint8_t *x, *xs;         // rows of codes, rows of scale bytes
@@ -177,6 +186,41 @@ __device__ __forceinline__ int64_t source_row(const MxArgs &a, int64_t r) {
 
 __device__ __forceinline__ i32x8_t codes32(u32x4_t v) {
   return i32x8_t{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
+}
+
+// 256-row tiles of a group and the height of the tile that takes what is left:
+// 0, 64 or 128 (a remainder above 128 rows is a full tile).
+__device__ __forceinline__ int mx_full_tiles(int rows, int *tail) {
+  const int r = rows % 256;
+  *tail = r == 0 || r > 128 ? 0 : r <= 64 ? 64 : 128;
+  return rows / 256 + (r > 128 ? 1 : 0);
+}
+
+// The least number of rows that a group of the tile kernel has, the same answer
+// in both kernels: 1 if the tiles of all groups fill the chip, tiles of more than
+// 16 rows counting twice, else kStreamRows + 1.  Timed at 7168 -> 2048 with 1, 16,
+// 17 and 64 rows a group, straight from memory and in tiles: 64 tiles 15, 22, 24,
+// 36 us and 34, 35, 35, 39; 128 tiles 27, 36, 39, 60 and 36, 37, 38, 41; 512 tiles
+// 88, 119, 125, 219 and 80, 83, 83, 91.  Also copies the groups' row counts into
+// LDS.  Every thread of the workgroup calls it.
+constexpr int kFill = 192;
+__device__ __forceinline__ int mx_tile_rows(const MxArgs &a, int tiles_wide, int threads, int *s_rows,
+                                            int *s_sum) {
+  if (threadIdx.x == 0) *s_sum = 0;
+  __syncthreads();
+  int sum = 0;
+  for (int g = threadIdx.x; g < a.groups; g += threads) {
+    const int rows = a.offsets[g + 1] - a.offsets[g];
+    int tail;
+    const int n = mx_full_tiles(rows, &tail) + (tail ? 1 : 0);
+    sum += rows <= 16 ? n : 2 * n;
+    s_rows[g] = rows;
+  }
+#pragma unroll
+  for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off);
+  if ((threadIdx.x & 63) == 0) atomicAdd(s_sum, sum);
+  __syncthreads();
+  return uniform(*s_sum) >= (kFill + tiles_wide - 1) / tiles_wide ? 1 : kStreamRows + 1;
 }
 
 // ---- few rows ----
@@ -428,13 +472,15 @@ template <bool SILU>
 __global__ __launch_bounds__(stream::NT, 2) void mx_stream_kernel(MxArgs a) {
   using namespace stream;
   __shared__ int64_t s_pref[kMaxGroups + 1];
+  __shared__ int s_rows[kMaxGroups], s_sum;
   const int tid = threadIdx.x, lane = tid & 63;
   const int per = (a.n_out + UN - 1) / UN;
+  if (mx_tile_rows(a, (a.n_out + tile::BN - 1) / tile::BN, NT, s_rows, &s_sum) == 1) return;
   if (tid < 64) {
     int64_t base = 0;
     for (int g0 = 0; g0 < a.groups; g0 += 64) {
       const int g = g0 + lane;
-      const int c = g < a.groups ? mx_unit_cost(a.offsets[g + 1] - a.offsets[g]) : 0;
+      const int c = g < a.groups ? mx_unit_cost(s_rows[g]) : 0;
       int incl = c;
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) {
@@ -474,17 +520,28 @@ __global__ __launch_bounds__(stream::NT, 2) void mx_stream_kernel(MxArgs a) {
 }
 
 // ---- many rows ----
-// Tiles of BM rows x 256 features, four waves of BM/2 x 128 (TM x 4 blocks of
-// 32 x 32).  A step of 256 elements is 128 bytes per row; two LDS buffers hold
-// the steps' codes, filled two steps ahead by global-to-LDS copies that are
-// spread among the matrix instructions, and every step's fragments sit in
-// registers before its first instruction.  The scale bytes come in pairs of
-// steps (16 bytes per row), in two LDS buffers of their own.
+// Tiles of BM rows x 256 features, eight waves of BM/2 x 64 (TM x 2 blocks of
+// 32 x 32), two on every SIMD so that one's LDS reads and epilogue arithmetic run
+// beside the other's matrix instructions (four waves of BM/2 x 128 read a third
+// less LDS and took 115, 620 and 362 us where these take 101, 571 and 334).  A
+// step of 256 elements is 128 bytes per row; two LDS buffers hold the steps'
+// codes.  Half a step's fragments are read while the other half is multiplied,
+// and once every wave holds the second half the copies of the step after next
+// take the buffer, spread among that half's matrix instructions.  The scale bytes
+// come in pairs of steps (16 bytes per row), in two LDS buffers of their own.
+//
+// What bounds it: with every tile's first copies and its stores between two tiles'
+// steps, memory and matrix units wait for each other at the ends of a tile (the
+// last of the cases above without the epilogue: 25 % less).  Copies of the next
+// tile's first step under the epilogue, tried with both kinds of staging, cost
+// more registers than they gave time (the 64 groups above: 133 and 146 us against 115), and
+// two workgroups a CU with 128 x 256 tiles read half a line at a time (101, 681 and
+// 414 us).
 //
 // 16-byte chunk c of tile row r lies at position c ^ ((r / 2) % 8) of its
 // 128-byte row, so that the 16 rows read together cover all banks once.
 namespace tile {
-constexpr int NT = 512, BN = 256, NS = 2, TN = 2, BUF = 2 * 512 * 128, SBUF = 512 * 16;
+constexpr int NT = 512, NS = 2, TN = 2, BUF = 2 * 512 * 128, SBUF = 512 * 16;
 
 __device__ __forceinline__ int swz(int r, int c) { return c ^ ((r >> 1) & 7); }
 
@@ -779,15 +836,6 @@ struct Tile {
 };
 }  // namespace tile
 
-// Full tiles of a group and the height of the tile that takes what is left:
-// 0, 64 or 128 (a remainder above 128 rows is a full tile).
-__device__ __forceinline__ int mx_full_tiles(int rows, int *tail) {
-  const int r = rows % 256;
-  *tail = rows <= kStreamRows || r == 0 || r > 128 ? 0 : r <= 64 ? 64 : 128;
-  if (rows <= kStreamRows) return 0;
-  return rows / 256 + (r > 128 ? 1 : 0);
-}
-
 // Persistent workgroups, one per CU.  The full tiles, in bands of four row
 // tiles, then the 128- and the 64-row tiles are each split into eight
 // contiguous shares, one per XCD (workgroups are dealt to the XCDs round-robin
@@ -799,15 +847,16 @@ __global__ __launch_bounds__(tile::NT, 2) void mx_tile_kernel(MxArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t s_sc[2 * SBUF];
   __shared__ int s_pref[kMaxGroups + 1];
   __shared__ int16_t s_t128[kMaxGroups], s_t64[kMaxGroups];
-  __shared__ int s_cnt[2];
-  const int tid = threadIdx.x;
+  __shared__ int s_cnt[2], s_sum;
+  const int tid = threadIdx.x, nt = (a.n_out + BN - 1) / BN;
+  const int least = mx_tile_rows(a, nt, NT, s_pref, &s_sum);
   if (tid < 64) {
     int full = 0, n128 = 0, n64 = 0;
     const uint64_t below = (1ull << tid) - 1;
     for (int g0 = 0; g0 < a.groups; g0 += 64) {
-      const int g = g0 + tid;
+      const int g = g0 + tid, rows = g < a.groups ? s_pref[g] : 0;
       int t = 0;
-      const int n = g < a.groups ? mx_full_tiles(a.offsets[g + 1] - a.offsets[g], &t) : 0;
+      const int n = rows >= least ? mx_full_tiles(rows, &t) : 0;
       int incl = n;
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) {
@@ -829,7 +878,6 @@ __global__ __launch_bounds__(tile::NT, 2) void mx_tile_kernel(MxArgs a) {
     }
   }
   __syncthreads();
-  const int nt = (a.n_out + BN - 1) / BN;
   const int total[3] = {uniform(s_pref[a.groups]) * nt, uniform(s_cnt[0]) * nt, uniform(s_cnt[1]) * nt};
   const int xcd = blockIdx.x % kXcds, slot = blockIdx.x / kXcds, slots = gridDim.x / kXcds;
   int begin[3], cnt[3];
@@ -884,7 +932,10 @@ hipError_t launch_linear_mxfp4(const MxLinear &p, hipStream_t s) {
   if (p.silu) hipLaunchKernelGGL(mx_stream_kernel<true>, sgrid, dim3(stream::NT), 0, s, a);
   else hipLaunchKernelGGL(mx_stream_kernel<false>, sgrid, dim3(stream::NT), 0, s, a);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.max_rows <= kStreamRows) return e;
+  if (e != hipSuccess) return e;
+  // not if there can neither be a group of more rows nor tiles enough
+  const int64_t wide = (p.n_out + tile::BN - 1) / tile::BN;
+  if (p.max_rows <= kStreamRows && (met + p.max_rows / 17) * wide < kFill) return e;
   const dim3 tgrid(256);
   if (p.silu) hipLaunchKernelGGL(mx_tile_kernel<true>, tgrid, dim3(tile::NT), 0, s, a);
   else hipLaunchKernelGGL(mx_tile_kernel<false>, tgrid, dim3(tile::NT), 0, s, a);

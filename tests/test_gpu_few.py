@@ -128,8 +128,10 @@ class Few:
         assert np.array_equal(self.counts.cpu().numpy(), ref["counts"]), label
         assert np.abs(self.gate.double().cpu().numpy() - ref["gates"]).max() <= 2e-6, label
         last = 2.0 ** -24 if self.kind == "f32" else 2.0 ** -8
-        tol = last * np.abs(ref["y"]) + ((0 if self.kind == "f32" else 2.0 ** -16) +
-                                         (d + f) * 2.0 ** -24 + 2e-6) * A * (1 + last)
+        # hidden rows: two bf16 parts leave 2^-8 of 2^-8, three E4M3 parts 2^-4 of
+        # 2^-4 of 2^-4 (half a step of four significant bits each)
+        hidden = {"f32": 0, "bf16": 2.0 ** -16, "mxfp4": 2.0 ** -12}[self.kind]
+        tol = last * np.abs(ref["y"]) + (hidden + (d + f) * 2.0 ** -24 + 2e-6) * A * (1 + last)
         diff = np.abs(self.y.double().cpu().numpy() - ref["y"])
         assert np.all(diff <= tol), (label, float(np.max(diff / np.maximum(tol, 1e-300))))
         if np.linalg.norm(ref["y"]):

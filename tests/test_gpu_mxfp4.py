@@ -160,6 +160,12 @@ LINEAR = [
     ([2] * 40 + [0] * 20 + [1] * 4, 512, 7168, True, True, False),
     ([0] * 5, 64, 128, False, False, False),
     ([0] * 1000 + [3] + [0] * 87, 16, 128, False, True, True),
+    # small groups with tiles enough for all CUs, and the same with a third of them
+    ([1, 2, 0, 7, 16, 17, 33, 64, 65, 8] * 12, 520, 384, True, True, True),
+    ([1, 2, 0, 7, 16, 17, 33, 64, 65, 8] * 12, 248, 384, True, True, True),
+    ([1] * 1088, 264, 128, False, False, False),
+    ([0, 48] * 96, 256, 640, False, False, True),
+    ([0, 16] * 96, 256, 640, True, False, False),
 ]
 
 
