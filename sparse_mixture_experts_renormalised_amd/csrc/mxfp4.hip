@@ -533,10 +533,10 @@ __global__ __launch_bounds__(stream::NT, 2) void mx_stream_kernel(MxArgs a) {
 // What bounds it: with every tile's first copies and its stores between two tiles'
 // steps, memory and matrix units wait for each other at the ends of a tile (the
 // last of the cases above without the epilogue: 25 % less).  Copies of the next
-// tile's first step under the epilogue, tried with both kinds of staging, cost
-// more registers than they gave time (the 64 groups above: 133 and 146 us against 115), and
-// two workgroups a CU with 128 x 256 tiles read half a line at a time (101, 681 and
-// 414 us).
+// tile's first step under the epilogue took longer all the same, as the second
+// step's then wait for the stores (111, 603 and 377 us), and so did two
+// workgroups a CU with 128 x 256 tiles, which read half a line at a time (101, 681
+// and 414 us).
 //
 // 16-byte chunk c of tile row r lies at position c ^ ((r / 2) % 8) of its
 // 128-byte row, so that the 16 rows read together cover all banks once.
