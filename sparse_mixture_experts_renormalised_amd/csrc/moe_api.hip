@@ -439,8 +439,7 @@ int moe_quantize_mxfp4(int32_t dtype, int64_t rows, int32_t d, const void *x, in
   if (!all_aligned16({x, codes, scales, widened})) return MOE_ERR_INVALID_ARG;
   const int64_t lanes = dtype == MOE_BF16 ? 8 : 4;    // elements of a 16-byte load
   if (rows > 1 && (x_stride < d || x_stride % lanes != 0)) return MOE_ERR_INVALID_ARG;
-  // one lane takes 8 elements, 256 lanes a workgroup, at most 2^31 - 1 workgroups
-  if (rows > (int64_t(1) << 39) / (d / 8)) return MOE_ERR_UNSUPPORTED;
+  if (rows >= (int64_t(1) << 42) / d) return MOE_ERR_UNSUPPORTED;
   return hip_status(moe::launch_quantize_mxfp4(dtype == MOE_BF16, x, rows, d, x_stride, codes,
                                                scales, widened, static_cast<hipStream_t>(stream)));
 }

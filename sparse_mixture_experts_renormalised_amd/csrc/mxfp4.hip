@@ -125,22 +125,33 @@ __global__ __launch_bounds__(256) void quantize_mxfp4_kernel(
   }
 }
 
+// A launch has fewer than 2^32 lanes: at most kLaunchUnits each, whole rows.
+constexpr int64_t kLaunchUnits = int64_t(1) << 30;
+
 template <typename T>
 hipError_t quantize(const void *x, int64_t rows, int d, int64_t stride, uint8_t *codes,
                     uint8_t *scales, void *wide, hipStream_t s) {
-  const int64_t units = rows * (d / 8);
   const uint32_t upr = static_cast<uint32_t>(d / 8);
   const uint64_t magic = upr > 1 ? ~uint64_t(0) / upr + 1 : 0;
-  const dim3 grid(static_cast<unsigned>((units + 255) / 256));
   const bool strided = stride != d && rows > 1;
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, static_cast<const T *>(x), units, upr, magic,
-                       stride, reinterpret_cast<uint32_t *>(codes), scales, static_cast<T *>(wide));
-    return hipGetLastError();
-  };
-  if (strided)
-    return wide ? go(quantize_mxfp4_kernel<T, true, true>) : go(quantize_mxfp4_kernel<T, true, false>);
-  return wide ? go(quantize_mxfp4_kernel<T, false, true>) : go(quantize_mxfp4_kernel<T, false, false>);
+  const int64_t most = kLaunchUnits / upr;               // 4 or more: d < 2^31
+  for (int64_t r = 0; r < rows; r += most) {
+    const int64_t units = (rows - r < most ? rows - r : most) * upr;
+    const dim3 grid(static_cast<unsigned>((units + 255) / 256));
+    auto go = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s,
+                         static_cast<const T *>(x) + r * (strided ? stride : d), units, upr, magic, stride,
+                         reinterpret_cast<uint32_t *>(codes) + r * upr, scales + r * (upr / 4),
+                         wide ? static_cast<T *>(wide) + r * d : nullptr);
+      return hipGetLastError();
+    };
+    const hipError_t e =
+        strided ? (wide ? go(quantize_mxfp4_kernel<T, true, true>) : go(quantize_mxfp4_kernel<T, true, false>))
+                : (wide ? go(quantize_mxfp4_kernel<T, false, true>)
+                        : go(quantize_mxfp4_kernel<T, false, false>));
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 // ---------------------------------------------------------------------------

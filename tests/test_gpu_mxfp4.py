@@ -97,6 +97,21 @@ def test_quantize_extreme_and_non_finite_blocks(B):
     check_quantized(x, *quantize(B, x))
 
 
+def test_quantize_more_elements_than_a_launch_takes(B):
+    g = torch.Generator(device="cuda").manual_seed(8)
+    block = torch.randn(4096, 2048, device="cuda", generator=g).bfloat16()
+    n = 1025                                                    # 2^33 elements and a block more
+    print("[mxfp4] quantize 8.6e9 elements", flush=True)
+    x = block.repeat(n, 1)
+    codes = torch.zeros(n * 4096, 1024, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(n * 4096, 64, dtype=torch.uint8, device="cuda")
+    B.quantize_mxfp4(x, codes, scales)
+    torch.cuda.synchronize()
+    c, s, _ = quantize(B, block, wide=False)
+    for i in range(n):
+        assert torch.equal(codes[i * 4096:(i + 1) * 4096], c) and torch.equal(scales[i * 4096:(i + 1) * 4096], s), i
+
+
 def mx_random(rng, rows, k, lo=-3, hi=3):
     codes = rng.integers(0, 16, (rows, k)).astype(np.uint8)
     scales = (127 + rng.integers(lo, hi, (rows, k // 32))).astype(np.uint8)
@@ -269,3 +284,51 @@ def test_quantize_then_two_linears_is_the_expert_ffn(B):
         full = (z * torch.sigmoid(z)) @ w2[e].double().t()
         cos = torch.nn.functional.cosine_similarity(full.flatten(), y[a:b].double().flatten(), dim=0)
         assert cos > 0.9
+
+
+@pytest.fixture(scope="module")
+def long_codes():
+    """2^20 - 1 rows of 8192 elements: just below the 4 GiB that the calls take."""
+    g = torch.Generator(device="cuda").manual_seed(21)
+    rows = (1 << 20) - 1
+    codes = torch.randint(0, 256, (rows, 4096), dtype=torch.uint8, device="cuda", generator=g)
+    scales = torch.randint(118, 124, (rows, 256), dtype=torch.uint8, device="cuda", generator=g)
+    return codes, scales
+
+
+def linear_reference(xc, xs, wc, ws):
+    X = oracle.dequantize_mxfp4(oracle.unpack_mxfp4(xc.cpu().numpy()), xs.cpu().numpy())
+    W = oracle.dequantize_mxfp4(oracle.unpack_mxfp4(wc.cpu().numpy()), ws.cpu().numpy())
+    return X @ W.T, np.abs(X) @ np.abs(W).T
+
+
+@pytest.mark.parametrize("rows", [5, 70])
+def test_linear_rows_far_into_the_tokens(B, long_codes, rows):
+    print(f"[mxfp4] {rows} rows out of 4 GiB", flush=True)
+    codes, scales = long_codes
+    idx = torch.linspace(0, codes.shape[0] - 1, rows, device="cuda", dtype=torch.float64).round().int()
+    w, ws = codes[-4000:-3936].clone(), scales[-4000:-3936].clone()
+    y = torch.zeros(rows, 64, dtype=torch.bfloat16, device="cuda")
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    B.grouped_linear_mxfp4(codes, scales, off, w[None], ws[None], y, row_index=idx)
+    torch.cuda.synchronize()
+    ref, mag = linear_reference(codes[idx.long()], scales[idx.long()], w, ws)
+    err = 8193 * 2.0 ** -24 * mag
+    assert np.all(np.abs(y.double().cpu().numpy() - ref) <= err * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(ref))
+
+
+@pytest.mark.parametrize("rows", [3, 70])
+def test_linear_features_far_into_a_matrix(B, long_codes, rows):
+    print(f"[mxfp4] {rows} rows on a matrix of 4 GiB", flush=True)
+    codes, scales = long_codes
+    n_out = codes.shape[0] // 8 * 8
+    x, xs = codes[-rows:].clone(), scales[-rows:].clone()
+    y = torch.zeros(rows, n_out, dtype=torch.bfloat16, device="cuda")
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    B.grouped_linear_mxfp4(x, xs, off, codes[None, :n_out], scales[None, :n_out], y)
+    torch.cuda.synchronize()
+    for a in (0, (1 << 19) - 32, n_out - 64):
+        ref, mag = linear_reference(x, xs, codes[a:a + 64], scales[a:a + 64])
+        err = 8193 * 2.0 ** -24 * mag
+        got = y[:, a:a + 64].double().cpu().numpy()
+        assert np.all(np.abs(got - ref) <= err * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(ref)), a
