@@ -162,17 +162,18 @@ hipError_t quantize(const void *x, int64_t rows, int d, int64_t stride, uint8_t 
 // scale bytes and adds in float32, so nothing is widened.  Weights are the
 // first operand, so a lane ends up with four consecutive features of a row.
 //
-// Two kernels:
+// Two ways, in one kernel where only the device can choose (a kernel each would
+// cost every call a launch, 3 us or more):
 //   * tiles of 256 x 256 (128 x 256 and 64 x 256 for a group's last rows),
 //     operands through LDS, one workgroup a CU: every group, where there are
 //     tiles for most of the CUs, and else the groups of more than kStreamRows
 //     rows;
 //   * else the groups of up to kStreamRows rows: units of 16 features, operands
 //     straight from memory to registers, which a few groups have enough of.
-// Measured on MI355X: 256 groups, 207 rows in about 110 of them, 7168 -> 2048:
-// 118 us, 5.6 TB/s (134 us straight from memory); 64 groups, 32768 rows, 2048 ->
-// 1408 with SiLU: 102 us; 256 groups, 32768 rows, 2048 -> 7168: 572 us, 4.4 TB/s;
-// 8 groups, 8192 rows, 4096 -> 14336 with bias and SiLU: 334 us, 2.9 PFLOP/s.
+// Measured on MI355X: 256 groups, 207 rows in about 84 of them, 7168 -> 2048:
+// 116 us, 5.7 TB/s (134 us straight from memory); 64 groups, 32768 rows, 2048 ->
+// 1408 with SiLU: 97 us; 256 groups, 32768 rows, 2048 -> 7168: 568 us, 4.4 TB/s;
+// 8 groups, 8192 rows, 4096 -> 14336 with bias and SiLU: 335 us, 2.9 PFLOP/s.
 // ---------------------------------------------------------------------------
 constexpr int kMaxGroups = kMaxRouted + kMaxShared;
 constexpr int kXcds = 8;
@@ -207,31 +208,45 @@ __device__ __forceinline__ int mx_full_tiles(int rows, int *tail) {
   return rows / 256 + (r > 128 ? 1 : 0);
 }
 
-// The least number of rows that a group of the tile kernel has, the same answer
-// in both kernels: 1 if the tiles of all groups fill the chip, tiles of more than
-// 16 rows counting twice, else kStreamRows + 1.  Timed at 7168 -> 2048 with 1, 16,
-// 17 and 64 rows a group, straight from memory and in tiles: 64 tiles 15, 22, 24,
-// 36 us and 34, 35, 35, 39; 128 tiles 27, 36, 39, 60 and 36, 37, 38, 41; 512 tiles
-// 88, 119, 125, 219 and 80, 83, 83, 91.  Also copies the groups' row counts into
-// LDS.  Every thread of the workgroup calls it.
+// The least number of rows that a group taken in tiles has: 1 if the tiles of all
+// groups fill the chip, tiles of more than 16 rows counting twice, else
+// kStreamRows + 1.  Timed at 7168 -> 2048 with 1, 16, 17 and 64 rows a group,
+// straight from memory and in tiles: 64 tiles 15, 22, 24, 36 us and 34, 35, 35, 39;
+// 128 tiles 27, 36, 39, 60 and 36, 37, 38, 41; 512 tiles 88, 119, 125, 219 and 80,
+// 83, 83, 91.
 constexpr int kFill = 192;
-__device__ __forceinline__ int mx_tile_rows(const MxArgs &a, int tiles_wide, int threads, int *s_rows,
-                                            int *s_sum) {
-  if (threadIdx.x == 0) *s_sum = 0;
+struct Plan {
+  int least;                           // of the groups taken in tiles
+  bool tiles, units;                   // is there any work of either kind
+};
+// Also copies the groups' row counts into LDS.  Every thread calls it.
+__device__ __forceinline__ Plan mx_plan(const MxArgs &a, int tiles_wide, int threads, int *s_rows,
+                                        int (&s_plan)[3]) {
+  if (threadIdx.x < 3) s_plan[threadIdx.x] = 0;
   __syncthreads();
   int sum = 0;
+  bool big = false, small = false;
   for (int g = threadIdx.x; g < a.groups; g += threads) {
     const int rows = a.offsets[g + 1] - a.offsets[g];
     int tail;
     const int n = mx_full_tiles(rows, &tail) + (tail ? 1 : 0);
     sum += rows <= 16 ? n : 2 * n;
+    big |= rows > kStreamRows;
+    small |= rows > 0 && rows <= kStreamRows;
     s_rows[g] = rows;
   }
 #pragma unroll
   for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off);
-  if ((threadIdx.x & 63) == 0) atomicAdd(s_sum, sum);
+  big = __ballot(big) != 0;
+  small = __ballot(small) != 0;
+  if ((threadIdx.x & 63) == 0) {
+    atomicAdd(&s_plan[0], sum);
+    if (big) s_plan[1] = 1;
+    if (small) s_plan[2] = 1;
+  }
   __syncthreads();
-  return uniform(*s_sum) >= (kFill + tiles_wide - 1) / tiles_wide ? 1 : kStreamRows + 1;
+  const bool all = uniform(s_plan[0]) >= (kFill + tiles_wide - 1) / tiles_wide;
+  return Plan{all ? 1 : kStreamRows + 1, all || uniform(s_plan[1]), !all && uniform(s_plan[2])};
 }
 
 // ---- few rows ----
@@ -250,7 +265,7 @@ __device__ __forceinline__ int mx_tile_rows(const MxArgs &a, int tiles_wide, int
 //   * up to 64: the loads r and lanes b are transposed, which gives sixteen
 //     whole rows for four instructions, W's and X's alike.
 namespace stream {
-constexpr int WAVES = 4, NT = WAVES * 64, R = 4, UN = 4 * R;
+constexpr int R = 4, UN = 4 * R;
 
 // Operands that MODE columns take: MODE 1, 2, 4 fours of rows (diagonal), or 8
 // and 16: two and four tiles of 16 (transposed).
@@ -477,16 +492,13 @@ __device__ __forceinline__ int mx_unit_cost(int rows) {
   return rows <= 0 || rows > kStreamRows ? 0 : rows <= 8 ? 4 : rows <= 16 ? 5 : rows <= 32 ? 7 : 10;
 }
 
-// Every wave takes a range of equal cost of all groups' units: those whose first
-// quarter lies in it.
+// Every wave takes a range of equal cost of the units of all groups of up to
+// kStreamRows rows: those whose first quarter lies in it.
 template <bool SILU>
-__global__ __launch_bounds__(stream::NT, 2) void mx_stream_kernel(MxArgs a) {
+__device__ __forceinline__ void mx_units(const MxArgs &a, const int *s_rows, int64_t *s_pref) {
   using namespace stream;
-  __shared__ int64_t s_pref[kMaxGroups + 1];
-  __shared__ int s_rows[kMaxGroups], s_sum;
   const int tid = threadIdx.x, lane = tid & 63;
   const int per = (a.n_out + UN - 1) / UN;
-  if (mx_tile_rows(a, (a.n_out + tile::BN - 1) / tile::BN, NT, s_rows, &s_sum) == 1) return;
   if (tid < 64) {
     int64_t base = 0;
     for (int g0 = 0; g0 < a.groups; g0 += 64) {
@@ -505,7 +517,7 @@ __global__ __launch_bounds__(stream::NT, 2) void mx_stream_kernel(MxArgs a) {
   }
   __syncthreads();
   const int64_t total = s_pref[a.groups];
-  const int v = blockIdx.x * WAVES + uniform(tid >> 6), waves = gridDim.x * WAVES;
+  const int mine = blockDim.x / 64, v = blockIdx.x * mine + uniform(tid >> 6), waves = gridDim.x * mine;
   const int64_t lo = total * v / waves, hi = total * (v + 1) / waves;
   if (lo >= hi) return;
   int g = 0, up = a.groups;                // s_pref[g] <= lo < s_pref[up]
@@ -530,11 +542,25 @@ __global__ __launch_bounds__(stream::NT, 2) void mx_stream_kernel(MxArgs a) {
   }
 }
 
+// Where the host knows that there are units alone, in smaller workgroups: a few
+// units then lie on more CUs, and the loads of the chunks ahead keep all registers
+// (8 groups, 7168 -> 2048, 1 and 8 rows each: 15 and 17 us, and 21 and 23 in the
+// kernel below; one group of 64 rows 30 and 52).
+constexpr int kUnitWaves = 4;
+template <bool SILU>
+__global__ __launch_bounds__(kUnitWaves * 64, 2) void mx_units_kernel(MxArgs a) {
+  __shared__ int64_t s_pref[kMaxGroups + 1];
+  __shared__ int s_rows[kMaxGroups];
+  for (int g = threadIdx.x; g < a.groups; g += kUnitWaves * 64) s_rows[g] = a.offsets[g + 1] - a.offsets[g];
+  __syncthreads();
+  mx_units<SILU>(a, s_rows, s_pref);
+}
+
 // ---- many rows ----
 // Tiles of BM rows x 256 features, eight waves of BM/2 x 64 (TM x 2 blocks of
 // 32 x 32), two on every SIMD so that one's LDS reads and epilogue arithmetic run
 // beside the other's matrix instructions (four waves of BM/2 x 128 read a third
-// less LDS and took 115, 620 and 362 us where these take 101, 571 and 334).  A
+// less LDS and took 115, 620 and 362 us where these took 101, 571 and 334).  A
 // step of 256 elements is 128 bytes per row; two LDS buffers hold the steps'
 // codes.  Half a step's fragments are read while the other half is multiplied,
 // and once every wave holds the second half the copies of the step after next
@@ -847,20 +873,28 @@ struct Tile {
 };
 }  // namespace tile
 
-// Persistent workgroups, one per CU.  The full tiles, in bands of four row
-// tiles, then the 128- and the 64-row tiles are each split into eight
-// contiguous shares, one per XCD (workgroups are dealt to the XCDs round-robin
-// by number), so that tiles running together on an XCD share operands in its L2.
+// Persistent workgroups, one per CU, first on the units, then on the tiles.  The
+// full tiles, in bands of four row tiles, then the 128- and the 64-row tiles are
+// each split into eight contiguous shares, one per XCD (workgroups are dealt to
+// the XCDs round-robin by number), so that tiles running together on an XCD share
+// operands in its L2.
 template <bool SILU>
-__global__ __launch_bounds__(tile::NT, 2) void mx_tile_kernel(MxArgs a) {
+__global__ __launch_bounds__(tile::NT, 2) void mx_linear_kernel(MxArgs a) {
   using namespace tile;
   __shared__ __attribute__((aligned(16))) uint8_t s_buf[BUF];
   __shared__ __attribute__((aligned(16))) uint8_t s_sc[2 * SBUF];
   __shared__ int s_pref[kMaxGroups + 1];
   __shared__ int16_t s_t128[kMaxGroups], s_t64[kMaxGroups];
-  __shared__ int s_cnt[2], s_sum;
+  __shared__ int s_cnt[2], s_plan[3];
   const int tid = threadIdx.x, nt = (a.n_out + BN - 1) / BN;
-  const int least = mx_tile_rows(a, nt, NT, s_pref, &s_sum);
+  const Plan plan = mx_plan(a, nt, NT, s_pref, s_plan);
+  if (plan.units) {
+    static_assert(sizeof(int64_t) * (kMaxGroups + 1) <= sizeof(s_buf), "");
+    mx_units<SILU>(a, s_pref, reinterpret_cast<int64_t *>(s_buf));
+  }
+  if (!plan.tiles) return;
+  __syncthreads();                       // s_buf and the row counts have been used
+  const int least = plan.least;
   if (tid < 64) {
     int full = 0, n128 = 0, n64 = 0;
     const uint64_t below = (1ull << tid) - 1;
@@ -934,22 +968,20 @@ hipError_t launch_quantize_mxfp4(bool bf16, const void *x, int64_t rows, int d, 
 hipError_t launch_linear_mxfp4(const MxLinear &p, hipStream_t s) {
   MxArgs a{p.x, p.xs, p.index, p.offsets, p.w, p.ws, static_cast<const uint16_t *>(p.bias),
            static_cast<uint16_t *>(p.y), p.groups, p.n_out, p.k};
-  // the groups' row counts are on the device: both kernels look, each takes
-  // the groups of its size
+  // The groups' row counts are on the device; but there may neither be a group of
+  // more than kStreamRows rows nor tiles enough.
   const int64_t met = p.max_rows < p.groups ? p.max_rows : p.groups;
-  const int64_t units = met * ((p.n_out + stream::UN - 1) / stream::UN);
-  const int64_t blocks = (units + stream::WAVES - 1) / stream::WAVES;
-  const dim3 sgrid(static_cast<unsigned>(blocks < 512 ? blocks : 512));
-  if (p.silu) hipLaunchKernelGGL(mx_stream_kernel<true>, sgrid, dim3(stream::NT), 0, s, a);
-  else hipLaunchKernelGGL(mx_stream_kernel<false>, sgrid, dim3(stream::NT), 0, s, a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  // not if there can neither be a group of more rows nor tiles enough
   const int64_t wide = (p.n_out + tile::BN - 1) / tile::BN;
-  if (p.max_rows <= kStreamRows && (met + p.max_rows / 17) * wide < kFill) return e;
-  const dim3 tgrid(256);
-  if (p.silu) hipLaunchKernelGGL(mx_tile_kernel<true>, tgrid, dim3(tile::NT), 0, s, a);
-  else hipLaunchKernelGGL(mx_tile_kernel<false>, tgrid, dim3(tile::NT), 0, s, a);
+  if (p.max_rows <= kStreamRows && (met + p.max_rows / 17) * wide < kFill) {
+    const int64_t units = met * ((p.n_out + stream::UN - 1) / stream::UN);
+    const int64_t blocks = (units + kUnitWaves - 1) / kUnitWaves;
+    const dim3 grid(static_cast<unsigned>(blocks < 512 ? blocks : 512)), block(kUnitWaves * 64);
+    if (p.silu) hipLaunchKernelGGL(mx_units_kernel<true>, grid, block, 0, s, a);
+    else hipLaunchKernelGGL(mx_units_kernel<false>, grid, block, 0, s, a);
+    return hipGetLastError();
+  }
+  if (p.silu) hipLaunchKernelGGL(mx_linear_kernel<true>, dim3(256), dim3(tile::NT), 0, s, a);
+  else hipLaunchKernelGGL(mx_linear_kernel<false>, dim3(256), dim3(tile::NT), 0, s, a);
   return hipGetLastError();
 }
 
