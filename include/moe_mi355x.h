@@ -426,7 +426,9 @@ size_t moe_grouped_linear_mxfp4_workspace_size(int32_t n_groups, int32_t n_out, 
  *   - ws holds moe_few_workspace_size(cfg) bytes, all scratch.  Nothing in it
  *     needs to be initialised.  Calls that overlap in time (other streams,
  *     parallel branches of a graph) need a workspace of their own each.
- * Results do not depend on timing.
+ * Results do not depend on timing.  A weight or token element that is not finite
+ * reaches the tokens it enters and no others (their outputs may be NaN where a sum
+ * would be infinite; calls with such outputs take longer).
  */
 #define MOE_FEW_TOKENS 16
 int moe_layer_forward_few(const moe_config *cfg, const moe_weights *w, const void *x, void *y,

@@ -989,6 +989,46 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
     };
     f32x4_t z = {0, 0, 0, 0};
     const uint8_t *hb = static_cast<const uint8_t *>(a.h);
+    // The zeros of tokens without a hidden row do not hide an infinity or a NaN
+    // among the weights.  A sum that is not finite is therefore added up again, by
+    // its lane, from the token's own entries.
+    auto own_entries = [&](int orow, int token) {
+      float sum = 0.0f;
+#pragma nounroll
+      for (int c = static_cast<int>(static_cast<int64_t>(total) * s / a.S); c < c1; ++c) {
+        const int i = c / h_chunks, hc = c - i * h_chunks, hr = hidden_row(i, token);
+        if (hr < 0) continue;
+        const int64_t wrow = (i < ne ? static_cast<int64_t>(s_list[i]) : i - ne) * d + orow;
+        const uint8_t *w = static_cast<const uint8_t *>(i < ne ? a.w2 : a.ws2) + wrow * pieces * 16;
+        const uint8_t *cw = W == kWMx ? (i < ne ? a.c2 : a.cs2) + wrow * pieces : nullptr;
+        const int64_t hat = static_cast<int64_t>(hr) * h_chunks + hc;
+        const uint8_t *hv = hb + hat * KD::CB;
+        const int k0 = hc * KD::CH, n = min(KD::CH, f - k0);
+#pragma nounroll
+        for (int k = 0; k < n; ++k) {
+          float x, y;
+          if constexpr (W == kWF32) {
+            x = reinterpret_cast<const float *>(hv)[k];
+            y = reinterpret_cast<const float *>(w)[k0 + k];
+          } else if constexpr (W == kWBf16) {
+            x = bf16_to_f32(reinterpret_cast<const uint16_t *>(hv)[k]) +
+                bf16_to_f32(reinterpret_cast<const uint16_t *>(hv + h_part)[k]);
+            y = bf16_to_f32(reinterpret_cast<const uint16_t *>(w)[k0 + k]);
+          } else {
+            const int hs = a.hs[hat * 16 + k / 32], ws = cw[(k0 + k) / 32];
+            x = 0.0f;
+            for (int p = 0; p < KD::PDN; ++p)
+              x += __builtin_ldexpf(__builtin_amdgcn_cvt_f32_fp8(hv[p * h_part + part_byte(k)], 0),
+                                    hs - 127 - 4 * p);
+            const uint32_t code = w[(k0 + k) / 2] >> (k & 1 ? 4 : 0);
+            y = __builtin_ldexpf(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code & 15, 1.0f, 0)[0], ws - 127);
+            if (hs == 255 || ws == 255) y = __uint_as_float(0x7FC00000u);
+          }
+          sum = fmaf(x, y, sum);
+        }
+      }
+      return sum;
+    };
     if constexpr (SHARE) {
       uint32_t rows[2], brow = 0;
       auto enter_b = [&](int i) {
@@ -1039,6 +1079,10 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) v[t] += s_red[w][min(wave, TB - 1)][lane];
     }
+#pragma unroll
+    for (int t = 0; t < OUT; ++t)
+      if (T > 1 && out && (__float_as_uint(v[t]) & 0x7F800000u) == 0x7F800000u)
+        v[t] = own_entries(row_of(t), token);
     bool finish = true;
     if (a.S > 1) {
       const int64_t size = static_cast<int64_t>(T) * d;

@@ -121,17 +121,20 @@ class Few:
                     A[t] += reach(t, ex("", int(ref["topk_idx"][t, k])), ref["gates"][t, k])
         return ref, A
 
-    def check(self, label=""):
+    def bound(self, ref, A):
         T, d, N, K, Ks, f = self.shape
-        ref, A = self.reference()
-        assert np.array_equal(self.idx.cpu().numpy(), ref["topk_idx"]), label
-        assert np.array_equal(self.counts.cpu().numpy(), ref["counts"]), label
-        assert np.abs(self.gate.double().cpu().numpy() - ref["gates"]).max() <= 2e-6, label
         last = 2.0 ** -24 if self.kind == "f32" else 2.0 ** -8
         # hidden rows: two bf16 parts leave 2^-8 of 2^-8, three E4M3 parts 2^-4 of
         # 2^-4 of 2^-4 (half a step of four significant bits each)
         hidden = {"f32": 0, "bf16": 2.0 ** -16, "mxfp4": 2.0 ** -12}[self.kind]
-        tol = last * np.abs(ref["y"]) + (hidden + (d + f) * 2.0 ** -24 + 2e-6) * A * (1 + last)
+        return last * np.abs(ref["y"]) + (hidden + (d + f) * 2.0 ** -24 + 2e-6) * A * (1 + last)
+
+    def check(self, label=""):
+        ref, A = self.reference()
+        assert np.array_equal(self.idx.cpu().numpy(), ref["topk_idx"]), label
+        assert np.array_equal(self.counts.cpu().numpy(), ref["counts"]), label
+        assert np.abs(self.gate.double().cpu().numpy() - ref["gates"]).max() <= 2e-6, label
+        tol = self.bound(ref, A)
         diff = np.abs(self.y.double().cpu().numpy() - ref["y"])
         assert np.all(diff <= tol), (label, float(np.max(diff / np.maximum(tol, 1e-300))))
         if np.linalg.norm(ref["y"]):
@@ -332,3 +335,41 @@ def test_repeats_bit_exact(B):
         if i % 50 == 49:
             torch.cuda.synchronize()
             assert all(torch.equal(p, q) for p, q in zip(ref, L.outputs())), i
+
+
+@pytest.mark.parametrize("kind", ["bf16", "mxfp4", "f32"])
+@pytest.mark.parametrize("T", [2, 7, 16])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_non_finite_weights_reach_their_experts_tokens_only(B, kind, T, bad):
+    """One element of W1 of one expert and of W2 of another is not finite: outputs
+    of tokens that neither expert computes are those of finite weights, and the
+    W2 row's output of a token that it computes is not finite."""
+    print(f"[few] non-finite weights {kind} T={T} {bad}", flush=True)
+    L = Few(B, T, 256, 10, 2, 1, 384, kind, seed=40 + T)
+    ref, A = L.reference()
+    tol, idx = L.bound(ref, A), torch.from_numpy(ref["topk_idx"])
+    met = sorted(set(idx.flatten().tolist()))
+    e1, e2 = met[0], met[-1]
+    if kind == "mxfp4":
+        L.w["k1"].view(10, 384, 8)[e1, 77, 3] = 255
+        L.w["k2"].view(10, 256, 12)[e2, 130, 7] = 255
+    else:
+        L.w["w1"][e1, 77, 100] = bad
+        L.w["w2"][e2, 130, 250] = bad
+    first = None
+    for _ in range(2):
+        L.spoil()
+        L()
+        torch.cuda.synchronize()
+        assert np.array_equal(L.idx.cpu().numpy(), ref["topk_idx"])
+        y, on1, on2 = L.y.double().cpu().numpy(), (idx == e1).any(1), (idx == e2).any(1)
+        for t in range(T):
+            if on1[t]:
+                assert not np.isfinite(y[t]).any(), t
+                continue
+            fine = np.ones(y.shape[1], dtype=bool)
+            fine[130] = not on2[t]
+            assert np.all(np.abs(y[t] - ref["y"][t])[fine] <= tol[t][fine]), t
+            assert fine[130] or not np.isfinite(y[t, 130]), t
+        assert first is None or torch.equal(L.y.nan_to_num(), first)
+        first = L.y.nan_to_num()
