@@ -31,7 +31,7 @@ class Few:
     """A layer on the GPU with its outputs and workspace."""
 
     def __init__(self, B, T, d, N, K, Ks, f, kind="bf16", cap=0.0, bias=False, router="none", seed=0,
-                 scale=1.0):
+                 scale=1.0, spread=0):
         self.B, self.kind = B, kind
         self.cfg = B.config(T, d, N, K, Ks, f, "f32" if kind == "f32" else "bf16", cap,
                             selection_only_bias=router == "select")
@@ -42,7 +42,10 @@ class Few:
         self.wr = rn(N, d, std=d ** -0.5)
         self.rb = None if router == "none" else rn(N, std=0.7)
         # tokens whose kept logits are further apart than their rounding
-        x = rn(40 * T + 40, d, std=scale).to(dt)
+        x = rn(40 * T + 40, d, std=scale)
+        if spread:                          # elements of very different size within a block
+            x = x * torch.exp2(-torch.randint(0, spread, x.shape, device="cuda", generator=g).float())
+        x = x.to(dt)
         key = x.double() @ self.wr.double().t() + (0 if self.rb is None else self.rb.double())
         top = key.sort(dim=1, descending=True).values[:, : K + 1]
         far = ((top[:, :-1] - top[:, 1:]) > 1e-5).all(dim=1) if N > 1 else torch.ones(len(x), dtype=torch.bool, device="cuda")
@@ -373,3 +376,47 @@ def test_non_finite_weights_reach_their_experts_tokens_only(B, kind, T, bad):
             assert fine[130] or not np.isfinite(y[t, 130]), t
         assert first is None or torch.equal(L.y.nan_to_num(), first)
         first = L.y.nan_to_num()
+
+
+@pytest.mark.parametrize("T", [1, 6, 16])
+def test_mxfp4_tokens_of_wide_range(B, T):
+    print(f"[few] wide range T={T}", flush=True)
+    L = Few(B, T, 512, 8, 2, 1, 256, "mxfp4", seed=60 + T, spread=24)
+    L()
+    torch.cuda.synchronize()
+    x = L.x.clone()
+    ref, A = L.reference()
+    # a token's element is off by at most 2^-21 of its block's largest: the reach of
+    # tokens whose elements all are that large, which bounds A too
+    L.x = x.view(T, -1, 32).abs().amax(2, keepdim=True).expand(T, 16, 32).reshape(T, 512).contiguous()
+    wide = np.zeros_like(A)
+    h = lambda t: t.double().cpu().numpy()  # noqa: E731
+    m = h(L.x)
+    for t in range(T):
+        pairs = [("", int(e), ref["gates"][t, k]) for k, e in enumerate(ref["topk_idx"][t])] + [("s", 0, 1.0)]
+        for p, e, g in pairs:
+            w1, w2 = np.abs(h(L.w["w" + p + "1"][e])), np.abs(h(L.w["w" + p + "2"][e]))
+            wide[t] += g * (w2 @ (1.1 * (w1 @ m[t])))
+    L.x = x
+    tol = L.bound(ref, A) + 2.0 ** -21 * wide * (1 + 2.0 ** -8)
+    assert np.array_equal(L.idx.cpu().numpy(), ref["topk_idx"])
+    assert np.all(np.abs(L.y.double().cpu().numpy() - ref["y"]) <= tol)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "mxfp4", "f32"])
+def test_non_finite_tokens_keep_to_themselves(B, kind):
+    L = Few(B, 12, 256, 10, 2, 1, 384, kind, seed=70)
+    ref, A = L.reference()
+    tol = L.bound(ref, A)
+    L.x[3, 40], L.x[8, 255] = float("nan"), float("inf")
+    L()
+    torch.cuda.synchronize()
+    y = L.y.double().cpu().numpy()
+    for t in range(12):
+        if t in (3, 8):
+            assert not np.isfinite(y[t]).any(), t
+        else:
+            assert np.array_equal(L.idx[t].cpu().numpy(), ref["topk_idx"][t])
+            assert np.all(np.abs(y[t] - ref["y"][t]) <= tol[t]), t
+    ids = L.idx.cpu()
+    assert ids.min() >= 0 and ids.max() < 10 and all(len(set(r)) == 2 for r in ids.tolist())

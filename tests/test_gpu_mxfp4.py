@@ -332,3 +332,42 @@ def test_linear_features_far_into_a_matrix(B, long_codes, rows):
         err = 8193 * 2.0 ** -24 * mag
         got = y[:, a:a + 64].double().cpu().numpy()
         assert np.all(np.abs(got - ref) <= err * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(ref)), a
+
+
+def test_quantise_and_linear_captured_beside_another_call(B):
+    """Quantise and multiply, captured on one stream and replayed while another
+    stream runs the same product eagerly: neither keeps anything between calls."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    counts, n_out, k = [70, 0, 3, 129, 20], 520, 768
+    rows = sum(counts)
+    off = torch.tensor([0] + list(np.cumsum(counts)), dtype=torch.int32, device="cuda")
+    x = torch.randn(rows, k, device="cuda", generator=g).bfloat16()
+    wc = torch.randint(0, 256, (5, n_out, k // 2), dtype=torch.uint8, device="cuda", generator=g)
+    ws = torch.randint(118, 124, (5, n_out, k // 32), dtype=torch.uint8, device="cuda", generator=g)
+
+    def buffers():
+        return (torch.zeros(rows, k // 2, dtype=torch.uint8, device="cuda"),
+                torch.zeros(rows, k // 32, dtype=torch.uint8, device="cuda"),
+                torch.zeros(rows, n_out, dtype=torch.bfloat16, device="cuda"))
+
+    def both(c, s, y, stream=None):
+        B.quantize_mxfp4(x, c, s, stream=stream)
+        B.grouped_linear_mxfp4(c, s, off, wc, ws, y, silu=True, stream=stream)
+
+    one, two = buffers(), buffers()
+    both(*one)
+    torch.cuda.synchronize()
+    ref = one[2].clone()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both(*one)
+    for _ in range(4):
+        one[2].zero_()
+        two[2].zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        both(*two, stream=side)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(one[2], ref) and torch.equal(two[2], ref)
