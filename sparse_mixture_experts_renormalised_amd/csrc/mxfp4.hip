@@ -172,8 +172,8 @@ hipError_t quantize(const void *x, int64_t rows, int d, int64_t stride, uint8_t 
 //     straight from memory to registers, which a few groups have enough of.
 // Measured on MI355X: 256 groups, 207 rows in about 84 of them, 7168 -> 2048:
 // 116 us, 5.7 TB/s (134 us straight from memory); 64 groups, 32768 rows, 2048 ->
-// 1408 with SiLU: 97 us; 256 groups, 32768 rows, 2048 -> 7168: 568 us, 4.4 TB/s;
-// 8 groups, 8192 rows, 4096 -> 14336 with bias and SiLU: 335 us, 2.9 PFLOP/s.
+// 1408 with SiLU: 98 us; 256 groups, 32768 rows, 2048 -> 7168: 573 us, 4.4 TB/s;
+// 8 groups, 8192 rows, 4096 -> 14336 with bias and SiLU: 331 us, 2.9 PFLOP/s.
 // ---------------------------------------------------------------------------
 constexpr int kMaxGroups = kMaxRouted + kMaxShared;
 constexpr int kXcds = 8;
@@ -655,9 +655,13 @@ struct Tile {
   static __device__ __forceinline__ int step_off(const Src &s, int kb) {
     return kb * 128 + (kb == s.nk - 1 ? s.tadj : 0);
   }
+  // Weights of the smaller tiles, which no other tile reads, go past the caches
+  // (the cases above: decode 127 -> 116 us, many 582 -> 573); those of full tiles
+  // mostly serve several (fine 101 without the caches, 98 with them).
   static __device__ __forceinline__ void copy(const Src &s, int i, int off, uint32_t base, int wave) {
     if (i < AC) dma::dma16s(s.a[i] + off, s.abase, base + (8 * i + wave) * 1024);
-    else dma::dma16s_nt(s.b[i - AC] + off, s.bbase, base + BM * 128 + (8 * (i - AC) + wave) * 1024);
+    else if (BM < 256) dma::dma16s_nt(s.b[i - AC] + off, s.bbase, base + BM * 128 + (8 * (i - AC) + wave) * 1024);
+    else dma::dma16s(s.b[i - AC] + off, s.bbase, base + BM * 128 + (8 * (i - AC) + wave) * 1024);
   }
   // Scale copies: the rows of X (which 0) or W (1) for the steps 2p and 2p + 1.
   static __device__ __forceinline__ int pair_off(const Src &s, int p, int lane) {
