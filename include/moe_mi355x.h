@@ -391,10 +391,9 @@ int moe_quantize_mxfp4(int32_t dtype, int64_t rows, int32_t d, const void *x, in
  *   w_codes [G][n_out][k/2], w_scales [G][n_out][k/32]
  *   bias        [G][n_out] bf16 or NULL;  silu 1: act = SiLU, 0: none
  *   y_rows      [max_rows][n_out] bf16 output
- *   ws          optional device scratch of
- *               moe_grouped_linear_mxfp4_workspace_size bytes (NULL allowed);
- *               a non-NULL ws smaller than that is MOE_ERR_WORKSPACE.  Calls
- *               that overlap in time need a scratch of their own each.
+ *   ws          device scratch of moe_grouped_linear_mxfp4_workspace_size
+ *               bytes.  That is 0 in this version: ws may be NULL, and calls may
+ *               overlap in time.
  * k is a multiple of 128 (one step of the matrix instruction) and n_out of 8
  * (16-byte output rows), n_groups <= 1088, and the codes of all token rows
  * and those of one group's matrix take less than 4 GiB each (32-bit offsets);

@@ -37,10 +37,7 @@ __device__ __forceinline__ void dma16s_nt(uint32_t voff, const void *sbase, uint
   asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt" : : "v"(voff), "s"(sbase), "{m0}"(m0) : "memory");
 }
 
-// 4 bytes per lane (256 B per wave), for the scale bytes of 128 elements.
-__device__ __forceinline__ void dma4(const void *src, uint32_t m0) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" : : "v"(src), "{m0}"(m0) : "memory");
-}
+// 4 bytes per lane (256 B per wave), for scale bytes.
 __device__ __forceinline__ void dma4s(uint32_t voff, const void *sbase, uint32_t m0) {
   asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, %1" : : "v"(voff), "s"(sbase), "{m0}"(m0) : "memory");
 }

@@ -455,8 +455,8 @@ static int check_linear_mxfp4(int32_t n_groups, int32_t n_out, int32_t k, int64_
 
 size_t moe_grouped_linear_mxfp4_workspace_size(int32_t n_groups, int32_t n_out, int32_t k,
                                                int64_t max_rows) {
-  if (check_linear_mxfp4(n_groups, n_out, k, max_rows) != MOE_OK) return 0;
-  return moe::linear_mxfp4_workspace_bytes(n_groups, n_out, k, max_rows);
+  (void)n_groups, (void)n_out, (void)k, (void)max_rows;
+  return 0;
 }
 
 int moe_grouped_linear_mxfp4(int32_t n_groups, int32_t n_out, int32_t k, int64_t x_rows,
@@ -474,8 +474,7 @@ int moe_grouped_linear_mxfp4(int32_t n_groups, int32_t n_out, int32_t k, int64_t
     return MOE_ERR_INVALID_ARG;
   if (!all_aligned16({x_codes, x_scales, row_index, offsets, w_codes, w_scales, bias, y_rows, ws}))
     return MOE_ERR_INVALID_ARG;
-  const size_t need = moe::linear_mxfp4_workspace_bytes(n_groups, n_out, k, max_rows);
-  if (ws && ws_bytes < need) return MOE_ERR_WORKSPACE;
+  (void)ws_bytes;                      // the product needs no scratch
   moe::MxLinear p{};
   p.x = x_codes;
   p.xs = x_scales;
@@ -490,8 +489,6 @@ int moe_grouped_linear_mxfp4(int32_t n_groups, int32_t n_out, int32_t k, int64_t
   p.k = k;
   p.max_rows = max_rows;
   p.silu = silu != 0;
-  p.scratch = need ? ws : nullptr;
-  p.scratch_bytes = p.scratch ? need : 0;
   return hip_status(moe::launch_linear_mxfp4(p, static_cast<hipStream_t>(stream)));
 }
 

@@ -139,10 +139,7 @@ struct MxLinear {
   int groups, n_out, k;
   int64_t max_rows;
   bool silu;
-  void *scratch;
-  size_t scratch_bytes;
 };
-size_t linear_mxfp4_workspace_bytes(int groups, int n_out, int k, int64_t max_rows);
 hipError_t launch_linear_mxfp4(const MxLinear &p, hipStream_t s);
 
 // The whole layer for at most kFewTokens tokens.

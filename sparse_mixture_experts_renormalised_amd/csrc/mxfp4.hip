@@ -996,6 +996,4 @@ hipError_t launch_linear_mxfp4(const MxLinear &p, hipStream_t s) {
   return hipGetLastError();
 }
 
-size_t linear_mxfp4_workspace_bytes(int, int, int, int64_t) { return 0; }
-
 }  // namespace moe
