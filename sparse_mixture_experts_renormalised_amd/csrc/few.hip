@@ -857,8 +857,9 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
                      f32_to_bf16(z[v] - bf16_to_f32(hi)));
         }
       }
+      // lanes without a tile hold another one's values, and not this row's gate
       uint32_t &most = amax[SHARE ? 0 : v];
-      most = max(most, __float_as_uint(z[v]) & 0x7FFFFFFFu);
+      if (tile < m) most = max(most, __float_as_uint(z[v]) & 0x7FFFFFFFu);
     }
     if constexpr (W == kWMx) {
       // largest of each token's values in the wave (lanes q, and b where those are
