@@ -413,8 +413,10 @@ size_t moe_grouped_linear_mxfp4_workspace_size(int32_t n_groups, int32_t n_out, 
  * decode step) in two kernels instead of one per stage.  Arguments, shapes,
  * capacity rule and optional outputs as moe_layer_forward, with these
  * differences:
- *   - T > MOE_FEW_TOKENS, cfg->dispatch == MOE_DISPATCH_FP8 and an expert matrix
- *     of 4 GiB or more in cfg->dtype return MOE_ERR_UNSUPPORTED;
+ *   - T > MOE_FEW_TOKENS, cfg->dispatch == MOE_DISPATCH_FP8, an expert matrix
+ *     of 4 GiB or more in cfg->dtype, and T * (top_k + n_shared) + 1 hidden rows
+ *     of 2^30 elements or more together (d_ff rounded up to 64 for MOE_F32)
+ *     return MOE_ERR_UNSUPPORTED;
  *   - the logits are float32 sums in a fixed tree order, not moe_route's
  *     chain, so two experts whose logits differ by no more than their rounding
  *     may be ordered differently than there; ties still go to the lower id;

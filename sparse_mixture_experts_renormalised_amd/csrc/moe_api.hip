@@ -497,11 +497,14 @@ static int check_few(const moe_config *cfg) {
   const int st = check_config(cfg, true, true);
   if (st != MOE_OK) return st;
   if (cfg->T > moe::kFewTokens || cfg->dispatch != MOE_DISPATCH_BF16) return MOE_ERR_UNSUPPORTED;
-  // 32-bit byte offsets into one expert's matrix and into the hidden rows
+  // 32-bit byte offsets into one expert's matrix and into the hidden rows: 4 bytes
+  // an element and rows of whole 64-element chunks for float32; bf16 rows and
+  // E4M3 parts stay below half of that with their padding
+  const int64_t width = cfg->dtype == MOE_F32 ? (static_cast<int64_t>(cfg->d_ff) + 63) / 64 * 64 : cfg->d_ff;
   const int64_t slots = cfg->T * (static_cast<int64_t>(cfg->top_k) + cfg->n_shared);
   const int64_t lim = int64_t(1) << 32;
   if (cfg->d_ff >= lim / static_cast<int64_t>(act_bytes(cfg)) / cfg->d_model) return MOE_ERR_UNSUPPORTED;
-  if ((slots + 1) * cfg->d_ff >= lim / 4) return MOE_ERR_UNSUPPORTED;
+  if ((slots + 1) * width >= lim / 4) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
