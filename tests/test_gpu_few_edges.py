@@ -1,4 +1,4 @@
-"""Edges of the few-token layer: kept gates that are very small."""
+"""Edges of the few-token layer: kept gates that are very small, NaNs of unusual bits."""
 import numpy as np
 import pytest
 import torch
@@ -63,3 +63,54 @@ def test_mxfp4_hidden_rows_of_small_gates(B, case, lead):  # noqa: F811
         err = np.linalg.norm(y[t] - ref["y"][t])
         assert err <= tol, (t, err / max(np.linalg.norm(ref["y"][t]), 1e-300), err / max(tol, 1e-300))
     assert alone > 0 or T == 1
+
+
+@pytest.mark.parametrize("bits", [0x7FFFFFFF, -1], ids=["plus", "minus"])
+@pytest.mark.parametrize("kind", ["bf16", "mxfp4", "f32"])
+@pytest.mark.parametrize("T", [1, 6, 16])
+def test_nan_of_all_ones_in_the_router(B, T, kind, bits):  # noqa: F811
+    """A NaN whose mantissa is all ones rounds to a NaN, not past it: a router bias that
+    holds one makes NaN gates and with them outputs that are NaN throughout."""
+    print(f"[few] NaN of all ones {kind} T={T}", flush=True)
+    L = Few(B, T, 128, 2, 2, 1, 128, kind, router="gauss", seed=30 + T)
+    L.rb.view(torch.int32)[1] = bits
+    L()
+    torch.cuda.synchronize()
+    assert L.gate.isnan().all()
+    assert L.y.isnan().all()
+
+
+@pytest.mark.parametrize("bits", [0x7FFFFFFF, -1, 0x7FC00000], ids=["plus", "minus", "usual"])
+def test_nan_gates_of_all_ones_in_the_combine(B, bits):  # noqa: F811
+    T, d = 5, 128
+    cfg = B.config(T, d, 4, 1, 0, 128, "bf16")
+    rows = torch.randn(T, d, device="cuda").bfloat16()
+    slot = torch.arange(T, dtype=torch.int32, device="cuda").view(T, 1)
+    gate = torch.ones(T, 1, device="cuda")
+    gate.view(torch.int32)[2] = bits
+    y = torch.zeros(T, d, dtype=torch.bfloat16, device="cuda")
+    B.combine(cfg, rows, slot, gate, None, y)
+    torch.cuda.synchronize()
+    assert y[2].isnan().all()
+    keep = [0, 1, 3, 4]
+    assert torch.equal(y[keep], rows[keep])
+
+
+def test_every_rounding_to_bf16(B):  # noqa: F811
+    """Gates of every sign, exponent and leading seven bits, with what follows below, at
+    and above half a step, times rows of ones: the nearest bf16, ties to even."""
+    high = torch.arange(65536, dtype=torch.int64, device="cuda") << 16
+    bits = torch.cat([high | low for low in (0, 1, 0x7FFF, 0x8000, 0x8001, 0xFFFF)])
+    T, d = bits.numel(), 64
+    gate = (((bits + 2 ** 31) % 2 ** 32) - 2 ** 31).int().view(torch.float32).view(T, 1)
+    rows = torch.ones(T, d, dtype=torch.bfloat16, device="cuda")
+    slot = torch.arange(T, dtype=torch.int32, device="cuda").view(T, 1)
+    y = torch.zeros(T, d, dtype=torch.bfloat16, device="cuda")
+    B.combine(B.config(T, d, 4, 1, 0, 64, "bf16"), rows, slot, gate, None, y)
+    torch.cuda.synchronize()
+    nan = (bits & 0x7FFFFFFF) > 0x7F800000
+    want = (bits + 0x7FFF + ((bits >> 16) & 1)) >> 16
+    want[bits == 1 << 31] = 0                # the sum starts at +0
+    got = y.view(torch.int16).long() & 0xFFFF
+    assert y[nan].isnan().all()
+    assert torch.equal(got[~nan], want[~nan].view(-1, 1).expand(-1, d))
