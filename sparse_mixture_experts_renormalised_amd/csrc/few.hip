@@ -347,10 +347,10 @@ __device__ __forceinline__ void transpose4(uint32_t (&v)[4], bool odd, bool high
   }
 }
 
-// Larger float, larger key; NaN sorts somewhere, so that a selection always
-// names distinct experts in range.
+// Larger float, larger key, and zeros of either sign the same one (-0 + 0 = +0);
+// NaN sorts somewhere, so that a selection always names distinct experts in range.
 __device__ __forceinline__ uint32_t order_key(float v) {
-  const uint32_t u = __float_as_uint(v);
+  const uint32_t u = __float_as_uint(v + 0.0f);
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 

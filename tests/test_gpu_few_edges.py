@@ -1,4 +1,5 @@
-"""Edges of the few-token layer: kept gates that are very small, NaNs of unusual bits."""
+"""Edges of the few-token layer: kept gates that are very small, NaNs of unusual bits, zeros of
+either sign."""
 import numpy as np
 import pytest
 import torch
@@ -114,3 +115,19 @@ def test_every_rounding_to_bf16(B):  # noqa: F811
     got = y.view(torch.int16).long() & 0xFFFF
     assert y[nan].isnan().all()
     assert torch.equal(got[~nan], want[~nan].view(-1, 1).expand(-1, d))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "mxfp4"])
+@pytest.mark.parametrize("T", [1, 9])
+def test_zeros_of_either_sign_tie(B, T, kind):  # noqa: F811
+    """Expert 0's logit is a product too small for float32 with a minus sign, -0; the
+    others' are +0.  Equal values tie, and the lowest ids win."""
+    print(f"[few] -0 ties {kind} T={T}", flush=True)
+    L = Few(B, T, 4096, 6, 2, 0, 128, kind, seed=31 + T)
+    L.x.fill_(2.0 ** -100)
+    L.wr.zero_()
+    L.wr[0] = -(2.0 ** -100)
+    L()
+    torch.cuda.synchronize()
+    assert L.idx.cpu().tolist() == [[0, 1]] * T
+    assert torch.all((L.gate - 0.5).abs() <= 1e-7)
