@@ -429,7 +429,9 @@ size_t moe_grouped_linear_mxfp4_workspace_size(int32_t n_groups, int32_t n_out, 
  *     parallel branches of a graph) need a workspace of their own each.
  * Results do not depend on timing.  A weight or token element that is not finite
  * reaches the tokens it enters and no others (their outputs may be NaN where a sum
- * would be infinite; calls with such outputs take longer).
+ * would be infinite).  A call takes no longer for a token or hidden value that is not
+ * finite; an infinity or NaN among the weights of a second Linear costs it up to some
+ * milliseconds, as the sums it enters are added up again one element after the other.
  */
 #define MOE_FEW_TOKENS 16
 int moe_layer_forward_few(const moe_config *cfg, const moe_weights *w, const void *x, void *y,

@@ -270,6 +270,7 @@ struct FewArgs {
   float *part;                           // [S][T][d] parts of split outputs
   uint32_t *state;                       // [grid] of the shares of hidden rows
   uint32_t *arrived;                     // [row blocks] finished parts of split outputs
+  uint32_t *over;                        // [kTok] tokens with a hidden value that is not finite
   void *y;
   int32_t *idx;
   float *gate;
@@ -405,7 +406,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t s_b[SHARE ? 2 : 1][SHARE ? KD::PDN * kTok * 512 : 16];
   __shared__ __attribute__((aligned(16))) uint8_t s_bs[SHARE ? 2 : 1][SHARE ? kTok * 16 : 16];
   __shared__ uint32_t s_amax[kWaves][kTok];
-  __shared__ uint32_t s_last;
+  __shared__ uint32_t s_last, s_over;
   __shared__ int s_free, s_claim;
   __shared__ int s_ne;
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
@@ -420,7 +421,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
   };
   int mine_claim = 0;                      // the last wave has the fewest tokens
   if (tid == kThreads - 64) mine_claim = claim(blockIdx.x);
-  if (tid == 0) s_free = kGrid;
+  if (tid == 0) s_free = kGrid, s_over = 0;
   for (int e = tid; e < N; e += kThreads) s_mask[e] = 0;
   for (int t = wave; t < T; t += kWaves) {
     constexpr int NJ = kMaxRouted / 64;
@@ -846,17 +847,20 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
       if (bias) z[v] += act_f32(bias, e * f + hidden, Act{});
       const float g = routed && hr >= 0 ? s_gate[token * 64 + (hr - token * K)] : 1.0f;
       z[v] = g * silu(z[v]);
+      bool over = (__float_as_uint(z[v]) & 0x7F800000u) == 0x7F800000u;
       uint8_t *hp = static_cast<uint8_t *>(a.h) + (static_cast<int64_t>(hr) * h_chunks + hidden / KD::CH) * KD::CB;
       if constexpr (W == kWF32) {
         if (hr >= 0) put_shared(reinterpret_cast<uint32_t *>(hp) + hidden % KD::CH, __float_as_uint(z[v]));
       } else if constexpr (W == kWBf16) {
         const uint16_t hi = f32_to_bf16(z[v]);
+        over = (hi & 0x7F80u) == 0x7F80u;
         if (hr >= 0) {
           put_shared(reinterpret_cast<uint16_t *>(hp) + hidden % KD::CH, hi);
           put_shared(reinterpret_cast<uint16_t *>(hp + h_part) + hidden % KD::CH,
                      f32_to_bf16(z[v] - bf16_to_f32(hi)));
         }
       }
+      if (over && hr >= 0) atomicOr(&s_over, 1u << token);
       // lanes without a tile hold another one's values, and not this row's gate
       uint32_t &most = amax[SHARE ? 0 : v];
       if (tile < m) most = max(most, __float_as_uint(z[v]) & 0x7FFFFFFFu);
@@ -928,7 +932,12 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
     }
     wait_stores();
     __syncthreads();
-    if (tid == 0) put_shared(a.state + w, static_cast<uint32_t>(kDone));
+    if (wave == 0) {
+      // one store a token in all, nearly: hundreds on one address take their time
+      if (lane < kTok && (s_over >> lane) & 1 && get_shared(a.over + lane) == 0) put_shared(a.over + lane, 1u);
+      wait_stores();
+      if (lane == 0) put_shared(a.state + w, static_cast<uint32_t>(kDone));
+    }
   };
   if (s_claim) up_share(blockIdx.x);
 
@@ -1018,40 +1027,51 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
     const uint8_t *hb = static_cast<const uint8_t *>(a.h);
     // The zeros of tokens without a hidden row do not hide an infinity or a NaN
     // among the weights.  A sum that is not finite is therefore added up again, by
-    // its lane, from the token's own entries.
+    // its lane, from the token's own entries, until it is NaN.  A token with a hidden
+    // value that is not finite has no finite output and keeps its sums: a padded
+    // batch may hold such tokens, and one lane takes milliseconds for a sum.
     auto own_entries = [&](int orow, int token) {
       float sum = 0.0f;
+      int c = static_cast<int>(static_cast<int64_t>(total) * s / a.S);
 #pragma nounroll
-      for (int c = static_cast<int>(static_cast<int64_t>(total) * s / a.S); c < c1; ++c) {
-        const int i = c / h_chunks, hc = c - i * h_chunks, hr = hidden_row(i, token);
-        if (hr < 0) continue;
+      while (c < c1) {
+        const int i = c / h_chunks, hr = hidden_row(i, token), end = min(c1, (i + 1) * h_chunks);
+        if (hr < 0) {
+          c = end;
+          continue;
+        }
         const int64_t wrow = (i < ne ? static_cast<int64_t>(s_list[i]) : i - ne) * d + orow;
         const uint8_t *w = static_cast<const uint8_t *>(i < ne ? a.w2 : a.ws2) + wrow * pieces * 16;
         const uint8_t *cw = W == kWMx ? (i < ne ? a.c2 : a.cs2) + wrow * pieces : nullptr;
-        const int64_t hat = static_cast<int64_t>(hr) * h_chunks + hc;
-        const uint8_t *hv = hb + hat * KD::CB;
-        const int k0 = hc * KD::CH, n = min(KD::CH, f - k0);
 #pragma nounroll
-        for (int k = 0; k < n; ++k) {
-          float x, y;
-          if constexpr (W == kWF32) {
-            x = reinterpret_cast<const float *>(hv)[k];
-            y = reinterpret_cast<const float *>(w)[k0 + k];
-          } else if constexpr (W == kWBf16) {
-            x = bf16_to_f32(reinterpret_cast<const uint16_t *>(hv)[k]) +
-                bf16_to_f32(reinterpret_cast<const uint16_t *>(hv + h_part)[k]);
-            y = bf16_to_f32(reinterpret_cast<const uint16_t *>(w)[k0 + k]);
-          } else {
-            const int hs = a.hs[hat * 16 + k / 32], ws = cw[(k0 + k) / 32];
-            x = 0.0f;
-            for (int p = 0; p < KD::PDN; ++p)
-              x += __builtin_ldexpf(__builtin_amdgcn_cvt_f32_fp8(hv[p * h_part + part_byte(k)], 0),
-                                    hs - 127 - 4 * p);
-            const uint32_t code = w[(k0 + k) / 2] >> (k & 1 ? 4 : 0);
-            y = __builtin_ldexpf(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code & 15, 1.0f, 0)[0], ws - 127);
-            if (hs == 255 || ws == 255) y = __uint_as_float(0x7FC00000u);
+        for (; c < end; ++c) {
+          const int hc = c - i * h_chunks;
+          const int64_t hat = static_cast<int64_t>(hr) * h_chunks + hc;
+          const uint8_t *hv = hb + hat * KD::CB;
+          const int k0 = hc * KD::CH, n = min(KD::CH, f - k0);
+#pragma nounroll
+          for (int k = 0; k < n; ++k) {
+            float x, y;
+            if constexpr (W == kWF32) {
+              x = reinterpret_cast<const float *>(hv)[k];
+              y = reinterpret_cast<const float *>(w)[k0 + k];
+            } else if constexpr (W == kWBf16) {
+              x = bf16_to_f32(reinterpret_cast<const uint16_t *>(hv)[k]) +
+                  bf16_to_f32(reinterpret_cast<const uint16_t *>(hv + h_part)[k]);
+              y = bf16_to_f32(reinterpret_cast<const uint16_t *>(w)[k0 + k]);
+            } else {
+              const int hs = a.hs[hat * 16 + k / 32], ws = cw[(k0 + k) / 32];
+              x = 0.0f;
+              for (int p = 0; p < KD::PDN; ++p)
+                x += __builtin_ldexpf(__builtin_amdgcn_cvt_f32_fp8(hv[p * h_part + part_byte(k)], 0),
+                                      hs - 127 - 4 * p);
+              const uint32_t code = w[(k0 + k) / 2] >> (k & 1 ? 4 : 0);
+              y = __builtin_ldexpf(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code & 15, 1.0f, 0)[0], ws - 127);
+              if (hs == 255 || ws == 255) y = __uint_as_float(0x7FC00000u);
+            }
+            sum = fmaf(x, y, sum);
+            if (__builtin_isnan(sum)) return sum;
           }
-          sum = fmaf(x, y, sum);
         }
       }
       return sum;
@@ -1108,7 +1128,8 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
     }
 #pragma unroll
     for (int t = 0; t < OUT; ++t)
-      if (T > 1 && out && (__float_as_uint(v[t]) & 0x7F800000u) == 0x7F800000u)
+      if (T > 1 && out && (__float_as_uint(v[t]) & 0x7F800000u) == 0x7F800000u &&
+          get_shared(a.over + token) == 0)
         v[t] = own_entries(row_of(t), token);
     bool finish = true;
     if (a.S > 1) {
@@ -1205,7 +1226,7 @@ FewWs few_ws(FewKind kind, int T, int d, int N, int K, int Ks, int f) {
   const DownPlan plan = down_plan(kind, T, d, N, K, Ks, f);
   w.parts = plan.parts;
   w.blocks = d / plan.rows;
-  w.n_ctr = kGrid + w.blocks;
+  w.n_ctr = kGrid + w.blocks + kTok;
   w.logits = take(sizeof(float) * T * N);
   w.ctr = take(sizeof(uint32_t) * w.n_ctr);
   w.h = take(h_parts * rows * few_row_bytes(kind, f));
@@ -1289,6 +1310,7 @@ hipError_t launch_few_layer(const FewLayer &p, void *ws, hipStream_t s) {
   a.part = reinterpret_cast<float *>(base + L.part);
   a.state = ctr;
   a.arrived = ctr + kGrid;
+  a.over = a.arrived + L.blocks;
   a.y = p.y; a.idx = p.idx; a.gate = p.gate; a.counts = p.counts;
   a.T = p.T; a.d = p.d; a.N = p.N; a.K = p.K; a.Ks = p.Ks; a.f = p.f;
   a.S = L.parts;

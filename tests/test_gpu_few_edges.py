@@ -1,5 +1,5 @@
 """Edges of the few-token layer: kept gates that are very small, NaNs of unusual bits, zeros of
-either sign."""
+either sign, tokens that are not finite."""
 import numpy as np
 import pytest
 import torch
@@ -131,3 +131,67 @@ def test_zeros_of_either_sign_tie(B, T, kind):  # noqa: F811
     torch.cuda.synchronize()
     assert L.idx.cpu().tolist() == [[0, 1]] * T
     assert torch.all((L.gate - 0.5).abs() <= 1e-7)
+
+
+def _micros(call, n=10):
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    least = float("inf")
+    for _ in range(5):
+        call()
+        a.record()
+        for _ in range(n):
+            call()
+        b.record()
+        b.synchronize()
+        least = min(least, a.elapsed_time(b) * 1e3 / n)
+    return least
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("case", [(8, 2048, 64, 8, 2, 1408, "bf16"), (16, 2048, 32, 4, 1, 2048, "mxfp4"),
+                                  (12, 512, 32, 4, 1, 768, "f32")], ids=lambda c: f"{c[6]}-T{c[0]}")
+def test_tokens_that_are_not_finite_do_not_hold_a_step_up(B, case, bad):  # noqa: F811
+    """A row of a padded batch may hold anything.  Its outputs are known not to be
+    finite after the first terms of their sums: a step takes no longer for it, but for
+    the little that finds it out (half again is allowed)."""
+    L = Few(B, *case, seed=32)
+    ref, A = L.reference()
+    tol = L.bound(ref, A)
+    usual = _micros(L)
+    L.x[3] = bad
+    held = _micros(L)
+    print(f"[few] {case} {bad}: {usual:.1f} us, {held:.1f} us with such a token", flush=True)
+    rest = [t for t in range(case[0]) if t != 3]
+    assert not torch.isfinite(L.y[3].float()).any()
+    # (not the same bits: the experts that token 3 meets now are others, and sums are cut
+    # where all entries' chunks are)
+    assert np.all((np.abs(L.y.double().cpu().numpy() - ref["y"]) <= tol)[rest])
+    assert held <= 1.5 * usual + 5.0
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("case", [(8, 2048, 64, 8, 2, 1408, "bf16"), (16, 2048, 32, 4, 1, 2048, "mxfp4"),
+                                  (12, 512, 32, 4, 1, 768, "f32")], ids=lambda c: f"{c[6]}-T{c[0]}")
+def test_hidden_values_that_are_not_finite_do_not_hold_a_step_up(B, case, bad):  # noqa: F811
+    """The same where one hidden value of an expert, its last, overflows or is NaN: no
+    output of the tokens that the expert computes is finite, and those of the others
+    are as before."""
+    L = Few(B, *case, seed=33)
+    ref, A = L.reference()
+    tol = L.bound(ref, A)
+    usual = _micros(L)
+    T, d, N, f = case[0], case[1], case[2], case[5]
+    e = int(ref["topk_idx"][1, 0])
+    if case[6] == "mxfp4":
+        L.w["k1"].view(N, f, d // 32)[e, f - 1, d // 32 - 1] = 255
+    else:
+        L.w["w1"][e, f - 1, d - 1] = bad
+    held = _micros(L)
+    print(f"[few] {case} {bad}: {usual:.1f} us, {held:.1f} us with such a value", flush=True)
+    y = L.y.double().cpu().numpy()
+    for t in range(T):
+        if e in ref["topk_idx"][t]:
+            assert not np.isfinite(y[t]).any(), t
+        else:
+            assert np.all(np.abs(y[t] - ref["y"][t]) <= tol[t]), t
+    assert held <= 1.5 * usual + 5.0
