@@ -433,13 +433,12 @@ int moe_quantize_mxfp4(int32_t dtype, int64_t rows, int32_t d, const void *x, in
                        uint8_t *codes, uint8_t *scales, void *widened, void *stream) {
   if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
   if (rows < 0 || d <= 0) return MOE_ERR_INVALID_ARG;
-  if (d % 32 != 0) return MOE_ERR_UNSUPPORTED;
+  if (d % 32 != 0 || rows > ((int64_t(1) << 42) - 1) / d) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   if (!x || !codes || !scales) return MOE_ERR_INVALID_ARG;
   if (!all_aligned16({x, codes, scales, widened})) return MOE_ERR_INVALID_ARG;
   const int64_t lanes = dtype == MOE_BF16 ? 8 : 4;    // elements of a 16-byte load
   if (rows > 1 && (x_stride < d || x_stride % lanes != 0)) return MOE_ERR_INVALID_ARG;
-  if (rows >= (int64_t(1) << 42) / d) return MOE_ERR_UNSUPPORTED;
   return hip_status(moe::launch_quantize_mxfp4(dtype == MOE_BF16, x, rows, d, x_stride, codes,
                                                scales, widened, static_cast<hipStream_t>(stream)));
 }
@@ -448,7 +447,7 @@ static int check_linear_mxfp4(int32_t n_groups, int32_t n_out, int32_t k, int64_
   if (n_groups <= 0 || n_out <= 0 || k <= 0 || max_rows < 0) return MOE_ERR_INVALID_ARG;
   if (n_groups > moe::kMaxRouted + moe::kMaxShared) return MOE_ERR_UNSUPPORTED;
   if (n_out % 8 != 0 || k % 128 != 0) return MOE_ERR_UNSUPPORTED;
-  if (n_out >= (int64_t(1) << 32) / (k / 2)) return MOE_ERR_UNSUPPORTED;
+  if (n_out > ((int64_t(1) << 32) - 1) / (k / 2)) return MOE_ERR_UNSUPPORTED;
   if (max_rows >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
@@ -467,7 +466,7 @@ int moe_grouped_linear_mxfp4(int32_t n_groups, int32_t n_out, int32_t k, int64_t
   const int st = check_linear_mxfp4(n_groups, n_out, k, max_rows);
   if (st != MOE_OK) return st;
   if (x_rows < 0 || (silu != 0 && silu != 1)) return MOE_ERR_INVALID_ARG;
-  if (x_rows >= (int64_t(1) << 32) / (k / 2)) return MOE_ERR_UNSUPPORTED;
+  if (x_rows > ((int64_t(1) << 32) - 1) / (k / 2)) return MOE_ERR_UNSUPPORTED;
   if (max_rows == 0) return MOE_OK;
   if (x_rows < (row_index ? 1 : max_rows)) return MOE_ERR_INVALID_ARG;
   if (!x_codes || !x_scales || !offsets || !w_codes || !w_scales || !y_rows)
@@ -503,7 +502,7 @@ static int check_few(const moe_config *cfg) {
   const int64_t width = cfg->dtype == MOE_F32 ? (static_cast<int64_t>(cfg->d_ff) + 63) / 64 * 64 : cfg->d_ff;
   const int64_t slots = cfg->T * (static_cast<int64_t>(cfg->top_k) + cfg->n_shared);
   const int64_t lim = int64_t(1) << 32;
-  if (cfg->d_ff >= lim / static_cast<int64_t>(act_bytes(cfg)) / cfg->d_model) return MOE_ERR_UNSUPPORTED;
+  if (cfg->d_ff > (lim - 1) / static_cast<int64_t>(act_bytes(cfg)) / cfg->d_model) return MOE_ERR_UNSUPPORTED;
   if ((slots + 1) * width >= lim / 4) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
