@@ -482,7 +482,9 @@ const char *moe_status_string(int status);
 
 /* Interface version, 0x00MMmmpp: the library returns MOE_VERSION of the
  * header it was built with; a caller built against another version should not
- * use it (struct layouts may differ). */
+ * use it (struct layouts may differ).  It stays as it is where calls are only
+ * added: a library from before them has the same version and lacks their
+ * symbols. */
 #define MOE_VERSION 0x000200
 int moe_version(void);
 

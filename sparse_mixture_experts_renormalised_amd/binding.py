@@ -114,12 +114,15 @@ def lib():
             "moe_status_string": (ctypes.c_char_p, [I]),
             "moe_version": (I, []),
         }
-        for name, (res, args) in sig.items():
-            f = getattr(L, name)
-            f.restype, f.argtypes = res, args
-        if L.moe_version() != INTERFACE_VERSION:
-            raise RuntimeError(f"{LIB_PATH} implements interface {L.moe_version():#08x}, this "
-                               f"binding {INTERFACE_VERSION:#08x}: rebuild the library")
+        # the version first: another one's calls may have other arguments
+        for name in ("moe_version", *sig):
+            f = getattr(L, name, None)
+            if f is None:
+                raise RuntimeError(f"{LIB_PATH} lacks {name}: rebuild the library")
+            f.restype, f.argtypes = sig[name]
+            if name == "moe_version" and f() != INTERFACE_VERSION:
+                raise RuntimeError(f"{LIB_PATH} implements interface {f():#08x}, this "
+                                   f"binding {INTERFACE_VERSION:#08x}: rebuild the library")
         _LIB = L
     return _LIB
 
