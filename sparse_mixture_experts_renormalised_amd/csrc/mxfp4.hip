@@ -588,7 +588,9 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-template <int BM>
+// ONCE: no other tile reads these weights (a group's last rows), which then go past
+// the caches; weights of full tiles and of their halves mostly serve several.
+template <int BM, bool ONCE = (BM < 256)>
 struct Tile {
   static constexpr int TM = BM / 64, AC = BM / 64, BC = 4, NCP = AC + BC;   // code copies per wave
   static constexpr int SC = 2, N = NCP + SC;                                // scale, all copies
@@ -616,7 +618,7 @@ struct Tile {
                                                 int64_t rows, int n0, int tid, Src &s) {
     const int64_t kb = a.k / 2, ksb = a.k / 32;
     const int c = (tid & 7) ^ ((tid >> 4) & 7);       // row = tid/8 + 32i
-    // scale copy j of wave w: rows 16 (w + 4 j) .. +15, four lanes of 4 bytes a
+    // scale copy j of wave w: rows 16 (w + 8 j) .. +15, four lanes of 4 bytes a
     // row (rows past the tile repeat the last one, here and for the codes)
     const int sr = (tid >> 6) * 16 + ((tid & 63) >> 2);
     int64_t ra[AC], rs[SC];
@@ -655,12 +657,11 @@ struct Tile {
   static __device__ __forceinline__ int step_off(const Src &s, int kb) {
     return kb * 128 + (kb == s.nk - 1 ? s.tadj : 0);
   }
-  // Weights of the smaller tiles, which no other tile reads, go past the caches
-  // (the cases above: decode 127 -> 116 us, many 582 -> 573); those of full tiles
-  // mostly serve several (fine 101 without the caches, 98 with them).
+  // Of the cases above, with the last rows' weights in the caches decode takes 127 us,
+  // many 582; with full tiles' past them fine 101 (98), with their halves' 91 (90).
   static __device__ __forceinline__ void copy(const Src &s, int i, int off, uint32_t base, int wave) {
     if (i < AC) dma::dma16s(s.a[i] + off, s.abase, base + (8 * i + wave) * 1024);
-    else if (BM < 256) dma::dma16s_nt(s.b[i - AC] + off, s.bbase, base + BM * 128 + (8 * (i - AC) + wave) * 1024);
+    else if (ONCE) dma::dma16s_nt(s.b[i - AC] + off, s.bbase, base + BM * 128 + (8 * (i - AC) + wave) * 1024);
     else dma::dma16s(s.b[i - AC] + off, s.bbase, base + BM * 128 + (8 * (i - AC) + wave) * 1024);
   }
   // Scale copies: the rows of X (which 0) or W (1) for the steps 2p and 2p + 1.
@@ -955,7 +956,7 @@ __global__ __launch_bounds__(tile::NT, 2) void mx_linear_kernel(MxArgs a) {
       const int g = uniform(lo);
       const int64_t row0 = static_cast<int64_t>(mt - s_pref[g]) * 256;
       if (half < 0) Tile<256>::run<SILU>(a, g, row0, n * BN, s_buf, s_sc);
-      else Tile<128>::run<SILU>(a, g, row0 + half * 128, n * BN, s_buf, s_sc);
+      else Tile<128, false>::run<SILU>(a, g, row0 + half * 128, n * BN, s_buf, s_sc);
     } else {
       const int i = it - fulls - 2 * split;
       const bool wide = i < cnt[1];
