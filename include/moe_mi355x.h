@@ -421,13 +421,16 @@ size_t moe_grouped_linear_mxfp4_workspace_size(int32_t n_groups, int32_t n_out, 
  *     chain, so two experts whose logits differ by no more than their rounding
  *     may be ordered differently than there; ties still go to the lower id;
  *   - hidden activations keep at least 16 significant bits (float32 layers:
- *     all) and expert outputs are not rounded before the sum over experts: y
- *     is rounded once.  Routed experts are summed in ascending expert id, the
- *     shared experts after them;
+ *     all; one too large for bf16 is not finite in a bf16 layer, as in
+ *     moe_layer_forward) and expert outputs are not rounded before the sum over
+ *     experts: y is rounded once.  Routed experts are summed in ascending expert
+ *     id, the shared experts after them;
  *   - ws holds moe_few_workspace_size(cfg) bytes, all scratch.  Nothing in it
  *     needs to be initialised.  Calls that overlap in time (other streams,
  *     parallel branches of a graph) need a workspace of their own each.
- * Results do not depend on timing.  A weight or token element that is not finite
+ * Equal calls give equal bits; where a token's sums are cut depends on the experts
+ * that all tokens of the call meet, so in another batch its last bits may differ.
+ * A weight or token element that is not finite
  * reaches the tokens it enters and no others (their outputs may be NaN where a sum
  * would be infinite).  A call takes no longer for a token or hidden value that is not
  * finite; an infinity or NaN among the weights of a second Linear costs it up to some
@@ -468,6 +471,8 @@ typedef struct {
  *           its 32, and within 2^-21 of that largest below;
  *   hidden  three parts, the rest at most 2^-12 of the element or 2^-25 of the
  *           largest of its 32.
+ * That is for a largest of 2^-111 or more; below, tokens are off by at most 2^-133 and
+ * hidden values by 2^-137.
  * cfg->dtype is MOE_BF16 and d_model and d_ff are multiples of 128, else
  * MOE_ERR_UNSUPPORTED. */
 int moe_layer_forward_few_mxfp4(const moe_config *cfg, const moe_weights_mxfp4 *w, const void *x,

@@ -210,10 +210,22 @@ __device__ __forceinline__ int mx_full_tiles(int rows, int *tail) {
 
 // The least number of rows that a group taken in tiles has: 1 if the tiles of all
 // groups fill the chip, tiles of more than 16 rows counting twice, else
-// kStreamRows + 1.  Timed at 7168 -> 2048 with 1, 16, 17 and 64 rows a group,
-// straight from memory and in tiles: 64 tiles 15, 22, 24, 36 us and 34, 35, 35, 39;
-// 128 tiles 27, 36, 39, 60 and 36, 37, 38, 41; 512 tiles 88, 119, 125, 219 and 80,
-// 83, 83, 91.
+// kStreamRows + 1.  Timed with 1, 16, 17 and 64 rows a group, straight from memory
+// and in tiles (us):
+//   7168 -> 2048   64 tiles  15  22  24  40    33  35  35  38
+//                 128        27  36  37  61    36  37  37  40
+//                 192        39  52  55  94    38  39  39  43
+//                 512        88 119 121 218    81  83  83  91
+//   2048 -> 1408   66 tiles 9.5  11  12  19    13  13  13  15
+//                 126        11  15  15  26    13  14  14  15
+//                 192        15  19  20  33    14  15  15  16
+//                 510        33  38  40  69    28  28  29  31
+//   2048 -> 7168   56 tiles 8.8 9.0 9.6  19    13  13  13  14
+//                 140        13  18  19  29    14  14  14  15
+//                 196        18  21  22  36    15  15  15  16
+//                 504        31  39  41  70    30  30  30  33
+// So the rule takes the faster way but for groups of 16 and of 64 rows somewhat below
+// the border (140 tiles of 16 rows: 18 us for 14; 66 of 64: 19 for 15).
 constexpr int kFill = 192;
 struct Plan {
   int least;                           // of the groups taken in tiles
