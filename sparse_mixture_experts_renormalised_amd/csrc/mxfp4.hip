@@ -171,9 +171,10 @@ hipError_t quantize(const void *x, int64_t rows, int d, int64_t stride, uint8_t 
 //   * else the groups of up to kStreamRows rows: units of 16 features, operands
 //     straight from memory to registers, which a few groups have enough of.
 // Measured on MI355X: 256 groups, 207 rows in about 84 of them, 7168 -> 2048:
-// 116 us, 5.7 TB/s (134 us straight from memory); 64 groups, 32768 rows, 2048 ->
-// 1408 with SiLU: 91 us; 256 groups, 32768 rows, 2048 -> 7168: 573 us, 4.4 TB/s;
-// 8 groups, 8192 rows, 4096 -> 14336 with bias and SiLU: 331 us, 2.9 PFLOP/s.
+// 115 us, 5.7 TB/s (134 us straight from memory); 64 groups, 32768 rows, 2048 ->
+// 1408 with SiLU: 93 us; 256 groups, 32768 rows, 2048 -> 7168: 581 us, 4.3 TB/s;
+// 8 groups, 8192 rows, 4096 -> 14336 with bias and SiLU: 340 us, 2.8 PFLOP/s.  Cards
+// differ by up to 8 %; the figures below compare two forms on one card each.
 // ---------------------------------------------------------------------------
 constexpr int kMaxGroups = kMaxRouted + kMaxShared;
 constexpr int kXcds = 8;
@@ -669,8 +670,9 @@ struct Tile {
   static __device__ __forceinline__ int step_off(const Src &s, int kb) {
     return kb * 128 + (kb == s.nk - 1 ? s.tadj : 0);
   }
-  // Of the cases above, with the last rows' weights in the caches decode takes 127 us,
-  // many 582; with full tiles' past them fine 101 (98), with their halves' 91 (90).
+  // Of the cases above, the first takes 127 us with the last rows' weights in the caches
+  // (116), the third 582 (573); the second 101 with full tiles' weights past them (98),
+  // and 91 with their halves' (90).
   static __device__ __forceinline__ void copy(const Src &s, int i, int off, uint32_t base, int wave) {
     if (i < AC) dma::dma16s(s.a[i] + off, s.abase, base + (8 * i + wave) * 1024);
     else if (ONCE) dma::dma16s_nt(s.b[i - AC] + off, s.bbase, base + BM * 128 + (8 * (i - AC) + wave) * 1024);
