@@ -1,8 +1,6 @@
 """Size limits of the few-token layer and the MXFP4 calls, at their borders: what is
 refused, and that the largest sizes below are not (no GPU needed; the accepted sizes
 are handed over with an argument missing, so that nothing is launched)."""
-import ctypes
-
 from test_mxfp4_few_args import B, few, linear, quant  # noqa: F401  (B: the fixture)
 
 
