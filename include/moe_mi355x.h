@@ -479,6 +479,193 @@ int moe_layer_forward_few_mxfp4(const moe_config *cfg, const moe_weights_mxfp4 *
                                 void *y, int32_t *topk_idx, float *topk_gate, int32_t *counts,
                                 void *ws, size_t ws_bytes, void *stream);
 
+/*
+ * Training the layer as a block of a model.  The calls below are the single
+ * Linears of the experts with their gradients, the block around the layer
+ * (norms, gate, residual) with its gradients, and dropout.  A step goes
+ *   moe_block_join (first norm) - moe_route - moe_permute -
+ *   moe_grouped_linear (W1, SiLU, pre) - moe_dropout - moe_grouped_linear (W2) -
+ *   moe_block_join
+ * and back through moe_block_join_grad - weight and input gradient of W2 -
+ * moe_dropout - weight and input gradient of W1 - moe_combine with gates of one
+ * (the sum of a token's rows over its slots) - moe_block_join_grad.
+ */
+
+/*
+ * moe_grouped_linear — one Linear of every group's expert on its own rows:
+ *   y[r] = act(x[row_index[r]] W_g^T + bias_g),   offsets[g] <= r < offsets[g+1]
+ * with float32 sums, rounded once.
+ *   dtype       moe_dtype of x, w, bias, y and pre
+ *   x           [x_rows][k], row_index [max_rows] int32 or NULL: source row of
+ *               each row (a dispatch's row_token), values in [0, x_rows); NULL:
+ *               row r reads row r, and x_rows >= max_rows
+ *   offsets     [n_groups+1] int32 DEVICE array, non-decreasing, offsets[0]=0
+ *   max_rows    host-side upper bound on offsets[n_groups], as for
+ *               moe_grouped_ffn; rows at or beyond offsets[n_groups] are
+ *               neither read nor written, here and in the gradients
+ *   w [G][n_out][k], bias [G][n_out] or NULL
+ *   silu        1: act = SiLU, 0: none
+ *   y           [max_rows][n_out] output
+ *   pre         [max_rows][n_out] output or NULL, with silu 1 only: the values
+ *               before the SiLU, which its gradient reads
+ *   ws          device scratch of moe_grouped_linear_workspace_size bytes, which
+ *               is one size for the three calls; nothing in it needs to be
+ *               initialised, and calls that overlap in time need one each
+ * n_out and k are multiples of 64 for MOE_BF16 and of 16 for MOE_F32 (as d_model
+ * and d_ff of the layer), n_groups <= 1088, max_rows < 2^31; else
+ * MOE_ERR_UNSUPPORTED.
+ */
+int moe_grouped_linear(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k, int64_t x_rows,
+                       const void *x, const int32_t *row_index, const int32_t *offsets,
+                       int64_t max_rows, const void *w, const void *bias, int32_t silu, void *y,
+                       void *pre, void *ws, size_t ws_bytes, void *stream);
+
+/* moe_grouped_linear_input_grad — the gradient of moe_grouped_linear's rows from
+ * that of its outputs (before its own SiLU, if it has one):
+ *   dx[r] = (dy[r] W_g) silu'(pre[r])
+ *   dy [max_rows][n_out], dx [max_rows][k] output
+ *   pre         [max_rows][k] or NULL: the values before the SiLU that made the
+ *               rows (moe_grouped_linear's pre of the Linear before); NULL: no
+ *               such factor
+ * Rows are those of the groups: where the forward read them through row_index,
+ * the sum over a token's rows is moe_combine with gates of one. */
+int moe_grouped_linear_input_grad(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k,
+                                  const void *dy, const int32_t *offsets, int64_t max_rows,
+                                  const void *w, const void *pre, void *dx, void *ws,
+                                  size_t ws_bytes, void *stream);
+
+/* moe_grouped_linear_weight_grad — the gradients of weights and bias, sums over
+ * each group's rows in float32, rounded once:
+ *   dw_g (+)= sum_r dy[r]^T x[row_index[r]],   dbias_g (+)= sum_r dy[r]
+ *   grad_dtype  moe_dtype of dw and dbias: MOE_F32, or MOE_BF16 for MOE_BF16 rows
+ *   dw          [G][n_out][k] output; dbias [G][n_out] output or NULL
+ *   accumulate  1: the sums are added to what dw and dbias hold; 0: they replace
+ *               it, and groups without rows (all of them, for max_rows 0) get
+ *               zeros
+ * Equal calls give equal bits. */
+int moe_grouped_linear_weight_grad(int32_t dtype, int32_t grad_dtype, int32_t n_groups,
+                                   int32_t n_out, int32_t k, const void *dy, int64_t x_rows,
+                                   const void *x, const int32_t *row_index,
+                                   const int32_t *offsets, int64_t max_rows, void *dw,
+                                   void *dbias, int32_t accumulate, void *ws, size_t ws_bytes,
+                                   void *stream);
+
+/* Device workspace of the three calls (0 when the sizes are invalid or
+ * unsupported, and where none is needed: ws may then be NULL). */
+size_t moe_grouped_linear_workspace_size(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k,
+                                         int64_t max_rows);
+
+/* Norm of a row v of d elements, with float32 statistics:
+ *   MOE_NORM_NONE   v w + b
+ *   MOE_NORM_RMS    v / sqrt(mean(v^2) + eps) w + b
+ *   MOE_NORM_LAYER  (v - m) / sqrt(mean((v - m)^2) + eps) w + b,  m = mean(v)
+ * Squares are float32's: rows with elements above about 1e18 do not normalise. */
+enum { MOE_NORM_NONE = 0, MOE_NORM_RMS = 1, MOE_NORM_LAYER = 2 };
+
+/* Shape and constants of a block around the layer. */
+typedef struct {
+    int64_t T;                /* tokens                                            */
+    double dropout_p;         /* probability of a dropped branch element, see
+                                 moe_dropout; 0: none                              */
+    int32_t d_model;          /* d, a multiple of 8, at most 16384                 */
+    int32_t dtype;            /* moe_dtype of the branch, expert rows and next rows */
+    int32_t res_dtype;        /* moe_dtype of the residual stream: dtype or MOE_F32 */
+    int32_t norm_out;         /* MOE_NORM_*: norm of the branch                    */
+    int32_t norm_in;          /* MOE_NORM_*: norm of the next block's input        */
+    int32_t top_k;            /* K, with expert rows (at most 64), else ignored    */
+    int32_t n_shared;         /* shared experts' rows beside them (at most 64)     */
+    float eps;                /* of both norms, > 0 where there is one             */
+    float scale;              /* of the branch                                     */
+} moe_block;
+
+/* Tensors that moe_block_join and its gradient read. */
+typedef struct {
+    const void *residual;       /* [T][d] res_dtype (not read by the gradient)     */
+    const void *branch;         /* [T][d] dtype or NULL, see below                 */
+    const void *y_rows;         /* expert rows [*][d] dtype, as in moe_combine, or NULL */
+    const int32_t *slot_row;    /* [T][K] with y_rows: row of (t, k), or -1        */
+    const float *topk_gate;     /* [T][K] with y_rows                              */
+    const void *shared_out;     /* [n_shared][T][d] dtype with y_rows and n_shared
+                                   > 0 (not read by the gradient)                  */
+    const float *gate;          /* [T] or NULL (one)                               */
+    const float *w_out, *b_out; /* [d] or NULL (one, zero): norm of the branch     */
+    const float *w_in, *b_in;   /* [d] or NULL (one, zero): norm of the next input */
+    const uint64_t *rng;        /* {seed, stream} for dropout_p > 0, see moe_dropout */
+} moe_block_tensors;
+
+/*
+ * moe_block_join — a block's branch into the residual stream, and the next
+ * block's input, in one pass over each token's row:
+ *   b    = branch[t], or moe_combine of y_rows, slot_row, topk_gate, shared_out
+ *   out  = residual[t] + scale gate[t] Drop(Norm_out(b))
+ *   next = Norm_in(out)
+ * in float32 (next from out before its rounding), each output rounded once.
+ * branch and y_rows exclude each other; without both, out is the residual (the
+ * norm before a model's first block) and everything of the branch is ignored.
+ *   out         [T][d] res_dtype output or NULL; it may be the residual itself
+ *   next        [T][d] dtype output or NULL
+ *   branch_out  [T][d] dtype output or NULL: b, which the gradient reads (with
+ *               y_rows; ignored without)
+ * Outputs overlap no input but that one.
+ */
+int moe_block_join(const moe_block *cfg, const moe_block_tensors *in, void *out, void *next,
+                   void *branch_out, void *stream);
+
+/* Gradients that moe_block_join_grad writes; each may be NULL. */
+typedef struct {
+    void *d_residual;           /* [T][d] res_dtype                                */
+    void *d_branch;             /* [T][d] dtype: of b, which is that of each shared
+                                   expert's row too                                */
+    void *d_y_rows;             /* rows slot_row[t][k] of [*][d] dtype: of the expert
+                                   rows; others stay as they are                   */
+    float *d_topk_gate;         /* [T][K], 0 where slot_row is -1                  */
+    float *d_gate;              /* [T]                                             */
+    float *d_w_out, *d_b_out;   /* [d], sums over the tokens                       */
+    float *d_w_in, *d_b_in;     /* [d], sums over the tokens                       */
+} moe_block_grads;
+
+/*
+ * moe_block_join_grad — the gradients of moe_block_join's inputs from those of
+ * its outputs.  Statistics, masks and normalised rows are made again from out
+ * and the branch as they were stored.
+ *   out         [T][d] res_dtype: the forward's out (needed with d_next)
+ *   d_out       [T][d] res_dtype or NULL (zero): gradient of out from behind
+ *   d_next      [T][d] dtype or NULL (zero): gradient of next
+ *   in->branch  the branch, or the forward's branch_out where it had y_rows;
+ *               NULL: the block had none, and its gradients must be NULL (sums
+ *               over tokens: zeros)
+ *   in->y_rows  needed for d_topk_gate; in->slot_row and in->topk_gate for
+ *               d_y_rows and d_topk_gate
+ *   ws          device scratch of moe_block_join_grad_workspace_size bytes where a
+ *               sum over tokens is asked for (else it may be NULL)
+ * d_residual may be d_out itself.  T == 0 writes zeros to the sums over tokens.
+ * Equal calls give equal bits.
+ */
+int moe_block_join_grad(const moe_block *cfg, const moe_block_tensors *in, const void *out,
+                        const void *d_out, const void *d_next, const moe_block_grads *grads,
+                        void *ws, size_t ws_bytes, void *stream);
+size_t moe_block_join_grad_workspace_size(const moe_block *cfg);
+
+/*
+ * moe_dropout — rows with elements dropped at random, and its own gradient:
+ *   y[i] = x[i] / (1 - q) where element i stays, 0 where it is dropped
+ * The probability is q = p rounded to a multiple of 2^-16, and exact: element i
+ * of the rows (flat index) is dropped where the 16-bit number i % 8 of block i / 8
+ * is below 65536 q.  Block j is Philox4x32-10 (Salmon et al., SC 2011) of the
+ * counter (j, stream) under the key seed; its four words are taken in order, low
+ * half first.  No mask is stored: the gradient of y, put through the same call,
+ * is that of x.
+ *   x, y        [rows][d] dtype; y may be x
+ *   n_rows      [1] int32 DEVICE value or NULL: rows at or beyond it (a
+ *               dispatch's offsets[N]) are neither read nor written
+ *   p           in [0, 1), at most 1 - 2^-16 after rounding
+ *   rng         [2] uint64 DEVICE array {seed, stream}, read when the call runs (a
+ *               captured graph draws anew when they change); NULL where q is 0
+ * rows * d < 2^42.
+ */
+int moe_dropout(int32_t dtype, int64_t rows, int64_t d, const void *x, void *y,
+                const int32_t *n_rows, double p, const uint64_t *rng, void *stream);
+
 /* Per-expert capacity the library applies for cfg (-1 = unlimited). */
 int64_t moe_capacity(const moe_config *cfg);
 

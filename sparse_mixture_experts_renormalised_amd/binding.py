@@ -30,7 +30,11 @@ EXPORTS = ("moe_route", "moe_permute", "moe_permute_workspace_size", "moe_groupe
            "moe_layer_forward_noalloc", "moe_workspace_size", "moe_workspace_layout",
            "moe_quantize_mxfp4", "moe_grouped_linear_mxfp4",
            "moe_grouped_linear_mxfp4_workspace_size", "moe_layer_forward_few",
-           "moe_layer_forward_few_mxfp4", "moe_few_workspace_size", "moe_capacity", "moe_status_string", "moe_version")
+           "moe_layer_forward_few_mxfp4", "moe_few_workspace_size", "moe_grouped_linear",
+           "moe_grouped_linear_input_grad", "moe_grouped_linear_weight_grad",
+           "moe_grouped_linear_workspace_size", "moe_block_join", "moe_block_join_grad",
+           "moe_block_join_grad_workspace_size", "moe_dropout", "moe_capacity",
+           "moe_status_string", "moe_version")
 STAGES = ("router", "topk", "dispatch", "up", "down", "combine")
 # moe_version() of the interface these ctypes declarations mirror (the structs
 # below must match the header's field for field)
@@ -72,6 +76,28 @@ class WeightsMxfp4(ctypes.Structure):
                  "ws1", "ws1_scales", "bs1", "ws2", "ws2_scales", "bs2")]
 
 
+class Block(ctypes.Structure):
+    """Mirror of moe_block."""
+    _fields_ = [("T", ctypes.c_int64), ("dropout_p", ctypes.c_double), ("d_model", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("res_dtype", ctypes.c_int32), ("norm_out", ctypes.c_int32),
+                ("norm_in", ctypes.c_int32), ("top_k", ctypes.c_int32), ("n_shared", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("scale", ctypes.c_float)]
+
+
+class BlockTensors(ctypes.Structure):
+    """Mirror of moe_block_tensors."""
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("residual", "branch", "y_rows", "slot_row", "topk_gate", "shared_out", "gate",
+                 "w_out", "b_out", "w_in", "b_in", "rng")]
+
+
+class BlockGrads(ctypes.Structure):
+    """Mirror of moe_block_grads."""
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("d_residual", "d_branch", "d_y_rows", "d_topk_gate", "d_gate", "d_w_out", "d_b_out",
+                 "d_w_in", "d_b_in")]
+
+
 _LIB = None
 
 
@@ -84,6 +110,7 @@ def lib():
                                "(run __graft_entry__.build())")
         L = ctypes.CDLL(LIB_PATH)
         P, I, Z, I64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int64
+        I32 = ctypes.c_int32
         C = ctypes.POINTER(Config)
         sig = {
             "moe_route": (I, [C, P, P, P, P, P, P, P]),
@@ -108,6 +135,17 @@ def lib():
             "moe_layer_forward_few_mxfp4": (I, [C, ctypes.POINTER(WeightsMxfp4), P, P, P, P, P, P,
                                                 Z, P]),
             "moe_few_workspace_size": (Z, [C]),
+            "moe_grouped_linear": (I, [I32, I32, I32, I32, I64, P, P, P, I64, P, P, I32, P, P, P, Z,
+                                       P]),
+            "moe_grouped_linear_input_grad": (I, [I32, I32, I32, I32, P, P, I64, P, P, P, P, Z, P]),
+            "moe_grouped_linear_weight_grad": (I, [I32, I32, I32, I32, I32, P, I64, P, P, P, I64, P,
+                                                   P, I32, P, Z, P]),
+            "moe_grouped_linear_workspace_size": (Z, [I32, I32, I32, I32, I64]),
+            "moe_block_join": (I, [ctypes.POINTER(Block), ctypes.POINTER(BlockTensors), P, P, P, P]),
+            "moe_block_join_grad": (I, [ctypes.POINTER(Block), ctypes.POINTER(BlockTensors), P, P, P,
+                                        ctypes.POINTER(BlockGrads), P, Z, P]),
+            "moe_block_join_grad_workspace_size": (Z, [ctypes.POINTER(Block)]),
+            "moe_dropout": (I, [I32, I64, I64, P, P, P, ctypes.c_double, P, P]),
             "moe_workspace_size": (Z, [C]),
             "moe_workspace_layout": (I, [C, ctypes.POINTER(WsLayout)]),
             "moe_capacity": (I64, [C]),
@@ -373,6 +411,205 @@ def layer_forward_few_mxfp4(cfg: Config, w: WeightsMxfp4, x, y, topk_idx=None, t
     """layer_forward_few on MXFP4 expert weights."""
     _layer_forward_few("moe_layer_forward_few_mxfp4", cfg, w, x, y, topk_idx, topk_gate, counts, ws,
                        stream)
+
+
+# --------------------------------------------------------------------------
+# Training the layer as a block
+# --------------------------------------------------------------------------
+_DTYPES = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
+_NAMES = {"f32": MOE_F32, "bf16": MOE_BF16, MOE_F32: MOE_F32, MOE_BF16: MOE_BF16}
+
+
+def _dtype(t, what: str) -> int:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{what} must be bf16 or f32")
+    return code
+
+
+def _fits(t, dtype, shape, what: str):
+    """None, or a tensor of that type and shape."""
+    if t is not None and (t.dtype is not dtype or t.shape != shape):
+        raise ValueError(f"{what} must be {list(shape)} {str(dtype)[6:]}")
+
+
+def grouped_linear_workspace_size(dtype, n_groups, n_out, k, max_rows) -> int:
+    """Workspace of grouped_linear and of its two gradients."""
+    return int(lib().moe_grouped_linear_workspace_size(_NAMES[dtype], int(n_groups), int(n_out), int(k),
+                                                       int(max_rows)))
+
+
+def _linear_sizes(w, offsets, what: str):
+    _need(w.dim() == 3, f"{what} must be [G, n_out, k]")
+    _need(offsets.dtype is torch.int32 and offsets.numel() == w.shape[0] + 1, "offsets must be [G + 1] int32")
+    return w.shape
+
+
+def _source_rows(x, row_index, k: int, max_rows: int) -> int:
+    _need(x.dim() == 2 and x.shape[1] == k, "x must be [., k]")
+    if row_index is None:
+        _need(x.shape[0] >= max_rows, "x has fewer rows than the groups may have (and no row_index)")
+    else:
+        _need(row_index.dtype is torch.int32 and row_index.numel() >= max_rows,
+              "row_index must be [max_rows] int32")
+    return x.shape[0]
+
+
+def _bytes(ws) -> int:
+    return 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def grouped_linear(x, offsets, w, y, row_index=None, bias=None, silu=False, pre=None, ws=None,
+                   stream=None):
+    """y [max_rows, n_out] of x rows [., k] and weights [G, n_out, k] (bf16 or
+    f32); with silu, pre keeps the values before it."""
+    _on_device(x, offsets, w, y, row_index, bias, pre, ws)
+    dt, act = _dtype(w, "w"), w.dtype
+    g, n_out, k = _linear_sizes(w, offsets, "w")
+    _need(y.dim() == 2, "y must be [max_rows, n_out]")
+    max_rows = y.shape[0]
+    _fits(y, act, (max_rows, n_out), "y")
+    _fits(pre, act, (max_rows, n_out), "pre")
+    _fits(bias, act, (g, n_out), "bias")
+    _need(x.dtype is act, "x must have the weights' type")
+    x_rows = _source_rows(x, row_index, k, max_rows)
+    _check("moe_grouped_linear", lib().moe_grouped_linear(
+        dt, g, n_out, k, x_rows, _ptr(x), _ptr(row_index), _ptr(offsets), max_rows, _ptr(w), _ptr(bias),
+        int(bool(silu)), _ptr(y), _ptr(pre), _ptr(ws), _bytes(ws), _stream(stream)))
+
+
+def grouped_linear_input_grad(dy, offsets, w, dx, pre=None, ws=None, stream=None):
+    """dx [max_rows, k] of dy [max_rows, n_out] and weights [G, n_out, k]; times
+    the SiLU's derivative at pre [max_rows, k], if given."""
+    _on_device(dy, offsets, w, dx, pre, ws)
+    dt, act = _dtype(w, "w"), w.dtype
+    g, n_out, k = _linear_sizes(w, offsets, "w")
+    _need(dx.dim() == 2, "dx must be [max_rows, k]")
+    max_rows = dx.shape[0]
+    _fits(dx, act, (max_rows, k), "dx")
+    _fits(pre, act, (max_rows, k), "pre")
+    _fits(dy, act, (max_rows, n_out), "dy")
+    _check("moe_grouped_linear_input_grad", lib().moe_grouped_linear_input_grad(
+        dt, g, n_out, k, _ptr(dy), _ptr(offsets), max_rows, _ptr(w), _ptr(pre), _ptr(dx), _ptr(ws),
+        _bytes(ws), _stream(stream)))
+
+
+def grouped_linear_weight_grad(dy, offsets, x, dw, row_index=None, dbias=None, accumulate=False, ws=None,
+                               stream=None):
+    """dw [G, n_out, k] and dbias [G, n_out] (the rows' type or f32) of dy
+    [max_rows, n_out] and x rows [., k]; added to what they hold, if asked."""
+    _on_device(dy, offsets, x, dw, row_index, dbias, ws)
+    dt, act = _dtype(dy, "dy"), dy.dtype
+    g, n_out, k = _linear_sizes(dw, offsets, "dw")
+    grad = _dtype(dw, "dw")
+    _need(dy.dim() == 2, "dy must be [max_rows, n_out]")
+    max_rows = dy.shape[0]
+    _fits(dy, act, (max_rows, n_out), "dy")
+    _fits(dbias, dw.dtype, (g, n_out), "dbias")
+    _need(x.dtype is act, "x must have dy's type")
+    x_rows = _source_rows(x, row_index, k, max_rows)
+    _check("moe_grouped_linear_weight_grad", lib().moe_grouped_linear_weight_grad(
+        dt, grad, g, n_out, k, _ptr(dy), x_rows, _ptr(x), _ptr(row_index), _ptr(offsets), max_rows,
+        _ptr(dw), _ptr(dbias), int(bool(accumulate)), _ptr(ws), _bytes(ws), _stream(stream)))
+
+
+MOE_NORM_NONE, MOE_NORM_RMS, MOE_NORM_LAYER = 0, 1, 2
+_NORMS = {"none": MOE_NORM_NONE, "rms": MOE_NORM_RMS, "layer": MOE_NORM_LAYER}
+
+
+def block(T, d_model, dtype, res_dtype=None, norm_out="none", norm_in="rms", eps=1e-6, scale=1.0,
+          dropout_p=0.0, top_k=0, n_shared=0) -> Block:
+    """Shape and constants of a block around the layer; the residual stream has
+    the branch's type unless res_dtype says otherwise."""
+    dt = _NAMES[dtype]
+    return Block(int(T), float(dropout_p), int(d_model), dt, dt if res_dtype is None else _NAMES[res_dtype],
+                 _NORMS[norm_out], _NORMS[norm_in], int(top_k), int(n_shared), float(eps), float(scale))
+
+
+_ACT = {MOE_BF16: torch.bfloat16, MOE_F32: torch.float32}
+
+
+def _block_tensors(cfg: Block, residual, branch, y_rows, slot_row, topk_gate, shared_out, gate, w_out, b_out,
+                   w_in, b_in, rng) -> BlockTensors:
+    _on_device(residual, branch, y_rows, slot_row, topk_gate, shared_out, gate, w_out, b_out, w_in, b_in, rng)
+    T, d, k, f32 = cfg.T, cfg.d_model, cfg.top_k, torch.float32
+    act = _ACT.get(cfg.dtype)
+    _fits(residual, _ACT.get(cfg.res_dtype), (T, d), "residual")
+    _fits(branch, act, (T, d), "branch")
+    if y_rows is not None:
+        _fits(y_rows, act, (y_rows.shape[0], d), "y_rows")
+    _fits(slot_row, torch.int32, (T, k), "slot_row")
+    _fits(topk_gate, f32, (T, k), "topk_gate")
+    _fits(shared_out, act, (cfg.n_shared, T, d), "shared_out")
+    _fits(gate, f32, (T,), "gate")
+    for name, t in (("w_out", w_out), ("b_out", b_out), ("w_in", w_in), ("b_in", b_in)):
+        _fits(t, f32, (d,), name)
+    _need(rng is None or (rng.dtype in (torch.int64, torch.uint64) and rng.numel() == 2),
+          "rng must be [2] int64 (seed, stream)")
+    return BlockTensors(*[_ptr(t) for t in (residual, branch, y_rows, slot_row, topk_gate, shared_out, gate,
+                                            w_out, b_out, w_in, b_in, rng)])
+
+
+def block_join(cfg: Block, residual, out=None, next=None, branch=None, y_rows=None, slot_row=None,
+               topk_gate=None, shared_out=None, branch_out=None, gate=None, w_out=None, b_out=None,
+               w_in=None, b_in=None, rng=None, stream=None):
+    """out = residual + scale gate Drop(Norm_out(branch or combined expert rows)),
+    next = Norm_in(out); branch_out keeps the combined rows."""
+    t = _block_tensors(cfg, residual, branch, y_rows, slot_row, topk_gate, shared_out, gate, w_out, b_out,
+                       w_in, b_in, rng)
+    _on_device(out, next, branch_out)
+    act, shape = _ACT.get(cfg.dtype), (cfg.T, cfg.d_model)
+    _fits(out, _ACT.get(cfg.res_dtype), shape, "out")
+    _fits(next, act, shape, "next")
+    _fits(branch_out, act, shape, "branch_out")
+    _check("moe_block_join", lib().moe_block_join(ctypes.byref(cfg), ctypes.byref(t), _ptr(out), _ptr(next),
+                                                  _ptr(branch_out), _stream(stream)))
+
+
+def block_join_grad_workspace_size(cfg: Block) -> int:
+    return int(lib().moe_block_join_grad_workspace_size(ctypes.byref(cfg)))
+
+
+def block_join_grad(cfg: Block, d_out, d_next, out, branch=None, y_rows=None, slot_row=None, topk_gate=None,
+                    gate=None, w_out=None, b_out=None, w_in=None, rng=None, d_residual=None, d_branch=None,
+                    d_y_rows=None, d_topk_gate=None, d_gate=None, d_w_out=None, d_b_out=None, d_w_in=None,
+                    d_b_in=None, ws=None, stream=None):
+    """Gradients of block_join's inputs (those given as outputs) from d_out and
+    d_next; out and branch as the forward left them."""
+    t = _block_tensors(cfg, None, branch, y_rows, slot_row, topk_gate, None, gate, w_out, b_out, w_in, None, rng)
+    _on_device(d_out, d_next, out, d_residual, d_branch, d_y_rows, d_topk_gate, d_gate, d_w_out, d_b_out, d_w_in,
+               d_b_in, ws)
+    act, res, f32, shape = _ACT.get(cfg.dtype), _ACT.get(cfg.res_dtype), torch.float32, (cfg.T, cfg.d_model)
+    for name, v, dt in (("d_out", d_out, res), ("out", out, res), ("d_residual", d_residual, res),
+                        ("d_next", d_next, act), ("d_branch", d_branch, act)):
+        _fits(v, dt, shape, name)
+    if d_y_rows is not None:
+        _need(y_rows is None or d_y_rows.shape == y_rows.shape, "d_y_rows must have y_rows' shape")
+        _fits(d_y_rows, act, (d_y_rows.shape[0], cfg.d_model), "d_y_rows")
+    _fits(d_topk_gate, f32, (cfg.T, cfg.top_k), "d_topk_gate")
+    _fits(d_gate, f32, (cfg.T,), "d_gate")
+    for name, v in (("d_w_out", d_w_out), ("d_b_out", d_b_out), ("d_w_in", d_w_in), ("d_b_in", d_b_in)):
+        _fits(v, f32, (cfg.d_model,), name)
+    g = BlockGrads(*[_ptr(v) for v in (d_residual, d_branch, d_y_rows, d_topk_gate, d_gate, d_w_out, d_b_out,
+                                       d_w_in, d_b_in)])
+    _check("moe_block_join_grad", lib().moe_block_join_grad(
+        ctypes.byref(cfg), ctypes.byref(t), _ptr(out), _ptr(d_out), _ptr(d_next), ctypes.byref(g), _ptr(ws),
+        _bytes(ws), _stream(stream)))
+
+
+def dropout(x, y, p, rng, n_rows=None, stream=None):
+    """y = x / (1 - p) or 0, by the numbers of rng [2] (seed, stream); rows at or
+    beyond n_rows [1] (int32, on the GPU) stay as they are.  y may be x."""
+    _on_device(x, y, rng, n_rows)
+    dt = _dtype(x, "x")
+    _need(x.dim() == 2, "x must be [rows, d]")
+    rows, d = x.shape
+    _fits(y, x.dtype, (rows, d), "y")
+    _need(rng is None or (rng.dtype in (torch.int64, torch.uint64) and rng.numel() == 2),
+          "rng must be [2] int64 (seed, stream)")
+    _need(n_rows is None or (n_rows.dtype is torch.int32 and n_rows.numel() == 1), "n_rows must be [1] int32")
+    _check("moe_dropout", lib().moe_dropout(dt, rows, d, _ptr(x), _ptr(y), _ptr(n_rows), float(p), _ptr(rng),
+                                            _stream(stream)))
 
 
 class HipEvents:

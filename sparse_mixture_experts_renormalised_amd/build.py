@@ -23,7 +23,8 @@ LIB = os.path.join(LIB_DIR, "libmoe_mi355x.so")
 ARCH = "gfx950"
 
 SOURCES = ["router.hip", "dispatch.hip", "fp8_dispatch.hip", "grouped_gemm.hip", "combine.hip",
-           "balance.hip", "mxfp4.hip", "few.hip", "moe_api.hip"]
+           "balance.hip", "mxfp4.hip", "few.hip", "linear.hip", "block.hip", "dropout.hip",
+           "moe_api.hip"]
 PER_FILE = {"router.hip": ["-ffp-contract=off"]}
 
 

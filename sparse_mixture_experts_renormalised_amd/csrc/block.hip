@@ -1,0 +1,526 @@
+// The layer as a residual block: the routed and shared expert rows combined,
+// normalised, dropped out, gated and added to the residual stream, and the
+// next block's normalised input, in one pass over the token's row; and the
+// gradients of all of it.
+//
+//   b = sum_i S_i[t] + sum_{k kept} g[t,k] Y[slot_row[t,k]]      (or a given row)
+//   n = Norm_out(b),  h = residual + scale gate[t] Drop(n),  next = Norm_in(h)
+//
+// with Norm(v) = v^ w + bias, v^ = v (none), v r (rms, r = (mean v^2 + eps)^-1/2)
+// or (v - m) r (layer).  Backward, for gradients G of h and N of next:
+//
+//   dh = G + r (N w - m2 - h^ m1),  m1 = mean(N w h^), m2 = mean(N w) (layer; rms: 0)
+//   u = scale gate Drop'(dh),  d_gate = scale sum Drop'(dh) n
+//   db = r (u w - m2' - b^ m1'),  dw = sum over tokens of u b^ and N h^
+//   dY[slot] = g db,  dg = <db, Y[slot]>
+//
+// A workgroup takes a token's whole row into registers (8 elements a thread and
+// chunk), so every tensor is read once and statistics cost a reduction instead
+// of a second read; sums and statistics are float32, variances are taken around
+// the mean.  Tokens are dealt to workgroups in a fixed way and the weights'
+// gradients are added in a fixed order: equal calls give equal bits.
+#include "block.h"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxPart = 4;   // weights whose gradients are summed: w_in, b_in, w_out, b_out
+
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, float (&v)[8]);
+template <>
+__device__ __forceinline__ void load8<float>(const float *p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+template <>
+__device__ __forceinline__ void load8<uint16_t>(const uint16_t *p, float (&v)[8]) {
+  const uint4 q = *reinterpret_cast<const uint4 *>(p);
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T *p, const float (&v)[8]);
+template <>
+__device__ __forceinline__ void store8<float>(float *p, const float (&v)[8]) {
+  reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+template <>
+__device__ __forceinline__ void store8<uint16_t>(uint16_t *p, const float (&v)[8]) {
+  *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                             pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
+// Sum of a wave's 64 values, in every lane.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float v) {
+  const int o = __builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xF, false);
+  return v + __int_as_float(o);
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = dpp_add<0xB1, 0xF>(v);     // quad_perm [1,0,3,2]
+  v = dpp_add<0x4E, 0xF>(v);     // quad_perm [2,3,0,1]
+  v = dpp_add<0x141, 0xF>(v);    // row_half_mirror: the other four of eight
+  v = dpp_add<0x140, 0xF>(v);    // row_mirror: the other eight of sixteen
+  v = dpp_add<0x142, 0xA>(v);    // row_bcast15 into rows 1 and 3
+  v = dpp_add<0x143, 0xC>(v);    // row_bcast31 into rows 2 and 3
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+// Sums of N values over the NW waves of a workgroup.  Two buffers in turn: a
+// wave that writes one again has passed the other's barrier, which every wave
+// reaches after it read the first.
+template <int NW, int N>
+struct Sums {
+  float buf[2][N][NW];
+};
+template <int NW, int N, int M>
+__device__ __forceinline__ void block_sum(Sums<NW, N> &s, int &turn, float (&v)[M]) {
+  static_assert(M <= N, "buffer too small");
+#pragma unroll
+  for (int i = 0; i < M; ++i) v[i] = wave_sum(v[i]);
+  if constexpr (NW > 1) {
+    if ((threadIdx.x & 63) == 0)
+#pragma unroll
+      for (int i = 0; i < M; ++i) s.buf[turn][i][threadIdx.x >> 6] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      v[i] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) v[i] += s.buf[turn][i][w];
+    }
+    turn ^= 1;
+  }
+}
+
+// Normalises v in place; returns r.  Chunks behind the row's end hold zeros.
+template <int NW, int CH, int N>
+__device__ __forceinline__ float normalise(float (&v)[CH][8], int kind, float eps, float inv_d, int nvec,
+                                           Sums<NW, N> &s, int &turn) {
+  if (kind == kNormNone) return 1.0f;
+  if (kind == kNormLayer) {
+    float m[1] = {0.0f};
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m[0] += v[c][j];
+    block_sum(s, turn, m);
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      if (static_cast<int>(threadIdx.x) + c * NW * 64 < nvec)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[c][j] -= m[0] * inv_d;
+  }
+  float q[1] = {0.0f};
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[0] += v[c][j] * v[c][j];
+  block_sum(s, turn, q);
+  const float r = 1.0f / sqrtf(q[0] * inv_d + eps);
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[c][j] *= r;
+  return r;
+}
+
+// Eight weights (ones or zeros where there are none).
+__device__ __forceinline__ void load_w(const float *w, int at, float none, float (&v)[8]) {
+  if (w) {
+    load8(w + at, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = none;
+  }
+}
+
+template <typename A, typename R, int NW, int CH>
+__global__ __launch_bounds__(NW * 64) void block_join_kernel(BlockJoin a) {
+  __shared__ Sums<NW, 1> s_sum;
+  int turn = 0;
+  const int tid = threadIdx.x, nvec = a.d / 8;
+  const float inv_d = 1.0f / static_cast<float>(a.d);
+  const DropKey key = drop_key(a.drop);
+  const A *y_rows = static_cast<const A *>(a.y_rows), *shared = static_cast<const A *>(a.shared_out);
+  const bool has_branch = a.branch || a.y_rows;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const int64_t row = t * a.d;
+    float h[CH][8], b[CH][8];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int vec = tid + c * NW * 64;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[c][j] = b[c][j] = 0.0f;
+      if (vec < nvec) {
+        load8(static_cast<const R *>(a.residual) + row + vec * 8, h[c]);
+        if (a.branch) load8(static_cast<const A *>(a.branch) + row + vec * 8, b[c]);
+      }
+    }
+    if (a.y_rows) {
+      // shared experts first, then slots in order, as moe_combine adds them
+      for (int i = 0; i < a.n_shared; ++i)
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          const int vec = tid + c * NW * 64;
+          if (vec < nvec) {
+            float v[8];
+            load8(shared + (i * a.T + t) * a.d + vec * 8, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) b[c][j] += v[j];
+          }
+        }
+      for (int k = 0; k < a.K; ++k) {
+        const int64_t r = a.slot_row[t * a.K + k];
+        if (r < 0) continue;
+        const float g = a.topk_gate[t * a.K + k];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          const int vec = tid + c * NW * 64;
+          if (vec < nvec) {
+            float v[8];
+            load8(y_rows + r * a.d + vec * 8, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) b[c][j] += g * v[j];
+          }
+        }
+      }
+    }
+    if (has_branch) {
+      if (a.branch_out)
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          const int vec = tid + c * NW * 64;
+          if (vec < nvec) store8(static_cast<A *>(a.branch_out) + row + vec * 8, b[c]);
+        }
+      normalise<NW, CH>(b, a.norm_out, a.eps, inv_d, nvec, s_sum, turn);
+      const float f = a.gate ? a.scale * a.gate[t] : a.scale;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int vec = tid + c * NW * 64;
+        if (vec >= nvec) continue;
+        float w[8], o[8];
+        load_w(a.w_out, vec * 8, 1.0f, w);
+        load_w(a.b_out, vec * 8, 0.0f, o);
+        const uint4 q = a.drop.cut ? philox_block(key, static_cast<uint64_t>(t) * nvec + vec)
+                                   : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float n = b[c][j] * w[j] + o[j];
+          h[c][j] += half_of(q, j) >= a.drop.cut ? f * a.drop.keep * n : 0.0f;
+        }
+      }
+    }
+    if (a.out)
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int vec = tid + c * NW * 64;
+        if (vec < nvec) store8(static_cast<R *>(a.out) + row + vec * 8, h[c]);
+      }
+    if (!a.next) continue;
+    normalise<NW, CH>(h, a.norm_in, a.eps, inv_d, nvec, s_sum, turn);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int vec = tid + c * NW * 64;
+      if (vec >= nvec) continue;
+      float w[8], o[8];
+      load_w(a.w_in, vec * 8, 1.0f, w);
+      load_w(a.b_in, vec * 8, 0.0f, o);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] += h[c][j] * w[j];
+      store8(static_cast<A *>(a.next) + row + vec * 8, o);
+    }
+  }
+}
+
+// Gradient of the rows before a norm, in place of that of the normalised ones
+// (already times the weights); hat and r as the norm left them.
+template <int NW, int CH, int N>
+__device__ __forceinline__ void norm_grad(float (&g)[CH][8], const float (&hat)[CH][8], float r, int kind,
+                                          float inv_d, Sums<NW, N> &s, int &turn) {
+  if (kind == kNormNone) return;
+  float m[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      m[0] += g[c][j] * hat[c][j];
+      m[1] += g[c][j];
+    }
+  block_sum(s, turn, m);
+  const float m1 = m[0] * inv_d, m2 = kind == kNormLayer ? m[1] * inv_d : 0.0f;
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) g[c][j] = r * (g[c][j] - m2 - hat[c][j] * m1);
+}
+
+constexpr int kSlots = 4;   // slots whose products are summed in one exchange
+
+template <typename A, typename R, int NW, int CH, bool BIAS>
+__global__ __launch_bounds__(NW * 64) void block_join_grad_kernel(BlockJoinGrad a) {
+  __shared__ Sums<NW, kSlots> s_sum;
+  int turn = 0;
+  const int tid = threadIdx.x, nvec = a.d / 8;
+  const float inv_d = 1.0f / static_cast<float>(a.d);
+  const DropKey key = drop_key(a.drop);
+  float swi[CH][8], swo[CH][8], sbi[BIAS ? CH : 1][8], sbo[BIAS ? CH : 1][8];
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      swi[c][j] = swo[c][j] = 0.0f;
+      if (BIAS) sbi[c][j] = sbo[c][j] = 0.0f;
+    }
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const int64_t row = t * a.d;
+    float dh[CH][8], hat[CH][8];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int vec = tid + c * NW * 64;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) dh[c][j] = hat[c][j] = 0.0f;
+      if (a.d_next && vec < nvec) {
+        load8(static_cast<const A *>(a.d_next) + row + vec * 8, dh[c]);
+        load8(static_cast<const R *>(a.h) + row + vec * 8, hat[c]);
+      }
+    }
+    if (a.d_next) {
+      const float r = normalise<NW, CH>(hat, a.norm_in, a.eps, inv_d, nvec, s_sum, turn);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int vec = tid + c * NW * 64;
+        if (vec >= nvec) continue;
+        float w[8];
+        load_w(a.w_in, vec * 8, 1.0f, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          swi[c][j] += dh[c][j] * hat[c][j];
+          if (BIAS) sbi[c][j] += dh[c][j];
+          dh[c][j] *= w[j];
+        }
+      }
+      norm_grad<NW, CH>(dh, hat, r, a.norm_in, inv_d, s_sum, turn);
+    }
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int vec = tid + c * NW * 64;
+      if (vec >= nvec) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dh[c][j] = 0.0f;
+        continue;
+      }
+      if (a.d_out) {
+        float v[8];
+        load8(static_cast<const R *>(a.d_out) + row + vec * 8, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dh[c][j] += v[j];
+      }
+      if (a.d_residual) store8(static_cast<R *>(a.d_residual) + row + vec * 8, dh[c]);
+    }
+    if (!a.branch) continue;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int vec = tid + c * NW * 64;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) hat[c][j] = 0.0f;
+      if (vec < nvec) load8(static_cast<const A *>(a.branch) + row + vec * 8, hat[c]);
+    }
+    const float r = normalise<NW, CH>(hat, a.norm_out, a.eps, inv_d, nvec, s_sum, turn);
+    const float f = a.gate ? a.scale * a.gate[t] : a.scale;
+    float dg[1] = {0.0f};
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int vec = tid + c * NW * 64;
+      if (vec >= nvec) continue;
+      float w[8], o[8];
+      load_w(a.w_out, vec * 8, 1.0f, w);
+      load_w(a.d_gate ? a.b_out : nullptr, vec * 8, 0.0f, o);
+      const uint4 q = a.drop.cut ? philox_block(key, static_cast<uint64_t>(t) * nvec + vec)
+                                 : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float u = half_of(q, j) >= a.drop.cut ? dh[c][j] * a.drop.keep : 0.0f;
+        dg[0] += u * (hat[c][j] * w[j] + o[j]);
+        const float g = f * u;
+        swo[c][j] += g * hat[c][j];
+        if (BIAS) sbo[c][j] += g;
+        dh[c][j] = g * w[j];
+      }
+    }
+    if (a.d_gate) {
+      block_sum(s_sum, turn, dg);
+      if (tid == 0) a.d_gate[t] = a.scale * dg[0];
+    }
+    if (!a.d_branch && !a.d_y_rows && !a.d_topk_gate) continue;
+    norm_grad<NW, CH>(dh, hat, r, a.norm_out, inv_d, s_sum, turn);
+    if (a.d_branch)
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int vec = tid + c * NW * 64;
+        if (vec < nvec) store8(static_cast<A *>(a.d_branch) + row + vec * 8, dh[c]);
+      }
+    if (!a.d_y_rows && !a.d_topk_gate) continue;
+    for (int k0 = 0; k0 < a.K; k0 += kSlots) {
+      float dot[kSlots];
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i) {
+        dot[i] = 0.0f;
+        const int k = k0 + i;
+        const int64_t sr = k < a.K ? a.slot_row[t * a.K + k] : -1;
+        if (sr < 0) continue;
+        const float g = a.topk_gate[t * a.K + k];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          const int vec = tid + c * NW * 64;
+          if (vec >= nvec) continue;
+          float v[8];
+          if (a.d_topk_gate) {
+            load8(static_cast<const A *>(a.y_rows) + sr * a.d + vec * 8, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dot[i] += dh[c][j] * v[j];
+          }
+          if (a.d_y_rows) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = g * dh[c][j];
+            store8(static_cast<A *>(a.d_y_rows) + sr * a.d + vec * 8, v);
+          }
+        }
+      }
+      if (a.d_topk_gate) {
+        block_sum(s_sum, turn, dot);
+        if (tid < kSlots && k0 + tid < a.K)
+          a.d_topk_gate[t * a.K + k0 + tid] = tid == 0 ? dot[0] : tid == 1 ? dot[1] : tid == 2 ? dot[2] : dot[3];
+      }
+    }
+  }
+  // this workgroup's part of the weights' gradients: part[which][workgroup][d]
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int vec = tid + c * NW * 64;
+    if (vec >= nvec) continue;
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * a.d + vec * 8, step = static_cast<int64_t>(gridDim.x) * a.d;
+    if (a.sum[0]) store8(a.part + at, swi[c]);
+    if (BIAS && a.sum[1]) store8(a.part + step + at, sbi[BIAS ? c : 0]);
+    if (a.sum[2]) store8(a.part + 2 * step + at, swo[c]);
+    if (BIAS && a.sum[3]) store8(a.part + 3 * step + at, sbo[BIAS ? c : 0]);
+  }
+}
+
+// Sums of the workgroups' parts: 64 columns a workgroup, 16 ranges of parts,
+// added in order.
+__global__ __launch_bounds__(1024) void block_sum_parts_kernel(const float *part, int parts, int d,
+                                                               float *o0, float *o1, float *o2, float *o3) {
+  float *out = blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : blockIdx.y == 2 ? o2 : o3;
+  if (!out) return;
+  __shared__ float s[16][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, col = blockIdx.x * 64 + lane;
+  float v = 0.0f;
+  if (col < d) {
+    const float *p = part + (static_cast<int64_t>(blockIdx.y) * parts) * d + col;
+    const int per = (parts + 15) / 16, end = min(parts, (w + 1) * per);
+#pragma unroll 8
+    for (int i = w * per; i < end; ++i) v += p[static_cast<int64_t>(i) * d];
+  }
+  s[w][lane] = v;
+  __syncthreads();
+  if (w == 0 && col < d) {
+    v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v += s[i][lane];
+    out[col] = v;
+  }
+}
+
+// Shape of a workgroup for rows of nvec chunks of 8 elements: one wave up to
+// 64 chunks, else four waves of up to 8 chunks a thread.
+struct Shape {
+  int nw, ch;
+};
+Shape shape_of(int nvec) {
+  if (nvec <= 64) return {1, 1};
+  if (nvec <= 256) return {4, 1};
+  if (nvec <= 512) return {4, 2};
+  if (nvec <= 1024) return {4, 4};
+  return {4, 8};
+}
+
+unsigned grad_grid(int64_t T, int d) {
+  const Shape s = shape_of(d / 8);
+  const int64_t most = s.nw == 1 ? 2048 : 512, want = (T + 3) / 4;
+  return static_cast<unsigned>(want < most ? want : most);
+}
+
+template <typename A, typename R, int NW, int CH>
+void launch_join(const BlockJoin &a, hipStream_t s) {
+  const int64_t most = NW == 1 ? 8192 : 2048;
+  const dim3 grid(static_cast<unsigned>(a.T < most ? a.T : most));
+  hipLaunchKernelGGL((block_join_kernel<A, R, NW, CH>), grid, dim3(NW * 64), 0, s, a);
+}
+
+template <typename A, typename R, int NW, int CH>
+void launch_grad(const BlockJoinGrad &a, hipStream_t s) {
+  const dim3 grid(grad_grid(a.T, a.d));
+  if (a.sum[1] || a.sum[3])
+    hipLaunchKernelGGL((block_join_grad_kernel<A, R, NW, CH, true>), grid, dim3(NW * 64), 0, s, a);
+  else
+    hipLaunchKernelGGL((block_join_grad_kernel<A, R, NW, CH, false>), grid, dim3(NW * 64), 0, s, a);
+}
+
+template <typename A, typename R, typename Args>
+void dispatch_shape(const Args &a, hipStream_t s) {
+  const Shape sh = shape_of(a.d / 8);
+  auto go = [&](auto nw, auto ch) {
+    if constexpr (std::is_same_v<Args, BlockJoin>)
+      launch_join<A, R, nw(), ch()>(a, s);
+    else
+      launch_grad<A, R, nw(), ch()>(a, s);
+  };
+  using std::integral_constant;
+  if (sh.nw == 1) go(integral_constant<int, 1>{}, integral_constant<int, 1>{});
+  else if (sh.ch == 1) go(integral_constant<int, 4>{}, integral_constant<int, 1>{});
+  else if (sh.ch == 2) go(integral_constant<int, 4>{}, integral_constant<int, 2>{});
+  else if (sh.ch == 4) go(integral_constant<int, 4>{}, integral_constant<int, 4>{});
+  else go(integral_constant<int, 4>{}, integral_constant<int, 8>{});
+}
+
+template <typename Args>
+void dispatch_types(const Args &a, hipStream_t s) {
+  if (!a.act_bf16) dispatch_shape<float, float>(a, s);
+  else if (a.res_bf16) dispatch_shape<uint16_t, uint16_t>(a, s);
+  else dispatch_shape<uint16_t, float>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_block_join(const BlockJoin &a, hipStream_t s) {
+  dispatch_types(a, s);
+  return hipGetLastError();
+}
+
+size_t block_join_grad_workspace_bytes(int64_t T, int d) {
+  return sizeof(float) * kMaxPart * grad_grid(T, d) * d;
+}
+
+hipError_t launch_block_join_grad(const BlockJoinGrad &a, hipStream_t s) {
+  if (a.T > 0) {
+    dispatch_types(a, s);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (a.sum[0] || a.sum[1] || a.sum[2] || a.sum[3]) {
+    hipLaunchKernelGGL(block_sum_parts_kernel, dim3((a.d + 63) / 64, 4), dim3(1024), 0, s, a.part,
+                       a.T > 0 ? static_cast<int>(grad_grid(a.T, a.d)) : 0, a.d, a.sum[0], a.sum[1], a.sum[2],
+                       a.sum[3]);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace moe

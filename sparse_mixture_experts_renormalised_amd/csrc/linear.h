@@ -1,0 +1,44 @@
+// Launchers of the single Linears of every expert and of their gradients
+// (linear.hip, linear_grad.hip).  Not part of the public interface.
+#pragma once
+
+#include "moe_common.h"
+
+namespace moe {
+
+// Three products of the rows offsets[g] .. offsets[g+1]-1 of every group:
+//   kLinForward     y[r]    = act(x[index[r]] W_g^T + bias_g)
+//   kLinInputGrad   dx[r]   = (dy[r] W_g) silu'(pre[r])
+//   kLinWeightGrad  dW_g (+)= sum_r dy[r]^T x[index[r]],  dbias_g (+)= sum_r dy[r]
+enum LinearMode { kLinForward, kLinInputGrad, kLinWeightGrad };
+
+struct Linear {
+  LinearMode mode;
+  bool bf16;                    // type of rows and weights
+  bool out_bf16;                // type of dw and dbias
+  const int32_t *offsets;       // [groups + 1], device
+  int groups, n_out, k;
+  int64_t max_rows;             // host upper bound on offsets[groups]
+  int64_t x_rows;               // rows of x
+  const void *x;                // forward, weight gradient: [x_rows][k]
+  const int32_t *index;         // row r reads x[index[r]] (null: r)
+  const void *dy;               // gradients: [max_rows][n_out]
+  const void *w;                // [groups][n_out][k]
+  const void *bias;             // [groups][n_out] or null
+  bool silu;
+  void *pre;                    // forward: values before the SiLU, or null
+  const void *act_pre;          // input gradient: values before the SiLU that made x, or null
+  void *out;                    // y, dx or dw
+  void *dbias;                  // [groups][n_out] or null
+  bool accumulate;              // add to dw and dbias
+};
+
+hipError_t launch_linear_f32(const Linear &p, hipStream_t s);
+
+// Derivative of z sigmoid(z).
+__device__ __forceinline__ float silu_slope(float z) {
+  const float s = 1.0f / (1.0f + __expf(-z));
+  return s * (1.0f + z * (1.0f - s));
+}
+
+}  // namespace moe

@@ -7,6 +7,8 @@
 #include <initializer_list>
 #include <mutex>
 
+#include "block.h"
+#include "linear.h"
 #include "moe_common.h"
 #include "moe_mi355x.h"
 
@@ -589,6 +591,268 @@ int moe_layer_forward_few_mxfp4(const moe_config *cfg, const moe_weights_mxfp4 *
   p.cs2 = w->ws2_scales;
   p.bs2 = w->bs2;
   return run_few(cfg, p, x, y, topk_idx, topk_gate, counts, ws, ws_bytes, stream);
+}
+
+// Sizes of the single Linears.
+static int check_linear(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k, int64_t max_rows) {
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (n_groups <= 0 || n_out <= 0 || k <= 0 || max_rows < 0) return MOE_ERR_INVALID_ARG;
+  const int mult = dtype == MOE_BF16 ? 64 : 16;
+  if (n_groups > moe::kMaxRouted + moe::kMaxShared) return MOE_ERR_UNSUPPORTED;
+  if (n_out % mult != 0 || k % mult != 0 || max_rows >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+size_t moe_grouped_linear_workspace_size(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k,
+                                         int64_t max_rows) {
+  if (check_linear(dtype, n_groups, n_out, k, max_rows) != MOE_OK) return 0;
+  return 0;
+}
+
+static moe::Linear linear_of(moe::LinearMode mode, int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k,
+                             const int32_t *offsets, int64_t max_rows) {
+  moe::Linear p{};
+  p.mode = mode;
+  p.bf16 = p.out_bf16 = dtype == MOE_BF16;
+  p.offsets = offsets;
+  p.groups = n_groups;
+  p.n_out = n_out;
+  p.k = k;
+  p.max_rows = max_rows;
+  return p;
+}
+
+int moe_grouped_linear(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k, int64_t x_rows,
+                       const void *x, const int32_t *row_index, const int32_t *offsets,
+                       int64_t max_rows, const void *w, const void *bias, int32_t silu, void *y,
+                       void *pre, void *ws, size_t ws_bytes, void *stream) {
+  const int st = check_linear(dtype, n_groups, n_out, k, max_rows);
+  if (st != MOE_OK) return st;
+  if (x_rows < 0 || (silu != 0 && silu != 1) || (pre && !silu)) return MOE_ERR_INVALID_ARG;
+  if (max_rows == 0) return MOE_OK;
+  if (x_rows < (row_index ? 1 : max_rows)) return MOE_ERR_INVALID_ARG;
+  if (!x || !offsets || !w || !y) return MOE_ERR_INVALID_ARG;
+  if (!all_aligned16({x, row_index, offsets, w, bias, y, pre, ws})) return MOE_ERR_INVALID_ARG;
+  const size_t need = moe_grouped_linear_workspace_size(dtype, n_groups, n_out, k, max_rows);
+  if (need && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  moe::Linear p = linear_of(moe::kLinForward, dtype, n_groups, n_out, k, offsets, max_rows);
+  p.x_rows = x_rows;
+  p.x = x;
+  p.index = row_index;
+  p.w = w;
+  p.bias = bias;
+  p.silu = silu != 0;
+  p.out = y;
+  p.pre = pre;
+  return hip_status(moe::launch_linear_f32(p, static_cast<hipStream_t>(stream)));
+}
+
+int moe_grouped_linear_input_grad(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k,
+                                  const void *dy, const int32_t *offsets, int64_t max_rows,
+                                  const void *w, const void *pre, void *dx, void *ws,
+                                  size_t ws_bytes, void *stream) {
+  const int st = check_linear(dtype, n_groups, n_out, k, max_rows);
+  if (st != MOE_OK) return st;
+  if (max_rows == 0) return MOE_OK;
+  if (!dy || !offsets || !w || !dx) return MOE_ERR_INVALID_ARG;
+  if (!all_aligned16({dy, offsets, w, pre, dx, ws})) return MOE_ERR_INVALID_ARG;
+  const size_t need = moe_grouped_linear_workspace_size(dtype, n_groups, n_out, k, max_rows);
+  if (need && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  moe::Linear p = linear_of(moe::kLinInputGrad, dtype, n_groups, n_out, k, offsets, max_rows);
+  p.dy = dy;
+  p.w = w;
+  p.act_pre = pre;
+  p.out = dx;
+  return hip_status(moe::launch_linear_f32(p, static_cast<hipStream_t>(stream)));
+}
+
+int moe_grouped_linear_weight_grad(int32_t dtype, int32_t grad_dtype, int32_t n_groups,
+                                   int32_t n_out, int32_t k, const void *dy, int64_t x_rows,
+                                   const void *x, const int32_t *row_index,
+                                   const int32_t *offsets, int64_t max_rows, void *dw,
+                                   void *dbias, int32_t accumulate, void *ws, size_t ws_bytes,
+                                   void *stream) {
+  const int st = check_linear(dtype, n_groups, n_out, k, max_rows);
+  if (st != MOE_OK) return st;
+  if (grad_dtype != MOE_F32 && grad_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (grad_dtype == MOE_BF16 && dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (x_rows < 0 || (accumulate != 0 && accumulate != 1)) return MOE_ERR_INVALID_ARG;
+  if (max_rows == 0 && accumulate) return MOE_OK;
+  if (max_rows > 0 && x_rows < (row_index ? 1 : max_rows)) return MOE_ERR_INVALID_ARG;
+  if (!offsets || !dw || (max_rows > 0 && (!dy || !x))) return MOE_ERR_INVALID_ARG;
+  if (!all_aligned16({dy, x, row_index, offsets, dw, dbias, ws})) return MOE_ERR_INVALID_ARG;
+  const size_t need = moe_grouped_linear_workspace_size(dtype, n_groups, n_out, k, max_rows);
+  if (need && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  moe::Linear p = linear_of(moe::kLinWeightGrad, dtype, n_groups, n_out, k, offsets, max_rows);
+  p.out_bf16 = grad_dtype == MOE_BF16;
+  p.dy = dy;
+  p.x_rows = x_rows;
+  p.x = x;
+  p.index = row_index;
+  p.out = dw;
+  p.dbias = dbias;
+  p.accumulate = accumulate != 0;
+  return hip_status(moe::launch_linear_f32(p, static_cast<hipStream_t>(stream)));
+}
+
+// The probability in steps of 2^-16 (ties to even), or -1 outside [0, 1).
+static int64_t dropout_cut(double p) {
+  if (!(p >= 0.0 && p < 1.0)) return -1;
+  const double cut = nearbyint(p * 65536.0);
+  return cut <= 65535.0 ? static_cast<int64_t>(cut) : -1;
+}
+static moe::Dropout dropout_of(int64_t cut, const uint64_t *rng) {
+  moe::Dropout d;
+  d.rng = cut ? rng : nullptr;
+  d.cut = static_cast<uint32_t>(cut);
+  d.keep = 65536.0f / static_cast<float>(65536 - cut);
+  return d;
+}
+
+static int check_block(const moe_block *c) {
+  if (!c) return MOE_ERR_INVALID_ARG;
+  if (c->T < 0 || c->d_model <= 0) return MOE_ERR_INVALID_ARG;
+  if (c->dtype != MOE_F32 && c->dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (c->res_dtype != MOE_F32 && c->res_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  const int32_t kinds[2] = {c->norm_out, c->norm_in};
+  for (int32_t kind : kinds)
+    if (kind != MOE_NORM_NONE && kind != MOE_NORM_RMS && kind != MOE_NORM_LAYER) return MOE_ERR_INVALID_ARG;
+  if ((c->norm_out || c->norm_in) && !(c->eps > 0.0f && c->eps < HUGE_VALF)) return MOE_ERR_INVALID_ARG;
+  if (dropout_cut(c->dropout_p) < 0) return MOE_ERR_INVALID_ARG;
+  if (c->dtype == MOE_F32 && c->res_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
+  if (c->d_model % 8 != 0 || c->d_model > moe::kMaxBlockWidth) return MOE_ERR_UNSUPPORTED;
+  if (c->T > ((int64_t(1) << 42) - 1) / c->d_model) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// Sizes and arrays of the expert rows.
+static int check_slots(const moe_block *c, const moe_block_tensors *in) {
+  if (c->top_k <= 0 || c->n_shared < 0 || !in->slot_row || !in->topk_gate) return MOE_ERR_INVALID_ARG;
+  if (c->top_k > 64 || c->n_shared > moe::kMaxShared) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+static bool block_aligned(const moe_block_tensors *in) {
+  return all_aligned16({in->residual, in->branch, in->y_rows, in->slot_row, in->topk_gate, in->shared_out, in->gate,
+                        in->w_out, in->b_out, in->w_in, in->b_in, in->rng});
+}
+
+int moe_block_join(const moe_block *cfg, const moe_block_tensors *in, void *out, void *next,
+                   void *branch_out, void *stream) {
+  int st = check_block(cfg);
+  if (st != MOE_OK) return st;
+  if (!in) return MOE_ERR_INVALID_ARG;
+  if (in->y_rows && (st = check_slots(cfg, in)) != MOE_OK) return st;
+  if (cfg->T == 0) return MOE_OK;
+  if (!in->residual || (!out && !next && !branch_out) || (in->branch && in->y_rows)) return MOE_ERR_INVALID_ARG;
+  if (in->y_rows && cfg->n_shared > 0 && !in->shared_out) return MOE_ERR_INVALID_ARG;
+  const int64_t cut = in->branch || in->y_rows ? dropout_cut(cfg->dropout_p) : 0;
+  if (cut > 0 && !in->rng) return MOE_ERR_INVALID_ARG;
+  if (!block_aligned(in) || !all_aligned16({out, next, branch_out})) return MOE_ERR_INVALID_ARG;
+  moe::BlockJoin p{};
+  p.act_bf16 = cfg->dtype == MOE_BF16;
+  p.res_bf16 = cfg->res_dtype == MOE_BF16;
+  p.T = cfg->T;
+  p.d = cfg->d_model;
+  p.K = cfg->top_k;
+  p.n_shared = in->shared_out ? cfg->n_shared : 0;
+  p.norm_out = cfg->norm_out;
+  p.norm_in = cfg->norm_in;
+  p.eps = cfg->eps;
+  p.scale = cfg->scale;
+  p.drop = dropout_of(cut, in->rng);
+  p.residual = in->residual;
+  p.branch = in->branch;
+  p.y_rows = in->y_rows;
+  p.slot_row = in->slot_row;
+  p.topk_gate = in->topk_gate;
+  p.shared_out = in->shared_out;
+  p.gate = in->gate;
+  p.w_out = in->w_out;
+  p.b_out = in->b_out;
+  p.w_in = in->w_in;
+  p.b_in = in->b_in;
+  p.out = out;
+  p.next = next;
+  p.branch_out = in->y_rows ? branch_out : nullptr;
+  return hip_status(moe::launch_block_join(p, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_block_join_grad_workspace_size(const moe_block *cfg) {
+  if (check_block(cfg) != MOE_OK) return 0;
+  return moe::block_join_grad_workspace_bytes(cfg->T, cfg->d_model);
+}
+
+int moe_block_join_grad(const moe_block *cfg, const moe_block_tensors *in, const void *out,
+                        const void *d_out, const void *d_next, const moe_block_grads *grads,
+                        void *ws, size_t ws_bytes, void *stream) {
+  int st = check_block(cfg);
+  if (st != MOE_OK) return st;
+  if (!in || !grads) return MOE_ERR_INVALID_ARG;
+  const moe_block_grads &g = *grads;
+  const bool slots = g.d_y_rows || g.d_topk_gate;
+  if (slots && (st = check_slots(cfg, in)) != MOE_OK) return st;
+  const bool sums = g.d_w_in || g.d_b_in || g.d_w_out || g.d_b_out;
+  if (cfg->T == 0 && !sums) return MOE_OK;
+  int64_t cut = 0;
+  if (cfg->T > 0) {
+    if (d_next && !out) return MOE_ERR_INVALID_ARG;
+    if (g.d_topk_gate && !in->y_rows) return MOE_ERR_INVALID_ARG;
+    if (!in->branch && (g.d_branch || slots || g.d_gate)) return MOE_ERR_INVALID_ARG;
+    if (in->branch) cut = dropout_cut(cfg->dropout_p);
+    if (cut > 0 && !in->rng) return MOE_ERR_INVALID_ARG;
+  }
+  if (!block_aligned(in) || !all_aligned16({out, d_out, d_next, g.d_residual, g.d_branch, g.d_y_rows, g.d_topk_gate,
+                                            g.d_gate, g.d_w_out, g.d_b_out, g.d_w_in, g.d_b_in, ws}))
+    return MOE_ERR_INVALID_ARG;
+  if (cfg->T > 0 && sums && (!ws || ws_bytes < moe_block_join_grad_workspace_size(cfg))) return MOE_ERR_WORKSPACE;
+  moe::BlockJoinGrad p{};
+  p.act_bf16 = cfg->dtype == MOE_BF16;
+  p.res_bf16 = cfg->res_dtype == MOE_BF16;
+  p.T = cfg->T;
+  p.d = cfg->d_model;
+  p.K = cfg->top_k;
+  p.norm_out = cfg->norm_out;
+  p.norm_in = cfg->norm_in;
+  p.eps = cfg->eps;
+  p.scale = cfg->scale;
+  p.drop = dropout_of(cut, in->rng);
+  p.d_out = d_out;
+  p.d_next = d_next;
+  p.h = out;
+  p.branch = in->branch;
+  p.y_rows = in->y_rows;
+  p.slot_row = in->slot_row;
+  p.topk_gate = in->topk_gate;
+  p.gate = in->gate;
+  p.w_out = in->w_out;
+  p.b_out = in->b_out;
+  p.w_in = in->w_in;
+  p.d_residual = g.d_residual;
+  p.d_branch = g.d_branch;
+  p.d_y_rows = g.d_y_rows;
+  p.d_gate = g.d_gate;
+  p.d_topk_gate = g.d_topk_gate;
+  p.sum[0] = g.d_w_in;
+  p.sum[1] = g.d_b_in;
+  p.sum[2] = g.d_w_out;
+  p.sum[3] = g.d_b_out;
+  p.part = static_cast<float *>(ws);
+  return hip_status(moe::launch_block_join_grad(p, static_cast<hipStream_t>(stream)));
+}
+
+int moe_dropout(int32_t dtype, int64_t rows, int64_t d, const void *x, void *y,
+                const int32_t *n_rows, double p, const uint64_t *rng, void *stream) {
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (rows < 0 || d <= 0) return MOE_ERR_INVALID_ARG;
+  const int64_t cut = dropout_cut(p);
+  if (cut < 0) return MOE_ERR_INVALID_ARG;
+  if (rows > ((int64_t(1) << 42) - 1) / d) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!x || !y || (cut > 0 && !rng)) return MOE_ERR_INVALID_ARG;
+  if (!all_aligned16({x, y, n_rows, rng})) return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_dropout(dtype == MOE_BF16, x, y, rows, d, n_rows, dropout_of(cut, rng),
+                                        static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"
