@@ -23,7 +23,7 @@ LIB = os.path.join(LIB_DIR, "libmoe_mi355x.so")
 ARCH = "gfx950"
 
 SOURCES = ["router.hip", "dispatch.hip", "fp8_dispatch.hip", "grouped_gemm.hip", "combine.hip",
-           "balance.hip", "mxfp4.hip", "few.hip", "linear.hip", "block.hip", "dropout.hip",
+           "balance.hip", "mxfp4.hip", "few.hip", "linear.hip", "linear_mfma.hip", "block.hip", "dropout.hip",
            "moe_api.hip"]
 PER_FILE = {"router.hip": ["-ffp-contract=off"]}
 

@@ -1,5 +1,5 @@
 // Launchers of the single Linears of every expert and of their gradients
-// (linear.hip, linear_grad.hip).  Not part of the public interface.
+// (linear.hip, linear_mfma.hip).  Not part of the public interface.
 #pragma once
 
 #include "moe_common.h"
@@ -34,6 +34,11 @@ struct Linear {
 };
 
 hipError_t launch_linear_f32(const Linear &p, hipStream_t s);
+
+// The gradients on bf16 operands, where linear_grad_fits (32-bit offsets of a
+// gathered x); ws: linear_grad_workspace_bytes of scratch.
+bool linear_grad_fits(const Linear &p);
+hipError_t launch_linear_grad(const Linear &p, void *ws, hipStream_t s);
 
 // Derivative of z sigmoid(z).
 __device__ __forceinline__ float silu_slope(float z) {

@@ -622,6 +622,10 @@ static moe::Linear linear_of(moe::LinearMode mode, int32_t dtype, int32_t n_grou
   return p;
 }
 
+static int run_linear_grad(const moe::Linear &p, void *ws, hipStream_t s) {
+  return hip_status(moe::linear_grad_fits(p) ? moe::launch_linear_grad(p, ws, s) : moe::launch_linear_f32(p, s));
+}
+
 int moe_grouped_linear(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k, int64_t x_rows,
                        const void *x, const int32_t *row_index, const int32_t *offsets,
                        int64_t max_rows, const void *w, const void *bias, int32_t silu, void *y,
@@ -663,7 +667,7 @@ int moe_grouped_linear_input_grad(int32_t dtype, int32_t n_groups, int32_t n_out
   p.w = w;
   p.act_pre = pre;
   p.out = dx;
-  return hip_status(moe::launch_linear_f32(p, static_cast<hipStream_t>(stream)));
+  return run_linear_grad(p, ws, static_cast<hipStream_t>(stream));
 }
 
 int moe_grouped_linear_weight_grad(int32_t dtype, int32_t grad_dtype, int32_t n_groups,
@@ -692,7 +696,7 @@ int moe_grouped_linear_weight_grad(int32_t dtype, int32_t grad_dtype, int32_t n_
   p.out = dw;
   p.dbias = dbias;
   p.accumulate = accumulate != 0;
-  return hip_status(moe::launch_linear_f32(p, static_cast<hipStream_t>(stream)));
+  return run_linear_grad(p, ws, static_cast<hipStream_t>(stream));
 }
 
 // The probability in steps of 2^-16 (ties to even), or -1 outside [0, 1).
