@@ -38,12 +38,14 @@ hipError_t launch_linear_f32(const Linear &p, hipStream_t s);
 // The gradients on bf16 operands, where linear_grad_fits (32-bit offsets of a
 // gathered x); ws: linear_grad_workspace_bytes of scratch.
 bool linear_grad_fits(const Linear &p);
+size_t linear_grad_workspace_bytes(int groups, int n_out, int k, int64_t max_rows);
 hipError_t launch_linear_grad(const Linear &p, void *ws, hipStream_t s);
 
-// Derivative of z sigmoid(z).
+// Derivative of z sigmoid(z): s + z s (1 - s), with the hardware exp2 and reciprocal
+// (about 1 ulp each).
 __device__ __forceinline__ float silu_slope(float z) {
-  const float s = 1.0f / (1.0f + __expf(-z));
-  return s * (1.0f + z * (1.0f - s));
+  const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-z * 1.4426950408889634f));
+  return fmaf(s, fmaf(-z, s, z), s);
 }
 
 }  // namespace moe

@@ -11,13 +11,15 @@
 // of four each); dy as Q of the input gradient lies [q][j] and is read in 16-byte
 // pieces.
 //
-// A workgroup of four waves computes 128 x 256 of C, a wave 64 x 128 (eight 32 x 32
-// blocks).  Steps of 32 along j are copied global -> LDS into a ring of three, two
-// steps ahead; the fragments of the next 16 j are read while those of the last are
-// multiplied; one barrier a step.  72 KB of LDS and at most 256 registers leave room
-// for two workgroups on a CU, so that one's first copies and its epilogue run under
-// the other's products.  P is the instruction's first operand: a lane ends up with
-// four neighbouring elements of one row of C.
+// Steps of 32 along j are copied global -> LDS into a ring, RING - 1 steps ahead; the
+// fragments of the next 16 j are read while those of the last are multiplied; one
+// barrier a step.  Workgroups are persistent and the stream of steps runs on from one
+// tile into the next: while a tile's sums go out, by way of the one ring stage that has
+// just been read, the next tile's first steps are on their way.  What a descriptor does
+// not cover reads as zero, so rows behind a group's end, steps behind a short tile's
+// and copies behind the last tile need no case of their own, and every wait counts the
+// same copies.  P is the instruction's first operand: a lane ends up with four
+// neighbouring elements of one row of C.
 #include "lds_dma.h"
 #include "linear.h"
 
@@ -26,28 +28,41 @@ namespace {
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
-typedef short s16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kQ = 128, kP = 256, kJ = 32, kRing = 3, kXcds = 8;
-constexpr int kQBytes = kQ * kJ * 2, kPBytes = kP * kJ * 2, kStage = kQBytes + kPBytes;
-constexpr int kQCopies = kQBytes / 4096, kPCopies = kPBytes / 4096, kCopies = kQCopies + kPCopies;
+constexpr int kJ = 32, kXcds = 8, kCus = 256;
 constexpr int kMaxGroups = kMaxRouted + kMaxShared;
-constexpr int kTileFloats = kQ * kP;
-constexpr int kSplitSlots = 512;         // workgroups that a split may fill: two a CU
-constexpr int kMinSteps = 8;             // steps of a part, at least
+constexpr int kMinSteps = 8;             // steps of a part of a split sum, at least
+constexpr int kTileCost = 6;             // what a tile costs beside its steps, in steps
+
+// A wave's 32 x 32 blocks along either axis of C, and the workgroup's tile of QW x 2
+// waves, 256 columns wide.
+template <int QB_, int QW_, int RING_>
+struct Shape {
+  static constexpr int QB = QB_, PB = 4, QW = QW_, WAVES = 2 * QW, NT = 64 * WAVES, RING = RING_;
+  static constexpr int Q = 32 * QB * QW, P = 64 * PB;
+  static constexpr int QBYTES = Q * kJ * 2, PBYTES = P * kJ * 2, STAGE = QBYTES + PBYTES;
+  static constexpr int QCOPIES = QBYTES / (1024 * WAVES), PCOPIES = PBYTES / (1024 * WAVES);
+  static constexpr int COPIES = QCOPIES + PCOPIES;
+  static constexpr int WGS = RING * STAGE <= 80 * 1024 ? 2 : 1;   // workgroups on a CU
+  static constexpr int SLOTS = kCus * WGS;
+  static constexpr int PART = Q * P + Q;   // floats of a part: a tile and its sums of dy
+  static_assert(QCOPIES * 1024 * WAVES == QBYTES && PCOPIES * 1024 * WAVES == PBYTES, "whole copies");
+  static_assert(STAGE >= WAVES * 4096, "4 KB of a stage for every wave's way out");
+};
 
 struct Args {
   Linear l;
-  float *part;                           // parts of split sums, kTileFloats each (or null)
+  float *part;                           // parts of split sums (or null)
   int most_parts;                        // parts of a tile, at most (1: never split)
 };
 
 // ---------------------------------------------------------------------------
 // Global to LDS
 // ---------------------------------------------------------------------------
-// Buffer descriptor of n bytes from p; what lies behind reads as zero.
+// Buffer descriptor of n bytes from p; what lies behind reads as zero and is not
+// written.
 __device__ __forceinline__ u32x4_t descriptor(const void *p, int64_t n) {
   const uint64_t a = reinterpret_cast<uint64_t>(p);
   u32x4_t d;
@@ -57,10 +72,31 @@ __device__ __forceinline__ u32x4_t descriptor(const void *p, int64_t n) {
   d[3] = 0x00020000;
   return d;
 }
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(u32x4_t d) {
+  void *p = reinterpret_cast<void *>((static_cast<uint64_t>(d[1]) << 32) | d[0]);
+  return __builtin_amdgcn_make_buffer_rsrc(p, 0, d[2], d[3]);
+}
 // One wave's 1 KB copy, 16 bytes a lane from the descriptor's start + off; lanes out of
 // its range write zeros.
 __device__ __forceinline__ void dma16b(uint32_t off, u32x4_t desc, uint32_t m0) {
   asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(off), "s"(desc), "{m0}"(m0) : "memory");
+}
+// 16 bytes a lane out, past the caches (whole lines that nothing here reads again).  As
+// the copies' waits count these stores, every lane issues all of them: the descriptor
+// drops what lies behind the tile's rows, and kNoColumn what lies behind its columns.
+constexpr uint32_t kNoColumn = 0xFFFFFF00u;
+__device__ __forceinline__ void store16b(uint32_t off, u32x4_t desc, u32x4_t v) {
+  __builtin_amdgcn_raw_buffer_store_b128(v, resource(desc), off, 0, 2);
+}
+
+// 16 bytes a lane; zeros where the descriptor does not reach.
+__device__ __forceinline__ u32x4_t load16b(uint32_t off, u32x4_t desc) {
+  return __builtin_amdgcn_raw_buffer_load_b128(resource(desc), off, 0, 0);
+}
+
+// This wave's LDS operations are done, and every wave is here; waits for no copy.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
 __device__ __forceinline__ const char *uniform_ptr(const void *p) {
@@ -92,25 +128,28 @@ __device__ __forceinline__ bf16x8_t read_turned(uint32_t at) {
   return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
+template <typename S>
 struct Frags {
-  bf16x8_t q[2], p[4];
+  bf16x8_t q[S::QB], p[S::PB];
 };
 
-// First element of 64-bit offsets that the tile needs.
+// ---------------------------------------------------------------------------
+// Tiles
+// ---------------------------------------------------------------------------
 struct Tile {
   int g, q0, p0;           // group, first row (or output feature), first column
   int64_t row0;            // first row of the group
-  int rows;
-  int s0, s1;              // steps of this part
+  int rows;                // of the group
+  int s0, s1;              // steps of this part of the sum
 };
 
-// Tile prefix over groups (input gradient), in LDS.
-__device__ int tile_prefix(const Linear &a, int *pref, int *tmp) {
-  const int per = (a.groups + 255) / 256, g0 = min(static_cast<int>(threadIdx.x) * per, a.groups);
-  const int g1 = min(g0 + per, a.groups);
-  auto tiles = [&](int g) { return (a.offsets[g + 1] - a.offsets[g] + kQ - 1) / kQ; };
+// Exclusive prefix over the groups, in LDS: 32-bit sums of count(g).
+template <int NT, typename F>
+__device__ int group_prefix(int groups, F count, int *pref, int *tmp) {
+  const int per = (groups + NT - 1) / NT, g0 = min(static_cast<int>(threadIdx.x) * per, groups);
+  const int g1 = min(g0 + per, groups);
   int local = 0;
-  for (int g = g0; g < g1; ++g) local += tiles(g);
+  for (int g = g0; g < g1; ++g) local += count(g);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int incl = local;
 #pragma unroll
@@ -122,178 +161,256 @@ __device__ int tile_prefix(const Linear &a, int *pref, int *tmp) {
   __syncthreads();
   int run = incl - local, total = 0;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 0; w < NT / 64; ++w) {
     if (w < wave) run += tmp[w];
     total += tmp[w];
   }
   for (int g = g0; g < g1; ++g) {
     pref[g] = run;
-    run += tiles(g);
+    run += count(g);
   }
-  if (threadIdx.x == 0) pref[a.groups] = total;
+  if (threadIdx.x == 0) pref[groups] = total;
   __syncthreads();
   return total;
 }
 
+// Largest g with pref[g] <= v (a group that is not empty, for v below the total).
+__device__ __forceinline__ int group_of(const int *pref, int groups, int v) {
+  int lo = 0, hi = groups;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (uniform(pref[mid]) <= v) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// x / y for 0 <= x < 2^31, 0 < y: the float quotient is off by at most 2^-22 of itself,
+// so two rounds of it leave a remainder within y, which the last step sets right.  The
+// compiler's own division takes several times as long.
+__device__ __forceinline__ int quotient(int x, int y) {
+  const float r = __builtin_amdgcn_rcpf(static_cast<float>(y));
+  int q = static_cast<int>(static_cast<float>(x) * r);
+  int rest = x - q * y;
+  const int more = static_cast<int>(static_cast<float>(rest) * r);
+  q += more;
+  rest -= more * y;
+  return uniform(q - (rest < 0 ? 1 : 0) + (rest >= y ? 1 : 0));
+}
+
 struct Plan {
-  int64_t tiles;
-  int qtiles, ptiles, parts, steps;
+  int tiles, first, end;       // tiles in all; this XCD's items (parts of tiles)
+  int qtiles, ptiles, parts;
 };
 
-// Parts of every tile's sum, so that few tiles still fill the chip.
+// Steps of a tile of a group of that many rows.
 template <int MODE>
-__device__ __forceinline__ Plan make_plan(const Args &a, int qtiles) {
+__device__ __forceinline__ int steps_of(const Linear &a, int rows) {
+  return MODE == kLinWeightGrad ? (rows + kJ - 1) / kJ : a.n_out / kJ;
+}
+
+// The work of this XCD.  Few tiles are split along their sums, so that they fill the
+// chip; many are dealt out so that every XCD gets a contiguous share (neighbours read
+// the same operands) of about the same cost.  pref: first q tile of every group (input
+// gradient), off: the offsets, both in LDS.
+template <typename S, int MODE>
+__device__ Plan make_plan(const Args &a, int *pref, int *off, int *tmp, int xcd) {
   Plan p;
-  p.qtiles = qtiles;
-  p.ptiles = (a.l.k + kP - 1) / kP;
-  p.tiles = static_cast<int64_t>(qtiles) * p.ptiles * (MODE == kLinWeightGrad ? a.l.groups : 1);
+  const Linear &l = a.l;
+  for (int g = threadIdx.x; g <= l.groups; g += S::NT) off[g] = l.offsets[g];
+  __syncthreads();
+  auto rows = [&](int g) { return off[g + 1] - off[g]; };
+  p.ptiles = (l.k + S::P - 1) / S::P;
+  if (MODE == kLinInputGrad) {
+    p.qtiles = uniform(group_prefix<S::NT>(l.groups, [&](int g) { return (rows(g) + S::Q - 1) / S::Q; }, pref, tmp));
+    p.tiles = p.qtiles * p.ptiles;
+  } else {
+    p.qtiles = (l.n_out + S::Q - 1) / S::Q;
+    p.tiles = p.qtiles * p.ptiles * l.groups;
+  }
   p.parts = 1;
-  if (a.most_parts > 1 && p.tiles > 0 && p.tiles * 2 <= kSplitSlots)
-    p.parts = min(a.most_parts, static_cast<int>(kSplitSlots / p.tiles));
+  if (a.most_parts > 1 && p.tiles > 0 && p.tiles * 2 <= S::SLOTS) p.parts = min(a.most_parts, S::SLOTS / p.tiles);
+  const int items = p.tiles * p.parts;
+  if (MODE == kLinInputGrad || p.parts > 1) {
+    p.first = static_cast<int>(static_cast<int64_t>(items) * xcd / kXcds);
+    p.end = static_cast<int>(static_cast<int64_t>(items) * (xcd + 1) / kXcds);
+  } else {
+    const int per = p.qtiles * p.ptiles;
+    auto cost = [&](int g) { return max(S::RING, steps_of<MODE>(l, rows(g))) + kTileCost; };
+    const int total = uniform(group_prefix<S::NT>(l.groups, cost, pref, tmp));
+    // item at which x eighths of the cost are done: whole groups, then tiles of one
+    auto border = [&](int x) {
+      if (x == kXcds) return items;
+      const int64_t want = static_cast<int64_t>(total) * x;          // in eighths
+      const int g = group_of(pref, l.groups, static_cast<int>(want / kXcds));
+      const int64_t in = want - static_cast<int64_t>(uniform(pref[g])) * kXcds;
+      return g * per + static_cast<int>(in * per / (static_cast<int64_t>(uniform(cost(g))) * kXcds));
+    };
+    p.first = border(xcd);
+    p.end = border(xcd + 1);
+  }
+  p.first = uniform(p.first);
+  p.end = uniform(p.end);
+  p.parts = uniform(p.parts);
   return p;
 }
 
-// Tile `at` of the list, in the order in which neighbours share operands: the rows of a
-// group (or output features) within a band of 8 tiles, then columns, then bands.
-template <int MODE>
-__device__ __forceinline__ Tile tile_at(const Args &a, const Plan &p, const int *pref, int64_t at, int part) {
+// An item: a part of a tile, in the order in which neighbours share operands: the q tiles
+// of a group within a band of 8, then columns, then bands.  g: a group that is not
+// behind the item's.
+template <typename S, int MODE>
+__device__ __forceinline__ Tile tile_at(const Args &a, const Plan &p, const int *pref, const int *off, int item, int g) {
   Tile t;
-  int q;
-  int64_t first = 0;                     // first q tile of the band's group
-  int in_group;                          // q tiles of that group
+  int at = p.parts > 1 ? quotient(item, p.parts) : item;
+  const int part = item - at * p.parts;
+  int in_group = p.qtiles;               // q tiles of the group
   if (MODE == kLinWeightGrad) {
-    const int64_t per = static_cast<int64_t>(p.qtiles) * p.ptiles;
-    t.g = static_cast<int>(at / per);
+    const int per = p.qtiles * p.ptiles;
+    t.g = quotient(at, per);
     at -= t.g * per;
-    in_group = p.qtiles;
   } else {
-    // all groups' q tiles before this one's times the columns
-    int lo = 0, hi = a.l.groups;
-    const int64_t u = at / p.ptiles;     // pref[lo] <= u < pref[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (pref[mid] <= u) lo = mid; else hi = mid;
-    }
-    t.g = lo;
-    first = pref[lo];
-    in_group = pref[lo + 1] - pref[lo];
+    const int q = quotient(at, p.ptiles);
+    int next = uniform(pref[g + 1]);
+    while (next <= q) next = uniform(pref[++g + 1]);
+    const int first = uniform(pref[g]);
+    t.g = g;
+    in_group = next - first;
     at -= first * p.ptiles;
   }
+  t.row0 = uniform(off[t.g]);
+  t.rows = uniform(off[t.g + 1]) - static_cast<int>(t.row0);
   constexpr int kBand = 8;
-  const int l = static_cast<int>(at), band = l / (kBand * p.ptiles), rest = l - band * kBand * p.ptiles;
-  const int h = min(kBand, in_group - band * kBand);
-  q = band * kBand + rest % h;
-  t.q0 = q * kQ;
-  t.p0 = (rest / h) * kP;
-  t.row0 = a.l.offsets[t.g];
-  t.rows = a.l.offsets[t.g + 1] - static_cast<int>(t.row0);
-  const int steps = MODE == kLinWeightGrad ? (t.rows + kJ - 1) / kJ : a.l.n_out / kJ;
-  const int per = (steps + p.parts - 1) / p.parts;
-  t.s0 = min(steps, part * per);
-  t.s1 = min(steps, t.s0 + per);
+  const int band = quotient(at, kBand * p.ptiles), rest = at - band * kBand * p.ptiles;
+  const int h = min(kBand, in_group - band * kBand), column = quotient(rest, h);
+  t.q0 = (band * kBand + rest - column * h) * S::Q;
+  t.p0 = column * S::P;
+  t.s0 = 0;
+  t.s1 = steps_of<MODE>(a.l, t.rows);
+  if (p.parts > 1) {
+    const int steps = t.s1, per = quotient(steps + p.parts - 1, p.parts);
+    t.s0 = min(steps, part * per);
+    t.s1 = min(steps, t.s0 + per);
+  }
   return t;
 }
 
 // ---------------------------------------------------------------------------
 // Sources of a tile's copies
 // ---------------------------------------------------------------------------
-template <int MODE, bool GATHER>
+template <typename S, int MODE, bool GATHER>
 struct Source {
-  uint32_t q[kQCopies], p[kPCopies];     // this lane's byte offsets in a step
-  const char *qbase, *pbase;             // step 0 of the part
-  int64_t qstep, pstep;                  // bytes of a step
-  int64_t left;                          // rows of the group from the part's step 0 (weight gradient)
-  const __attribute__((address_space(4))) int32_t *index;
-  int rows, j0;
-  uint32_t pcol;
+  uint32_t q[S::QCOPIES], p[S::PCOPIES]; // this lane's byte offsets in a step
+  u32x4_t dq, dp;                        // where the step lies
+  uint32_t qstep, pstep, pcol;           // bytes of a step; byte offset of this lane's column
+  int left;                              // rows (input gradient: steps) of the part from this step on
+  // a gathered x: rows of the group, its next step's first, and that step's indexes
+  int row0, rows, j;
+  int at[GATHER ? 2 * S::PCOPIES : 1];
 
   __device__ __forceinline__ void init(const Args &a, const Tile &t, int wave, int lane) {
     const int n = a.l.n_out, k = a.l.k;
+    const int64_t j0 = static_cast<int64_t>(t.s0) * kJ;
+    pcol = lines<S::P, S::PCOPIES>(p, k, t.p0, wave, lane);
+    pstep = static_cast<uint32_t>(kJ) * k * 2;
     if constexpr (MODE == kLinInputGrad) {
       // [q][j]: 16 rows of 64 bytes a copy
       const int c = (lane & 3) ^ ((lane >> 4) & 3);
 #pragma unroll
-      for (int i = 0; i < kQCopies; ++i) {
-        const int r = min(16 * (4 * i + wave) + (lane >> 2), t.rows - 1 - t.q0);
+      for (int i = 0; i < S::QCOPIES; ++i) {
+        const int r = min(16 * (S::WAVES * i + wave) + (lane >> 2), t.rows - 1 - t.q0);
         q[i] = static_cast<uint32_t>(r) * n * 2 + c * 16;
       }
-      qbase = uniform_ptr(static_cast<const uint16_t *>(a.l.dy) + (t.row0 + t.q0) * n + t.s0 * kJ);
+      left = t.s1 - t.s0;
       qstep = kJ * 2;
+      dq = descriptor(static_cast<const uint16_t *>(a.l.dy) + (t.row0 + t.q0) * n + j0, 0);
+      dp = descriptor(static_cast<const uint16_t *>(a.l.w) + (static_cast<int64_t>(t.g) * n + j0) * k, 0);
     } else {
-      // [j][128 columns]: 4 rows of 256 bytes a copy
-      const int c = (lane & 15) ^ ((lane >> 4) * 4);
-#pragma unroll
-      for (int i = 0; i < kQCopies; ++i)
-        q[i] = static_cast<uint32_t>(4 * (4 * i + wave) + (lane >> 4)) * n * 2 + min(t.q0 + c * 8, n - 8) * 2;
-      qbase = uniform_ptr(static_cast<const uint16_t *>(a.l.dy) + (t.row0 + static_cast<int64_t>(t.s0) * kJ) * n);
-      qstep = static_cast<int64_t>(kJ) * n * 2;
-    }
-    // [j][256 columns]: 2 rows of 512 bytes a copy
-    const int j = 2 * wave + (lane >> 5), c = (lane & 31) ^ ((j & 3) * 4);
-    pcol = min(t.p0 + c * 8, k - 8) * 2;
-#pragma unroll
-    for (int i = 0; i < kPCopies; ++i) p[i] = static_cast<uint32_t>(8 * i + j) * k * 2 + pcol;
-    pstep = static_cast<int64_t>(kJ) * k * 2;
-    if constexpr (MODE == kLinInputGrad) {
-      pbase = uniform_ptr(static_cast<const uint16_t *>(a.l.w) +
-                          (static_cast<int64_t>(t.g) * n + static_cast<int64_t>(t.s0) * kJ) * k);
-    } else if constexpr (GATHER) {
-      pbase = uniform_ptr(a.l.x);
-      index = (const __attribute__((address_space(4))) int32_t *)(uniform_ptr(a.l.index + t.row0));
-    } else {
-      pbase = uniform_ptr(static_cast<const uint16_t *>(a.l.x) + (t.row0 + static_cast<int64_t>(t.s0) * kJ) * k);
-    }
-    j0 = t.s0 * kJ;
-    // rows of this part's steps end where the part ends
-    rows = MODE == kLinWeightGrad ? min(t.rows, t.s1 * kJ) : 0;
-    left = rows - j0;
-  }
-
-  // The copies of step s (counted from the part's first) into the stage at LDS byte m0.
-  __device__ __forceinline__ void copy(const Args &a, int s, uint32_t m0, int wave, int lane) const {
-    m0 += wave * 1024;
-    if constexpr (MODE == kLinInputGrad) {
-      const char *qb = qbase + s * qstep, *pb = pbase + s * pstep;
-#pragma unroll
-      for (int i = 0; i < kQCopies; ++i) dma::dma16s(q[i], qb, m0 + i * 4096);
-#pragma unroll
-      for (int i = 0; i < kPCopies; ++i) dma::dma16s(p[i], pb, m0 + kQBytes + i * 4096);
-    } else {
-      const int64_t have = left - static_cast<int64_t>(s) * kJ;    // rows from this step on
-      const u32x4_t dq = descriptor(qbase + s * qstep, have * a.l.n_out * 2);
-#pragma unroll
-      for (int i = 0; i < kQCopies; ++i) dma16b(q[i], dq, m0 + i * 4096);
+      left = static_cast<int>(min(t.rows, t.s1 * kJ) - j0);
+      lines<S::Q, S::QCOPIES>(q, n, t.q0, wave, lane);
+      qstep = static_cast<uint32_t>(kJ) * n * 2;
+      dq = descriptor(static_cast<const uint16_t *>(a.l.dy) + (t.row0 + j0) * n, 0);
       if constexpr (GATHER) {
-        const uint32_t bytes = static_cast<uint32_t>(a.l.x_rows * a.l.k * 2);
-        const u32x4_t dp = descriptor(pbase, a.l.x_rows * a.l.k * 2);
-#pragma unroll
-        for (int i = 0; i < kPCopies; ++i) {
-          const int j = j0 + s * kJ + 8 * i + 2 * wave;
-          const int i0 = index[max(0, min(j, rows - 1))], i1 = index[max(0, min(j + 1, rows - 1))];
-          const uint32_t at = static_cast<uint32_t>(lane >> 5 ? i1 : i0) * static_cast<uint32_t>(a.l.k * 2) + pcol;
-          dma16b(j + (lane >> 5) < rows ? at : bytes, dp, m0 + kQBytes + i * 4096);
-        }
+        dp = descriptor(a.l.x, 0);
+        row0 = static_cast<int>(t.row0);
+        rows = t.rows;
+        j = static_cast<int>(j0);
+        load_index(a, wave);
       } else {
-        const u32x4_t dp = descriptor(pbase + s * pstep, have * a.l.k * 2);
-#pragma unroll
-        for (int i = 0; i < kPCopies; ++i) dma16b(p[i], dp, m0 + kQBytes + i * 4096);
+        dp = descriptor(static_cast<const uint16_t *>(a.l.x) + (t.row0 + j0) * k, 0);
       }
     }
+    cover(a);
+  }
+  // Behind the last tile: steps without data.
+  __device__ __forceinline__ void none(const Args &a) {
+    left = 0;
+    cover(a);
+  }
+  // To the next step.
+  __device__ __forceinline__ void advance(const Args &a) {
+    left -= MODE == kLinInputGrad ? 1 : kJ;
+    add(dq, qstep);
+    if constexpr (!GATHER) add(dp, pstep);
+    cover(a);
+  }
+
+  // Offsets of an operand [j][N columns] with lines of `width` elements: 1 KB copies
+  // of 512 / N lines each.  Returns the column's byte offset.
+  template <int N, int COPIES>
+  static __device__ __forceinline__ uint32_t lines(uint32_t (&at)[COPIES], int width, int col0, int wave, int lane) {
+    constexpr int LINES = 512 / N, LANES = 64 / LINES;   // lines of a copy, lanes of a line
+    const int j = LINES * wave + lane / LANES, c = (lane % LANES) ^ ((j & 3) * 4);
+    const uint32_t col = min(col0 + c * 8, width - 8) * 2;
+#pragma unroll
+    for (int i = 0; i < COPIES; ++i) at[i] = static_cast<uint32_t>(S::WAVES * LINES * i + j) * width * 2 + col;
+    return col;
+  }
+  static __device__ __forceinline__ void add(u32x4_t &d, uint32_t bytes) {
+    const uint64_t v = ((static_cast<uint64_t>(d[1]) << 32) | d[0]) + bytes;
+    d[0] = uniform(static_cast<int>(v));
+    d[1] = uniform(static_cast<int>(v >> 32));
+  }
+  // The rows of this step that are there.
+  __device__ __forceinline__ void cover(const Args &a) {
+    if constexpr (MODE == kLinInputGrad) {
+      dq[2] = uniform(left > 0 ? S::Q * a.l.n_out * 2 : 0);   // rows are clamped
+      dp[2] = uniform(left > 0 ? pstep : 0);
+    } else {
+      const uint32_t have = min(max(left, 0), kJ);
+      dq[2] = uniform(have * a.l.n_out * 2);
+      dp[2] = uniform(GATHER ? (left > 0 ? static_cast<uint32_t>(a.l.x_rows * a.l.k * 2) : 0) : have * a.l.k * 2);
+    }
+  }
+  // Indexes of the step at j (rows of the group from 0 on).  They go through the scalar
+  // cache: vector loads would be counted with the copies.
+  __device__ __forceinline__ void load_index(const Args &a, int wave) {
+    const auto *index = (const __attribute__((address_space(4))) int32_t *)(a.l.index);
+    const int most = max(0, min(rows, static_cast<int>(a.l.max_rows) - row0) - 1), none = row0 < a.l.max_rows ? row0 : 0;
+#pragma unroll
+    for (int i = 0; i < 2 * S::PCOPIES; ++i)
+      at[i] = index[none + min(j + 2 * (S::WAVES * (i / 2) + wave) + i % 2, most)];
+    j += kJ;
+  }
+  // This lane's offsets of the step whose indexes were loaded, and the next one's indexes.
+  __device__ __forceinline__ void gather(const Args &a, int wave, int lane) {
+    if constexpr (GATHER) {
+      static_assert(S::P == 256, "two lines a copy");
+#pragma unroll
+      for (int i = 0; i < S::PCOPIES; ++i) {
+        const uint32_t r = lane >> 5 ? at[2 * i + 1] : at[2 * i];
+        const bool there = 2 * (S::WAVES * i + wave) + (lane >> 5) < left;
+        p[i] = there ? r * static_cast<uint32_t>(a.l.k * 2) + pcol : kNoColumn;
+      }
+      load_index(a, wave);
+    }
+  }
+  // Copy number i of the step into the stage at LDS byte m0 (this wave's first KB).
+  __device__ __forceinline__ void copy(int i, uint32_t m0) const {
+    const int pi = i - S::QCOPIES;
+    m0 += i * 1024 * S::WAVES;
+    if (pi < 0) dma16b(q[i], dq, m0);
+    else dma16b(p[pi], dp, m0);
   }
 };
-
-// ---------------------------------------------------------------------------
-// Kernel
-// ---------------------------------------------------------------------------
-typedef f32x16_t Acc[4][2];              // [column block][row block] of 32 x 32
-
-__device__ __forceinline__ void multiply(const Frags &f, Acc &acc) {
-#pragma unroll
-  for (int p = 0; p < 4; ++p)
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-      acc[p][q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.p[p], f.q[q], acc[p][q], 0, 0, 0);
-}
 
 __device__ __forceinline__ float sum8(bf16x8_t v) {
   float s = 0.0f;
@@ -302,183 +419,528 @@ __device__ __forceinline__ float sum8(bf16x8_t v) {
   return s;
 }
 
-// The other workgroup of the CU has its own ring: 72 KB each.
-template <int MODE, bool GATHER>
-__global__ __launch_bounds__(256, 2) void linear_grad_kernel(Args a) {
-  __shared__ __attribute__((aligned(1024))) char s_ring[kRing * kStage];
-  __shared__ int s_pref[MODE == kLinInputGrad ? kMaxGroups + 1 : 1], s_tmp[4];
-  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-  const int wq = wave & 1, wp = wave >> 1;
-  const Plan plan = make_plan<MODE>(a, MODE == kLinInputGrad ? tile_prefix(a.l, s_pref, s_tmp)
-                                                             : (a.l.n_out + kQ - 1) / kQ);
-  // workgroups are dealt to the XCDs in turn: each XCD takes a contiguous share
-  const int64_t items = plan.tiles * plan.parts, share = (items + kXcds - 1) / kXcds;
-  const int64_t slot = blockIdx.x / kXcds, item = (blockIdx.x % kXcds) * share + slot;
-  if (slot >= share || item >= items) return;
-  const int64_t at = item / plan.parts;
-  const int part = static_cast<int>(item % plan.parts);
-  const Tile t = tile_at<MODE>(a, plan, s_pref, at, part);
-
-  Acc acc;
+// Reads of the fragments of one slice (16 j), number i of them: rows first.
+template <typename S, int MODE>
+struct Reader {
+  uint32_t q[S::QB], p[S::PB];           // this lane's byte addresses in stage 0
+  __device__ __forceinline__ void init(uint32_t ring, int wq, int wp, int lane) {
 #pragma unroll
-  for (int p = 0; p < 4; ++p)
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[p][q][i] = 0.0f;
-  float bias[2] = {0.0f, 0.0f};
-  const bool sum_dy = MODE == kLinWeightGrad && a.l.dbias && t.p0 == 0 && wp == 0;
-
-  const uint32_t ring = uniform(static_cast<int>(dma::lds_addr(s_ring)));
-  // read offsets of this lane within a stage
-  uint32_t qat[2], pat[4];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if constexpr (MODE == kLinInputGrad) {
-      const int row = wq * 64 + i * 32 + (lane & 31);
-      qat[i] = ring + row * 64 + (((lane >> 5) ^ ((row >> 2) & 3)) << 4);
-    } else {
-      qat[i] = ring + turned_at<kQ>(wq * 2 + i, lane);
+    for (int i = 0; i < S::QB; ++i) {
+      if constexpr (MODE == kLinInputGrad) {
+        const int row = (wq * S::QB + i) * 32 + (lane & 31);
+        q[i] = ring + row * 64 + (((lane >> 5) ^ ((row >> 2) & 3)) << 4);
+      } else {
+        q[i] = ring + turned_at<S::Q>(wq * S::QB + i, lane);
+      }
     }
+#pragma unroll
+    for (int i = 0; i < S::PB; ++i) p[i] = ring + S::QBYTES + turned_at<S::P>(wp * S::PB + i, lane);
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) pat[i] = ring + kQBytes + turned_at<kP>(wp * 4 + i, lane);
-  auto read = [&](Frags &f, uint32_t stage, int slice) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
+  __device__ __forceinline__ void read(Frags<S> &f, uint32_t stage, int slice, int i) const {
+    if (i < S::QB) {
       if constexpr (MODE == kLinInputGrad)   // pieces 2 slice + half: slice flips bit 1
-        f.q[i] = *reinterpret_cast<lds_bf16x8_t *>((qat[i] ^ (slice << 5)) + stage);
+        f.q[i] = *reinterpret_cast<lds_bf16x8_t *>((q[i] ^ (slice << 5)) + stage);
       else
-        f.q[i] = read_turned<kQ>(qat[i] + stage + slice * (16 * kQ * 2));
+        f.q[i] = read_turned<S::Q>(q[i] + stage + slice * (16 * S::Q * 2));
+    } else {
+      f.p[i - S::QB] = read_turned<S::P>(p[i - S::QB] + stage + slice * (16 * S::P * 2));
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f.p[i] = read_turned<kP>(pat[i] + stage + slice * (16 * kP * 2));
-  };
-
-  const int steps = t.s1 - t.s0;
-  if (steps > 0) {
-    Source<MODE, GATHER> src;
-    src.init(a, t, wave, lane);
-    const int last = steps - 1;
-    // Steps behind the last are copied too, from the last one's place: what they
-    // bring is not multiplied, and every wait counts the same copies.
-    auto copy = [&](int s, uint32_t stage) { src.copy(a, min(s, last), ring + stage, wave, lane); };
-    copy(0, 0);
-    copy(1, kStage);
-    copy(2, 2 * kStage);
-    dma::wait_and_barrier<2 * kCopies>();
-    Frags f0, f1;
-    read(f0, 0, 0);
-    uint32_t stage = 0;
-    for (int s = 0; s < steps; ++s) {
-      const uint32_t next = stage == (kRing - 1) * kStage ? 0 : stage + kStage;
-      read(f1, stage, 1);
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(f0, acc);
-      if (sum_dy) {
-        bias[0] += sum8(f0.q[0]);
-        bias[1] += sum8(f0.q[1]);
-      }
-      // this step's stage is read, the next one has landed for every wave
-      dma::wait_and_barrier<kCopies>();
-      copy(s + 3, stage);
-      read(f0, next, 0);
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(f1, acc);
-      if (sum_dy) {
-        bias[0] += sum8(f1.q[0]);
-        bias[1] += sum8(f1.q[1]);
-      }
-      stage = next;
-    }
-    dma::wait_and_barrier<0>();
   }
+};
 
-  if (sum_dy && plan.parts == 1) {
+// ---------------------------------------------------------------------------
+// A tile's sums to memory
+// ---------------------------------------------------------------------------
+// Each wave takes its blocks through 4 KB of LDS of its own, so that stores are whole
+// lines of 128 bytes: a lane holds four columns of each of 32 rows, and storing those
+// as they are took 417 us of 741 for 1.48 GB of weight gradients.  Rows of 128 bytes
+// keep their 16-byte piece c at c ^ (row % 8).
+// Lanes hand elements to each other there: LDS operations of one wave run in order, and
+// this keeps the compiler from moving or merging them across lanes' accesses.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <typename S>
+constexpr int kStores16 = S::QB * (S::PB / 2) * 4;   // stores of a wave's tile in bf16
+
+// float32: 32 x 32 elements a pass.
+template <typename S>
+__device__ __forceinline__ void out_f32(const f32x16_t (&acc)[S::PB][S::QB], char *lds, u32x4_t dst, int pitch, int r0,
+                                        int c0, int columns, bool accumulate, int lane) {
+  const int piece = lane & 7;
+#pragma unroll
+  for (int qi = 0; qi < S::QB; ++qi)
+#pragma unroll
+    for (int pi = 0; pi < S::PB; ++pi) {
+      const int w = lane & 31;
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        *reinterpret_cast<float4 *>(lds + w * 128 + (((b * 2 + (lane >> 5)) ^ (w & 7)) << 4)) =
+            make_float4(acc[pi][qi][4 * b], acc[pi][qi][4 * b + 1], acc[pi][qi][4 * b + 2], acc[pi][qi][4 * b + 3]);
+      wave_order();
+      const int c = c0 + pi * 32 + piece * 4;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 3);
+        u32x4_t v = *reinterpret_cast<const u32x4_t *>(lds + r * 128 + ((piece ^ (r & 7)) << 4));
+        const uint32_t at = c < columns ? (static_cast<uint32_t>(r0 + qi * 32 + r) * pitch + c) * 4 : kNoColumn;
+        if (accumulate) {
+          const u32x4_t z = load16b(at, dst);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + __uint_as_float(z[e]));
+        }
+        store16b(at, dst, v);
+      }
+      wave_order();
+    }
+}
+
+// bf16: 32 x 64 elements a pass.
+template <typename S>
+__device__ __forceinline__ void out_bf16(const f32x16_t (&acc)[S::PB][S::QB], char *lds, u32x4_t dst, int pitch, int r0,
+                                         int c0, int columns, int lane) {
+  const int piece = lane & 7;
+#pragma unroll
+  for (int qi = 0; qi < S::QB; ++qi)
+#pragma unroll
+    for (int pp = 0; pp < S::PB / 2; ++pp) {
+      const int w = lane & 31;
+#pragma unroll
+      for (int h = 0; h < 8; ++h) {
+        const f32x16_t &x = acc[pp * 2 + h / 4][qi];
+        const int b = h % 4;
+        *reinterpret_cast<uint2 *>(lds + w * 128 + ((h ^ (w & 7)) << 4) + ((lane >> 5) << 3)) =
+            make_uint2(pack_bf16x2(x[4 * b], x[4 * b + 1]), pack_bf16x2(x[4 * b + 2], x[4 * b + 3]));
+      }
+      wave_order();
+      const int c = c0 + pp * 64 + piece * 8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 3);
+        const u32x4_t v = *reinterpret_cast<const u32x4_t *>(lds + r * 128 + ((piece ^ (r & 7)) << 4));
+        store16b(c < columns ? (static_cast<uint32_t>(r0 + qi * 32 + r) * pitch + c) * 2 : kNoColumn, dst, v);
+      }
+      wave_order();
+    }
+}
+
+// bf16 with another array of C's shape: `other` added (dw as it was), or its SiLU's
+// slope as a factor.  The sums stay float32 until then: 16 x 64 elements a pass, rows of
+// 256 bytes with piece c at c ^ row; the other array comes a pass ahead.
+template <typename S, bool SLOPE>
+__device__ __forceinline__ void out_bf16_with(const f32x16_t (&acc)[S::PB][S::QB], char *lds, u32x4_t dst, u32x4_t other,
+                                              int pitch, int r0, int c0, int columns, int lane) {
+  constexpr int PASSES = S::QB * (S::PB / 2) * 2;
+  const int piece = lane & 7;
+  auto where = [&](int pass, int i) {
+    const int qi = pass / S::PB, pp = pass / 2 % (S::PB / 2), half = pass & 1;
+    const int r = r0 + qi * 32 + half * 16 + i * 8 + (lane >> 3), c = c0 + pp * 64 + piece * 8;
+    return c < columns ? (static_cast<uint32_t>(r) * pitch + c) * 2 : kNoColumn;
+  };
+  u32x4_t z[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) z[0][i] = load16b(where(0, i), other);
+#pragma unroll
+  for (int pass = 0; pass < PASSES; ++pass) {
+    const int qi = pass / S::PB, pp = pass / 2 % (S::PB / 2), half = pass & 1, w = lane & 15;
+    if (pass + 1 < PASSES)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) z[(pass + 1) & 1][i] = load16b(where(pass + 1, i), other);
+    if (((lane >> 4) & 1) == half)
+#pragma unroll
+      for (int h = 0; h < 8; ++h) {
+        const f32x16_t &x = acc[pp * 2 + h / 4][qi];
+        const int b = h % 4;
+        *reinterpret_cast<float4 *>(lds + w * 256 + (((h * 2 + (lane >> 5)) ^ w) << 4)) =
+            make_float4(x[4 * b], x[4 * b + 1], x[4 * b + 2], x[4 * b + 3]);
+      }
+    wave_order();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float v = bias[i] + __shfl_xor(bias[i], 32);
-      const int q = t.q0 + wq * 64 + i * 32 + (lane & 31);
-      if (lane < 32 && q < a.l.n_out) {
-        const int64_t o = static_cast<int64_t>(t.g) * a.l.n_out + q;
-        if (a.l.out_bf16) {
-          uint16_t *d = static_cast<uint16_t *>(a.l.dbias) + o;
-          *d = f32_to_bf16(a.l.accumulate ? bf16_to_f32(*d) + v : v);
-        } else {
-          float *d = static_cast<float *>(a.l.dbias) + o;
-          *d = a.l.accumulate ? *d + v : v;
-        }
+      const int r = i * 8 + (lane >> 3);
+      float v[8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 f = *reinterpret_cast<const float4 *>(lds + r * 256 + (((piece * 2 + h) ^ r) << 4));
+        v[4 * h] = f.x, v[4 * h + 1] = f.y, v[4 * h + 2] = f.z, v[4 * h + 3] = f.w;
       }
+      const u32x4_t o = z[pass & 1][i];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float u = __uint_as_float(e & 1 ? o[e / 2] & 0xFFFF0000u : o[e / 2] << 16);
+        v[e] = SLOPE ? v[e] * silu_slope(u) : v[e] + u;
+      }
+      const u32x4_t packed = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                              pack_bf16x2(v[6], v[7])};
+      store16b(where(pass, i), dst, packed);
     }
-  }
-
-  const int np = a.l.k, nq = MODE == kLinWeightGrad ? a.l.n_out : t.rows;
-  const int64_t out_row = MODE == kLinWeightGrad ? static_cast<int64_t>(t.g) * a.l.n_out : t.row0;
-#pragma unroll
-  for (int qi = 0; qi < 2; ++qi) {
-    const int q = t.q0 + wq * 64 + qi * 32 + (lane & 31);
-    if (q >= nq) continue;
-#pragma unroll
-    for (int pi = 0; pi < 4; ++pi)
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int p = t.p0 + wp * 128 + pi * 32 + b * 8 + (lane >> 5) * 4;
-        if (p >= np) continue;
-        float v[4] = {acc[pi][qi][4 * b], acc[pi][qi][4 * b + 1], acc[pi][qi][4 * b + 2], acc[pi][qi][4 * b + 3]};
-        const int64_t o = (out_row + q) * np + p;
-        if (MODE == kLinInputGrad || a.l.out_bf16) {
-          uint2 *d = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.l.out) + o);
-          if (MODE == kLinInputGrad && a.l.act_pre) {
-            const uint2 z = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.l.act_pre) + o);
-            v[0] *= silu_slope(__uint_as_float(z.x << 16));
-            v[1] *= silu_slope(__uint_as_float(z.x & 0xFFFF0000u));
-            v[2] *= silu_slope(__uint_as_float(z.y << 16));
-            v[3] *= silu_slope(__uint_as_float(z.y & 0xFFFF0000u));
-          }
-          if (MODE == kLinWeightGrad && a.l.accumulate) {
-            const uint2 z = *d;
-            v[0] += __uint_as_float(z.x << 16);
-            v[1] += __uint_as_float(z.x & 0xFFFF0000u);
-            v[2] += __uint_as_float(z.y << 16);
-            v[3] += __uint_as_float(z.y & 0xFFFF0000u);
-          }
-          *d = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-        } else {
-          float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(a.l.out) + o);
-          if (a.l.accumulate) {
-            const float4 z = *d;
-            v[0] += z.x, v[1] += z.y, v[2] += z.z, v[3] += z.w;
-          }
-          *d = make_float4(v[0], v[1], v[2], v[3]);
-        }
-      }
+    wave_order();
   }
 }
+
+template <typename O>
+__device__ __forceinline__ void store_bias(O *d, float v, bool accumulate) {
+  *d = Act<O>::from_f32(accumulate ? Act<O>::to_f32(*d) + v : v);
+}
+
+// ---------------------------------------------------------------------------
+// Kernel
+// ---------------------------------------------------------------------------
+template <typename S, int MODE, bool GATHER>
+__global__ __launch_bounds__(S::NT, S::WGS * S::WAVES / 4) void linear_grad_kernel(Args a) {
+  constexpr int QB = S::QB, PB = S::PB, NF = QB + PB, NM = QB * PB, GROUPS = 8, PER = NM / GROUPS, RING = S::RING;
+  static_assert(NM % GROUPS == 0 && NF <= GROUPS && RING >= 3, "reads among the products, two steps ahead");
+  // The copies of a step are spread over the half step behind the barrier that frees its
+  // stage, and the half step after: together they would wait for each other.
+  constexpr int EARLY = S::COPIES / 2, LATE = S::COPIES - EARLY;
+  static_assert(EARLY * 2 <= GROUPS && LATE * 2 <= GROUPS, "at most one for two products");
+  __shared__ __attribute__((aligned(1024))) char s_ring[RING * S::STAGE];
+  __shared__ int s_pref[kMaxGroups + 1], s_off[kMaxGroups + 1], s_tmp[S::WAVES];
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  // Waves w and w + 4 share a SIMD: with blocks that lie behind a tile's rows (or columns)
+  // left out, the SIMDs still have about the same to multiply.
+  const int wp = wave / S::QW, wq = (wave + wp * (S::QW / 2)) % S::QW;
+  // workgroups are dealt to the XCDs in turn
+  const Plan plan = make_plan<S, MODE>(a, s_pref, s_off, s_tmp, blockIdx.x % kXcds);
+  const int stride = gridDim.x / kXcds;
+  int item = plan.first + blockIdx.x / kXcds;
+  if (item >= plan.end) return;
+
+  const uint32_t ring = uniform(static_cast<int>(dma::lds_addr(s_ring)));
+  const uint32_t base = ring + wave * 1024;
+  Reader<S, MODE> rd;
+  rd.init(ring, wq, wp, lane);
+
+  // The stream of steps: `fill` is the tile whose steps are being copied, RING ahead of
+  // the one that is multiplied.  A tile has RING steps at least, so that `fill` is that
+  // one's tile or the next.
+  Source<S, MODE, GATHER> src;
+  int fill_item = item;
+  Tile fill = tile_at<S, MODE>(a, plan, s_pref, s_off, item, 0);
+  src.init(a, fill, wave, lane);
+  int fill_left = max(fill.s1 - fill.s0, RING), steps = fill_left;   // the one at hand among them
+  bool fresh = false;
+  src.gather(a, wave, lane);
+  // the next tile, where this one's steps are all copied; else the next step
+  auto next_tile = [&]() {
+    if (fill_left > 1) return;
+    fill_item += stride;
+    if (fill_item < plan.end) {
+      int el = lane;
+      asm volatile("" : "+v"(el));       // as for the sums below
+      fill = tile_at<S, MODE>(a, plan, s_pref, s_off, fill_item, fill.g);
+      src.init(a, fill, wave, el);
+      fill_left = max(fill.s1 - fill.s0, RING) + 1;
+    } else {
+      src.none(a);
+      fill_left = 0x7FFFFFFF;
+    }
+    fresh = true;
+  };
+  auto next_step = [&]() {
+    if (!fresh) src.advance(a);
+    fresh = false;
+    --fill_left;
+    src.gather(a, wave, lane);
+  };
+#pragma unroll
+  for (int s = 0; s < RING; ++s) {
+#pragma unroll
+    for (int i = 0; i < (s == RING - 1 ? EARLY : S::COPIES); ++i) src.copy(i, base + s * S::STAGE);
+    if (s < RING - 1) next_step();
+  }
+  dma::wait_and_barrier<(RING - 2) * S::COPIES + EARLY>();
+  Frags<S> f0, f1;
+#pragma unroll
+  for (int i = 0; i < NF; ++i) rd.read(f0, 0, 0, i);
+
+  Tile t = fill;
+  uint32_t stage = 0;
+  bool stored = false;                   // this wave's last tile had stores
+  f32x16_t acc[PB][QB];
+  auto before = [&](uint32_t at) { return at == 0 ? (RING - 1) * S::STAGE : at - S::STAGE; };
+  auto after = [&](uint32_t at) { return at == (RING - 1) * S::STAGE ? 0u : at + S::STAGE; };
+  // products of fragments f; after the first product of group i, `start(i)` starts reads
+  // or copies
+  auto multiply = [&](const Frags<S> &f, auto start) {
+#pragma unroll
+    for (int i = 0; i < GROUPS; ++i) {
+#pragma unroll
+      for (int m = i * PER; m < (i + 1) * PER; ++m) {
+        acc[m / QB][m % QB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.p[m / QB], f.q[m % QB], acc[m / QB][m % QB], 0, 0, 0);
+        if (m == i * PER) {
+          __builtin_amdgcn_sched_barrier(0);
+          start(i);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // Fragments of the next slice, the last of them some products before the barrier that
+  // waits for it.
+  auto read_some = [&](Frags<S> &f, uint32_t at, int slice, int group) {
+    constexpr int AHEAD = NF > 6 ? NF - 6 : 0;             // all read after six groups
+#pragma unroll
+    for (int i = 0; i < NF; ++i)
+      if ((i < 2 * AHEAD ? i / 2 : i - AHEAD) == group) rd.read(f, at, slice, i);
+  };
+
+  while (true) {
+#pragma unroll
+    for (int p = 0; p < PB; ++p)
+#pragma unroll
+      for (int q = 0; q < QB; ++q)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[p][q][i] = 0.0f;
+    float bias[QB];
+#pragma unroll
+    for (int q = 0; q < QB; ++q) bias[q] = 0.0f;
+    const int nq = (MODE == kLinWeightGrad ? a.l.n_out : t.rows) - t.q0, np = a.l.k;
+    const bool busy = wq * QB * 32 < nq && t.p0 + wp * PB * 32 < np;   // blocks of this wave are there
+    const bool sum_dy = MODE == kLinWeightGrad && a.l.dbias && t.p0 == 0 && wp == 0;
+    auto add_dy = [&](const Frags<S> &f) {
+      if (sum_dy)
+#pragma unroll
+        for (int q = 0; q < QB; ++q) bias[q] += sum8(f.q[q]);
+    };
+    // First half of a step, with the rest of the last step's copies.
+    auto half = [&]() {
+      const uint32_t old = base + before(stage);
+      if (busy) {
+        multiply(f0, [&](int i) {
+          read_some(f1, stage, 1, i);
+          if (i % (GROUPS / LATE) == 1 && i / (GROUPS / LATE) < LATE) src.copy(EARLY + i / (GROUPS / LATE), old);
+        });
+        add_dy(f0);
+      } else {
+#pragma unroll
+        for (int i = 0; i < LATE; ++i) src.copy(EARLY + i, old);
+      }
+    };
+    // Second half, behind the barrier: this step's stage is read, the next one has landed.
+    auto rest = [&]() {
+      const uint32_t next = after(stage);
+      if (busy) {
+        multiply(f1, [&](int i) {
+          if (i == 0) next_step();
+          read_some(f0, next, 0, i);
+          if (i % (GROUPS / EARLY) == 1 && i / (GROUPS / EARLY) < EARLY) src.copy(i / (GROUPS / EARLY), base + stage);
+        });
+        add_dy(f1);
+      } else {
+        next_step();
+#pragma unroll
+        for (int i = 0; i < EARLY; ++i) src.copy(i, base + stage);
+      }
+      stage = next;
+    };
+    // The last tile's stores are younger than the next stage's copies in these steps.
+    for (int s = 0; s < RING - 2; ++s) {
+      half();
+      next_tile();
+      if (stored) dma::wait_and_barrier<(RING - 2) * S::COPIES + kStores16<S>>();
+      else dma::wait_and_barrier<(RING - 2) * S::COPIES>();
+      __builtin_amdgcn_sched_barrier(0);
+      rest();
+    }
+    for (int s = RING - 2; s < steps - 1; ++s) {
+      half();
+      next_tile();
+      dma::wait_and_barrier<(RING - 2) * S::COPIES>();
+      __builtin_amdgcn_sched_barrier(0);
+      rest();
+    }
+    half();
+    next_tile();
+    dma::wait_and_barrier<(RING - 2) * S::COPIES>();
+    __builtin_amdgcn_sched_barrier(0);
+    const uint32_t next = after(stage);
+    if (busy) {
+      multiply(f1, [&](int i) { read_some(f0, next, 0, i); });
+      add_dy(f1);
+    } else {
+      // the next tile may have work for this wave
+#pragma unroll
+      for (int i = 0; i < NF; ++i) rd.read(f0, next, 0, i);
+    }
+    stored = busy;
+
+    // the sums, by way of the stage just read.  The lane is hidden from the compiler, or
+    // it would keep the offsets of every pass in registers through all tiles.
+    int el = lane;
+    asm volatile("" : "+v"(el));
+    char *lds = s_ring + stage + wave * 4096;
+    const int r0 = wq * QB * 32, c0 = t.p0 + wp * PB * 32;
+    if (!busy) {
+    } else if (plan.parts > 1) {
+      float *part = a.part + static_cast<int64_t>(item) * S::PART;
+      out_f32<S>(acc, lds, descriptor(part, S::Q * S::P * 4), S::P, r0, wp * PB * 32, S::P, false, el);
+    } else {
+      const int64_t row = (MODE == kLinWeightGrad ? static_cast<int64_t>(t.g) * a.l.n_out : t.row0) + t.q0;
+      const int64_t size = static_cast<int64_t>(min(S::Q, nq)) * np;
+      if (MODE == kLinWeightGrad && !a.l.out_bf16) {
+        out_f32<S>(acc, lds, descriptor(static_cast<float *>(a.l.out) + row * np, size * 4), np, r0, c0, np,
+                   a.l.accumulate, el);
+      } else {
+        const u32x4_t dst = descriptor(static_cast<uint16_t *>(a.l.out) + row * np, size * 2);
+        if (MODE == kLinInputGrad && a.l.act_pre)
+          out_bf16_with<S, true>(acc, lds, dst, descriptor(static_cast<const uint16_t *>(a.l.act_pre) + row * np, size * 2),
+                                 np, r0, c0, np, el);
+        else if (MODE == kLinWeightGrad && a.l.accumulate)
+          out_bf16_with<S, false>(acc, lds, dst, dst, np, r0, c0, np, el);
+        else
+          out_bf16<S>(acc, lds, dst, np, r0, c0, np, el);
+      }
+    }
+    if (sum_dy && busy)
+#pragma unroll
+      for (int i = 0; i < QB; ++i) {
+        const float v = bias[i] + __shfl_xor(bias[i], 32);
+        const int q = t.q0 + r0 + i * 32 + (el & 31);
+        if (el >= 32) continue;
+        if (plan.parts > 1) {
+          a.part[static_cast<int64_t>(item) * S::PART + S::Q * S::P + q - t.q0] = v;
+        } else if (q < a.l.n_out) {
+          const int64_t o = static_cast<int64_t>(t.g) * a.l.n_out + q;
+          if (a.l.out_bf16) store_bias(static_cast<uint16_t *>(a.l.dbias) + o, v, a.l.accumulate);
+          else store_bias(static_cast<float *>(a.l.dbias) + o, v, a.l.accumulate);
+        }
+      }
+    item += stride;
+    if (item >= plan.end) break;
+    // every wave is through with the stage; its copies now make `fill` the next tile
+    lds_barrier();
+    next_step();
+#pragma unroll
+    for (int i = 0; i < EARLY; ++i) src.copy(i, base + stage);
+    t = fill;
+    steps = max(t.s1 - t.s0, RING);
+    stage = next;
+  }
+  // copies in flight write to LDS, which may be another workgroup's once this one ends
+  dma::wait_and_barrier<0>();
+}
+
+template <typename S>
+struct Threads256 : S {
+  static constexpr int NT = 256;
+};
+
+// Sums of the parts of split tiles, in order, and what the kernel would have done with
+// them.  Sixteen workgroups a tile; float32, float4 a thread.
+template <typename S, int MODE>
+__global__ __launch_bounds__(256) void linear_grad_parts_kernel(Args a) {
+  __shared__ int s_pref[kMaxGroups + 1], s_off[kMaxGroups + 1], s_tmp[4];
+  const Plan plan = make_plan<Threads256<S>, MODE>(a, s_pref, s_off, s_tmp, 0);
+  const int at = blockIdx.x / 16;
+  if (plan.parts <= 1 || at >= plan.tiles) return;
+  const Tile t = tile_at<S, MODE>(a, plan, s_pref, s_off, at * plan.parts, 0);
+  const float *part = a.part + static_cast<int64_t>(at) * plan.parts * S::PART;
+  const int np = a.l.k, rows = MODE == kLinWeightGrad ? a.l.n_out : t.rows;
+  const int64_t row = (MODE == kLinWeightGrad ? static_cast<int64_t>(t.g) * a.l.n_out : t.row0) + t.q0;
+  constexpr int kEach = S::Q * S::P / 4 / 16;   // float4 of a workgroup
+  for (int e = threadIdx.x; e < kEach; e += 256) {
+    const int i = (blockIdx.x % 16) * kEach + e, r = i / (S::P / 4), c = i % (S::P / 4) * 4;
+    if (t.q0 + r >= rows || t.p0 + c >= np) continue;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int k = 0; k < plan.parts; ++k) {
+      const float4 x = *reinterpret_cast<const float4 *>(part + static_cast<int64_t>(k) * S::PART + i * 4);
+      v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+    }
+    const int64_t o = (row + r) * np + t.p0 + c;
+    if (MODE == kLinWeightGrad && !a.l.out_bf16) {
+      float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(a.l.out) + o);
+      if (a.l.accumulate) {
+        const float4 z = *d;
+        v.x += z.x, v.y += z.y, v.z += z.z, v.w += z.w;
+      }
+      *d = v;
+    } else {
+      uint2 *d = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.l.out) + o);
+      if (MODE == kLinWeightGrad ? a.l.accumulate : a.l.act_pre != nullptr) {
+        const uint2 z = MODE == kLinWeightGrad
+                            ? *d : *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.l.act_pre) + o);
+        const float u[4] = {__uint_as_float(z.x << 16), __uint_as_float(z.x & 0xFFFF0000u), __uint_as_float(z.y << 16),
+                            __uint_as_float(z.y & 0xFFFF0000u)};
+        if (MODE == kLinWeightGrad)
+          v.x += u[0], v.y += u[1], v.z += u[2], v.w += u[3];
+        else
+          v.x *= silu_slope(u[0]), v.y *= silu_slope(u[1]), v.z *= silu_slope(u[2]), v.w *= silu_slope(u[3]);
+      }
+      *d = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    }
+  }
+  if (MODE == kLinWeightGrad && a.l.dbias && t.p0 == 0 && blockIdx.x % 16 == 0)
+    for (int r = threadIdx.x; r < S::Q && t.q0 + r < rows; r += 256) {
+      float v = 0.0f;
+      for (int k = 0; k < plan.parts; ++k) v += part[static_cast<int64_t>(k) * S::PART + S::Q * S::P + r];
+      const int64_t o = row + r;
+      if (a.l.out_bf16) store_bias(static_cast<uint16_t *>(a.l.dbias) + o, v, a.l.accumulate);
+      else store_bias(static_cast<float *>(a.l.dbias) + o, v, a.l.accumulate);
+    }
+}
+
+// Tiles at most, and parts of a tile at most (1: the sizes never need a split).
+template <typename S>
+int64_t tile_bound(int mode, int groups, int n_out, int k, int64_t max_rows) {
+  const int64_t pt = (k + S::P - 1) / S::P;
+  if (mode == kLinWeightGrad) return pt * groups * ((n_out + S::Q - 1) / S::Q);
+  return pt * (max_rows / S::Q + (max_rows < groups ? max_rows : groups));
+}
+template <typename S>
+int part_bound(int mode, int groups, int n_out, int k, int64_t max_rows) {
+  if (tile_bound<S>(mode, groups, n_out, k, max_rows) > S::SLOTS) return 1;
+  const int64_t steps = mode == kLinWeightGrad ? (max_rows + kJ - 1) / kJ : n_out / kJ;
+  const int64_t parts = steps / kMinSteps;
+  return static_cast<int>(parts < 1 ? 1 : parts < S::SLOTS ? parts : S::SLOTS);
+}
+
+template <typename S, int MODE, bool GATHER>
+void launch_mode(const Args &a, hipStream_t s) {
+  const int64_t items = tile_bound<S>(MODE, a.l.groups, a.l.n_out, a.l.k, a.l.max_rows) * a.most_parts;
+  const int64_t want = (items + kXcds - 1) / kXcds * kXcds;
+  hipLaunchKernelGGL((linear_grad_kernel<S, MODE, GATHER>), dim3(static_cast<unsigned>(want < S::SLOTS ? want : S::SLOTS)),
+                     dim3(S::NT), 0, s, a);
+  if (a.most_parts > 1) {
+    const int64_t tiles = tile_bound<S>(MODE, a.l.groups, a.l.n_out, a.l.k, a.l.max_rows);
+    const int64_t split = tiles < S::SLOTS / 2 ? tiles : S::SLOTS / 2;
+    hipLaunchKernelGGL((linear_grad_parts_kernel<S, MODE>), dim3(static_cast<unsigned>(split * 16)), dim3(256), 0, s, a);
+  }
+}
+
+template <typename S>
+hipError_t launch_shape(const Linear &p, void *ws, hipStream_t s) {
+  const Args a{p, static_cast<float *>(ws), part_bound<S>(p.mode, p.groups, p.n_out, p.k, p.max_rows)};
+  if (p.mode == kLinInputGrad) launch_mode<S, kLinInputGrad, false>(a, s);
+  else if (p.index && p.max_rows > 0) launch_mode<S, kLinWeightGrad, true>(a, s);
+  else launch_mode<S, kLinWeightGrad, false>(a, s);
+  return hipGetLastError();
+}
+
+using Tiles = Shape<2, 4, 4>;
 
 }  // namespace
 
+// Widths whose lines of a tile stay below 4 GiB, a gathered x that does, and items that
+// are counted in 31 bits.
 bool linear_grad_fits(const Linear &p) {
-  // a gathered x is addressed by 32-bit byte offsets, lines of a step by 32-bit ones
-  if (!p.bf16 || p.mode == kLinForward) return false;
-  if (p.mode == kLinWeightGrad && p.index && p.x_rows > (0xFFFFFF00ll / 2) / p.k) return false;
-  return p.n_out < (1 << 22) && p.k < (1 << 22);
+  if (!p.bf16 || p.mode == kLinForward || p.n_out >= (1 << 20) || p.k >= (1 << 20)) return false;
+  if (tile_bound<Tiles>(p.mode, p.groups, p.n_out, p.k, p.max_rows) >= (int64_t(1) << 30)) return false;
+  return p.mode != kLinWeightGrad || !p.index || p.x_rows <= 0xFFFFFE00ll / 2 / p.k;
+}
+
+size_t linear_grad_workspace_bytes(int groups, int n_out, int k, int64_t max_rows) {
+  for (int mode : {kLinInputGrad, kLinWeightGrad})
+    if (part_bound<Tiles>(mode, groups, n_out, k, max_rows) > 1)
+      return static_cast<size_t>(Tiles::SLOTS) * Tiles::PART * sizeof(float);
+  return 0;
 }
 
 hipError_t launch_linear_grad(const Linear &p, void *ws, hipStream_t s) {
-  Args a{p, static_cast<float *>(ws), 1};
-  const int64_t pt = (p.k + kP - 1) / kP;
-  const int64_t qt = p.mode == kLinWeightGrad ? static_cast<int64_t>(p.groups) * ((p.n_out + kQ - 1) / kQ)
-                                              : p.max_rows / kQ + (p.max_rows < p.groups ? p.max_rows : p.groups);
-  const int64_t share = (pt * qt + kXcds - 1) / kXcds;
-  if (share * kXcds >= (int64_t(1) << 31)) return hipErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(share * kXcds));
-  if (p.mode == kLinInputGrad)
-    hipLaunchKernelGGL((linear_grad_kernel<kLinInputGrad, false>), grid, dim3(256), 0, s, a);
-  else if (p.index)
-    hipLaunchKernelGGL((linear_grad_kernel<kLinWeightGrad, true>), grid, dim3(256), 0, s, a);
-  else
-    hipLaunchKernelGGL((linear_grad_kernel<kLinWeightGrad, false>), grid, dim3(256), 0, s, a);
-  return hipGetLastError();
+  return launch_shape<Tiles>(p, ws, s);
 }
 
 }  // namespace moe

@@ -605,8 +605,8 @@ static int check_linear(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t 
 
 size_t moe_grouped_linear_workspace_size(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k,
                                          int64_t max_rows) {
-  if (check_linear(dtype, n_groups, n_out, k, max_rows) != MOE_OK) return 0;
-  return 0;
+  if (check_linear(dtype, n_groups, n_out, k, max_rows) != MOE_OK || dtype != MOE_BF16) return 0;
+  return moe::linear_grad_workspace_bytes(n_groups, n_out, k, max_rows);
 }
 
 static moe::Linear linear_of(moe::LinearMode mode, int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k,
