@@ -62,6 +62,7 @@ struct GemmArgs {
   const void *bias_sh;
   void *C;
   void *C_sh;
+  void *pre;                 // EPI == kEpiBiasSiluPre
   int64_t T_sh;
   int64_t a_sh_stride;
   int n_routed;
@@ -198,6 +199,14 @@ __device__ __forceinline__ const T *a_row_ptr(const GemmArgs &a, const TileView<
   }
   const int gs = v.g - a.n_routed;
   return static_cast<const T *>(a.A_sh) + static_cast<int64_t>(gs) * a.a_sh_stride + r * a.K;
+}
+
+// Four values before the SiLU, at element `at` of the rows (routed groups only).
+template <int EPI>
+__device__ __forceinline__ void store_pre(const GemmArgs &a, int64_t at, const float (&o)[4]) {
+  if constexpr (EPI == kEpiBiasSiluPre)
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.pre) + at) =
+        make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
 }
 
 // Decode a linear tile index into (m-tile, n-tile), banded by GM m-tiles.
@@ -535,10 +544,16 @@ __device__ __forceinline__ void rs_epilogue(const f32x16_t (&acc)[rs::TN][rs::TM
                                             const GemmArgs &a, const TileView<uint16_t> &v,
                                             int n0, uint16_t *s_tile, int lane, int wm, int wn,
                                             int tid) {
-  if (v.bias)
+  if constexpr (EPI == kEpiBiasSiluPre) {   // the tile twice: before the SiLU, and behind
+    TileView<uint16_t> vp = v;
+    vp.C = static_cast<uint16_t *>(a.pre);
+    rs_epilogue<kEpiBias>(acc, a, vp, n0, s_tile, lane, wm, wn, tid);
+    rs_epilogue<kEpiBiasSilu>(acc, a, v, n0, s_tile, lane, wm, wn, tid);
+  } else if (v.bias) {
     rs_epilogue<EPI, true>(acc, a, v, n0, s_tile, lane, wm, wn, tid);
-  else
+  } else {
     rs_epilogue<EPI, false>(acc, a, v, n0, s_tile, lane, wm, wn, tid);
+  }
 }
 
 // Splitting the last, partly filled round of tiles along K.  Per XCD the
@@ -889,6 +904,13 @@ __device__ __forceinline__ void Rh<H>::epilogue(const f32x16_t (&acc)[TN][TM], c
                                                 const TileView<uint16_t> &v, int n0,
                                                 uint16_t *s_tile, int lane, int wm, int wn,
                                                 int tid) {
+  if constexpr (EPI == kEpiBiasSiluPre) {
+    TileView<uint16_t> vp = v;
+    vp.C = static_cast<uint16_t *>(a.pre);
+    epilogue<kEpiBias>(acc, a, vp, n0, s_tile, lane, wm, wn, tid);
+    epilogue<kEpiBiasSilu>(acc, a, v, n0, s_tile, lane, wm, wn, tid);
+    return;
+  }
   int el = lane, ewm = wm, ewn = wn, etid = tid;
   asm volatile("" : "+v"(el), "+v"(etid), "+s"(ewm), "+s"(ewn));
   constexpr int CH = BN / 8;
@@ -1004,7 +1026,7 @@ void grouped_gemm_bf16_rs_kernel(GemmArgs a, RsSplit sp) {
         // at quarter height in the first Linear (measured: in the second one
         // the extra path costs the K loop registers and time)
         bool quarter = false;
-        if constexpr (EPI == kEpiBiasSilu) {
+        if constexpr (EPI != kEpiBias) {
           quarter = v.rows - v.row0 <= Rh<64>::BM;
           if (quarter) {
             f32x16_t accq[Rh<64>::TN][Rh<64>::TM];
@@ -1118,7 +1140,8 @@ __global__ __launch_bounds__(256) void rs_fixup_kernel(GemmArgs a, RsSplit sp, i
       o[2] += __uint_as_float(bq.y << 16);
       o[3] += __uint_as_float(bq.y & 0xFFFF0000u);
     }
-    if (EPI == kEpiBiasSilu)
+    store_pre<EPI>(a, (v.out_base + row) * a.Nout + n, o);
+    if (EPI != kEpiBias)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[e] = silu_fast(o[e]);
     uint2 packed;
@@ -1295,10 +1318,11 @@ __device__ __forceinline__ void stream_store(const f32x16_t (&acc)[MB][NTB], con
             }
             float o[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              o[e] = acc[i][j][4 * q + e] + bv[e];
-              if (EPI == kEpiBiasSilu) o[e] = silu_fast(o[e]);
-            }
+            for (int e = 0; e < 4; ++e) o[e] = acc[i][j][4 * q + e] + bv[e];
+            store_pre<EPI>(a, (v.out_base + lr) * a.Nout + n, o);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (EPI != kEpiBias) o[e] = silu_fast(o[e]);
             uint2 packed;
             packed.x = pack_bf16x2(o[0], o[1]);
             packed.y = pack_bf16x2(o[2], o[3]);
@@ -1512,7 +1536,8 @@ __device__ __forceinline__ void reduce_parts(const GemmArgs &a, const StreamSpli
     o[2] += __uint_as_float(bq.y << 16);
     o[3] += __uint_as_float(bq.y & 0xFFFF0000u);
   }
-  if (EPI == kEpiBiasSilu)
+  store_pre<EPI>(a, prow * a.Nout + n, o);
+  if (EPI != kEpiBias)
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] = silu_fast(o[e]);
   uint2 packed;
@@ -1602,7 +1627,8 @@ __global__ __launch_bounds__(256) void stream_finish_kernel(GemmArgs a, StreamSp
       o[2] += __uint_as_float(bq.y << 16);
       o[3] += __uint_as_float(bq.y & 0xFFFF0000u);
     }
-    if (EPI == kEpiBiasSilu)
+    store_pre<EPI>(a, (v.out_base + lr) * a.Nout + n, o);
+    if (EPI != kEpiBias)
 #pragma unroll
       for (int q = 0; q < 4; ++q) o[q] = silu_fast(o[q]);
     uint2 packed;
@@ -1716,6 +1742,7 @@ GemmArgs make_args(const GemmGroups &g) {
   a.bias_sh = g.bias_sh;
   a.C = g.C;
   a.C_sh = g.C_sh;
+  a.pre = g.pre;
   a.T_sh = g.T_sh;
   a.a_sh_stride = g.a_sh_stride;
   a.n_routed = g.n_routed;
@@ -1775,7 +1802,10 @@ hipError_t launch_bf16_stream(const GemmArgs &a, const GemmGroups &g, Epilogue e
   }
   const unsigned grid =
       persistent_grid(tiles_upper_bound(g, 32 * NTB, 128 * MB) * sp.ks_cap, per_cu);
-  if (epi == kEpiBiasSilu)
+  if (epi == kEpiBiasSiluPre)
+    hipLaunchKernelGGL((grouped_gemm_bf16_stream_kernel<MB, NTB, NTB2, S, kEpiBiasSiluPre>),
+                       dim3(grid), dim3(256), 0, s, a, sp);
+  else if (epi == kEpiBiasSilu)
     hipLaunchKernelGGL((grouped_gemm_bf16_stream_kernel<MB, NTB, NTB2, S, kEpiBiasSilu>),
                        dim3(grid), dim3(256), 0, s, a, sp);
   else
@@ -1795,7 +1825,10 @@ hipError_t launch_bf16_stream(const GemmArgs &a, const GemmGroups &g, Epilogue e
     const int64_t cap_blocks = need < kFinishMaxUniform ? need : kFinishMaxUniform;
     if (cap_blocks > fgrid) fgrid = cap_blocks;
   }
-  if (epi == kEpiBiasSilu)
+  if (epi == kEpiBiasSiluPre)
+    hipLaunchKernelGGL((stream_finish_kernel<MB, NTB, NTB2, kEpiBiasSiluPre>), dim3(static_cast<unsigned>(fgrid)),
+                       dim3(256), 0, s, a, sp, static_cast<int>(grid), fpu);
+  else if (epi == kEpiBiasSilu)
     hipLaunchKernelGGL((stream_finish_kernel<MB, NTB, NTB2, kEpiBiasSilu>), dim3(static_cast<unsigned>(fgrid)),
                        dim3(256), 0, s, a, sp, static_cast<int>(grid), fpu);
   else
@@ -1836,7 +1869,8 @@ hipError_t launch_bf16_rs(const GemmArgs &a, const GemmGroups &g, Epilogue epi, 
       hipLaunchKernelGGL((grouped_gemm_bf16_rs_kernel<EPI, GM, PIECE, false>), dim3(grid),       \
                          dim3(256), 0, s, a, sp);                                                \
   }
-  if (epi == kEpiBiasSilu) MOE_RS_LAUNCH(kEpiBiasSilu, false)
+  if (epi == kEpiBiasSiluPre) MOE_RS_LAUNCH(kEpiBiasSiluPre, false)
+  else if (epi == kEpiBiasSilu) MOE_RS_LAUNCH(kEpiBiasSilu, false)
   else MOE_RS_LAUNCH(kEpiBias, false)
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !sp.partial) return e;
@@ -1846,7 +1880,9 @@ hipError_t launch_bf16_rs(const GemmArgs &a, const GemmGroups &g, Epilogue epi, 
   // at most half of each XCD's workgroups hold remainder tiles; four
   // fixup workgroups per tile
   const dim3 fgrid(static_cast<unsigned>(kXcds * 4 * (grid / kXcds / 2 > 0 ? grid / kXcds / 2 : 1)));
-  if (epi == kEpiBiasSilu)
+  if (epi == kEpiBiasSiluPre)
+    hipLaunchKernelGGL((rs_fixup_kernel<kEpiBiasSiluPre, GM>), fgrid, dim3(256), 0, s, a, sp, static_cast<int>(grid));
+  else if (epi == kEpiBiasSilu)
     hipLaunchKernelGGL((rs_fixup_kernel<kEpiBiasSilu, GM>), fgrid, dim3(256), 0, s, a, sp, static_cast<int>(grid));
   else
     hipLaunchKernelGGL((rs_fixup_kernel<kEpiBias, GM>), fgrid, dim3(256), 0, s, a, sp, static_cast<int>(grid));
@@ -1898,7 +1934,7 @@ hipError_t launch_grouped_gemm(bool bf16, const GemmGroups &g, Epilogue epi, hip
   }
   // bf16 widths are multiples of 64 (checked at the interface), so only
   // float32 operands reach the VALU kernel
-  if (bf16) return hipErrorInvalidValue;
+  if (bf16 || epi == kEpiBiasSiluPre) return hipErrorInvalidValue;
   const unsigned grid = persistent_grid(tiles_upper_bound(g, 64, 64), 4);
   if (epi == kEpiBiasSilu)
     hipLaunchKernelGGL((grouped_gemm_valu_kernel<float, kEpiBiasSilu>), dim3(grid), dim3(256), 0, s, a);

@@ -254,7 +254,7 @@ void launch(const Linear &p, hipStream_t s) {
 
 template <typename T>
 void dispatch(const Linear &p, hipStream_t s) {
-  if (p.mode == kLinForward) launch<T, T, kLinForward>(p, s);
+  if (p.mode == kLinForward) launch<float, float, kLinForward>(p, s);   // bf16: launch_grouped_gemm
   else if (p.mode == kLinInputGrad) launch<T, T, kLinInputGrad>(p, s);
   else if (p.out_bf16) launch<T, uint16_t, kLinWeightGrad>(p, s);
   else launch<T, float, kLinWeightGrad>(p, s);

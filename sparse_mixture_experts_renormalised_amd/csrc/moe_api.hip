@@ -606,7 +606,14 @@ static int check_linear(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t 
 size_t moe_grouped_linear_workspace_size(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k,
                                          int64_t max_rows) {
   if (check_linear(dtype, n_groups, n_out, k, max_rows) != MOE_OK || dtype != MOE_BF16) return 0;
-  return moe::linear_grad_workspace_bytes(n_groups, n_out, k, max_rows);
+  // the gradients' parts of split sums, or the forward's
+  GemmGroups g{};
+  g.n_routed = n_groups;
+  g.max_routed_rows = max_rows;
+  g.Nout = n_out;
+  const size_t forward = moe::grouped_gemm_split_bytes(g);
+  const size_t grad = moe::linear_grad_workspace_bytes(n_groups, n_out, k, max_rows);
+  return forward > grad ? forward : grad;
 }
 
 static moe::Linear linear_of(moe::LinearMode mode, int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k,
@@ -639,6 +646,26 @@ int moe_grouped_linear(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k
   if (!all_aligned16({x, row_index, offsets, w, bias, y, pre, ws})) return MOE_ERR_INVALID_ARG;
   const size_t need = moe_grouped_linear_workspace_size(dtype, n_groups, n_out, k, max_rows);
   if (need && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (dtype == MOE_BF16) {
+    GemmGroups g{};
+    g.offsets = offsets;
+    g.n_routed = n_groups;
+    g.A = x;
+    g.a_index = row_index;
+    g.T_sh = x_rows;                     // rows that row_index may name
+    g.W = w;
+    g.bias = bias;
+    g.C = y;
+    g.pre = pre;
+    g.Nout = n_out;
+    g.K = k;
+    g.max_routed_rows = max_rows;
+    g.max_group_rows = max_rows;
+    g.split_ws = ws;
+    g.split_bytes = need;
+    return hip_status(moe::launch_grouped_gemm(
+        true, g, pre ? moe::kEpiBiasSiluPre : silu ? moe::kEpiBiasSilu : moe::kEpiBias, static_cast<hipStream_t>(stream)));
+  }
   moe::Linear p = linear_of(moe::kLinForward, dtype, n_groups, n_out, k, offsets, max_rows);
   p.x_rows = x_rows;
   p.x = x;

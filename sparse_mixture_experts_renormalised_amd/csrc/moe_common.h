@@ -88,6 +88,7 @@ struct GemmGroups {
   // Outputs: routed row r -> C + r*Nout; shared group g row t ->
   // C_sh + (g*T_sh + t)*Nout.
   void *C, *C_sh;
+  void *pre;                 // kEpiBiasSiluPre: values before the SiLU, rows as C's
   int Nout, K;
   int64_t max_routed_rows;   // host upper bound on offsets[n_routed]
   int64_t max_group_rows;    // host upper bound on the rows of one routed group
@@ -102,7 +103,9 @@ struct GemmGroups {
 // T_sh and max_routed_rows.
 size_t grouped_gemm_split_bytes(const GemmGroups &g);
 
-enum Epilogue { kEpiBias = 0, kEpiBiasSilu = 1 };
+// kEpiBiasSiluPre: the SiLU's values to C and those before it to pre (bf16,
+// routed groups only).
+enum Epilogue { kEpiBias = 0, kEpiBiasSilu = 1, kEpiBiasSiluPre = 2 };
 
 hipError_t launch_router_logits(bool bf16, const void *x, const float *w, const float *bias,
                                 float *logits, int64_t T, int d, int N, hipStream_t s);
