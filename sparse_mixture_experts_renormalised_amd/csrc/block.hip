@@ -26,35 +26,66 @@ namespace {
 
 constexpr int kMaxPart = 4;   // weights whose gradients are summed: w_in, b_in, w_out, b_out
 
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+// Eight elements as they lie in memory, so that many can be on their way at once.
 template <typename T>
-__device__ __forceinline__ void load8(const T *p, float (&v)[8]);
-template <>
-__device__ __forceinline__ void load8<float>(const float *p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-template <>
-__device__ __forceinline__ void load8<uint16_t>(const uint16_t *p, float (&v)[8]) {
-  const uint4 q = *reinterpret_cast<const uint4 *>(p);
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+struct Raw {
+  static constexpr int N = sizeof(T) / 2;   // 16-byte pieces
+  u32x4_t q[N];
+  __device__ __forceinline__ void load(const T *p) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    for (int i = 0; i < N; ++i) q[i] = reinterpret_cast<const u32x4_t *>(p)[i];
   }
+  // past the caches, for rows that are read once
+  __device__ __forceinline__ void load_once(const T *p) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) q[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t *>(p) + i);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) q[i] = (u32x4_t){0, 0, 0, 0};
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (N == 2) return __uint_as_float(q[i / 4][i % 4]);
+    const uint32_t w = q[0][i / 2];
+    return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, float (&v)[8]) {
+  Raw<T> r;
+  r.load(p);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = r.get(i);
 }
 
 template <typename T>
-__device__ __forceinline__ void store8(T *p, const float (&v)[8]);
-template <>
-__device__ __forceinline__ void store8<float>(float *p, const float (&v)[8]) {
-  reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void pack8(const float (&v)[8], Raw<T> &r) {
+  if constexpr (Raw<T>::N == 2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.q[i / 4][i % 4] = __float_as_uint(v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.q[0][i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+  }
 }
-template <>
-__device__ __forceinline__ void store8<uint16_t>(uint16_t *p, const float (&v)[8]) {
-  *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                             pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+template <typename T>
+__device__ __forceinline__ void store8(T *p, const float (&v)[8]) {
+  Raw<T> r;
+  pack8(v, r);
+#pragma unroll
+  for (int i = 0; i < Raw<T>::N; ++i) reinterpret_cast<u32x4_t *>(p)[i] = r.q[i];
+}
+// past the caches: rows that are not read again soon (with these, wide rows take 187 us
+// instead of 194, their gradient 288 instead of 294)
+template <typename T>
+__device__ __forceinline__ void store8_once(T *p, const float (&v)[8]) {
+  Raw<T> r;
+  pack8(v, r);
+#pragma unroll
+  for (int i = 0; i < Raw<T>::N; ++i) __builtin_nontemporal_store(r.q[i], reinterpret_cast<u32x4_t *>(p) + i);
 }
 
 // Sum of a wave's 64 values, in every lane.
@@ -153,14 +184,18 @@ __global__ __launch_bounds__(NW * 64) void block_join_kernel(BlockJoin a) {
   const bool has_branch = a.branch || a.y_rows;
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
     const int64_t row = t * a.d;
+    // expert rows in batches: a batch is on its way before its first row is added
+    constexpr int BATCH = CH * static_cast<int>(sizeof(A)) >= 8 ? 4 : 8;
+    Raw<R> res[CH];
     float h[CH][8], b[CH][8];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int vec = tid + c * NW * 64;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) h[c][j] = b[c][j] = 0.0f;
+      for (int j = 0; j < 8; ++j) b[c][j] = 0.0f;
+      res[c].zero();
       if (vec < nvec) {
-        load8(static_cast<const R *>(a.residual) + row + vec * 8, h[c]);
+        res[c].load(static_cast<const R *>(a.residual) + row + vec * 8);
         if (a.branch) load8(static_cast<const A *>(a.branch) + row + vec * 8, b[c]);
       }
     }
@@ -171,34 +206,45 @@ __global__ __launch_bounds__(NW * 64) void block_join_kernel(BlockJoin a) {
         for (int c = 0; c < CH; ++c) {
           const int vec = tid + c * NW * 64;
           if (vec < nvec) {
-            float v[8];
-            load8(shared + (i * a.T + t) * a.d + vec * 8, v);
+            Raw<A> v;
+            v.load_once(shared + (i * a.T + t) * a.d + vec * 8);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) b[c][j] += v[j];
+            for (int j = 0; j < 8; ++j) b[c][j] += v.get(j);
           }
         }
-      for (int k = 0; k < a.K; ++k) {
-        const int64_t r = a.slot_row[t * a.K + k];
-        if (r < 0) continue;
-        const float g = a.topk_gate[t * a.K + k];
+      for (int k0 = 0; k0 < a.K; k0 += BATCH) {
+        Raw<A> v[BATCH][CH];
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          const int vec = tid + c * NW * 64;
-          if (vec < nvec) {
-            float v[8];
-            load8(y_rows + r * a.d + vec * 8, v);
+        for (int i = 0; i < BATCH; ++i) {
+          const int64_t r = k0 + i < a.K ? a.slot_row[t * a.K + k0 + i] : -1;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) b[c][j] += g * v[j];
+          for (int c = 0; c < CH; ++c) {
+            const int vec = tid + c * NW * 64;
+            if (r >= 0 && vec < nvec) v[i][c].load_once(y_rows + r * a.d + vec * 8);
           }
+        }
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          if (k0 + i >= a.K || a.slot_row[t * a.K + k0 + i] < 0) continue;
+          const float g = a.topk_gate[t * a.K + k0 + i];
+#pragma unroll
+          for (int c = 0; c < CH; ++c)
+            if (tid + c * NW * 64 < nvec)
+#pragma unroll
+              for (int j = 0; j < 8; ++j) b[c][j] += g * v[i][c].get(j);
         }
       }
     }
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[c][j] = res[c].get(j);
     if (has_branch) {
       if (a.branch_out)
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
           const int vec = tid + c * NW * 64;
-          if (vec < nvec) store8(static_cast<A *>(a.branch_out) + row + vec * 8, b[c]);
+          if (vec < nvec) store8_once(static_cast<A *>(a.branch_out) + row + vec * 8, b[c]);
         }
       normalise<NW, CH>(b, a.norm_out, a.eps, inv_d, nvec, s_sum, turn);
       const float f = a.gate ? a.scale * a.gate[t] : a.scale;
@@ -222,7 +268,7 @@ __global__ __launch_bounds__(NW * 64) void block_join_kernel(BlockJoin a) {
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int vec = tid + c * NW * 64;
-        if (vec < nvec) store8(static_cast<R *>(a.out) + row + vec * 8, h[c]);
+        if (vec < nvec) store8_once(static_cast<R *>(a.out) + row + vec * 8, h[c]);
       }
     if (!a.next) continue;
     normalise<NW, CH>(h, a.norm_in, a.eps, inv_d, nvec, s_sum, turn);
@@ -262,15 +308,16 @@ __device__ __forceinline__ void norm_grad(float (&g)[CH][8], const float (&hat)[
     for (int j = 0; j < 8; ++j) g[c][j] = r * (g[c][j] - m2 - hat[c][j] * m1);
 }
 
-constexpr int kSlots = 4;   // slots whose products are summed in one exchange
+constexpr int kSlots = 2;   // slots whose rows are read, and whose products are summed, together
 
 template <typename A, typename R, int NW, int CH, bool BIAS>
-__global__ __launch_bounds__(NW * 64) void block_join_grad_kernel(BlockJoinGrad a) {
+__global__ __launch_bounds__(NW * 64, NW == 8 && CH <= 2 ? 4 : 1) void block_join_grad_kernel(BlockJoinGrad a) {
   __shared__ Sums<NW, kSlots> s_sum;
   int turn = 0;
   const int tid = threadIdx.x, nvec = a.d / 8;
   const float inv_d = 1.0f / static_cast<float>(a.d);
   const DropKey key = drop_key(a.drop);
+  const bool slots = a.branch && (a.d_y_rows || a.d_topk_gate);
   float swi[CH][8], swo[CH][8], sbi[BIAS ? CH : 1][8], sbo[BIAS ? CH : 1][8];
 #pragma unroll
   for (int c = 0; c < CH; ++c)
@@ -281,17 +328,29 @@ __global__ __launch_bounds__(NW * 64) void block_join_grad_kernel(BlockJoinGrad 
     }
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
     const int64_t row = t * a.d;
-    float dh[CH][8], hat[CH][8];
+    // everything of the token's own rows is on its way before the first sum
+    Raw<A> rn[CH], rb[CH];
+    Raw<R> rh[CH], ro[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int vec = tid + c * NW * 64;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) dh[c][j] = hat[c][j] = 0.0f;
-      if (a.d_next && vec < nvec) {
-        load8(static_cast<const A *>(a.d_next) + row + vec * 8, dh[c]);
-        load8(static_cast<const R *>(a.h) + row + vec * 8, hat[c]);
+      rn[c].zero(), rb[c].zero(), rh[c].zero(), ro[c].zero();
+      if (vec >= nvec) continue;
+      if (a.d_next) {
+        rh[c].load(static_cast<const R *>(a.h) + row + vec * 8);
+        rn[c].load(static_cast<const A *>(a.d_next) + row + vec * 8);
       }
+      if (a.branch) rb[c].load(static_cast<const A *>(a.branch) + row + vec * 8);
+      if (a.d_out) ro[c].load(static_cast<const R *>(a.d_out) + row + vec * 8);
     }
+    float dh[CH][8], hat[CH][8];
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        hat[c][j] = rh[c].get(j);
+        dh[c][j] = rn[c].get(j);
+      }
     if (a.d_next) {
       const float r = normalise<NW, CH>(hat, a.norm_in, a.eps, inv_d, nvec, s_sum, turn);
 #pragma unroll
@@ -312,27 +371,15 @@ __global__ __launch_bounds__(NW * 64) void block_join_grad_kernel(BlockJoinGrad 
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int vec = tid + c * NW * 64;
-      if (vec >= nvec) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dh[c][j] = 0.0f;
-        continue;
+      for (int j = 0; j < 8; ++j) {
+        // behind the row's end LayerNorm's mean left something
+        dh[c][j] = vec < nvec ? dh[c][j] + ro[c].get(j) : 0.0f;
+        hat[c][j] = rb[c].get(j);
       }
-      if (a.d_out) {
-        float v[8];
-        load8(static_cast<const R *>(a.d_out) + row + vec * 8, v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dh[c][j] += v[j];
-      }
-      if (a.d_residual) store8(static_cast<R *>(a.d_residual) + row + vec * 8, dh[c]);
+      if (a.d_residual && vec < nvec) store8_once(static_cast<R *>(a.d_residual) + row + vec * 8, dh[c]);
     }
     if (!a.branch) continue;
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int vec = tid + c * NW * 64;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) hat[c][j] = 0.0f;
-      if (vec < nvec) load8(static_cast<const A *>(a.branch) + row + vec * 8, hat[c]);
-    }
     const float r = normalise<NW, CH>(hat, a.norm_out, a.eps, inv_d, nvec, s_sum, turn);
     const float f = a.gate ? a.scale * a.gate[t] : a.scale;
     float dg[1] = {0.0f};
@@ -359,45 +406,53 @@ __global__ __launch_bounds__(NW * 64) void block_join_grad_kernel(BlockJoinGrad 
       block_sum(s_sum, turn, dg);
       if (tid == 0) a.d_gate[t] = a.scale * dg[0];
     }
-    if (!a.d_branch && !a.d_y_rows && !a.d_topk_gate) continue;
+    if (!a.d_branch && !slots) continue;
     norm_grad<NW, CH>(dh, hat, r, a.norm_out, inv_d, s_sum, turn);
     if (a.d_branch)
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int vec = tid + c * NW * 64;
-        if (vec < nvec) store8(static_cast<A *>(a.d_branch) + row + vec * 8, dh[c]);
+        if (vec < nvec) store8_once(static_cast<A *>(a.d_branch) + row + vec * 8, dh[c]);
       }
-    if (!a.d_y_rows && !a.d_topk_gate) continue;
+    if (!slots) continue;
     for (int k0 = 0; k0 < a.K; k0 += kSlots) {
+      Raw<A> y[kSlots][CH];
+      if (a.d_topk_gate)
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) {
+          const int64_t sr = k0 + i < a.K ? a.slot_row[t * a.K + k0 + i] : -1;
+#pragma unroll
+          for (int c = 0; c < CH; ++c) {
+            const int vec = tid + c * NW * 64;
+            y[i][c].zero();
+            if (sr >= 0 && vec < nvec) y[i][c].load_once(static_cast<const A *>(a.y_rows) + sr * a.d + vec * 8);
+          }
+        }
       float dot[kSlots];
 #pragma unroll
       for (int i = 0; i < kSlots; ++i) {
         dot[i] = 0.0f;
-        const int k = k0 + i;
-        const int64_t sr = k < a.K ? a.slot_row[t * a.K + k] : -1;
+        const int64_t sr = k0 + i < a.K ? a.slot_row[t * a.K + k0 + i] : -1;
         if (sr < 0) continue;
-        const float g = a.topk_gate[t * a.K + k];
+        const float g = a.topk_gate[t * a.K + k0 + i];
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
           const int vec = tid + c * NW * 64;
-          if (vec >= nvec) continue;
-          float v[8];
-          if (a.d_topk_gate) {
-            load8(static_cast<const A *>(a.y_rows) + sr * a.d + vec * 8, v);
+          if (a.d_topk_gate)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) dot[i] += dh[c][j] * v[j];
-          }
-          if (a.d_y_rows) {
+            for (int j = 0; j < 8; ++j) dot[i] += dh[c][j] * y[i][c].get(j);
+          if (a.d_y_rows && vec < nvec) {
+            float v[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = g * dh[c][j];
-            store8(static_cast<A *>(a.d_y_rows) + sr * a.d + vec * 8, v);
+            store8_once(static_cast<A *>(a.d_y_rows) + sr * a.d + vec * 8, v);
           }
         }
       }
       if (a.d_topk_gate) {
         block_sum(s_sum, turn, dot);
         if (tid < kSlots && k0 + tid < a.K)
-          a.d_topk_gate[t * a.K + k0 + tid] = tid == 0 ? dot[0] : tid == 1 ? dot[1] : tid == 2 ? dot[2] : dot[3];
+          a.d_topk_gate[t * a.K + k0 + tid] = tid == 0 ? dot[0] : dot[1];
       }
     }
   }
@@ -414,53 +469,69 @@ __global__ __launch_bounds__(NW * 64) void block_join_grad_kernel(BlockJoinGrad 
   }
 }
 
-// Sums of the workgroups' parts: 64 columns a workgroup, 16 ranges of parts,
-// added in order.
+// Sums of the workgroups' parts: 64 columns a workgroup, four a thread, 64 ranges of
+// parts whose sums are added in order.
 __global__ __launch_bounds__(1024) void block_sum_parts_kernel(const float *part, int parts, int d,
                                                                float *o0, float *o1, float *o2, float *o3) {
   float *out = blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : blockIdx.y == 2 ? o2 : o3;
   if (!out) return;
-  __shared__ float s[16][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, col = blockIdx.x * 64 + lane;
-  float v = 0.0f;
+  __shared__ __attribute__((aligned(16))) float s[64][64];
+  const int quad = threadIdx.x & 15, w = threadIdx.x >> 4, col = blockIdx.x * 64 + quad * 4;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (col < d) {
     const float *p = part + (static_cast<int64_t>(blockIdx.y) * parts) * d + col;
-    const int per = (parts + 15) / 16, end = min(parts, (w + 1) * per);
+    const int per = (parts + 63) / 64, end = min(parts, (w + 1) * per);
 #pragma unroll 8
-    for (int i = w * per; i < end; ++i) v += p[static_cast<int64_t>(i) * d];
+    for (int i = w * per; i < end; ++i) {
+      const float4 x = *reinterpret_cast<const float4 *>(p + static_cast<int64_t>(i) * d);
+      v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+    }
   }
-  s[w][lane] = v;
+  *reinterpret_cast<float4 *>(&s[w][quad * 4]) = v;
   __syncthreads();
-  if (w == 0 && col < d) {
-    v = 0.0f;
+  const int c = threadIdx.x, at = blockIdx.x * 64 + c;
+  if (c < 64 && at < d) {
+    float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v += s[i][lane];
-    out[col] = v;
+    for (int i = 0; i < 64; ++i) sum += s[i][c];
+    out[at] = sum;
   }
 }
 
-// Shape of a workgroup for rows of nvec chunks of 8 elements: one wave up to
-// 64 chunks, else four waves of up to 8 chunks a thread.
+// Shape of a workgroup for rows of nvec chunks of 8 elements: waves, and chunks a thread.
 struct Shape {
   int nw, ch;
 };
-Shape shape_of(int nvec) {
+Shape join_shape(int nvec) {
   if (nvec <= 64) return {1, 1};
+  if (nvec <= 128) return {2, 1};
   if (nvec <= 256) return {4, 1};
   if (nvec <= 512) return {4, 2};
   if (nvec <= 1024) return {4, 4};
-  return {4, 8};
+  return {8, 4};
+}
+Shape grad_shape(int nvec) {
+  if (nvec <= 64) return {1, 1};
+  if (nvec <= 128) return {2, 1};
+  if (nvec <= 256) return {4, 1};
+  if (nvec <= 512) return {8, 1};
+  if (nvec <= 1024) return {8, 2};
+  return {8, 4};
 }
 
+// Workgroups of the gradient: eight of four waves fill a CU.  Every one leaves a part of
+// each sum over tokens, which costs as much as a token's row, so that only few tokens
+// get one each (33 tokens of 1408: 8.5 us, two each 10.9, four each 16.2; 1001: 24.3,
+// 20.0 and 21.5).
 unsigned grad_grid(int64_t T, int d) {
-  const Shape s = shape_of(d / 8);
-  const int64_t most = s.nw == 1 ? 2048 : 512, want = (T + 3) / 4;
+  const Shape s = grad_shape(d / 8);
+  const int64_t most = 4096 / s.nw < 2048 ? 4096 / s.nw : 2048, want = T <= 128 ? T : (T + 1) / 2;
   return static_cast<unsigned>(want < most ? want : most);
 }
 
 template <typename A, typename R, int NW, int CH>
 void launch_join(const BlockJoin &a, hipStream_t s) {
-  const int64_t most = NW == 1 ? 8192 : 2048;
+  const int64_t most = 8192 / NW;
   const dim3 grid(static_cast<unsigned>(a.T < most ? a.T : most));
   hipLaunchKernelGGL((block_join_kernel<A, R, NW, CH>), grid, dim3(NW * 64), 0, s, a);
 }
@@ -474,21 +545,25 @@ void launch_grad(const BlockJoinGrad &a, hipStream_t s) {
     hipLaunchKernelGGL((block_join_grad_kernel<A, R, NW, CH, false>), grid, dim3(NW * 64), 0, s, a);
 }
 
-template <typename A, typename R, typename Args>
-void dispatch_shape(const Args &a, hipStream_t s) {
-  const Shape sh = shape_of(a.d / 8);
-  auto go = [&](auto nw, auto ch) {
-    if constexpr (std::is_same_v<Args, BlockJoin>)
-      launch_join<A, R, nw(), ch()>(a, s);
-    else
-      launch_grad<A, R, nw(), ch()>(a, s);
-  };
-  using std::integral_constant;
-  if (sh.nw == 1) go(integral_constant<int, 1>{}, integral_constant<int, 1>{});
-  else if (sh.ch == 1) go(integral_constant<int, 4>{}, integral_constant<int, 1>{});
-  else if (sh.ch == 2) go(integral_constant<int, 4>{}, integral_constant<int, 2>{});
-  else if (sh.ch == 4) go(integral_constant<int, 4>{}, integral_constant<int, 4>{});
-  else go(integral_constant<int, 4>{}, integral_constant<int, 8>{});
+template <typename A, typename R>
+void dispatch_shape(const BlockJoin &a, hipStream_t s) {
+  const Shape sh = join_shape(a.d / 8);
+  if (sh.nw == 1) launch_join<A, R, 1, 1>(a, s);
+  else if (sh.nw == 2) launch_join<A, R, 2, 1>(a, s);
+  else if (sh.ch == 1) launch_join<A, R, 4, 1>(a, s);
+  else if (sh.ch == 2) launch_join<A, R, 4, 2>(a, s);
+  else if (sh.nw == 4) launch_join<A, R, 4, 4>(a, s);
+  else launch_join<A, R, 8, 4>(a, s);
+}
+template <typename A, typename R>
+void dispatch_shape(const BlockJoinGrad &a, hipStream_t s) {
+  const Shape sh = grad_shape(a.d / 8);
+  if (sh.nw == 1) launch_grad<A, R, 1, 1>(a, s);
+  else if (sh.nw == 2) launch_grad<A, R, 2, 1>(a, s);
+  else if (sh.nw == 4) launch_grad<A, R, 4, 1>(a, s);
+  else if (sh.ch == 1) launch_grad<A, R, 8, 1>(a, s);
+  else if (sh.ch == 2) launch_grad<A, R, 8, 2>(a, s);
+  else launch_grad<A, R, 8, 4>(a, s);
 }
 
 template <typename Args>
