@@ -1,6 +1,11 @@
 // Dropout of rows: y = x / (1 - p) where an element stays, 0 where it is dropped.
 // The same call on the gradient is its backward: the mask is made again from
 // seed, stream and the element's index (philox.h).
+//
+// One pass: a thread makes the eight numbers of one block for eight elements, about
+// 100 operations for 32 bytes of bf16, which the loads and stores still cover (without
+// the generator: 36 us where this takes 37).  32011 x 1408 bf16 elements take 31 us,
+// 5.8 TB/s in and out, with stores past the caches (37 us without).
 #include "moe_common.h"
 #include "philox.h"
 
@@ -32,7 +37,7 @@ __global__ __launch_bounds__(256) void dropout_kernel(const T *x, T *y, int64_t 
           const float f = Act<T>::to_f32(v.e[j]) * drop.keep;
           v.e[j] = Act<T>::from_f32(half_of(r, h * kVec + j) >= drop.cut ? f : 0.0f);
         }
-        *reinterpret_cast<uint4 *>(y + at + h * kVec) = v.q;
+        __builtin_nontemporal_store(__builtin_bit_cast(u32x4_nt_t, v.q), reinterpret_cast<u32x4_nt_t *>(y + at + h * kVec));
       }
     } else {
 #pragma unroll
