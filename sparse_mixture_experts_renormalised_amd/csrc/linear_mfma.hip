@@ -81,6 +81,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(u32x4_t d) {
 __device__ __forceinline__ void dma16b(uint32_t off, u32x4_t desc, uint32_t m0) {
   asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(off), "s"(desc), "{m0}"(m0) : "memory");
 }
+// The same with 4 bytes a lane.
+__device__ __forceinline__ void dma4b(uint32_t off, u32x4_t desc, uint32_t m0) {
+  asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" : : "v"(off), "s"(desc), "{m0}"(m0) : "memory");
+}
 // 16 bytes a lane out, past the caches (whole lines that nothing here reads again).  As
 // the copies' waits count these stores, every lane issues all of them: the descriptor
 // drops what lies behind the tile's rows, and kNoColumn what lies behind its columns.
@@ -302,9 +306,7 @@ struct Source {
   u32x4_t dq, dp;                        // where the step lies
   uint32_t qstep, pstep, pcol;           // bytes of a step; byte offset of this lane's column
   int left;                              // rows (input gradient: steps) of the part from this step on
-  // a gathered x: rows of the group, its next step's first, and that step's indexes
-  int row0, rows, j;
-  int at[GATHER ? 2 * S::PCOPIES : 1];
+  uint32_t at[GATHER ? S::PCOPIES : 1];  // a gathered x: indexes of this lane's rows in the step to come
 
   __device__ __forceinline__ void init(const Args &a, const Tile &t, int wave, int lane) {
     const int n = a.l.n_out, k = a.l.k;
@@ -330,10 +332,6 @@ struct Source {
       dq = descriptor(static_cast<const uint16_t *>(a.l.dy) + (t.row0 + j0) * n, 0);
       if constexpr (GATHER) {
         dp = descriptor(a.l.x, 0);
-        row0 = static_cast<int>(t.row0);
-        rows = t.rows;
-        j = static_cast<int>(j0);
-        load_index(a, wave);
       } else {
         dp = descriptor(static_cast<const uint16_t *>(a.l.x) + (t.row0 + j0) * k, 0);
       }
@@ -380,27 +378,19 @@ struct Source {
       dp[2] = uniform(GATHER ? (left > 0 ? static_cast<uint32_t>(a.l.x_rows * a.l.k * 2) : 0) : have * a.l.k * 2);
     }
   }
-  // Indexes of the step at j (rows of the group from 0 on).  They go through the scalar
-  // cache: vector loads would be counted with the copies.
-  __device__ __forceinline__ void load_index(const Args &a, int wave) {
-    const auto *index = (const __attribute__((address_space(4))) int32_t *)(a.l.index);
-    const int most = max(0, min(rows, static_cast<int>(a.l.max_rows) - row0) - 1), none = row0 < a.l.max_rows ? row0 : 0;
+  // The step's indexes, which lie at LDS byte `from`; and this lane's offsets from them.
+  __device__ __forceinline__ void load_index(uint32_t from, int lane) {
+    static_assert(!GATHER || (S::P == 256 && S::PCOPIES == 2), "two copies of two lines");
+    typedef __attribute__((address_space(3))) const volatile uint32_t lds_u32_t;
+    const lds_u32_t *r = reinterpret_cast<lds_u32_t *>(from + (lane >> 5) * 4);
 #pragma unroll
-    for (int i = 0; i < 2 * S::PCOPIES; ++i)
-      at[i] = index[none + min(j + 2 * (S::WAVES * (i / 2) + wave) + i % 2, most)];
-    j += kJ;
+    for (int i = 0; i < S::PCOPIES; ++i) at[i] = r[2 * i];
   }
-  // This lane's offsets of the step whose indexes were loaded, and the next one's indexes.
   __device__ __forceinline__ void gather(const Args &a, int wave, int lane) {
-    if constexpr (GATHER) {
-      static_assert(S::P == 256, "two lines a copy");
 #pragma unroll
-      for (int i = 0; i < S::PCOPIES; ++i) {
-        const uint32_t r = lane >> 5 ? at[2 * i + 1] : at[2 * i];
-        const bool there = 2 * (S::WAVES * i + wave) + (lane >> 5) < left;
-        p[i] = there ? r * static_cast<uint32_t>(a.l.k * 2) + pcol : kNoColumn;
-      }
-      load_index(a, wave);
+    for (int i = 0; i < S::PCOPIES; ++i) {
+      const uint32_t o = at[i] * static_cast<uint32_t>(a.l.k * 2) + pcol;
+      p[i] = 2 * (S::WAVES * i + wave) + (lane >> 5) < left ? o : kNoColumn;
     }
   }
   // Copy number i of the step into the stage at LDS byte m0 (this wave's first KB).
@@ -409,6 +399,46 @@ struct Source {
     m0 += i * 1024 * S::WAVES;
     if (pi < 0) dma16b(q[i], dq, m0);
     else dma16b(p[pi], dp, m0);
+  }
+};
+
+// Indexes of a gathered x, for one wave: it needs four rows a step, so that one copy of
+// 64 dwords brings sixteen steps' into a slot of its own, in a ring of four.  They come
+// four steps ahead and are read one step ahead, when a wait for copies has covered them.  (As scalar loads
+// they cost a sixth of the products: every wait for LDS reads then waits for them too.)
+template <typename S>
+struct IndexStream {
+  static constexpr int STEPS = 16, SLOTS = 4, BYTES = SLOTS * S::WAVES * 256;
+  u32x4_t desc;
+  uint32_t base;           // this wave's part of slot 0
+  int issue, use, pos;     // slot to fill, slot in use, step in it
+  int row, end;            // first row of the next chunk of the tile, and the group's end
+
+  __device__ __forceinline__ void init(const Args &a, uint32_t lds, int wave) {
+    desc = descriptor(a.l.index, a.l.max_rows * 4);
+    base = lds + wave * 256;
+    issue = 0;
+    use = pos = 0;
+  }
+  static __device__ __forceinline__ uint32_t slot(int i) { return i * S::WAVES * 256; }
+  __device__ __forceinline__ void chunk(int wave, int lane) {
+    const int r = row + (lane >> 2) * kJ + 2 * (S::WAVES * ((lane >> 1) & 1) + wave) + (lane & 1);
+    dma4b(r < end ? static_cast<uint32_t>(r) * 4 : kNoColumn, desc, base + slot(issue));
+    issue = (issue + 1) % SLOTS;
+    row += STEPS * kJ;
+  }
+  // The first chunk of a tile that comes next.
+  __device__ __forceinline__ void start(const Tile &t, int wave, int lane) {
+    row = static_cast<int>(t.row0) + t.s0 * kJ;
+    end = static_cast<int>(t.row0) + t.rows;
+    chunk(wave, lane);
+  }
+  __device__ __forceinline__ uint32_t place() const { return base + slot(use) + pos * 16; }
+  // At a step behind which `left` steps of its tile are left: to the next one.
+  __device__ __forceinline__ void next(int left, int wave, int lane) {
+    if (pos == STEPS - 4 && left > 3) chunk(wave, lane);
+    pos = left > 0 ? (pos + 1) % STEPS : 0;
+    if (pos == 0) use = (use + 1) % SLOTS;
   }
 };
 
@@ -599,6 +629,7 @@ __global__ __launch_bounds__(S::NT, S::WGS * S::WAVES / 4) void linear_grad_kern
   static_assert(EARLY * 2 <= GROUPS && LATE * 2 <= GROUPS, "at most one for two products");
   __shared__ __attribute__((aligned(1024))) char s_ring[RING * S::STAGE];
   __shared__ int s_pref[kMaxGroups + 1], s_off[kMaxGroups + 1], s_tmp[S::WAVES];
+  __shared__ __attribute__((aligned(256))) char s_index[GATHER ? IndexStream<S>::BYTES : 4];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   // Waves w and w + 4 share a SIMD: with blocks that lie behind a tile's rows (or columns)
   // left out, the SIMDs still have about the same to multiply.
@@ -618,34 +649,58 @@ __global__ __launch_bounds__(S::NT, S::WGS * S::WAVES / 4) void linear_grad_kern
   // the one that is multiplied.  A tile has RING steps at least, so that `fill` is that
   // one's tile or the next.
   Source<S, MODE, GATHER> src;
+  IndexStream<S> rows;
   int fill_item = item;
-  Tile fill = tile_at<S, MODE>(a, plan, s_pref, s_off, item, 0);
-  src.init(a, fill, wave, lane);
+  Tile fill = tile_at<S, MODE>(a, plan, s_pref, s_off, item, 0), ahead = fill;
   int fill_left = max(fill.s1 - fill.s0, RING), steps = fill_left;   // the one at hand among them
+  // Four steps before a tile's end, the next one is looked up.
+  auto look_ahead = [&]() {
+    static_assert(RING >= 4, "a tile has four steps at least");
+    if (fill_left != 4 || fill_item + stride >= plan.end) return;
+    ahead = tile_at<S, MODE>(a, plan, s_pref, s_off, fill_item + stride, fill.g);
+    if constexpr (GATHER) rows.start(ahead, wave, lane);
+  };
+  // The next tile, where this one's steps are all copied; then the next step.
   bool fresh = false;
-  src.gather(a, wave, lane);
-  // the next tile, where this one's steps are all copied; else the next step
   auto next_tile = [&]() {
     if (fill_left > 1) return;
     fill_item += stride;
     if (fill_item < plan.end) {
       int el = lane;
       asm volatile("" : "+v"(el));       // as for the sums below
-      fill = tile_at<S, MODE>(a, plan, s_pref, s_off, fill_item, fill.g);
+      fill = ahead;
       src.init(a, fill, wave, el);
       fill_left = max(fill.s1 - fill.s0, RING) + 1;
+      fresh = true;
     } else {
       src.none(a);
       fill_left = 0x7FFFFFFF;
     }
-    fresh = true;
   };
   auto next_step = [&]() {
     if (!fresh) src.advance(a);
-    fresh = false;
     --fill_left;
-    src.gather(a, wave, lane);
+    fresh = false;
+    if constexpr (GATHER) src.gather(a, wave, lane);
+    look_ahead();
+    if constexpr (GATHER) {
+      rows.next(fill_left - 1, wave, lane);
+      src.load_index(rows.place(), lane);
+    }
   };
+  src.init(a, fill, wave, lane);
+  if constexpr (GATHER) {
+    rows.init(a, uniform(static_cast<int>(dma::lds_addr(s_index))), wave);
+    rows.start(fill, wave, lane);
+  }
+  look_ahead();
+  if constexpr (GATHER) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copies yet that would cover these
+    src.load_index(rows.place(), lane);
+    src.gather(a, wave, lane);
+    rows.next(fill_left - 1, wave, lane);
+    src.load_index(rows.place(), lane);
+  }
 #pragma unroll
   for (int s = 0; s < RING; ++s) {
 #pragma unroll
@@ -924,12 +979,12 @@ using Tiles = Shape<2, 4, 4>;
 
 }  // namespace
 
-// Widths whose lines of a tile stay below 4 GiB, a gathered x that does, and items that
+// Widths whose lines of a tile stay below 4 GiB, a gathered x and its indexes that do, and items that
 // are counted in 31 bits.
 bool linear_grad_fits(const Linear &p) {
   if (!p.bf16 || p.mode == kLinForward || p.n_out >= (1 << 20) || p.k >= (1 << 20)) return false;
   if (tile_bound<Tiles>(p.mode, p.groups, p.n_out, p.k, p.max_rows) >= (int64_t(1) << 30)) return false;
-  return p.mode != kLinWeightGrad || !p.index || p.x_rows <= 0xFFFFFE00ll / 2 / p.k;
+  return p.mode != kLinWeightGrad || !p.index || (p.x_rows <= 0xFFFFFE00ll / 2 / p.k && p.max_rows < (1 << 30));
 }
 
 size_t linear_grad_workspace_bytes(int groups, int n_out, int k, int64_t max_rows) {
