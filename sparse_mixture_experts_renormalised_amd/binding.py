@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -141,9 +142,8 @@ def lib():
             "moe_grouped_linear_weight_grad": (I, [I32, I32, I32, I32, I32, P, I64, P, P, P, I64, P,
                                                    P, I32, P, Z, P]),
             "moe_grouped_linear_workspace_size": (Z, [I32, I32, I32, I32, I64]),
-            "moe_block_join": (I, [ctypes.POINTER(Block), ctypes.POINTER(BlockTensors), P, P, P, P]),
-            "moe_block_join_grad": (I, [ctypes.POINTER(Block), ctypes.POINTER(BlockTensors), P, P, P,
-                                        ctypes.POINTER(BlockGrads), P, Z, P]),
+            "moe_block_join": (I, [ctypes.POINTER(Block), P, P, P, P, P]),
+            "moe_block_join_grad": (I, [ctypes.POINTER(Block), P, P, P, P, P, P, Z, P]),
             "moe_block_join_grad_workspace_size": (Z, [ctypes.POINTER(Block)]),
             "moe_dropout": (I, [I32, I64, I64, P, P, P, ctypes.c_double, P, P]),
             "moe_workspace_size": (Z, [C]),
@@ -418,6 +418,7 @@ def layer_forward_few_mxfp4(cfg: Config, w: WeightsMxfp4, x, y, topk_idx=None, t
 # --------------------------------------------------------------------------
 _DTYPES = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
 _NAMES = {"f32": MOE_F32, "bf16": MOE_BF16, MOE_F32: MOE_F32, MOE_BF16: MOE_BF16}
+_I32, _F32 = torch.int32, torch.float32
 
 
 def _dtype(t, what: str) -> int:
@@ -427,10 +428,54 @@ def _dtype(t, what: str) -> int:
     return code
 
 
-def _fits(t, dtype, shape, what: str):
-    """None, or a tensor of that type and shape."""
-    if t is not None and (t.dtype is not dtype or t.shape != shape):
+def _device() -> int:
+    """The current GPU, on whose streams the calls work (-2: none was used yet)."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+
+
+def _arg(t, dev: int, dtype, shape, what: str) -> int:
+    """Address of a dense tensor of that type and shape on the GPU `dev` (0 for
+    None).  One check after the other costs a small call less than one pass of
+    each over all tensors."""
+    if t is None:
+        return 0
+    if t.get_device() != dev:
+        raise ValueError(f"{what} must be on the current GPU")
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{what} must be {list(shape)} {str(dtype)[6:]}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def _list(t, dev: int, dtype, least: int, what: str) -> int:
+    """Address of a dense tensor of at least that many elements."""
+    if t is None:
+        return 0
+    if t.get_device() != dev:
+        raise ValueError(f"{what} must be on the current GPU")
+    if t.dtype is not dtype or t.numel() < least or not t.is_contiguous():
+        raise ValueError(f"{what} must be [{least}] {str(dtype)[6:]}, contiguous")
+    return t.data_ptr()
+
+
+def _scratch(ws, dev: int):
+    """Address and bytes of a workspace."""
+    if ws is None:
+        return 0, 0
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws must be contiguous and on the current GPU")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _rng(t, dev: int) -> int:
+    """Address of {seed, stream}."""
+    if t is None:
+        return 0
+    if t.get_device() != dev or t.element_size() != 8 or t.is_floating_point() or t.numel() != 2 or \
+            not t.is_contiguous():
+        raise ValueError("rng must be [2] int64 (seed, stream) on the current GPU")
+    return t.data_ptr()
 
 
 def grouped_linear_workspace_size(dtype, n_groups, n_out, k, max_rows) -> int:
@@ -439,78 +484,62 @@ def grouped_linear_workspace_size(dtype, n_groups, n_out, k, max_rows) -> int:
                                                        int(max_rows)))
 
 
-def _linear_sizes(w, offsets, what: str):
+def _linear_sizes(w, offsets, rows, dev: int, what: str, rows_what: str):
+    """G, n_out, k, the offsets' address, and the rows that the groups may have."""
     _need(w.dim() == 3, f"{what} must be [G, n_out, k]")
-    _need(offsets.dtype is torch.int32 and offsets.numel() == w.shape[0] + 1, "offsets must be [G + 1] int32")
-    return w.shape
+    _need(rows.dim() == 2, f"{rows_what} must have two dimensions")
+    g, n_out, k = w.shape
+    _need(offsets.numel() == g + 1, "offsets must be [G + 1] int32")
+    return g, n_out, k, _list(offsets, dev, _I32, g + 1, "offsets"), rows.shape[0]
 
 
-def _source_rows(x, row_index, k: int, max_rows: int) -> int:
-    _need(x.dim() == 2 and x.shape[1] == k, "x must be [., k]")
-    if row_index is None:
-        _need(x.shape[0] >= max_rows, "x has fewer rows than the groups may have (and no row_index)")
-    else:
-        _need(row_index.dtype is torch.int32 and row_index.numel() >= max_rows,
-              "row_index must be [max_rows] int32")
-    return x.shape[0]
-
-
-def _bytes(ws) -> int:
-    return 0 if ws is None else ws.numel() * ws.element_size()
+def _source_rows(x, dtype, row_index, k: int, max_rows: int, dev: int):
+    """Addresses of x and row_index, and the rows of x."""
+    _need(x.dim() == 2, "x must be [., k]")
+    n = x.shape[0]
+    _need(row_index is not None or n >= max_rows, "x has fewer rows than the groups may have (and no row_index)")
+    return _arg(x, dev, dtype, (n, k), "x"), _list(row_index, dev, _I32, max_rows, "row_index"), n
 
 
 def grouped_linear(x, offsets, w, y, row_index=None, bias=None, silu=False, pre=None, ws=None,
                    stream=None):
     """y [max_rows, n_out] of x rows [., k] and weights [G, n_out, k] (bf16 or
     f32); with silu, pre keeps the values before it."""
-    _on_device(x, offsets, w, y, row_index, bias, pre, ws)
-    dt, act = _dtype(w, "w"), w.dtype
-    g, n_out, k = _linear_sizes(w, offsets, "w")
-    _need(y.dim() == 2, "y must be [max_rows, n_out]")
-    max_rows = y.shape[0]
-    _fits(y, act, (max_rows, n_out), "y")
-    _fits(pre, act, (max_rows, n_out), "pre")
-    _fits(bias, act, (g, n_out), "bias")
-    _need(x.dtype is act, "x must have the weights' type")
-    x_rows = _source_rows(x, row_index, k, max_rows)
+    dev, act = _device(), w.dtype
+    g, n_out, k, off, max_rows = _linear_sizes(w, offsets, y, dev, "w", "y")
+    xp, index, x_rows = _source_rows(x, act, row_index, k, max_rows, dev)
+    out = (max_rows, n_out)
+    wsp, nbytes = _scratch(ws, dev)
     _check("moe_grouped_linear", lib().moe_grouped_linear(
-        dt, g, n_out, k, x_rows, _ptr(x), _ptr(row_index), _ptr(offsets), max_rows, _ptr(w), _ptr(bias),
-        int(bool(silu)), _ptr(y), _ptr(pre), _ptr(ws), _bytes(ws), _stream(stream)))
+        _dtype(w, "w"), g, n_out, k, x_rows, xp, index, off, max_rows, _arg(w, dev, act, (g, n_out, k), "w"),
+        _arg(bias, dev, act, (g, n_out), "bias"), 1 if silu else 0, _arg(y, dev, act, out, "y"),
+        _arg(pre, dev, act, out, "pre"), wsp, nbytes, _stream(stream)))
 
 
 def grouped_linear_input_grad(dy, offsets, w, dx, pre=None, ws=None, stream=None):
     """dx [max_rows, k] of dy [max_rows, n_out] and weights [G, n_out, k]; times
     the SiLU's derivative at pre [max_rows, k], if given."""
-    _on_device(dy, offsets, w, dx, pre, ws)
-    dt, act = _dtype(w, "w"), w.dtype
-    g, n_out, k = _linear_sizes(w, offsets, "w")
-    _need(dx.dim() == 2, "dx must be [max_rows, k]")
-    max_rows = dx.shape[0]
-    _fits(dx, act, (max_rows, k), "dx")
-    _fits(pre, act, (max_rows, k), "pre")
-    _fits(dy, act, (max_rows, n_out), "dy")
+    dev, act = _device(), w.dtype
+    g, n_out, k, off, max_rows = _linear_sizes(w, offsets, dx, dev, "w", "dx")
+    wsp, nbytes = _scratch(ws, dev)
     _check("moe_grouped_linear_input_grad", lib().moe_grouped_linear_input_grad(
-        dt, g, n_out, k, _ptr(dy), _ptr(offsets), max_rows, _ptr(w), _ptr(pre), _ptr(dx), _ptr(ws),
-        _bytes(ws), _stream(stream)))
+        _dtype(w, "w"), g, n_out, k, _arg(dy, dev, act, (max_rows, n_out), "dy"), off, max_rows,
+        _arg(w, dev, act, (g, n_out, k), "w"), _arg(pre, dev, act, (max_rows, k), "pre"),
+        _arg(dx, dev, act, (max_rows, k), "dx"), wsp, nbytes, _stream(stream)))
 
 
 def grouped_linear_weight_grad(dy, offsets, x, dw, row_index=None, dbias=None, accumulate=False, ws=None,
                                stream=None):
     """dw [G, n_out, k] and dbias [G, n_out] (the rows' type or f32) of dy
     [max_rows, n_out] and x rows [., k]; added to what they hold, if asked."""
-    _on_device(dy, offsets, x, dw, row_index, dbias, ws)
-    dt, act = _dtype(dy, "dy"), dy.dtype
-    g, n_out, k = _linear_sizes(dw, offsets, "dw")
-    grad = _dtype(dw, "dw")
-    _need(dy.dim() == 2, "dy must be [max_rows, n_out]")
-    max_rows = dy.shape[0]
-    _fits(dy, act, (max_rows, n_out), "dy")
-    _fits(dbias, dw.dtype, (g, n_out), "dbias")
-    _need(x.dtype is act, "x must have dy's type")
-    x_rows = _source_rows(x, row_index, k, max_rows)
+    dev, act, grad = _device(), dy.dtype, dw.dtype
+    g, n_out, k, off, max_rows = _linear_sizes(dw, offsets, dy, dev, "dw", "dy")
+    xp, index, x_rows = _source_rows(x, act, row_index, k, max_rows, dev)
+    wsp, nbytes = _scratch(ws, dev)
     _check("moe_grouped_linear_weight_grad", lib().moe_grouped_linear_weight_grad(
-        dt, grad, g, n_out, k, _ptr(dy), x_rows, _ptr(x), _ptr(row_index), _ptr(offsets), max_rows,
-        _ptr(dw), _ptr(dbias), int(bool(accumulate)), _ptr(ws), _bytes(ws), _stream(stream)))
+        _dtype(dy, "dy"), _dtype(dw, "dw"), g, n_out, k, _arg(dy, dev, act, (max_rows, n_out), "dy"), x_rows, xp,
+        index, off, max_rows, _arg(dw, dev, grad, (g, n_out, k), "dw"),
+        _arg(dbias, dev, grad, (g, n_out), "dbias"), 1 if accumulate else 0, wsp, nbytes, _stream(stream)))
 
 
 MOE_NORM_NONE, MOE_NORM_RMS, MOE_NORM_LAYER = 0, 1, 2
@@ -527,27 +556,9 @@ def block(T, d_model, dtype, res_dtype=None, norm_out="none", norm_in="rms", eps
 
 
 _ACT = {MOE_BF16: torch.bfloat16, MOE_F32: torch.float32}
-
-
-def _block_tensors(cfg: Block, residual, branch, y_rows, slot_row, topk_gate, shared_out, gate, w_out, b_out,
-                   w_in, b_in, rng) -> BlockTensors:
-    _on_device(residual, branch, y_rows, slot_row, topk_gate, shared_out, gate, w_out, b_out, w_in, b_in, rng)
-    T, d, k, f32 = cfg.T, cfg.d_model, cfg.top_k, torch.float32
-    act = _ACT.get(cfg.dtype)
-    _fits(residual, _ACT.get(cfg.res_dtype), (T, d), "residual")
-    _fits(branch, act, (T, d), "branch")
-    if y_rows is not None:
-        _fits(y_rows, act, (y_rows.shape[0], d), "y_rows")
-    _fits(slot_row, torch.int32, (T, k), "slot_row")
-    _fits(topk_gate, f32, (T, k), "topk_gate")
-    _fits(shared_out, act, (cfg.n_shared, T, d), "shared_out")
-    _fits(gate, f32, (T,), "gate")
-    for name, t in (("w_out", w_out), ("b_out", b_out), ("w_in", w_in), ("b_in", b_in)):
-        _fits(t, f32, (d,), name)
-    _need(rng is None or (rng.dtype in (torch.int64, torch.uint64) and rng.numel() == 2),
-          "rng must be [2] int64 (seed, stream)")
-    return BlockTensors(*[_ptr(t) for t in (residual, branch, y_rows, slot_row, topk_gate, shared_out, gate,
-                                            w_out, b_out, w_in, b_in, rng)])
+# moe_block_tensors and moe_block_grads as bytes: quicker than filling a Structure
+_TENSORS = struct.Struct(f"{len(BlockTensors._fields_)}P")
+_GRADS = struct.Struct(f"{len(BlockGrads._fields_)}P")
 
 
 def block_join(cfg: Block, residual, out=None, next=None, branch=None, y_rows=None, slot_row=None,
@@ -555,15 +566,19 @@ def block_join(cfg: Block, residual, out=None, next=None, branch=None, y_rows=No
                w_in=None, b_in=None, rng=None, stream=None):
     """out = residual + scale gate Drop(Norm_out(branch or combined expert rows)),
     next = Norm_in(out); branch_out keeps the combined rows."""
-    t = _block_tensors(cfg, residual, branch, y_rows, slot_row, topk_gate, shared_out, gate, w_out, b_out,
-                       w_in, b_in, rng)
-    _on_device(out, next, branch_out)
-    act, shape = _ACT.get(cfg.dtype), (cfg.T, cfg.d_model)
-    _fits(out, _ACT.get(cfg.res_dtype), shape, "out")
-    _fits(next, act, shape, "next")
-    _fits(branch_out, act, shape, "branch_out")
-    _check("moe_block_join", lib().moe_block_join(ctypes.byref(cfg), ctypes.byref(t), _ptr(out), _ptr(next),
-                                                  _ptr(branch_out), _stream(stream)))
+    dev, act, res = _device(), _ACT.get(cfg.dtype), _ACT.get(cfg.res_dtype)
+    T, d = cfg.T, cfg.d_model
+    rows, wide, slots = (T, d), (d,), (T, cfg.top_k)
+    t = _TENSORS.pack(
+        _arg(residual, dev, res, rows, "residual"), _arg(branch, dev, act, rows, "branch"),
+        _arg(y_rows, dev, act, rows if y_rows is None else (y_rows.shape[0], d), "y_rows"),
+        _arg(slot_row, dev, _I32, slots, "slot_row"), _arg(topk_gate, dev, _F32, slots, "topk_gate"),
+        _arg(shared_out, dev, act, (cfg.n_shared, T, d), "shared_out"), _arg(gate, dev, _F32, (T,), "gate"),
+        _arg(w_out, dev, _F32, wide, "w_out"), _arg(b_out, dev, _F32, wide, "b_out"),
+        _arg(w_in, dev, _F32, wide, "w_in"), _arg(b_in, dev, _F32, wide, "b_in"), _rng(rng, dev))
+    _check("moe_block_join", lib().moe_block_join(
+        ctypes.byref(cfg), t, _arg(out, dev, res, rows, "out"), _arg(next, dev, act, rows, "next"),
+        _arg(branch_out, dev, act, rows, "branch_out"), _stream(stream)))
 
 
 def block_join_grad_workspace_size(cfg: Block) -> int:
@@ -576,40 +591,37 @@ def block_join_grad(cfg: Block, d_out, d_next, out, branch=None, y_rows=None, sl
                     d_b_in=None, ws=None, stream=None):
     """Gradients of block_join's inputs (those given as outputs) from d_out and
     d_next; out and branch as the forward left them."""
-    t = _block_tensors(cfg, None, branch, y_rows, slot_row, topk_gate, None, gate, w_out, b_out, w_in, None, rng)
-    _on_device(d_out, d_next, out, d_residual, d_branch, d_y_rows, d_topk_gate, d_gate, d_w_out, d_b_out, d_w_in,
-               d_b_in, ws)
-    act, res, f32, shape = _ACT.get(cfg.dtype), _ACT.get(cfg.res_dtype), torch.float32, (cfg.T, cfg.d_model)
-    for name, v, dt in (("d_out", d_out, res), ("out", out, res), ("d_residual", d_residual, res),
-                        ("d_next", d_next, act), ("d_branch", d_branch, act)):
-        _fits(v, dt, shape, name)
-    if d_y_rows is not None:
-        _need(y_rows is None or d_y_rows.shape == y_rows.shape, "d_y_rows must have y_rows' shape")
-        _fits(d_y_rows, act, (d_y_rows.shape[0], cfg.d_model), "d_y_rows")
-    _fits(d_topk_gate, f32, (cfg.T, cfg.top_k), "d_topk_gate")
-    _fits(d_gate, f32, (cfg.T,), "d_gate")
-    for name, v in (("d_w_out", d_w_out), ("d_b_out", d_b_out), ("d_w_in", d_w_in), ("d_b_in", d_b_in)):
-        _fits(v, f32, (cfg.d_model,), name)
-    g = BlockGrads(*[_ptr(v) for v in (d_residual, d_branch, d_y_rows, d_topk_gate, d_gate, d_w_out, d_b_out,
-                                       d_w_in, d_b_in)])
+    dev, act, res = _device(), _ACT.get(cfg.dtype), _ACT.get(cfg.res_dtype)
+    T, d = cfg.T, cfg.d_model
+    rows, wide, slots = (T, d), (d,), (T, cfg.top_k)
+    of_y = None if y_rows is None else (y_rows.shape[0], d)
+    of_dy = of_y or (None if d_y_rows is None else (d_y_rows.shape[0], d))
+    t = _TENSORS.pack(
+        0, _arg(branch, dev, act, rows, "branch"), _arg(y_rows, dev, act, of_y, "y_rows"),
+        _arg(slot_row, dev, _I32, slots, "slot_row"), _arg(topk_gate, dev, _F32, slots, "topk_gate"), 0,
+        _arg(gate, dev, _F32, (T,), "gate"), _arg(w_out, dev, _F32, wide, "w_out"),
+        _arg(b_out, dev, _F32, wide, "b_out"), _arg(w_in, dev, _F32, wide, "w_in"), 0, _rng(rng, dev))
+    g = _GRADS.pack(
+        _arg(d_residual, dev, res, rows, "d_residual"), _arg(d_branch, dev, act, rows, "d_branch"),
+        _arg(d_y_rows, dev, act, of_dy, "d_y_rows"), _arg(d_topk_gate, dev, _F32, slots, "d_topk_gate"),
+        _arg(d_gate, dev, _F32, (T,), "d_gate"), _arg(d_w_out, dev, _F32, wide, "d_w_out"),
+        _arg(d_b_out, dev, _F32, wide, "d_b_out"), _arg(d_w_in, dev, _F32, wide, "d_w_in"),
+        _arg(d_b_in, dev, _F32, wide, "d_b_in"))
+    wsp, nbytes = _scratch(ws, dev)
     _check("moe_block_join_grad", lib().moe_block_join_grad(
-        ctypes.byref(cfg), ctypes.byref(t), _ptr(out), _ptr(d_out), _ptr(d_next), ctypes.byref(g), _ptr(ws),
-        _bytes(ws), _stream(stream)))
+        ctypes.byref(cfg), t, _arg(out, dev, res, rows, "out"), _arg(d_out, dev, res, rows, "d_out"),
+        _arg(d_next, dev, act, rows, "d_next"), g, wsp, nbytes, _stream(stream)))
 
 
 def dropout(x, y, p, rng, n_rows=None, stream=None):
     """y = x / (1 - p) or 0, by the numbers of rng [2] (seed, stream); rows at or
     beyond n_rows [1] (int32, on the GPU) stay as they are.  y may be x."""
-    _on_device(x, y, rng, n_rows)
-    dt = _dtype(x, "x")
-    _need(x.dim() == 2, "x must be [rows, d]")
+    dev, dt = _device(), x.dtype
     rows, d = x.shape
-    _fits(y, x.dtype, (rows, d), "y")
-    _need(rng is None or (rng.dtype in (torch.int64, torch.uint64) and rng.numel() == 2),
-          "rng must be [2] int64 (seed, stream)")
-    _need(n_rows is None or (n_rows.dtype is torch.int32 and n_rows.numel() == 1), "n_rows must be [1] int32")
-    _check("moe_dropout", lib().moe_dropout(dt, rows, d, _ptr(x), _ptr(y), _ptr(n_rows), float(p), _ptr(rng),
-                                            _stream(stream)))
+    shape = (rows, d)
+    _check("moe_dropout", lib().moe_dropout(
+        _dtype(x, "x"), rows, d, _arg(x, dev, dt, shape, "x"), _arg(y, dev, dt, shape, "y"),
+        _list(n_rows, dev, _I32, 1, "n_rows"), p, _rng(rng, dev), _stream(stream)))
 
 
 class HipEvents:
