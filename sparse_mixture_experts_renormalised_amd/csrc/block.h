@@ -2,8 +2,6 @@
 // dropout.hip).  Not part of the public interface.
 #pragma once
 
-#include <type_traits>
-
 #include "moe_common.h"
 #include "philox.h"
 

@@ -394,10 +394,12 @@ __global__ __launch_bounds__(NW * 64, NW == 8 && CH <= 2 ? 4 : 1) void block_joi
                                  : make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float u = half_of(q, j) >= a.drop.cut ? dh[c][j] * a.drop.keep : 0.0f;
-        dg[0] += u * (hat[c][j] * w[j] + o[j]);
+        // a dropped element takes no part, whatever its value is
+        const bool stays = half_of(q, j) >= a.drop.cut;
+        const float u = stays ? dh[c][j] * a.drop.keep : 0.0f, v = stays ? hat[c][j] : 0.0f;
+        dg[0] += u * (v * w[j] + o[j]);
         const float g = f * u;
-        swo[c][j] += g * hat[c][j];
+        swo[c][j] += g * v;
         if (BIAS) sbo[c][j] += g;
         dh[c][j] = g * w[j];
       }

@@ -337,3 +337,26 @@ def test_other_streams_and_graphs(B):
         for k in gref:
             assert torch.equal(gref[k], ggot[k]) and torch.equal(gref[k], gside[k]), k
         run(B, case, act, res, t, 0.5, outs=ref)
+
+
+def test_a_dropped_element_takes_no_part(B):
+    """Without a norm of the branch, what a dropped element holds reaches no output."""
+    case = (9, 264, 0, 0, "none", "none", False, True, 0.4)
+    t = make(case, "bf16", "f32", 12)
+    t["w_out"] = torch.rand(264, device="cuda") + 0.5
+    keep = torch.from_numpy(oracle.dropout_keep(9 * 264, 0.4, 12, 77).reshape(9, 264)).cuda()
+    got = []
+    for value in (0.0, float("inf"), float("nan")):
+        t["branch"] = t["branch"].masked_fill(~keep.bool(), value)
+        cfg, o = run(B, case, "bf16", "f32", t, 0.5)
+        g = {"d_residual": torch.empty(9, 264, device="cuda"), "d_gate": torch.empty(9, device="cuda"),
+             "d_branch": torch.empty(9, 264, dtype=torch.bfloat16, device="cuda"), "d_w_out": torch.empty(264, device="cuda")}
+        ws = torch.empty(B.block_join_grad_workspace_size(cfg), dtype=torch.uint8, device="cuda")
+        B.block_join_grad(cfg, t["residual"], o["next"], o["out"], branch=t["branch"], gate=t["gate"], w_out=t["w_out"],
+                          w_in=t["w_in"], rng=t["rng"], ws=ws, **g)
+        torch.cuda.synchronize()
+        got.append([o["out"], o["next"], *g.values()])
+    assert all(v.isfinite().all() for v in got[0])
+    for other in got[1:]:
+        for a, b in zip(got[0], other):
+            assert torch.equal(a, b)
