@@ -512,8 +512,8 @@ int moe_layer_forward_few_mxfp4(const moe_config *cfg, const moe_weights_mxfp4 *
  *               is one size for the three calls; nothing in it needs to be
  *               initialised, and calls that overlap in time need one each
  * n_out and k are multiples of 64 for MOE_BF16 and of 16 for MOE_F32 (as d_model
- * and d_ff of the layer), n_groups <= 1088, max_rows < 2^31; else
- * MOE_ERR_UNSUPPORTED.
+ * and d_ff of the layer), n_groups <= 1088, max_rows < 2^30; else
+ * MOE_ERR_UNSUPPORTED.  Here and in the gradients, outputs overlap no input.
  */
 int moe_grouped_linear(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k, int64_t x_rows,
                        const void *x, const int32_t *row_index, const int32_t *offsets,
@@ -638,7 +638,8 @@ typedef struct {
  *               d_y_rows and d_topk_gate
  *   ws          device scratch of moe_block_join_grad_workspace_size bytes where a
  *               sum over tokens is asked for (else it may be NULL)
- * d_residual may be d_out itself.  T == 0 writes zeros to the sums over tokens.
+ * d_residual may be d_out itself, else outputs overlap no input.  With d_y_rows no
+ * row is named twice in slot_row (a dispatch names none twice).  T == 0 writes zeros to the sums over tokens.
  * Equal calls give equal bits.
  */
 int moe_block_join_grad(const moe_block *cfg, const moe_block_tensors *in, const void *out,
@@ -657,7 +658,7 @@ size_t moe_block_join_grad_workspace_size(const moe_block *cfg);
  * is that of x.
  *   x, y        [rows][d] dtype; y may be x
  *   n_rows      [1] int32 DEVICE value or NULL: rows at or beyond it (a
- *               dispatch's offsets[N]) are neither read nor written
+ *               dispatch's offsets[N], 4-byte aligned) are neither read nor written
  *   p           in [0, 1), at most 1 - 2^-16 after rounding
  *   rng         [2] uint64 DEVICE array {seed, stream}, read when the call runs (a
  *               captured graph draws anew when they change); NULL where q is 0

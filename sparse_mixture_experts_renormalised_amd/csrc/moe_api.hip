@@ -599,7 +599,7 @@ static int check_linear(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t 
   if (n_groups <= 0 || n_out <= 0 || k <= 0 || max_rows < 0) return MOE_ERR_INVALID_ARG;
   const int mult = dtype == MOE_BF16 ? 64 : 16;
   if (n_groups > moe::kMaxRouted + moe::kMaxShared) return MOE_ERR_UNSUPPORTED;
-  if (n_out % mult != 0 || k % mult != 0 || max_rows >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (n_out % mult != 0 || k % mult != 0 || max_rows >= (int64_t(1) << 30)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -881,7 +881,7 @@ int moe_dropout(int32_t dtype, int64_t rows, int64_t d, const void *x, void *y,
   if (rows > ((int64_t(1) << 42) - 1) / d) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   if (!x || !y || (cut > 0 && !rng)) return MOE_ERR_INVALID_ARG;
-  if (!all_aligned16({x, y, n_rows, rng})) return MOE_ERR_INVALID_ARG;
+  if (!all_aligned16({x, y, rng}) || reinterpret_cast<uintptr_t>(n_rows) % 4 != 0) return MOE_ERR_INVALID_ARG;
   return hip_status(moe::launch_dropout(dtype == MOE_BF16, x, y, rows, d, n_rows, dropout_of(cut, rng),
                                         static_cast<hipStream_t>(stream)));
 }

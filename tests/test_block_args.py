@@ -40,7 +40,7 @@ def weight_grad(B, dt=1, gd=1, g=3, n=64, k=128, dy=4096, xr=8, x=4096, idx=None
 
 SIZES = [({"dt": 2}, -1), ({"g": 0}, -1), ({"n": 0}, -1), ({"k": -64}, -1), ({"rows": -1}, -1),
          ({"g": 1089}, -2), ({"n": 72}, -2), ({"k": 32}, -2), ({"dt": 0, "n": 24, "gd": 0}, -2),
-         ({"rows": 1 << 31, "xr": 1 << 31}, -2), ({"off": None}, -1), ({"off": 4100}, -1), ({"ws": 4104}, -1)]
+         ({"rows": 1 << 30, "xr": 1 << 30}, -2), ({"off": None}, -1), ({"off": 4100}, -1), ({"ws": 4104}, -1)]
 
 
 def only(call, kw):
@@ -154,7 +154,7 @@ def drop(B, dt=1, rows=8, d=33, x=4096, y=4096, n=None, p=0.5, rng=4096):
 def test_dropout_refusals(B):
     assert drop(B, rows=0, x=None, y=None) == 0
     for bad in ({"dt": 2}, {"rows": -1}, {"d": 0}, {"x": None}, {"y": None}, {"rng": None}, {"p": 1.0}, {"p": -0.01},
-                {"p": float("nan")}, {"p": 0.999995}, {"x": 4104}, {"y": 4104}, {"n": 4100}, {"rng": 4104}):
+                {"p": float("nan")}, {"p": 0.999995}, {"x": 4104}, {"y": 4104}, {"n": 4098}, {"rng": 4104}):
         assert drop(B, **bad) == -1, bad
     assert drop(B, rows=1 << 40) == -2
 

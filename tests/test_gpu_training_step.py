@@ -78,7 +78,7 @@ class Step:
                   None, ws)
         B.grouped_linear(s["xn"], s["offsets"], p["w1"], s["h"], row_index=s["row_token"], bias=p["b1"], silu=True,
                          pre=s["z"], ws=ws)
-        s["rows"] = s["offsets"][N:].clone()
+        s["rows"] = s["offsets"][N:]
         B.dropout(s["h"], s["h"], P_HID, self.rng_hid, n_rows=s["rows"])
         B.grouped_linear(s["h"], s["offsets"], p["w2"], s["y"], bias=p["b2"], ws=ws)
         B.grouped_linear(s["xn"], self.whole, p["ws1"], s["hs"], silu=True, pre=s["zs"], ws=ws)
