@@ -1,0 +1,183 @@
+"""Gradients of the single Linears where a workgroup takes several tiles, where sums
+are split, and where offsets pass 32 bits, against float64 products on the GPU.
+
+Bounds as for the small cases: float32 sums of n products are off by at most
+(n + 4) 2^-24 times the sum of magnitudes (parts of split sums hold 256 terms or more
+each, so that adding them rounds less often than n), and a store to bf16 rounds by
+2^-8 relative, one to float32 by 2^-24.  The SiLU's slope is at most 1.1 and within
+2^-19 (1 + |z|) of its own size (for z that normal rows reach)."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+HALF = {BF16: 2.0 ** -8, F32: 2.0 ** -24}
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def B():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from sparse_mixture_experts_renormalised_amd import binding
+    binding.lib()
+    return binding
+
+
+def close(got, ref, bound, what):
+    g = got.double()
+    assert g.isfinite().all(), what
+    over = (g - ref).abs() - (bound + HALF[got.dtype] * (ref.abs() + bound))
+    assert not over.numel() or over.max() <= 0, f"{what}: beyond its bound by {over.max().item():.3e}"
+
+
+class Data:
+    def __init__(self, B, counts, n_out, k, seed, tokens=0):
+        """tokens: rows of a gathered x (0: x has the groups' rows)."""
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        off = [0]
+        for c in counts:
+            off.append(off[-1] + c)
+        self.off, self.n_out, self.k, self.G, rows = off, n_out, k, len(counts), off[-1]
+
+        def normal(*shape, std=1.0):
+            return torch.randn(*shape, generator=g, device="cuda").mul_(std).to(BF16)
+
+        self.rows, room = rows, rows + 3
+        self.x, self.dy, self.z = normal(tokens or room, k), normal(room, n_out), normal(room, k)
+        self.w = normal(self.G, n_out, k, std=k ** -0.5)
+        self.index = None
+        if tokens:
+            self.index = torch.randint(0, tokens, (room,), generator=g, dtype=torch.int32, device="cuda")
+            self.index[:min(2, rows)] = tokens - 1           # the last row, and it twice
+        else:
+            self.x[rows:] = float("nan")
+        self.dy[rows:] = float("nan")
+        self.z[rows:] = float("nan")
+        self.offsets = torch.tensor(off, dtype=torch.int32, device="cuda")
+        n = B.grouped_linear_workspace_size("bf16", self.G, n_out, k, room)
+        self.ws = torch.full((n,), 0x7F, dtype=torch.uint8, device="cuda") if n else None
+
+    def source(self, g):
+        a, b = self.off[g], self.off[g + 1]
+        return self.x[a:b] if self.index is None else self.x[self.index[a:b].long()]
+
+
+def check_weight_grad(B, d, out, accumulate=False, columns=None):
+    old = 3.0 if accumulate else float("nan")
+    dw = torch.full((d.G, d.n_out, d.k), old, dtype=out, device="cuda")
+    db = torch.full((d.G, d.n_out), old, dtype=out, device="cuda")
+    B.grouped_linear_weight_grad(d.dy, d.offsets, d.x, dw, row_index=d.index, dbias=db, accumulate=accumulate, ws=d.ws)
+    torch.cuda.synchronize()
+    add = 3.0 if accumulate else 0.0
+    for g in range(d.G):
+        dy, x = d.dy[d.off[g]:d.off[g + 1]].double(), d.source(g).double()
+        n = dy.shape[0]
+        ref, mag = dy.t().contiguous() @ x, dy.abs().t().contiguous() @ x.abs()
+        extra = U * (ref.abs() + add) if accumulate else 0.0
+        close(dw[g], ref + add, (n + 4) * U * mag + extra, f"dw of group {g}")
+        rb = dy.sum(0)
+        extra = U * (rb.abs() + add) if accumulate else 0.0
+        close(db[g], rb + add, (n + 4) * U * dy.abs().sum(0) + extra, f"dbias of group {g}")
+
+
+def check_input_grad(B, d, pre):
+    dx = torch.full((d.rows + 3, d.k), 0.5, dtype=BF16, device="cuda")
+    B.grouped_linear_input_grad(d.dy, d.offsets, d.w, dx, pre=d.z if pre else None, ws=d.ws)
+    torch.cuda.synchronize()
+    assert (dx[d.rows:] == 0.5).all()
+    for g in range(d.G):
+        a, b = d.off[g], d.off[g + 1]
+        dy, w = d.dy[a:b].double(), d.w[g].double()
+        ref, bound = dy @ w, (d.n_out + 4) * U * (dy.abs() @ w.abs())
+        if pre:
+            z = d.z[a:b].double()
+            s = torch.sigmoid(z)
+            slope = s + z * s * (1 - s)
+            # the slope's own error is absolute where its two terms cancel
+            bound = 1.1 * bound + 2.0 ** -19 * (1 + z.abs()) * ref.abs() * (s + (z * s * (1 - s)).abs())
+            ref = ref * slope
+        close(dx[a:b], ref, bound, f"dx of group {g}")
+
+
+SHORT = [0, 1, 31, 32, 33, 64, 97, 128, 130, 5]
+WEIGHT = [
+    # counts, n_out, k: short tiles after another, long ones, groups of very different lengths
+    (SHORT * 20, 320, 320),
+    ([900, 0, 1700], 2560, 2560),
+    ([1] * 70 + [4000] + [0] * 30 + [33] * 90, 256, 832),
+    ([511, 513] * 40 + [0, 2], 576, 448),
+]
+SPLIT = [([5000], 128, 192), ([4000, 3, 0, 900], 256, 320), ([2600, 2601], 448, 64)]
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("out,accumulate", [(BF16, False), (F32, False), (BF16, True), (F32, True)])
+@pytest.mark.parametrize("n", range(len(WEIGHT) + len(SPLIT)))
+def test_weight_grad(B, n, out, accumulate, gather):
+    counts, n_out, k = (WEIGHT + SPLIT)[n]
+    print(f"[linear] weight gradient {n} {out} {accumulate} {gather}", flush=True)
+    check_weight_grad(B, Data(B, counts, n_out, k, 40 + n, sum(counts) // 2 if gather else 0), out, accumulate)
+
+
+INPUT = [
+    (SHORT * 20, 64, 512),
+    ([700, 0, 256, 257, 3, 511] * 6, 576, 1088),
+    ([5, 300, 0, 1], 4096, 256),
+    ([256 * 30], 2048, 320),
+    ([1] * 1088, 64, 64),
+]
+
+
+@pytest.mark.parametrize("pre", [False, True])
+@pytest.mark.parametrize("n", range(len(INPUT)))
+def test_input_grad(B, n, pre):
+    counts, n_out, k = INPUT[n]
+    print(f"[linear] input gradient {n} {pre}", flush=True)
+    check_input_grad(B, Data(B, counts, n_out, k, 60 + n), pre)
+
+
+def test_widths_beyond_the_tiles(B):
+    """A width of 2^20, which the float32 kernel takes."""
+    d = Data(B, [3, 0, 2], 64, 1 << 20, 71)
+    check_weight_grad(B, d, BF16)
+    check_input_grad(B, d, True)
+
+
+def test_gathered_rows_beyond_4_gib(B):
+    d = Data(B, [40, 0, 3], 64, 65536, 72, tokens=33000)
+    check_weight_grad(B, d, F32)
+    y = torch.full((d.rows + 3, 64), 0.5, dtype=BF16, device="cuda")
+    B.grouped_linear(d.x, d.offsets, d.w, y, row_index=d.index, ws=d.ws)
+    torch.cuda.synchronize()
+    assert (y[d.rows:] == 0.5).all()
+    for g in range(3):
+        x, w = d.source(g).double(), d.w[g].double().t().contiguous()
+        close(y[d.off[g]:d.off[g + 1]], x @ w, (d.k + 4) * U * (x.abs() @ w.abs()), f"y of group {g}")
+
+
+def test_rows_beyond_4_gib(B):
+    """Weight gradients, input gradients and outputs whose arrays pass 4 GiB: the last
+    group's rows lie there."""
+    k, n_out, rows = 2048, 64, (1 << 20) + 70000
+    x = torch.zeros(rows, k, dtype=BF16, device="cuda")
+    dy = torch.zeros(rows, n_out, dtype=BF16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(73)
+    last = 300
+    x[-last:] = torch.randn(last, k, generator=g, device="cuda").to(BF16)
+    dy[-last:] = torch.randn(last, n_out, generator=g, device="cuda").to(BF16)
+    w = torch.randn(2, n_out, k, generator=g, device="cuda").to(BF16)
+    off = torch.tensor([0, rows - last, rows], dtype=torch.int32, device="cuda")
+    n = B.grouped_linear_workspace_size("bf16", 2, n_out, k, rows)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda") if n else None
+    dw = torch.full((2, n_out, k), float("nan"), dtype=F32, device="cuda")
+    B.grouped_linear_weight_grad(dy, off, x, dw, ws=ws)
+    xs, ds, ww = x[-last:].double(), dy[-last:].double(), w[1].double()
+    assert (dw[0] == 0).all()
+    close(dw[1], ds.t().contiguous() @ xs, (last + 4) * U * (ds.abs().t().contiguous() @ xs.abs()), "dw")
+    dx = x.fill_(0.5)
+    B.grouped_linear_input_grad(dy, off, w, dx, ws=ws)
+    torch.cuda.synchronize()
+    assert (dx[:1000] == 0).all() and (dx[-last - 1000:-last] == 0).all()
+    close(dx[-last:], ds @ ww, (n_out + 4) * U * (ds.abs() @ ww.abs()), "dx")
