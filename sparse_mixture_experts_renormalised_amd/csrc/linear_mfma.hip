@@ -89,8 +89,9 @@ __device__ __forceinline__ void dma4b(uint32_t off, u32x4_t desc, uint32_t m0) {
 // the copies' waits count these stores, every lane issues all of them: the descriptor
 // drops what lies behind the tile's rows, and kNoColumn what lies behind its columns.
 constexpr uint32_t kNoColumn = 0xFFFFFF00u;
+template <bool ONCE = true>
 __device__ __forceinline__ void store16b(uint32_t off, u32x4_t desc, u32x4_t v) {
-  __builtin_amdgcn_raw_buffer_store_b128(v, resource(desc), off, 0, 2);
+  __builtin_amdgcn_raw_buffer_store_b128(v, resource(desc), off, 0, ONCE ? 2 : 0);
 }
 
 // 16 bytes a lane; zeros where the descriptor does not reach.
@@ -496,8 +497,9 @@ __device__ __forceinline__ void wave_order() {
 template <typename S>
 constexpr int kStores16 = S::QB * (S::PB / 2) * 4;   // stores of a wave's tile in bf16
 
-// float32: 32 x 32 elements a pass.
-template <typename S>
+// float32: 32 x 32 elements a pass.  PART: a part of a split sum, which is read again at
+// once and stays in the caches.
+template <typename S, bool PART>
 __device__ __forceinline__ void out_f32(const f32x16_t (&acc)[S::PB][S::QB], char *lds, u32x4_t dst, int pitch, int r0,
                                         int c0, int columns, bool accumulate, int lane) {
   const int piece = lane & 7;
@@ -517,12 +519,12 @@ __device__ __forceinline__ void out_f32(const f32x16_t (&acc)[S::PB][S::QB], cha
         const int r = i * 8 + (lane >> 3);
         u32x4_t v = *reinterpret_cast<const u32x4_t *>(lds + r * 128 + ((piece ^ (r & 7)) << 4));
         const uint32_t at = c < columns ? (static_cast<uint32_t>(r0 + qi * 32 + r) * pitch + c) * 4 : kNoColumn;
-        if (accumulate) {
+        if (!PART && accumulate) {
           const u32x4_t z = load16b(at, dst);
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + __uint_as_float(z[e]));
         }
-        store16b(at, dst, v);
+        store16b<!PART>(at, dst, v);
       }
       wave_order();
     }
@@ -832,12 +834,12 @@ __global__ __launch_bounds__(S::NT, S::WGS * S::WAVES / 4) void linear_grad_kern
     if (!busy) {
     } else if (plan.parts > 1) {
       float *part = a.part + static_cast<int64_t>(item) * S::PART;
-      out_f32<S>(acc, lds, descriptor(part, S::Q * S::P * 4), S::P, r0, wp * PB * 32, S::P, false, el);
+      out_f32<S, true>(acc, lds, descriptor(part, S::Q * S::P * 4), S::P, r0, wp * PB * 32, S::P, false, el);
     } else {
       const int64_t row = (MODE == kLinWeightGrad ? static_cast<int64_t>(t.g) * a.l.n_out : t.row0) + t.q0;
       const int64_t size = static_cast<int64_t>(min(S::Q, nq)) * np;
       if (MODE == kLinWeightGrad && !a.l.out_bf16) {
-        out_f32<S>(acc, lds, descriptor(static_cast<float *>(a.l.out) + row * np, size * 4), np, r0, c0, np,
+        out_f32<S, false>(acc, lds, descriptor(static_cast<float *>(a.l.out) + row * np, size * 4), np, r0, c0, np,
                    a.l.accumulate, el);
       } else {
         const u32x4_t dst = descriptor(static_cast<uint16_t *>(a.l.out) + row * np, size * 2);
@@ -885,22 +887,25 @@ struct Threads256 : S {
 };
 
 // Sums of the parts of split tiles, in order, and what the kernel would have done with
-// them.  Sixteen workgroups a tile; float32, float4 a thread.
+// them.  32 workgroups a tile, float4 a thread, several parts on their way together (with
+// 16 workgroups and one part after another, 9 tiles of 28 parts took 51 us).
+constexpr int kPartGroups = 32;
 template <typename S, int MODE>
 __global__ __launch_bounds__(256) void linear_grad_parts_kernel(Args a) {
   __shared__ int s_pref[kMaxGroups + 1], s_off[kMaxGroups + 1], s_tmp[4];
   const Plan plan = make_plan<Threads256<S>, MODE>(a, s_pref, s_off, s_tmp, 0);
-  const int at = blockIdx.x / 16;
+  const int at = blockIdx.x / kPartGroups;
   if (plan.parts <= 1 || at >= plan.tiles) return;
   const Tile t = tile_at<S, MODE>(a, plan, s_pref, s_off, at * plan.parts, 0);
   const float *part = a.part + static_cast<int64_t>(at) * plan.parts * S::PART;
   const int np = a.l.k, rows = MODE == kLinWeightGrad ? a.l.n_out : t.rows;
   const int64_t row = (MODE == kLinWeightGrad ? static_cast<int64_t>(t.g) * a.l.n_out : t.row0) + t.q0;
-  constexpr int kEach = S::Q * S::P / 4 / 16;   // float4 of a workgroup
+  constexpr int kEach = S::Q * S::P / 4 / kPartGroups;   // float4 of a workgroup
   for (int e = threadIdx.x; e < kEach; e += 256) {
-    const int i = (blockIdx.x % 16) * kEach + e, r = i / (S::P / 4), c = i % (S::P / 4) * 4;
+    const int i = (blockIdx.x % kPartGroups) * kEach + e, r = i / (S::P / 4), c = i % (S::P / 4) * 4;
     if (t.q0 + r >= rows || t.p0 + c >= np) continue;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
     for (int k = 0; k < plan.parts; ++k) {
       const float4 x = *reinterpret_cast<const float4 *>(part + static_cast<int64_t>(k) * S::PART + i * 4);
       v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
@@ -928,7 +933,7 @@ __global__ __launch_bounds__(256) void linear_grad_parts_kernel(Args a) {
       *d = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
     }
   }
-  if (MODE == kLinWeightGrad && a.l.dbias && t.p0 == 0 && blockIdx.x % 16 == 0)
+  if (MODE == kLinWeightGrad && a.l.dbias && t.p0 == 0 && blockIdx.x % kPartGroups == 0)
     for (int r = threadIdx.x; r < S::Q && t.q0 + r < rows; r += 256) {
       float v = 0.0f;
       for (int k = 0; k < plan.parts; ++k) v += part[static_cast<int64_t>(k) * S::PART + S::Q * S::P + r];
@@ -948,7 +953,9 @@ int64_t tile_bound(int mode, int groups, int n_out, int k, int64_t max_rows) {
 template <typename S>
 int part_bound(int mode, int groups, int n_out, int k, int64_t max_rows) {
   if (tile_bound<S>(mode, groups, n_out, k, max_rows) > S::SLOTS) return 1;
-  const int64_t steps = mode == kLinWeightGrad ? (max_rows + kJ - 1) / kJ : n_out / kJ;
+  // groups of several times the mean's rows are split, where all are short nothing is
+  const int64_t rows = max_rows / groups < max_rows / 4 ? max_rows / groups * 4 + 4 : max_rows;
+  const int64_t steps = mode == kLinWeightGrad ? (rows + kJ - 1) / kJ : n_out / kJ;
   const int64_t parts = steps / kMinSteps;
   return static_cast<int>(parts < 1 ? 1 : parts < S::SLOTS ? parts : S::SLOTS);
 }
@@ -962,7 +969,7 @@ void launch_mode(const Args &a, hipStream_t s) {
   if (a.most_parts > 1) {
     const int64_t tiles = tile_bound<S>(MODE, a.l.groups, a.l.n_out, a.l.k, a.l.max_rows);
     const int64_t split = tiles < S::SLOTS / 2 ? tiles : S::SLOTS / 2;
-    hipLaunchKernelGGL((linear_grad_parts_kernel<S, MODE>), dim3(static_cast<unsigned>(split * 16)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((linear_grad_parts_kernel<S, MODE>), dim3(static_cast<unsigned>(split * kPartGroups)), dim3(256), 0, s, a);
   }
 }
 
