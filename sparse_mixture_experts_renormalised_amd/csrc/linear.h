@@ -33,7 +33,10 @@ struct Linear {
   bool accumulate;              // add to dw and dbias
 };
 
-hipError_t launch_linear_f32(const Linear &p, hipStream_t s);
+// float32 (all three) and the bf16 gradients that launch_linear_grad does not take; ws:
+// linear_f32_workspace_bytes of scratch for float32, not read for bf16.
+size_t linear_f32_workspace_bytes(int groups, int n_out, int k, int64_t max_rows);
+hipError_t launch_linear_f32(const Linear &p, void *ws, hipStream_t s);
 
 // The gradients on bf16 operands, where linear_grad_fits (32-bit offsets of a
 // gathered x); ws: linear_grad_workspace_bytes of scratch.

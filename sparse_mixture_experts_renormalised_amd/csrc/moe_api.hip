@@ -605,7 +605,8 @@ static int check_linear(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t 
 
 size_t moe_grouped_linear_workspace_size(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k,
                                          int64_t max_rows) {
-  if (check_linear(dtype, n_groups, n_out, k, max_rows) != MOE_OK || dtype != MOE_BF16) return 0;
+  if (check_linear(dtype, n_groups, n_out, k, max_rows) != MOE_OK) return 0;
+  if (dtype == MOE_F32) return moe::linear_f32_workspace_bytes(n_groups, n_out, k, max_rows);
   // the gradients' parts of split sums, or the forward's
   GemmGroups g{};
   g.n_routed = n_groups;
@@ -630,7 +631,7 @@ static moe::Linear linear_of(moe::LinearMode mode, int32_t dtype, int32_t n_grou
 }
 
 static int run_linear_grad(const moe::Linear &p, void *ws, hipStream_t s) {
-  return hip_status(moe::linear_grad_fits(p) ? moe::launch_linear_grad(p, ws, s) : moe::launch_linear_f32(p, s));
+  return hip_status(moe::linear_grad_fits(p) ? moe::launch_linear_grad(p, ws, s) : moe::launch_linear_f32(p, ws, s));
 }
 
 int moe_grouped_linear(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k, int64_t x_rows,
@@ -675,7 +676,7 @@ int moe_grouped_linear(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k
   p.silu = silu != 0;
   p.out = y;
   p.pre = pre;
-  return hip_status(moe::launch_linear_f32(p, static_cast<hipStream_t>(stream)));
+  return hip_status(moe::launch_linear_f32(p, ws, static_cast<hipStream_t>(stream)));
 }
 
 int moe_grouped_linear_input_grad(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k,

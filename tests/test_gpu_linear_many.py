@@ -33,7 +33,7 @@ def close(got, ref, bound, what):
 
 
 class Data:
-    def __init__(self, B, counts, n_out, k, seed, tokens=0):
+    def __init__(self, B, counts, n_out, k, seed, tokens=0, dtype=BF16):
         """tokens: rows of a gathered x (0: x has the groups' rows)."""
         g = torch.Generator(device="cuda").manual_seed(seed)
         off = [0]
@@ -42,7 +42,7 @@ class Data:
         self.off, self.n_out, self.k, self.G, rows = off, n_out, k, len(counts), off[-1]
 
         def normal(*shape, std=1.0):
-            return torch.randn(*shape, generator=g, device="cuda").mul_(std).to(BF16)
+            return torch.randn(*shape, generator=g, device="cuda").mul_(std).to(dtype)
 
         self.rows, room = rows, rows + 3
         self.x, self.dy, self.z = normal(tokens or room, k), normal(room, n_out), normal(room, k)
@@ -56,7 +56,7 @@ class Data:
         self.dy[rows:] = float("nan")
         self.z[rows:] = float("nan")
         self.offsets = torch.tensor(off, dtype=torch.int32, device="cuda")
-        n = B.grouped_linear_workspace_size("bf16", self.G, n_out, k, room)
+        n = B.grouped_linear_workspace_size("bf16" if dtype == BF16 else "f32", self.G, n_out, k, room)
         self.ws = torch.full((n,), 0x7F, dtype=torch.uint8, device="cuda") if n else None
 
     def source(self, g):
@@ -83,7 +83,7 @@ def check_weight_grad(B, d, out, accumulate=False, columns=None):
 
 
 def check_input_grad(B, d, pre):
-    dx = torch.full((d.rows + 3, d.k), 0.5, dtype=BF16, device="cuda")
+    dx = torch.full((d.rows + 3, d.k), 0.5, dtype=d.w.dtype, device="cuda")
     B.grouped_linear_input_grad(d.dy, d.offsets, d.w, dx, pre=d.z if pre else None, ws=d.ws)
     torch.cuda.synchronize()
     assert (dx[d.rows:] == 0.5).all()
@@ -136,6 +136,34 @@ def test_input_grad(B, n, pre):
     counts, n_out, k = INPUT[n]
     print(f"[linear] input gradient {n} {pre}", flush=True)
     check_input_grad(B, Data(B, counts, n_out, k, 60 + n), pre)
+
+
+# few tiles and long sums in float32: counts, n_out, k
+LONG = [([2967], 80, 208), ([700, 0, 3, 5000, 12], 48, 112), ([1988], 1808, 80), ([5, 0, 70, 130], 2048, 2032),
+        ([1], 64, 16384), ([64, 1], 16400, 16)]
+
+
+@pytest.mark.parametrize("n", range(len(LONG)))
+def test_float32_split(B, n):
+    counts, n_out, k = LONG[n]
+    print(f"[linear] float32 split {n}", flush=True)
+    d = Data(B, counts, n_out, k, 80 + n, sum(counts) // 2 + 1 if n % 2 else 0, F32)
+    assert d.ws is not None
+    check_weight_grad(B, d, F32)
+    check_weight_grad(B, d, F32, True)
+    check_input_grad(B, d, n % 2 == 0)
+    bias = torch.randn(d.G, n_out, device="cuda")
+    y, pre = (torch.full((d.rows + 3, n_out), 0.5, device="cuda") for _ in range(2))
+    B.grouped_linear(d.x, d.offsets, d.w, y, row_index=d.index, bias=bias, silu=True, pre=pre, ws=d.ws)
+    torch.cuda.synchronize()
+    assert (y[d.rows:] == 0.5).all() and (pre[d.rows:] == 0.5).all()
+    for g in range(d.G):
+        a, b = d.off[g], d.off[g + 1]
+        x, w = d.source(g).double(), d.w[g].double().t().contiguous()
+        z, bound = x @ w + bias[g].double(), (k + 4) * U * (x.abs() @ w.abs() + bias[g].double().abs())
+        close(pre[a:b], z, bound, f"pre of group {g}")
+        silu = z * torch.sigmoid(z)
+        close(y[a:b], silu, 1.1 * bound + 2.0 ** -19 * (1 + z.abs()) * silu.abs(), f"y of group {g}")
 
 
 def test_widths_beyond_the_tiles(B):
