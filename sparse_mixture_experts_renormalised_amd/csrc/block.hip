@@ -19,6 +19,13 @@
 // of a second read; sums and statistics are float32, variances are taken around
 // the mean.  Tokens are dealt to workgroups in a fixed way and the weights'
 // gradients are added in a fixed order: equal calls give equal bits.
+//
+// Bound by memory, with loads in batches (a token's own rows, then two or four to eight
+// expert rows) so that many are on their way.  4096 tokens of 7168 in bf16, eight experts
+// and a shared one: forward 188 us (0.76 GB, 4.1 TB/s), gradient 288 us (1.29 GB, 4.5
+// TB/s), where a copy of two 4 GiB halves reaches 4.8.  1001 tokens of 1408 in float32 with
+// LayerNorms and biases: gradient 20 us, 34 MB in the caches and two launches.  16 tokens of
+// 2048: forward 5.6 us, a launch and three dependent reads.
 #include "block.h"
 
 namespace moe {
@@ -145,7 +152,7 @@ __device__ __forceinline__ float normalise(float (&v)[CH][8], int kind, float ep
     block_sum(s, turn, m);
 #pragma unroll
     for (int c = 0; c < CH; ++c)
-      if (static_cast<int>(threadIdx.x) + c * NW * 64 < nvec)
+      if (static_cast<int>(NW == 1 ? threadIdx.x & 63 : threadIdx.x) + c * NW * 64 < nvec)
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[c][j] -= m[0] * inv_d;
   }
@@ -310,11 +317,16 @@ __device__ __forceinline__ void norm_grad(float (&g)[CH][8], const float (&hat)[
 
 constexpr int kSlots = 2;   // slots whose rows are read, and whose products are summed, together
 
-template <typename A, typename R, int NW, int CH, bool BIAS>
-__global__ __launch_bounds__(NW * 64, NW == 8 && CH <= 2 ? 4 : 1) void block_join_grad_kernel(BlockJoinGrad a) {
+// TOKENS: tokens that a workgroup has in hand (rows of one wave), so that they leave one
+// part of each sum over tokens.
+template <typename A, typename R, int NW, int CH, int TOKENS, bool BIAS>
+__global__ __launch_bounds__(NW * 64 * TOKENS, NW == 8 && CH <= 2 ? 4 : 1) void block_join_grad_kernel(BlockJoinGrad a) {
   __shared__ Sums<NW, kSlots> s_sum;
   int turn = 0;
-  const int tid = threadIdx.x, nvec = a.d / 8;
+  static_assert(TOKENS == 1 || (NW == 1 && CH == 1), "several tokens: rows of one wave");
+  // (the token's number stays in scalar registers: its slots and gates are scalar loads)
+  const int tid = TOKENS == 1 ? threadIdx.x : threadIdx.x & 63, nvec = a.d / 8;
+  const int mine = TOKENS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const float inv_d = 1.0f / static_cast<float>(a.d);
   const DropKey key = drop_key(a.drop);
   const bool slots = a.branch && (a.d_y_rows || a.d_topk_gate);
@@ -326,7 +338,7 @@ __global__ __launch_bounds__(NW * 64, NW == 8 && CH <= 2 ? 4 : 1) void block_joi
       swi[c][j] = swo[c][j] = 0.0f;
       if (BIAS) sbi[c][j] = sbo[c][j] = 0.0f;
     }
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * TOKENS + mine; t < a.T; t += static_cast<int64_t>(gridDim.x) * TOKENS) {
     const int64_t row = t * a.d;
     // everything of the token's own rows is on its way before the first sum
     Raw<A> rn[CH], rb[CH];
@@ -458,6 +470,32 @@ __global__ __launch_bounds__(NW * 64, NW == 8 && CH <= 2 ? 4 : 1) void block_joi
       }
     }
   }
+  if constexpr (TOKENS > 1) {
+    // the sums of its tokens, in order, in the first one's registers
+    __shared__ float s_rows[kMaxPart][TOKENS - 1][8][64];
+    auto give = [&](int which, const float (&v)[8]) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s_rows[which][mine - 1][j][tid] = v[j];
+    };
+    auto take = [&](int which, float (&v)[8]) {
+#pragma unroll
+      for (int i = 0; i < TOKENS - 1; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += s_rows[which][i][j][tid];
+    };
+    if (mine > 0) {
+      if (a.sum[0]) give(0, swi[0]);
+      if (BIAS && a.sum[1]) give(1, sbi[0]);
+      if (a.sum[2]) give(2, swo[0]);
+      if (BIAS && a.sum[3]) give(3, sbo[0]);
+    }
+    __syncthreads();
+    if (mine > 0) return;
+    if (a.sum[0]) take(0, swi[0]);
+    if (BIAS && a.sum[1]) take(1, sbi[0]);
+    if (a.sum[2]) take(2, swo[0]);
+    if (BIAS && a.sum[3]) take(3, sbo[0]);
+  }
   // this workgroup's part of the weights' gradients: part[which][workgroup][d]
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
@@ -471,18 +509,19 @@ __global__ __launch_bounds__(NW * 64, NW == 8 && CH <= 2 ? 4 : 1) void block_joi
   }
 }
 
-// Sums of the workgroups' parts: 64 columns a workgroup, four a thread, 64 ranges of
-// parts whose sums are added in order.
+// Sums of the workgroups' parts: 32 columns (a line) a workgroup, four a thread, 128
+// ranges of parts whose sums are added in order.
 __global__ __launch_bounds__(1024) void block_sum_parts_kernel(const float *part, int parts, int d,
                                                                float *o0, float *o1, float *o2, float *o3) {
   float *out = blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : blockIdx.y == 2 ? o2 : o3;
   if (!out) return;
-  __shared__ __attribute__((aligned(16))) float s[64][64];
-  const int quad = threadIdx.x & 15, w = threadIdx.x >> 4, col = blockIdx.x * 64 + quad * 4;
+  __shared__ __attribute__((aligned(16))) float s[128][32];
+  __shared__ float s_last[16][32];
+  const int quad = threadIdx.x & 7, w = threadIdx.x >> 3, col = blockIdx.x * 32 + quad * 4;
   float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (col < d) {
     const float *p = part + (static_cast<int64_t>(blockIdx.y) * parts) * d + col;
-    const int per = (parts + 63) / 64, end = min(parts, (w + 1) * per);
+    const int per = (parts + 127) / 128, end = min(parts, (w + 1) * per);
 #pragma unroll 8
     for (int i = w * per; i < end; ++i) {
       const float4 x = *reinterpret_cast<const float4 *>(p + static_cast<int64_t>(i) * d);
@@ -491,43 +530,54 @@ __global__ __launch_bounds__(1024) void block_sum_parts_kernel(const float *part
   }
   *reinterpret_cast<float4 *>(&s[w][quad * 4]) = v;
   __syncthreads();
-  const int c = threadIdx.x, at = blockIdx.x * 64 + c;
-  if (c < 64 && at < d) {
+  const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
+  if (r < 16) {
     float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 64; ++i) sum += s[i][c];
-    out[at] = sum;
+    for (int i = 0; i < 8; ++i) sum += s[r * 8 + i][c];
+    s_last[r][c] = sum;
+  }
+  __syncthreads();
+  if (r == 0 && blockIdx.x * 32 + c < d) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum += s_last[i][c];
+    out[blockIdx.x * 32 + c] = sum;
   }
 }
 
 // Shape of a workgroup for rows of nvec chunks of 8 elements: waves, and chunks a thread.
 struct Shape {
-  int nw, ch;
+  int nw, ch, tokens;
 };
 Shape join_shape(int nvec) {
-  if (nvec <= 64) return {1, 1};
-  if (nvec <= 128) return {2, 1};
-  if (nvec <= 256) return {4, 1};
-  if (nvec <= 512) return {4, 2};
-  if (nvec <= 1024) return {4, 4};
-  return {8, 4};
+  if (nvec <= 64) return {1, 1, 1};
+  if (nvec <= 128) return {2, 1, 1};
+  if (nvec <= 256) return {4, 1, 1};
+  if (nvec <= 512) return {4, 2, 1};
+  if (nvec <= 1024) return {4, 4, 1};
+  return {8, 4, 1};
 }
-Shape grad_shape(int nvec) {
-  if (nvec <= 64) return {1, 1};
-  if (nvec <= 128) return {2, 1};
-  if (nvec <= 256) return {4, 1};
-  if (nvec <= 512) return {8, 1};
-  if (nvec <= 1024) return {8, 2};
-  return {8, 4};
+// Rows of one wave: four of 129 tokens or more to a workgroup (3861 tokens of 296: 26.0 us
+// with parts of one, 15.8; 108 tokens of 8: 10.5 and 12.5).
+Shape grad_shape(int64_t T, int nvec) {
+  if (nvec <= 64) return {1, 1, T <= 128 ? 1 : 4};
+  if (nvec <= 128) return {2, 1, 1};
+  if (nvec <= 256) return {4, 1, 1};
+  if (nvec <= 512) return {8, 1, 1};
+  if (nvec <= 1024) return {8, 2, 1};
+  return {8, 4, 1};
 }
 
-// Workgroups of the gradient: eight of four waves fill a CU.  Every one leaves a part of
-// each sum over tokens, which costs as much as a token's row, so that only few tokens
-// get one each (33 tokens of 1408: 8.5 us, two each 10.9, four each 16.2; 1001: 24.3,
-// 20.0 and 21.5).
+// Workgroups of the gradient: sixteen waves fill a CU.  Every one leaves a part of each
+// sum over tokens, which costs as much as a token's row, so that it takes two tokens or
+// more where there are many (33 tokens of 1408: 8.5 us, two each 10.9, four each 16.2;
+// 1001: 24.3, 20.0 and 21.5; 187 of 248, four waves: 11.1, two a wave 16.1).
 unsigned grad_grid(int64_t T, int d) {
-  const Shape s = grad_shape(d / 8);
-  const int64_t most = 4096 / s.nw < 2048 ? 4096 / s.nw : 2048, want = T <= 128 ? T : (T + 1) / 2;
+  const Shape s = grad_shape(T, d / 8);
+  const int64_t most = 4096 / (s.nw * s.tokens) < 2048 ? 4096 / (s.nw * s.tokens) : 2048;
+  const int64_t each = s.tokens == 1 ? (T <= 128 ? 1 : 2) : s.tokens * (T <= 1024 ? 1 : 2);
+  const int64_t want = (T + each - 1) / each;
   return static_cast<unsigned>(want < most ? want : most);
 }
 
@@ -538,13 +588,13 @@ void launch_join(const BlockJoin &a, hipStream_t s) {
   hipLaunchKernelGGL((block_join_kernel<A, R, NW, CH>), grid, dim3(NW * 64), 0, s, a);
 }
 
-template <typename A, typename R, int NW, int CH>
+template <typename A, typename R, int NW, int CH, int TOKENS = 1>
 void launch_grad(const BlockJoinGrad &a, hipStream_t s) {
-  const dim3 grid(grad_grid(a.T, a.d));
+  const dim3 grid(grad_grid(a.T, a.d)), threads(NW * 64 * TOKENS);
   if (a.sum[1] || a.sum[3])
-    hipLaunchKernelGGL((block_join_grad_kernel<A, R, NW, CH, true>), grid, dim3(NW * 64), 0, s, a);
+    hipLaunchKernelGGL((block_join_grad_kernel<A, R, NW, CH, TOKENS, true>), grid, threads, 0, s, a);
   else
-    hipLaunchKernelGGL((block_join_grad_kernel<A, R, NW, CH, false>), grid, dim3(NW * 64), 0, s, a);
+    hipLaunchKernelGGL((block_join_grad_kernel<A, R, NW, CH, TOKENS, false>), grid, threads, 0, s, a);
 }
 
 template <typename A, typename R>
@@ -559,8 +609,9 @@ void dispatch_shape(const BlockJoin &a, hipStream_t s) {
 }
 template <typename A, typename R>
 void dispatch_shape(const BlockJoinGrad &a, hipStream_t s) {
-  const Shape sh = grad_shape(a.d / 8);
-  if (sh.nw == 1) launch_grad<A, R, 1, 1>(a, s);
+  const Shape sh = grad_shape(a.T, a.d / 8);
+  if (sh.tokens == 4) launch_grad<A, R, 1, 1, 4>(a, s);
+  else if (sh.nw == 1) launch_grad<A, R, 1, 1>(a, s);
   else if (sh.nw == 2) launch_grad<A, R, 2, 1>(a, s);
   else if (sh.nw == 4) launch_grad<A, R, 4, 1>(a, s);
   else if (sh.ch == 1) launch_grad<A, R, 8, 1>(a, s);
@@ -593,7 +644,7 @@ hipError_t launch_block_join_grad(const BlockJoinGrad &a, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   if (a.sum[0] || a.sum[1] || a.sum[2] || a.sum[3]) {
-    hipLaunchKernelGGL(block_sum_parts_kernel, dim3((a.d + 63) / 64, 4), dim3(1024), 0, s, a.part,
+    hipLaunchKernelGGL(block_sum_parts_kernel, dim3((a.d + 31) / 32, 4), dim3(1024), 0, s, a.part,
                        a.T > 0 ? static_cast<int>(grad_grid(a.T, a.d)) : 0, a.d, a.sum[0], a.sum[1], a.sum[2],
                        a.sum[3]);
   }

@@ -60,6 +60,8 @@ CASES = [
     (3, 16384, 2, 0, "rms", "layer", True, True, 0.0),
     (2100, 72, 2, 0, "layer", "rms", True, True, 0.1),
     (600, 2304, 2, 1, "rms", "layer", True, True, 0.0),
+    (301, 136, 3, 1, "layer", "rms", True, True, 0.2),
+    (1030, 512, 0, 0, "rms", "layer", True, False, 0.0),
 ]
 
 
