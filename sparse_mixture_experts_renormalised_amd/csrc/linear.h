@@ -33,16 +33,16 @@ struct Linear {
   bool accumulate;              // add to dw and dbias
 };
 
-// float32 (all three) and the bf16 gradients that launch_linear_grad does not take; ws:
+// float32 (all three) and the bf16 gradients that launch_linear_mfma does not take; ws:
 // linear_f32_workspace_bytes of scratch for float32, not read for bf16.
 size_t linear_f32_workspace_bytes(int groups, int n_out, int k, int64_t max_rows);
 hipError_t launch_linear_f32(const Linear &p, void *ws, hipStream_t s);
 
-// The gradients on bf16 operands, where linear_grad_fits (32-bit offsets of a
-// gathered x); ws: linear_grad_workspace_bytes of scratch.
-bool linear_grad_fits(const Linear &p);
-size_t linear_grad_workspace_bytes(int groups, int n_out, int k, int64_t max_rows);
-hipError_t launch_linear_grad(const Linear &p, void *ws, hipStream_t s);
+// bf16 operands, where linear_mfma_fits (32-bit offsets of a gathered x; the forward where
+// the layer's kernels would be slower); ws: linear_mfma_workspace_bytes of scratch.
+bool linear_mfma_fits(const Linear &p);
+size_t linear_mfma_workspace_bytes(int groups, int n_out, int k, int64_t max_rows);
+hipError_t launch_linear_mfma(const Linear &p, void *ws, hipStream_t s);
 
 // Derivative of z sigmoid(z): s + z s (1 - s), with the hardware exp2 and reciprocal
 // (about 1 ulp each).

@@ -1,15 +1,16 @@
-// Gradients of the single Linears of every expert on the bf16 matrix
+// Single Linears of every expert and their gradients on the bf16 matrix
 // instructions (v_mfma_f32_32x32x16_bf16, float32 sums):
 //
+//   forward          y[r][p] = act(sum_j x[idx r][j] W_g[p][j] + bias_g[p])
 //   input gradient   dx[r][p] = sum_j dy[r][j] W_g[j][p]      (times silu'(pre))
 //   weight gradient  dw_g[q][p] = sum_r dy[r][q] x[idx r][p]  (and dbias)
 //
-// Both are C[q][p] = sum_j Q(j, q) P(j, p) with operands whose memory does not run
-// along the sum: P (weights, or x) lies [j][p], and so does dy as Q of the weight
+// All are C[q][p] = sum_j Q(j, q) P(j, p).  The gradients have operands whose memory does
+// not run along the sum: P (weights, or x) lies [j][p], and so does dy as Q of the weight
 // gradient.  Such an operand goes to LDS as it lies and is turned by the transposing
 // LDS reads (ds_read_b64_tr_b16: sixteen lanes read 4 x 16 elements and get a column
-// of four each); dy as Q of the input gradient lies [q][j] and is read in 16-byte
-// pieces.
+// of four each); those that lie along the sum (both of the forward, dy as Q of the input
+// gradient) are read in 16-byte pieces.
 //
 // Steps of 32 along j are copied global -> LDS into a ring, RING - 1 steps ahead; the
 // fragments of the next 16 j are read while those of the last are multiplied; one
@@ -20,6 +21,21 @@
 // and copies behind the last tile need no case of their own, and every wait counts the
 // same copies.  P is the instruction's first operand: a lane ends up with four
 // neighbouring elements of one row of C.
+//
+// Measured (clocks of the chip move between 1.5 and 2.2 GHz under the power limit, so that
+// times differ by several per cent from run to run):
+//   input gradient, 8192 rows on 8 experts of 4096 x 14336 with the SiLU's slope: 895 to
+//     970 us, 1000 to 1070 TFLOP/s (one library product an expert, without the slope: 845).
+//     Matrix instructions are busy 59% of the clocks, workgroups 92%; a step takes 1250
+//     clocks of the 1024 that its products take, a tile's slopes and stores 12 000.
+//   weight gradient of one group of 32768 rows, 4096 x 4096: 854 us, 1290 TFLOP/s;
+//     gathered rows 935.  64 groups of 512, 2048 x 1408, to float32: 255 to 310 us, where
+//     the 850 MB alone take 178 at a copy's rate: steps and stores take turns, as all
+//     workgroups come to a tile's end at about the same time.  256 groups of 128, to bf16:
+//     450 us, 3.8 TB/s.
+//   input gradient of 207 rows on 256 experts of 2048 x 7168: 425 us, 5.8 TB/s of weights.
+// Tiles of 128 x 256 with two workgroups a CU took 1134 us for the first and 306 for the
+// 64 groups, four waves of 128 x 128 1099 and 391.
 #include "lds_dma.h"
 #include "linear.h"
 
@@ -207,10 +223,20 @@ struct Plan {
   int qtiles, ptiles, parts;
 };
 
+// Elements of a row of C, and of a sum that is not over rows.
+template <int MODE>
+__device__ __forceinline__ int columns_of(const Linear &a) {
+  return MODE == kLinForward ? a.n_out : a.k;
+}
+template <int MODE>
+__device__ __forceinline__ int terms_of(const Linear &a) {
+  return MODE == kLinForward ? a.k : a.n_out;
+}
+
 // Steps of a tile of a group of that many rows.
 template <int MODE>
 __device__ __forceinline__ int steps_of(const Linear &a, int rows) {
-  return MODE == kLinWeightGrad ? (rows + kJ - 1) / kJ : a.n_out / kJ;
+  return MODE == kLinWeightGrad ? (rows + kJ - 1) / kJ : terms_of<MODE>(a) / kJ;
 }
 
 // The work of this XCD.  Few tiles are split along their sums, so that they fill the
@@ -224,8 +250,8 @@ __device__ Plan make_plan(const Args &a, int *pref, int *off, int *tmp, int xcd)
   for (int g = threadIdx.x; g <= l.groups; g += S::NT) off[g] = l.offsets[g];
   __syncthreads();
   auto rows = [&](int g) { return off[g + 1] - off[g]; };
-  p.ptiles = (l.k + S::P - 1) / S::P;
-  if (MODE == kLinInputGrad) {
+  p.ptiles = (columns_of<MODE>(l) + S::P - 1) / S::P;
+  if (MODE != kLinWeightGrad) {
     p.qtiles = uniform(group_prefix<S::NT>(l.groups, [&](int g) { return (rows(g) + S::Q - 1) / S::Q; }, pref, tmp));
     p.tiles = p.qtiles * p.ptiles;
   } else {
@@ -235,7 +261,7 @@ __device__ Plan make_plan(const Args &a, int *pref, int *off, int *tmp, int xcd)
   p.parts = 1;
   if (a.most_parts > 1 && p.tiles > 0 && p.tiles * 2 <= S::SLOTS) p.parts = min(a.most_parts, S::SLOTS / p.tiles);
   const int items = p.tiles * p.parts;
-  if (MODE == kLinInputGrad || p.parts > 1) {
+  if (MODE != kLinWeightGrad || p.parts > 1) {
     p.first = static_cast<int>(static_cast<int64_t>(items) * xcd / kXcds);
     p.end = static_cast<int>(static_cast<int64_t>(items) * (xcd + 1) / kXcds);
   } else {
@@ -301,41 +327,77 @@ __device__ __forceinline__ Tile tile_at(const Args &a, const Plan &p, const int 
 // ---------------------------------------------------------------------------
 // Sources of a tile's copies
 // ---------------------------------------------------------------------------
+// Indexes of a gathered x in the forward, for one wave: those of a tile's rows that it
+// copies, a dword each, in one of two slots in turn.  They come four steps ahead of the
+// tile's first copy, when waits for copies have covered them.
+template <typename S>
+struct RowIndex {
+  static constexpr int BYTES = 2 * S::WAVES * 256;
+  static_assert(S::QCOPIES * 16 <= 64, "one copy for the rows of a wave");
+  u32x4_t desc;
+  uint32_t base;           // this wave's part of slot 0
+  int slot;                // the one that was filled last
+
+  __device__ __forceinline__ void init(const Args &a, uint32_t lds, int wave) {
+    desc = descriptor(a.l.index, a.l.max_rows * 4);
+    base = lds + wave * 256;
+    slot = 0;
+  }
+  __device__ __forceinline__ uint32_t place() const { return base + slot * S::WAVES * 256; }
+  __device__ __forceinline__ void start(const Tile &t, int wave, int lane) {
+    slot ^= 1;
+    const int r = min(16 * (S::WAVES * (lane >> 4) + wave) + (lane & 15), t.rows - 1 - t.q0);
+    dma4b(lane < 16 * S::QCOPIES ? static_cast<uint32_t>(t.row0 + t.q0 + r) * 4 : kNoColumn, desc, place());
+  }
+};
+
+// GATHER: the rows of x through the index (weight gradient: P, step by step; forward: Q,
+// once for the tile).
 template <typename S, int MODE, bool GATHER>
 struct Source {
+  static constexpr bool STEPWISE = GATHER && MODE == kLinWeightGrad;
   uint32_t q[S::QCOPIES], p[S::PCOPIES]; // this lane's byte offsets in a step
   u32x4_t dq, dp;                        // where the step lies
   uint32_t qstep, pstep, pcol;           // bytes of a step; byte offset of this lane's column
-  int left;                              // rows (input gradient: steps) of the part from this step on
-  uint32_t at[GATHER ? S::PCOPIES : 1];  // a gathered x: indexes of this lane's rows in the step to come
+  int left;                              // rows (not weight gradient: steps) of the part from this step on
+  uint32_t at[STEPWISE ? S::PCOPIES : 1];  // a gathered x: indexes of this lane's rows in the step to come
 
-  __device__ __forceinline__ void init(const Args &a, const Tile &t, int wave, int lane) {
+  // index: where RowIndex put the tile's (forward)
+  __device__ __forceinline__ void init(const Args &a, const Tile &t, uint32_t index, int wave, int lane) {
     const int n = a.l.n_out, k = a.l.k;
     const int64_t j0 = static_cast<int64_t>(t.s0) * kJ;
-    pcol = lines<S::P, S::PCOPIES>(p, k, t.p0, wave, lane);
-    pstep = static_cast<uint32_t>(kJ) * k * 2;
-    if constexpr (MODE == kLinInputGrad) {
-      // [q][j]: 16 rows of 64 bytes a copy
-      const int c = (lane & 3) ^ ((lane >> 4) & 3);
-#pragma unroll
-      for (int i = 0; i < S::QCOPIES; ++i) {
-        const int r = min(16 * (S::WAVES * i + wave) + (lane >> 2), t.rows - 1 - t.q0);
-        q[i] = static_cast<uint32_t>(r) * n * 2 + c * 16;
-      }
-      left = t.s1 - t.s0;
-      qstep = kJ * 2;
-      dq = descriptor(static_cast<const uint16_t *>(a.l.dy) + (t.row0 + t.q0) * n + j0, 0);
-      dp = descriptor(static_cast<const uint16_t *>(a.l.w) + (static_cast<int64_t>(t.g) * n + j0) * k, 0);
-    } else {
+    if constexpr (MODE == kLinWeightGrad) {
       left = static_cast<int>(min(t.rows, t.s1 * kJ) - j0);
       lines<S::Q, S::QCOPIES>(q, n, t.q0, wave, lane);
       qstep = static_cast<uint32_t>(kJ) * n * 2;
       dq = descriptor(static_cast<const uint16_t *>(a.l.dy) + (t.row0 + j0) * n, 0);
+    } else {
+      const int nj = terms_of<MODE>(a.l);
+      const uint16_t *from = static_cast<const uint16_t *>(MODE == kLinForward ? a.l.x : a.l.dy) + j0;
       if constexpr (GATHER) {
-        dp = descriptor(a.l.x, 0);
+        typedef __attribute__((address_space(3))) const volatile uint32_t lds_u32_t;
+        const lds_u32_t *r = reinterpret_cast<lds_u32_t *>(index + (lane >> 2) * 4);
+#pragma unroll
+        for (int i = 0; i < S::QCOPIES; ++i) q[i] = r[16 * i] * static_cast<uint32_t>(nj * 2) + piece(lane);
       } else {
-        dp = descriptor(static_cast<const uint16_t *>(a.l.x) + (t.row0 + j0) * k, 0);
+        rows_along<S::QCOPIES>(q, nj, t.rows - 1 - t.q0, wave, lane);
+        from += (t.row0 + t.q0) * nj;
       }
+      left = t.s1 - t.s0;
+      qstep = kJ * 2;
+      dq = descriptor(from, 0);
+    }
+    if constexpr (MODE == kLinForward) {
+      rows_along<S::PCOPIES>(p, k, n - 1 - t.p0, wave, lane);
+      pstep = kJ * 2;
+      dp = descriptor(static_cast<const uint16_t *>(a.l.w) + (static_cast<int64_t>(t.g) * n + t.p0) * k + j0, 0);
+    } else {
+      pcol = lines<S::P, S::PCOPIES>(p, k, t.p0, wave, lane);
+      pstep = static_cast<uint32_t>(kJ) * k * 2;
+      if constexpr (MODE == kLinInputGrad)
+        dp = descriptor(static_cast<const uint16_t *>(a.l.w) + (static_cast<int64_t>(t.g) * n + j0) * k, 0);
+      else
+        dp = descriptor(static_cast<const uint16_t *>(a.l.x) + (GATHER ? 0 : (t.row0 + j0) * k), 0);
     }
     cover(a);
   }
@@ -346,12 +408,21 @@ struct Source {
   }
   // To the next step.
   __device__ __forceinline__ void advance(const Args &a) {
-    left -= MODE == kLinInputGrad ? 1 : kJ;
+    left -= MODE == kLinWeightGrad ? kJ : 1;
     add(dq, qstep);
-    if constexpr (!GATHER) add(dp, pstep);
+    if constexpr (!STEPWISE) add(dp, pstep);
     cover(a);
   }
 
+  // Offsets of an operand [line][j] of lines of nj elements, clamped to the last one: 1 KB
+  // copies of 16 lines each.
+  static __device__ __forceinline__ uint32_t piece(int lane) { return ((lane & 3) ^ ((lane >> 4) & 3)) * 16; }
+  template <int COPIES>
+  static __device__ __forceinline__ void rows_along(uint32_t (&at)[COPIES], int nj, int last, int wave, int lane) {
+#pragma unroll
+    for (int i = 0; i < COPIES; ++i)
+      at[i] = static_cast<uint32_t>(min(16 * (S::WAVES * i + wave) + (lane >> 2), last)) * nj * 2 + piece(lane);
+  }
   // Offsets of an operand [j][N columns] with lines of `width` elements: 1 KB copies
   // of 512 / N lines each.  Returns the column's byte offset.
   template <int N, int COPIES>
@@ -370,9 +441,10 @@ struct Source {
   }
   // The rows of this step that are there.
   __device__ __forceinline__ void cover(const Args &a) {
-    if constexpr (MODE == kLinInputGrad) {
-      dq[2] = uniform(left > 0 ? S::Q * a.l.n_out * 2 : 0);   // rows are clamped
-      dp[2] = uniform(left > 0 ? pstep : 0);
+    if constexpr (MODE != kLinWeightGrad) {   // lines along j are clamped
+      const uint32_t line = terms_of<MODE>(a.l) * 2;
+      dq[2] = uniform(left > 0 ? GATHER ? static_cast<uint32_t>(a.l.x_rows) * line : S::Q * line : 0);
+      dp[2] = uniform(left > 0 ? MODE == kLinForward ? S::P * line : pstep : 0);
     } else {
       const uint32_t have = min(max(left, 0), kJ);
       dq[2] = uniform(have * a.l.n_out * 2);
@@ -381,7 +453,7 @@ struct Source {
   }
   // The step's indexes, which lie at LDS byte `from`; and this lane's offsets from them.
   __device__ __forceinline__ void load_index(uint32_t from, int lane) {
-    static_assert(!GATHER || (S::P == 256 && S::PCOPIES == 2), "two copies of two lines");
+    static_assert(!STEPWISE || (S::P == 256 && S::PCOPIES == 2), "two copies of two lines");
     typedef __attribute__((address_space(3))) const volatile uint32_t lds_u32_t;
     const lds_u32_t *r = reinterpret_cast<lds_u32_t *>(from + (lane >> 5) * 4);
 #pragma unroll
@@ -457,22 +529,28 @@ struct Reader {
   __device__ __forceinline__ void init(uint32_t ring, int wq, int wp, int lane) {
 #pragma unroll
     for (int i = 0; i < S::QB; ++i) {
-      if constexpr (MODE == kLinInputGrad) {
-        const int row = (wq * S::QB + i) * 32 + (lane & 31);
-        q[i] = ring + row * 64 + (((lane >> 5) ^ ((row >> 2) & 3)) << 4);
+      if constexpr (MODE != kLinWeightGrad) {
+        q[i] = ring + along(wq * S::QB + i, lane);
       } else {
         q[i] = ring + turned_at<S::Q>(wq * S::QB + i, lane);
       }
     }
 #pragma unroll
-    for (int i = 0; i < S::PB; ++i) p[i] = ring + S::QBYTES + turned_at<S::P>(wp * S::PB + i, lane);
+    for (int i = 0; i < S::PB; ++i)
+      p[i] = ring + S::QBYTES + (MODE == kLinForward ? along(wp * S::PB + i, lane) : turned_at<S::P>(wp * S::PB + i, lane));
+  }
+  static __device__ __forceinline__ uint32_t along(int block, int lane) {
+    const int row = block * 32 + (lane & 31);
+    return row * 64 + (((lane >> 5) ^ ((row >> 2) & 3)) << 4);
   }
   __device__ __forceinline__ void read(Frags<S> &f, uint32_t stage, int slice, int i) const {
     if (i < S::QB) {
-      if constexpr (MODE == kLinInputGrad)   // pieces 2 slice + half: slice flips bit 1
+      if constexpr (MODE != kLinWeightGrad)   // pieces 2 slice + half: slice flips bit 1
         f.q[i] = *reinterpret_cast<lds_bf16x8_t *>((q[i] ^ (slice << 5)) + stage);
       else
         f.q[i] = read_turned<S::Q>(q[i] + stage + slice * (16 * S::Q * 2));
+    } else if constexpr (MODE == kLinForward) {
+      f.p[i - S::QB] = *reinterpret_cast<lds_bf16x8_t *>((p[i - S::QB] ^ (slice << 5)) + stage);
     } else {
       f.p[i - S::QB] = read_turned<S::P>(p[i - S::QB] + stage + slice * (16 * S::P * 2));
     }
@@ -492,6 +570,12 @@ __device__ __forceinline__ void wave_order() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
   asm volatile("" ::: "memory");
+}
+
+// v plus four bf16.
+__device__ __forceinline__ void add4(float (&v)[4], uint2 z) {
+  v[0] += __uint_as_float(z.x << 16), v[1] += __uint_as_float(z.x & 0xFFFF0000u);
+  v[2] += __uint_as_float(z.y << 16), v[3] += __uint_as_float(z.y & 0xFFFF0000u);
 }
 
 template <typename S>
@@ -530,10 +614,10 @@ __device__ __forceinline__ void out_f32(const f32x16_t (&acc)[S::PB][S::QB], cha
     }
 }
 
-// bf16: 32 x 64 elements a pass.
-template <typename S>
+// bf16: 32 x 64 elements a pass, with C's biases (or null) added and through the SiLU.
+template <typename S, bool SILU>
 __device__ __forceinline__ void out_bf16(const f32x16_t (&acc)[S::PB][S::QB], char *lds, u32x4_t dst, int pitch, int r0,
-                                         int c0, int columns, int lane) {
+                                         int c0, int columns, const uint16_t *bias, int lane) {
   const int piece = lane & 7;
 #pragma unroll
   for (int qi = 0; qi < S::QB; ++qi)
@@ -544,8 +628,14 @@ __device__ __forceinline__ void out_bf16(const f32x16_t (&acc)[S::PB][S::QB], ch
       for (int h = 0; h < 8; ++h) {
         const f32x16_t &x = acc[pp * 2 + h / 4][qi];
         const int b = h % 4;
+        float v[4] = {x[4 * b], x[4 * b + 1], x[4 * b + 2], x[4 * b + 3]};
+        const int bc = c0 + pp * 64 + h * 8 + (lane >> 5) * 4;
+        if (bias && bc < columns) add4(v, *reinterpret_cast<const uint2 *>(bias + bc));
+        if (SILU)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = silu_fast(v[e]);
         *reinterpret_cast<uint2 *>(lds + w * 128 + ((h ^ (w & 7)) << 4) + ((lane >> 5) << 3)) =
-            make_uint2(pack_bf16x2(x[4 * b], x[4 * b + 1]), pack_bf16x2(x[4 * b + 2], x[4 * b + 3]));
+            make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
       }
       wave_order();
       const int c = c0 + pp * 64 + piece * 8;
@@ -622,7 +712,8 @@ __device__ __forceinline__ void store_bias(O *d, float v, bool accumulate) {
 // Kernel
 // ---------------------------------------------------------------------------
 template <typename S, int MODE, bool GATHER>
-__global__ __launch_bounds__(S::NT, S::WGS * S::WAVES / 4) void linear_grad_kernel(Args a) {
+__global__ __launch_bounds__(S::NT, S::WGS * S::WAVES / 4) void linear_mfma_kernel(Args a) {
+  constexpr bool STEPWISE = Source<S, MODE, GATHER>::STEPWISE;
   constexpr int QB = S::QB, PB = S::PB, NF = QB + PB, NM = QB * PB, GROUPS = 8, PER = NM / GROUPS, RING = S::RING;
   static_assert(NM % GROUPS == 0 && NF <= GROUPS && RING >= 3, "reads among the products, two steps ahead");
   // The copies of a step are spread over the half step behind the barrier that frees its
@@ -631,7 +722,7 @@ __global__ __launch_bounds__(S::NT, S::WGS * S::WAVES / 4) void linear_grad_kern
   static_assert(EARLY * 2 <= GROUPS && LATE * 2 <= GROUPS, "at most one for two products");
   __shared__ __attribute__((aligned(1024))) char s_ring[RING * S::STAGE];
   __shared__ int s_pref[kMaxGroups + 1], s_off[kMaxGroups + 1], s_tmp[S::WAVES];
-  __shared__ __attribute__((aligned(256))) char s_index[GATHER ? IndexStream<S>::BYTES : 4];
+  __shared__ __attribute__((aligned(256))) char s_index[STEPWISE ? IndexStream<S>::BYTES : GATHER ? RowIndex<S>::BYTES : 4];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   // Waves w and w + 4 share a SIMD: with blocks that lie behind a tile's rows (or columns)
   // left out, the SIMDs still have about the same to multiply.
@@ -651,7 +742,9 @@ __global__ __launch_bounds__(S::NT, S::WGS * S::WAVES / 4) void linear_grad_kern
   // the one that is multiplied.  A tile has RING steps at least, so that `fill` is that
   // one's tile or the next.
   Source<S, MODE, GATHER> src;
+  constexpr bool ROWWISE = GATHER && !STEPWISE;
   IndexStream<S> rows;
+  RowIndex<S> once;
   int fill_item = item;
   Tile fill = tile_at<S, MODE>(a, plan, s_pref, s_off, item, 0), ahead = fill;
   int fill_left = max(fill.s1 - fill.s0, RING), steps = fill_left;   // the one at hand among them
@@ -660,7 +753,8 @@ __global__ __launch_bounds__(S::NT, S::WGS * S::WAVES / 4) void linear_grad_kern
     static_assert(RING >= 4, "a tile has four steps at least");
     if (fill_left != 4 || fill_item + stride >= plan.end) return;
     ahead = tile_at<S, MODE>(a, plan, s_pref, s_off, fill_item + stride, fill.g);
-    if constexpr (GATHER) rows.start(ahead, wave, lane);
+    if constexpr (STEPWISE) rows.start(ahead, wave, lane);
+    if constexpr (ROWWISE) once.start(ahead, wave, lane);
   };
   // The next tile, where this one's steps are all copied; then the next step.
   bool fresh = false;
@@ -671,7 +765,7 @@ __global__ __launch_bounds__(S::NT, S::WGS * S::WAVES / 4) void linear_grad_kern
       int el = lane;
       asm volatile("" : "+v"(el));       // as for the sums below
       fill = ahead;
-      src.init(a, fill, wave, el);
+      src.init(a, fill, ROWWISE ? once.place() : 0, wave, el);
       fill_left = max(fill.s1 - fill.s0, RING) + 1;
       fresh = true;
     } else {
@@ -683,20 +777,25 @@ __global__ __launch_bounds__(S::NT, S::WGS * S::WAVES / 4) void linear_grad_kern
     if (!fresh) src.advance(a);
     --fill_left;
     fresh = false;
-    if constexpr (GATHER) src.gather(a, wave, lane);
+    if constexpr (STEPWISE) src.gather(a, wave, lane);
     look_ahead();
-    if constexpr (GATHER) {
+    if constexpr (STEPWISE) {
       rows.next(fill_left - 1, wave, lane);
       src.load_index(rows.place(), lane);
     }
   };
-  src.init(a, fill, wave, lane);
-  if constexpr (GATHER) {
+  if constexpr (ROWWISE) {
+    once.init(a, uniform(static_cast<int>(dma::lds_addr(s_index))), wave);
+    once.start(fill, wave, lane);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  }
+  src.init(a, fill, ROWWISE ? once.place() : 0, wave, lane);
+  if constexpr (STEPWISE) {
     rows.init(a, uniform(static_cast<int>(dma::lds_addr(s_index))), wave);
     rows.start(fill, wave, lane);
   }
   look_ahead();
-  if constexpr (GATHER) {
+  if constexpr (STEPWISE) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copies yet that would cover these
     src.load_index(rows.place(), lane);
     src.gather(a, wave, lane);
@@ -755,7 +854,7 @@ __global__ __launch_bounds__(S::NT, S::WGS * S::WAVES / 4) void linear_grad_kern
     float bias[QB];
 #pragma unroll
     for (int q = 0; q < QB; ++q) bias[q] = 0.0f;
-    const int nq = (MODE == kLinWeightGrad ? a.l.n_out : t.rows) - t.q0, np = a.l.k;
+    const int nq = (MODE == kLinWeightGrad ? a.l.n_out : t.rows) - t.q0, np = columns_of<MODE>(a.l);
     const bool busy = wq * QB * 32 < nq && t.p0 + wp * PB * 32 < np;   // blocks of this wave are there
     const bool sum_dy = MODE == kLinWeightGrad && a.l.dbias && t.p0 == 0 && wp == 0;
     auto add_dy = [&](const Frags<S> &f) {
@@ -843,13 +942,21 @@ __global__ __launch_bounds__(S::NT, S::WGS * S::WAVES / 4) void linear_grad_kern
                    a.l.accumulate, el);
       } else {
         const u32x4_t dst = descriptor(static_cast<uint16_t *>(a.l.out) + row * np, size * 2);
-        if (MODE == kLinInputGrad && a.l.act_pre)
+        if (MODE == kLinForward) {
+          const uint16_t *bias =
+              a.l.bias ? static_cast<const uint16_t *>(a.l.bias) + static_cast<int64_t>(t.g) * np : nullptr;
+          if (a.l.pre)
+            out_bf16<S, false>(acc, lds, descriptor(static_cast<uint16_t *>(a.l.pre) + row * np, size * 2), np, r0, c0, np,
+                               bias, el);
+          if (a.l.silu) out_bf16<S, true>(acc, lds, dst, np, r0, c0, np, bias, el);
+          else out_bf16<S, false>(acc, lds, dst, np, r0, c0, np, bias, el);
+        } else if (MODE == kLinInputGrad && a.l.act_pre)
           out_bf16_with<S, true>(acc, lds, dst, descriptor(static_cast<const uint16_t *>(a.l.act_pre) + row * np, size * 2),
                                  np, r0, c0, np, el);
         else if (MODE == kLinWeightGrad && a.l.accumulate)
           out_bf16_with<S, false>(acc, lds, dst, dst, np, r0, c0, np, el);
         else
-          out_bf16<S>(acc, lds, dst, np, r0, c0, np, el);
+          out_bf16<S, false>(acc, lds, dst, np, r0, c0, np, nullptr, el);
       }
     }
     if (sum_dy && busy)
@@ -891,14 +998,14 @@ struct Threads256 : S {
 // 16 workgroups and one part after another, 9 tiles of 28 parts took 51 us).
 constexpr int kPartGroups = 32;
 template <typename S, int MODE>
-__global__ __launch_bounds__(256) void linear_grad_parts_kernel(Args a) {
+__global__ __launch_bounds__(256) void linear_mfma_parts_kernel(Args a) {
   __shared__ int s_pref[kMaxGroups + 1], s_off[kMaxGroups + 1], s_tmp[4];
   const Plan plan = make_plan<Threads256<S>, MODE>(a, s_pref, s_off, s_tmp, 0);
   const int at = blockIdx.x / kPartGroups;
   if (plan.parts <= 1 || at >= plan.tiles) return;
   const Tile t = tile_at<S, MODE>(a, plan, s_pref, s_off, at * plan.parts, 0);
   const float *part = a.part + static_cast<int64_t>(at) * plan.parts * S::PART;
-  const int np = a.l.k, rows = MODE == kLinWeightGrad ? a.l.n_out : t.rows;
+  const int np = columns_of<MODE>(a.l), rows = MODE == kLinWeightGrad ? a.l.n_out : t.rows;
   const int64_t row = (MODE == kLinWeightGrad ? static_cast<int64_t>(t.g) * a.l.n_out : t.row0) + t.q0;
   constexpr int kEach = S::Q * S::P / 4 / kPartGroups;   // float4 of a workgroup
   for (int e = threadIdx.x; e < kEach; e += 256) {
@@ -920,7 +1027,17 @@ __global__ __launch_bounds__(256) void linear_grad_parts_kernel(Args a) {
       *d = v;
     } else {
       uint2 *d = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.l.out) + o);
-      if (MODE == kLinWeightGrad ? a.l.accumulate : a.l.act_pre != nullptr) {
+      if (MODE == kLinForward) {
+        float u[4] = {v.x, v.y, v.z, v.w};
+        if (a.l.bias)
+          add4(u, *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.l.bias) + static_cast<int64_t>(t.g) * np +
+                                                   t.p0 + c));
+        v = make_float4(u[0], u[1], u[2], u[3]);
+        if (a.l.pre)
+          *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.l.pre) + o) =
+              make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        if (a.l.silu) v.x = silu_fast(v.x), v.y = silu_fast(v.y), v.z = silu_fast(v.z), v.w = silu_fast(v.w);
+      } else if (MODE == kLinWeightGrad ? a.l.accumulate : a.l.act_pre != nullptr) {
         const uint2 z = MODE == kLinWeightGrad
                             ? *d : *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.l.act_pre) + o);
         const float u[4] = {__uint_as_float(z.x << 16), __uint_as_float(z.x & 0xFFFF0000u), __uint_as_float(z.y << 16),
@@ -946,7 +1063,7 @@ __global__ __launch_bounds__(256) void linear_grad_parts_kernel(Args a) {
 // Tiles at most, and parts of a tile at most (1: the sizes never need a split).
 template <typename S>
 int64_t tile_bound(int mode, int groups, int n_out, int k, int64_t max_rows) {
-  const int64_t pt = (k + S::P - 1) / S::P;
+  const int64_t pt = ((mode == kLinForward ? n_out : k) + S::P - 1) / S::P;
   if (mode == kLinWeightGrad) return pt * groups * ((n_out + S::Q - 1) / S::Q);
   return pt * (max_rows / S::Q + (max_rows < groups ? max_rows : groups));
 }
@@ -955,7 +1072,7 @@ int part_bound(int mode, int groups, int n_out, int k, int64_t max_rows) {
   if (tile_bound<S>(mode, groups, n_out, k, max_rows) > S::SLOTS) return 1;
   // groups of several times the mean's rows are split, where all are short nothing is
   const int64_t rows = max_rows / groups < max_rows / 4 ? max_rows / groups * 4 + 4 : max_rows;
-  const int64_t steps = mode == kLinWeightGrad ? (rows + kJ - 1) / kJ : n_out / kJ;
+  const int64_t steps = mode == kLinWeightGrad ? (rows + kJ - 1) / kJ : (mode == kLinForward ? k : n_out) / kJ;
   const int64_t parts = steps / kMinSteps;
   return static_cast<int>(parts < 1 ? 1 : parts < S::SLOTS ? parts : S::SLOTS);
 }
@@ -964,12 +1081,12 @@ template <typename S, int MODE, bool GATHER>
 void launch_mode(const Args &a, hipStream_t s) {
   const int64_t items = tile_bound<S>(MODE, a.l.groups, a.l.n_out, a.l.k, a.l.max_rows) * a.most_parts;
   const int64_t want = (items + kXcds - 1) / kXcds * kXcds;
-  hipLaunchKernelGGL((linear_grad_kernel<S, MODE, GATHER>), dim3(static_cast<unsigned>(want < S::SLOTS ? want : S::SLOTS)),
+  hipLaunchKernelGGL((linear_mfma_kernel<S, MODE, GATHER>), dim3(static_cast<unsigned>(want < S::SLOTS ? want : S::SLOTS)),
                      dim3(S::NT), 0, s, a);
   if (a.most_parts > 1) {
     const int64_t tiles = tile_bound<S>(MODE, a.l.groups, a.l.n_out, a.l.k, a.l.max_rows);
     const int64_t split = tiles < S::SLOTS / 2 ? tiles : S::SLOTS / 2;
-    hipLaunchKernelGGL((linear_grad_parts_kernel<S, MODE>), dim3(static_cast<unsigned>(split * kPartGroups)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((linear_mfma_parts_kernel<S, MODE>), dim3(static_cast<unsigned>(split * kPartGroups)), dim3(256), 0, s, a);
   }
 }
 
@@ -977,6 +1094,8 @@ template <typename S>
 hipError_t launch_shape(const Linear &p, void *ws, hipStream_t s) {
   const Args a{p, static_cast<float *>(ws), part_bound<S>(p.mode, p.groups, p.n_out, p.k, p.max_rows)};
   if (p.mode == kLinInputGrad) launch_mode<S, kLinInputGrad, false>(a, s);
+  else if (p.mode == kLinForward && p.index) launch_mode<S, kLinForward, true>(a, s);
+  else if (p.mode == kLinForward) launch_mode<S, kLinForward, false>(a, s);
   else if (p.index && p.max_rows > 0) launch_mode<S, kLinWeightGrad, true>(a, s);
   else launch_mode<S, kLinWeightGrad, false>(a, s);
   return hipGetLastError();
@@ -984,24 +1103,44 @@ hipError_t launch_shape(const Linear &p, void *ws, hipStream_t s) {
 
 using Tiles = Shape<2, 4, 4>;
 
-}  // namespace
-
-// Widths whose lines of a tile stay below 4 GiB, a gathered x and its indexes that do, and items that
-// are counted in 31 bits.
-bool linear_grad_fits(const Linear &p) {
-  if (!p.bf16 || p.mode == kLinForward || p.n_out >= (1 << 20) || p.k >= (1 << 20)) return false;
-  if (tile_bound<Tiles>(p.mode, p.groups, p.n_out, p.k, p.max_rows) >= (int64_t(1) << 30)) return false;
-  return p.mode != kLinWeightGrad || !p.index || (p.x_rows <= 0xFFFFFE00ll / 2 / p.k && p.max_rows < (1 << 30));
+// The forward goes here from 64 rows a group on, up to 512 where there are more than 256
+// tiles; below, the layer's kernels stream weights faster, above, their 256 x 256 tiles are.
+// Layer's kernels / this one, us, by rows of each group:
+//                            16        32        64       128       256       512      1024
+//   8 x 2048 x 2048        35/31     39/31     48/33     76/39     65/48     61/60   101/113
+//   64 x 2048 x 2048     115/141   130/142   178/148   196/190   232/207   353/334
+//   256 x 2048 x 1408    289/321   306/331   357/346   450/419
+//   64 x 4096 x 512        82/93     90/95   145/100   143/114   127/129   195/213
+//   8 x 4096 x 14336     199/183   211/188   253/199   318/223   345/330   531/556   903/949
+// and with few tiles 1221 rows on 2 x 6272 x 2304 172/65, 138 on 1 x 5376 x 128 113/24
+// (split sums); 28962 rows on 8 x 512 x 192 29/38 is the other way (a quarter of each tile
+// lies behind the columns).
+constexpr int64_t kFewTiles = 256;
+bool forward_pays(const Linear &p) {
+  const int64_t tiles = tile_bound<Tiles>(kLinForward, p.groups, p.n_out, p.k, p.max_rows);
+  const int64_t rows = p.max_rows / p.groups;
+  return rows >= 64 && (rows <= 512 || tiles <= kFewTiles);
 }
 
-size_t linear_grad_workspace_bytes(int groups, int n_out, int k, int64_t max_rows) {
-  for (int mode : {kLinInputGrad, kLinWeightGrad})
+}  // namespace
+
+// Widths whose lines of a tile stay below 4 GiB, a gathered x and its indexes that do, and
+// items that are counted in 31 bits.
+bool linear_mfma_fits(const Linear &p) {
+  if (!p.bf16 || p.n_out >= (1 << 20) || p.k >= (1 << 20)) return false;
+  if (tile_bound<Tiles>(p.mode, p.groups, p.n_out, p.k, p.max_rows) >= (int64_t(1) << 30)) return false;
+  if (p.mode == kLinForward && !forward_pays(p)) return false;
+  return p.mode == kLinInputGrad || !p.index || (p.x_rows <= 0xFFFFFE00ll / 2 / p.k && p.max_rows < (1 << 30));
+}
+
+size_t linear_mfma_workspace_bytes(int groups, int n_out, int k, int64_t max_rows) {
+  for (int mode : {kLinForward, kLinInputGrad, kLinWeightGrad})
     if (part_bound<Tiles>(mode, groups, n_out, k, max_rows) > 1)
       return static_cast<size_t>(Tiles::SLOTS) * Tiles::PART * sizeof(float);
   return 0;
 }
 
-hipError_t launch_linear_grad(const Linear &p, void *ws, hipStream_t s) {
+hipError_t launch_linear_mfma(const Linear &p, void *ws, hipStream_t s) {
   return launch_shape<Tiles>(p, ws, s);
 }
 

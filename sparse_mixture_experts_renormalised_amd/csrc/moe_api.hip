@@ -613,7 +613,7 @@ size_t moe_grouped_linear_workspace_size(int32_t dtype, int32_t n_groups, int32_
   g.max_routed_rows = max_rows;
   g.Nout = n_out;
   const size_t forward = moe::grouped_gemm_split_bytes(g);
-  const size_t grad = moe::linear_grad_workspace_bytes(n_groups, n_out, k, max_rows);
+  const size_t grad = moe::linear_mfma_workspace_bytes(n_groups, n_out, k, max_rows);
   return forward > grad ? forward : grad;
 }
 
@@ -630,8 +630,8 @@ static moe::Linear linear_of(moe::LinearMode mode, int32_t dtype, int32_t n_grou
   return p;
 }
 
-static int run_linear_grad(const moe::Linear &p, void *ws, hipStream_t s) {
-  return hip_status(moe::linear_grad_fits(p) ? moe::launch_linear_grad(p, ws, s) : moe::launch_linear_f32(p, ws, s));
+static int run_linear(const moe::Linear &p, void *ws, hipStream_t s) {
+  return hip_status(moe::linear_mfma_fits(p) ? moe::launch_linear_mfma(p, ws, s) : moe::launch_linear_f32(p, ws, s));
 }
 
 int moe_grouped_linear(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k, int64_t x_rows,
@@ -647,7 +647,16 @@ int moe_grouped_linear(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k
   if (!all_aligned16({x, row_index, offsets, w, bias, y, pre, ws})) return MOE_ERR_INVALID_ARG;
   const size_t need = moe_grouped_linear_workspace_size(dtype, n_groups, n_out, k, max_rows);
   if (need && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
-  if (dtype == MOE_BF16) {
+  moe::Linear p = linear_of(moe::kLinForward, dtype, n_groups, n_out, k, offsets, max_rows);
+  p.x_rows = x_rows;
+  p.x = x;
+  p.index = row_index;
+  p.w = w;
+  p.bias = bias;
+  p.silu = silu != 0;
+  p.out = y;
+  p.pre = pre;
+  if (dtype == MOE_BF16 && !moe::linear_mfma_fits(p)) {
     GemmGroups g{};
     g.offsets = offsets;
     g.n_routed = n_groups;
@@ -667,16 +676,7 @@ int moe_grouped_linear(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k
     return hip_status(moe::launch_grouped_gemm(
         true, g, pre ? moe::kEpiBiasSiluPre : silu ? moe::kEpiBiasSilu : moe::kEpiBias, static_cast<hipStream_t>(stream)));
   }
-  moe::Linear p = linear_of(moe::kLinForward, dtype, n_groups, n_out, k, offsets, max_rows);
-  p.x_rows = x_rows;
-  p.x = x;
-  p.index = row_index;
-  p.w = w;
-  p.bias = bias;
-  p.silu = silu != 0;
-  p.out = y;
-  p.pre = pre;
-  return hip_status(moe::launch_linear_f32(p, ws, static_cast<hipStream_t>(stream)));
+  return run_linear(p, ws, static_cast<hipStream_t>(stream));
 }
 
 int moe_grouped_linear_input_grad(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k,
@@ -695,7 +695,7 @@ int moe_grouped_linear_input_grad(int32_t dtype, int32_t n_groups, int32_t n_out
   p.w = w;
   p.act_pre = pre;
   p.out = dx;
-  return run_linear_grad(p, ws, static_cast<hipStream_t>(stream));
+  return run_linear(p, ws, static_cast<hipStream_t>(stream));
 }
 
 int moe_grouped_linear_weight_grad(int32_t dtype, int32_t grad_dtype, int32_t n_groups,
@@ -724,7 +724,7 @@ int moe_grouped_linear_weight_grad(int32_t dtype, int32_t grad_dtype, int32_t n_
   p.out = dw;
   p.dbias = dbias;
   p.accumulate = accumulate != 0;
-  return run_linear_grad(p, ws, static_cast<hipStream_t>(stream));
+  return run_linear(p, ws, static_cast<hipStream_t>(stream));
 }
 
 // The probability in steps of 2^-16 (ties to even), or -1 outside [0, 1).

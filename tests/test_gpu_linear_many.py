@@ -1,4 +1,4 @@
-"""Gradients of the single Linears where a workgroup takes several tiles, where sums
+"""The single Linears and their gradients where a workgroup takes several tiles, where sums
 are split, and where offsets pass 32 bits, against float64 products on the GPU.
 
 Bounds as for the small cases: float32 sums of n products are off by at most
@@ -101,6 +101,26 @@ def check_input_grad(B, d, pre):
         close(dx[a:b], ref, bound, f"dx of group {g}")
 
 
+def check_forward(B, d, bias, silu, pre):
+    dt = d.w.dtype
+    y, z = (torch.full((d.rows + 3, d.n_out), 0.5, dtype=dt, device="cuda") for _ in range(2))
+    b = torch.randn(d.G, d.n_out, device="cuda").to(dt) if bias else None
+    B.grouped_linear(d.x, d.offsets, d.w, y, row_index=d.index, bias=b, silu=silu, pre=z if pre else None, ws=d.ws)
+    torch.cuda.synchronize()
+    assert (y[d.rows:] == 0.5).all() and (z[d.rows:] == 0.5).all()
+    for g in range(d.G):
+        a, e = d.off[g], d.off[g + 1]
+        x, w = d.source(g).double(), d.w[g].double().t().contiguous()
+        add = b[g].double() if bias else torch.zeros(d.n_out, dtype=torch.float64, device="cuda")
+        ref, bound = x @ w + add, (d.k + 4) * U * (x.abs() @ w.abs() + add.abs())
+        if pre:
+            close(z[a:e], ref, bound, f"pre of group {g}")
+        if silu:
+            ref = ref * torch.sigmoid(ref)
+            bound = 1.1 * bound + 2.0 ** -19 * (1 + (x @ w + add).abs()) * ref.abs()
+        close(y[a:e], ref, bound, f"y of group {g}")
+
+
 SHORT = [0, 1, 31, 32, 33, 64, 97, 128, 130, 5]
 WEIGHT = [
     # counts, n_out, k: short tiles after another, long ones, groups of very different lengths
@@ -138,6 +158,25 @@ def test_input_grad(B, n, pre):
     check_input_grad(B, Data(B, counts, n_out, k, 60 + n), pre)
 
 
+FORWARD = [
+    ([700, 0, 256, 257, 3, 511] * 6, 576, 1088),
+    ([138], 128, 5376),                      # split along the sum
+    ([1221, 0, 900], 320, 2048),
+    ([512] * 60 + [0, 1, 513], 256, 448),
+    ([65] * 90 + [0, 200], 192, 64),         # two steps
+    ([640, 641, 639], 2304, 128),
+]
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("bias,silu,pre", [(False, False, False), (True, False, False), (False, True, False), (True, True, True)])
+@pytest.mark.parametrize("n", range(len(FORWARD)))
+def test_forward(B, n, bias, silu, pre, gather):
+    counts, n_out, k = FORWARD[n]
+    print(f"[linear] forward {n} {bias} {silu} {pre} {gather}", flush=True)
+    check_forward(B, Data(B, counts, n_out, k, 90 + n, sum(counts) // 2 if gather else 0), bias, silu, pre)
+
+
 # few tiles and long sums in float32: counts, n_out, k
 LONG = [([2967], 80, 208), ([700, 0, 3, 5000, 12], 48, 112), ([1988], 1808, 80), ([5, 0, 70, 130], 2048, 2032),
         ([1], 64, 16384), ([64, 1], 16400, 16)]
@@ -152,18 +191,7 @@ def test_float32_split(B, n):
     check_weight_grad(B, d, F32)
     check_weight_grad(B, d, F32, True)
     check_input_grad(B, d, n % 2 == 0)
-    bias = torch.randn(d.G, n_out, device="cuda")
-    y, pre = (torch.full((d.rows + 3, n_out), 0.5, device="cuda") for _ in range(2))
-    B.grouped_linear(d.x, d.offsets, d.w, y, row_index=d.index, bias=bias, silu=True, pre=pre, ws=d.ws)
-    torch.cuda.synchronize()
-    assert (y[d.rows:] == 0.5).all() and (pre[d.rows:] == 0.5).all()
-    for g in range(d.G):
-        a, b = d.off[g], d.off[g + 1]
-        x, w = d.source(g).double(), d.w[g].double().t().contiguous()
-        z, bound = x @ w + bias[g].double(), (k + 4) * U * (x.abs() @ w.abs() + bias[g].double().abs())
-        close(pre[a:b], z, bound, f"pre of group {g}")
-        silu = z * torch.sigmoid(z)
-        close(y[a:b], silu, 1.1 * bound + 2.0 ** -19 * (1 + z.abs()) * silu.abs(), f"y of group {g}")
+    check_forward(B, d, True, True, True)
 
 
 def test_widths_beyond_the_tiles(B):
