@@ -128,6 +128,8 @@ WEIGHT = [
     ([900, 0, 1700], 2560, 2560),
     ([1] * 70 + [4000] + [0] * 30 + [33] * 90, 256, 832),
     ([511, 513] * 40 + [0, 2], 576, 448),
+    ([9000, 700, 0, 1300, 64, 5000, 33, 1], 1088, 832),   # lengths far apart
+    ([40] * 60 + [3000] + [20] * 100, 320, 320),
 ]
 SPLIT = [([5000], 128, 192), ([4000, 3, 0, 900], 256, 320), ([2600, 2601], 448, 64)]
 
