@@ -33,13 +33,13 @@ struct Linear {
   bool accumulate;              // add to dw and dbias
 };
 
-// float32 (all three) and the bf16 gradients that launch_linear_mfma does not take; ws:
+// float32 (all three) and the bf16 gradients that linear_mfma_fits leaves to it; ws:
 // linear_f32_workspace_bytes of scratch for float32, not read for bf16.
 size_t linear_f32_workspace_bytes(int groups, int n_out, int k, int64_t max_rows);
 hipError_t launch_linear_f32(const Linear &p, void *ws, hipStream_t s);
 
-// bf16 operands, where linear_mfma_fits (32-bit offsets of a gathered x; the forward where
-// the layer's kernels would be slower); ws: linear_mfma_workspace_bytes of scratch.
+// bf16 operands, where linear_mfma_fits: 32-bit offsets, gradients with more than a little
+// to do, the forward where the layer's kernels would be slower; ws: linear_mfma_workspace_bytes of scratch.
 bool linear_mfma_fits(const Linear &p);
 size_t linear_mfma_workspace_bytes(int groups, int n_out, int k, int64_t max_rows);
 hipError_t launch_linear_mfma(const Linear &p, void *ws, hipStream_t s);

@@ -460,7 +460,7 @@ hipError_t launch_linear_f32(const Linear &p, void *ws, hipStream_t s) {
     if (p.mode == kLinForward) launch<float, float, kLinForward>(p, ws, s);
     else if (p.mode == kLinInputGrad) launch<float, float, kLinInputGrad>(p, ws, s);
     else launch<float, float, kLinWeightGrad>(p, ws, s);
-  } else if (p.mode == kLinInputGrad) {   // never split: ws is not for these sizes
+  } else if (p.mode == kLinInputGrad) {   // never split: the sums are short, or the widths enough
     launch<uint16_t, uint16_t, kLinInputGrad>(p, nullptr, s);
   } else if (p.out_bf16) {
     launch<uint16_t, uint16_t, kLinWeightGrad>(p, nullptr, s);

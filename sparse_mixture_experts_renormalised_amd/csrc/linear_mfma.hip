@@ -1125,6 +1125,22 @@ bool forward_pays(const Linear &p) {
   return rows >= 64 && (rows <= 512 || tiles <= kFewTiles);
 }
 
+
+// Gradients whose sums take a few steps and that have little to do go through the float32
+// kernel's 64 x 64 tiles: here a launch alone takes 8 to 10 us, in a prologue that fills the
+// ring and a code of many lines.  This kernel / the float32 one, us in a graph:
+//   weight gradient, rows of all groups x n_out x k: 8 x 2 x 320 x 448 10.1/4.5, 31 x 64 x
+//   320 8.3/4.7, 13 x 182 x 128 x 576 21.0/13.6, 43 x 3 x 64 x 8576 10.3/7.1; beyond, 136 x
+//   2 x 1856 x 768 10.3/10.3, 4 x 4 x 576 x 9280 18.4/28.4, 1275 x 256 x 320 17.7/45.9
+//   input gradient: 1898 rows, 64 x 64 11.4/7.0, 94 of 192 x 64 16.1/10.3, 1814 of 64 x 2048
+//   47.6/41.5; beyond, 1839 of 128 x 10496 35.0/86.4, 657 of 704 x 128 14.6/24.4
+bool little(const Linear &p) {
+  if (p.mode == kLinForward) return false;
+  if (p.mode == kLinWeightGrad)
+    return p.max_rows <= 128 && static_cast<int64_t>(p.groups) * p.n_out * p.k <= (1 << 24);
+  return p.n_out <= 192 && p.max_rows * p.k * p.n_out <= (1 << 28);
+}
+
 }  // namespace
 
 // Widths whose lines of a tile stay below 4 GiB, a gathered x and its indexes that do, and
@@ -1132,7 +1148,7 @@ bool forward_pays(const Linear &p) {
 bool linear_mfma_fits(const Linear &p) {
   if (!p.bf16 || p.n_out >= (1 << 20) || p.k >= (1 << 20)) return false;
   if (tile_bound<Tiles>(p.mode, p.groups, p.n_out, p.k, p.max_rows) >= (int64_t(1) << 30)) return false;
-  if (p.mode == kLinForward && !forward_pays(p)) return false;
+  if (little(p) || (p.mode == kLinForward && !forward_pays(p))) return false;
   return p.mode == kLinInputGrad || !p.index || (p.x_rows <= 0xFFFFFE00ll / 2 / p.k && p.max_rows < (1 << 30));
 }
 
