@@ -1149,7 +1149,7 @@ bool linear_mfma_fits(const Linear &p) {
   if (!p.bf16 || p.n_out >= (1 << 20) || p.k >= (1 << 20)) return false;
   if (tile_bound<Tiles>(p.mode, p.groups, p.n_out, p.k, p.max_rows) >= (int64_t(1) << 30)) return false;
   if (little(p) || (p.mode == kLinForward && !forward_pays(p))) return false;
-  return p.mode == kLinInputGrad || !p.index || (p.x_rows <= 0xFFFFFE00ll / 2 / p.k && p.max_rows < (1 << 30));
+  return p.mode == kLinInputGrad || !p.index || (p.x_rows <= 0xFFFFFE00ll / 2 / p.k && p.max_rows <= 0xFFFFFE00ll / 4);
 }
 
 size_t linear_mfma_workspace_bytes(int groups, int n_out, int k, int64_t max_rows) {
