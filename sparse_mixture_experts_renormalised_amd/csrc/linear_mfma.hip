@@ -34,7 +34,7 @@
 //     workgroups come to a tile's end at about the same time.  256 groups of 128, to bf16:
 //     450 us, 3.8 TB/s.
 //   forward of 64 groups of 512 gathered rows, 2048 -> 1408, with the SiLU and the values
-//     before it: 245 to 300 us; 3.3 rounds of tiles (CUs are busy 79% of the time), matrix
+//     before it: 245 to 300 us; 3.7 rounds of tiles (CUs are busy 79% of the time), matrix
 //     instructions 36%.
 //   input gradient of 207 rows on 256 experts of 2048 x 7168: 425 us, 5.8 TB/s of weights.
 // Tiles of 128 x 256 with two workgroups a CU took 1134 us for the first and 306 for the
