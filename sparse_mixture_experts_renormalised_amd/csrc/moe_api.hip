@@ -757,9 +757,11 @@ static int check_block(const moe_block *c) {
   return MOE_OK;
 }
 
-// Sizes and arrays of the expert rows.
+// Sizes and arrays of the expert rows.  Without tokens the slots' arrays are empty, and may
+// have no address.
 static int check_slots(const moe_block *c, const moe_block_tensors *in) {
-  if (c->top_k <= 0 || c->n_shared < 0 || !in->slot_row || !in->topk_gate) return MOE_ERR_INVALID_ARG;
+  if (c->top_k <= 0 || c->n_shared < 0) return MOE_ERR_INVALID_ARG;
+  if (c->T > 0 && (!in->slot_row || !in->topk_gate)) return MOE_ERR_INVALID_ARG;
   if (c->top_k > 64 || c->n_shared > moe::kMaxShared) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }

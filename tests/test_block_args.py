@@ -174,3 +174,19 @@ def test_binding_refuses_shapes(B):
         B.dropout(x, x, 0.5, None)
     with pytest.raises(ValueError):
         B.block_join(B.block(4, 64, "bf16"), x, out=x)
+
+
+def test_no_tokens_with_expert_rows(B):
+    """A step without tokens: slot arrays are empty (and have no address), while expert rows
+    and their gradients are usually buffers with room.  Sizes are checked all the same."""
+    empty = cfg_of(B, T=0)
+    rows = {"residual": None, "branch": None, "y_rows": 4096}
+    assert join(B, empty, out=None, nxt=None, **rows) == 0
+    assert join(B, empty, out=None, nxt=None, **rows, slot_row=4096) == 0
+    asked = {"branch": None, "d_branch": None, "d_w_in": None, "y_rows": 4096, "d_y_rows": 4096, "d_topk_gate": 4096}
+    assert grad(B, empty, out=None, d_out=None, d_next=None, ws=None, **asked) == 0
+    for call in (lambda c: join(B, c, **rows), lambda c: grad(B, c, **asked)):
+        assert call(cfg_of(B, T=0, top_k=0)) == -1
+        assert call(cfg_of(B, T=0, n_shared=-1)) == -1
+        assert call(cfg_of(B, T=0, top_k=65)) == -2
+        assert call(cfg_of(B, T=0, n_shared=65)) == -2

@@ -362,3 +362,22 @@ def test_a_dropped_element_takes_no_part(B):
     for other in got[1:]:
         for a, b in zip(got[0], other):
             assert torch.equal(a, b)
+
+
+def test_no_tokens_with_expert_rows(B):
+    """Empty slot arrays beside expert rows with room: nothing is written but the sums over
+    tokens, which are zeros."""
+    d, k = 64, 3
+    cfg = B.block(0, d, "bf16", norm_out="rms", top_k=k, n_shared=1)
+    x = torch.empty(0, d, dtype=torch.bfloat16, device="cuda")
+    slots, gates = torch.empty(0, k, dtype=torch.int32, device="cuda"), torch.empty(0, k, device="cuda")
+    y, dy = (torch.full((4, d), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    shared = torch.empty(1, 0, d, dtype=torch.bfloat16, device="cuda")
+    B.block_join(cfg, x, out=x, next=x, y_rows=y, slot_row=slots, topk_gate=gates, shared_out=shared, branch_out=x)
+    sums = {n: torch.full((d,), 5.0, device="cuda") for n in ("d_w_out", "d_b_out", "d_w_in", "d_b_in")}
+    B.block_join_grad(cfg, x, x, x, branch=x, y_rows=y, slot_row=slots, topk_gate=gates, d_residual=x, d_branch=x,
+                      d_y_rows=dy, d_topk_gate=torch.empty_like(gates), **sums)
+    torch.cuda.synchronize()
+    for n, v in sums.items():
+        assert (v == 0).all(), n
+    assert (y == 5).all() and (dy == 5).all()
