@@ -34,7 +34,7 @@ struct Linear {
 };
 
 // float32 (all three) and the bf16 gradients that linear_mfma_fits leaves to it; ws:
-// linear_f32_workspace_bytes of scratch for float32, not read for bf16.
+// linear_f32_workspace_bytes of scratch.
 size_t linear_f32_workspace_bytes(int groups, int n_out, int k, int64_t max_rows);
 hipError_t launch_linear_f32(const Linear &p, void *ws, hipStream_t s);
 

@@ -17,7 +17,9 @@
 // workspace and a second kernel adds them in order.  A step takes about 1.2 us, however
 // few workgroups there are (a load's latency and the products), so that one group of 2967
 // rows took 125 us and takes 18.5 in parts of 128 rows (20.6 of 256, 28.2 of 512, 25.7 of
-// 64).
+// 64).  So it is for the bf16 gradients that come here with long sums, those of a gathered x
+// of 4 GiB and more (400000 rows, 64 x 7168: 16400 us whole, 3800 split) and of widths of 2^20
+// and more (3 rows, input gradient through 2^20 outputs to 64: 33700 and 174).
 //
 // 16 groups of 512 rows, 1024 x 1024: forward 229-241 us, input gradient 205, weight
 // gradient 203 (71 to 85 TFLOP/s of the 149 that one large library product reaches), bound
@@ -460,12 +462,12 @@ hipError_t launch_linear_f32(const Linear &p, void *ws, hipStream_t s) {
     if (p.mode == kLinForward) launch<float, float, kLinForward>(p, ws, s);
     else if (p.mode == kLinInputGrad) launch<float, float, kLinInputGrad>(p, ws, s);
     else launch<float, float, kLinWeightGrad>(p, ws, s);
-  } else if (p.mode == kLinInputGrad) {   // never split: the sums are short, or the widths enough
-    launch<uint16_t, uint16_t, kLinInputGrad>(p, nullptr, s);
+  } else if (p.mode == kLinInputGrad) {
+    launch<uint16_t, uint16_t, kLinInputGrad>(p, ws, s);
   } else if (p.out_bf16) {
-    launch<uint16_t, uint16_t, kLinWeightGrad>(p, nullptr, s);
+    launch<uint16_t, uint16_t, kLinWeightGrad>(p, ws, s);
   } else {
-    launch<uint16_t, float, kLinWeightGrad>(p, nullptr, s);
+    launch<uint16_t, float, kLinWeightGrad>(p, ws, s);
   }
   return hipGetLastError();
 }

@@ -606,15 +606,17 @@ static int check_linear(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t 
 size_t moe_grouped_linear_workspace_size(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k,
                                          int64_t max_rows) {
   if (check_linear(dtype, n_groups, n_out, k, max_rows) != MOE_OK) return 0;
-  if (dtype == MOE_F32) return moe::linear_f32_workspace_bytes(n_groups, n_out, k, max_rows);
-  // the gradients' parts of split sums, or the forward's
+  const size_t f32 = moe::linear_f32_workspace_bytes(n_groups, n_out, k, max_rows);
+  if (dtype == MOE_F32) return f32;
+  // the gradients' parts of split sums, on either kernel, or the forward's
   GemmGroups g{};
   g.n_routed = n_groups;
   g.max_routed_rows = max_rows;
   g.Nout = n_out;
   const size_t forward = moe::grouped_gemm_split_bytes(g);
   const size_t grad = moe::linear_mfma_workspace_bytes(n_groups, n_out, k, max_rows);
-  return forward > grad ? forward : grad;
+  const size_t most = forward > grad ? forward : grad;
+  return most > f32 ? most : f32;
 }
 
 static moe::Linear linear_of(moe::LinearMode mode, int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k,

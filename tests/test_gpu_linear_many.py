@@ -239,3 +239,50 @@ def test_rows_beyond_4_gib(B):
     torch.cuda.synchronize()
     assert (dx[:1000] == 0).all() and (dx[-last - 1000:-last] == 0).all()
     close(dx[-last:], ds @ ww, (n_out + 4) * U * (ds.abs() @ ww.abs()), "dx")
+
+
+def test_long_sums_of_gathered_rows_beyond_4_gib(B):
+    """Thousands of gathered rows from an x of more than 4 GiB, few tiles: the sums are split,
+    here as well as where x is smaller."""
+    d = Data(B, [5000, 0, 700], 64, 8192, 74, tokens=262144 + 5)
+    assert d.x.numel() * 2 > 1 << 32
+    check_weight_grad(B, d, F32)
+    check_weight_grad(B, d, BF16, True)
+
+
+def one_large(n, device="cuda"):
+    """2^26 and then ones: beside the first, a one is below half a step of float32 (8), so that
+    a sum in order loses every one, and a split sum those of its first part alone."""
+    v = torch.ones(n, dtype=BF16, device=device)
+    v[0] = 2.0 ** 26
+    return v
+
+
+def test_parts_of_sums_of_gathered_rows_beyond_4_gib(B):
+    rows, n_out, k, tokens = 8000, 64, 8192, 262144 + 5
+    x = torch.zeros(tokens, k, dtype=BF16, device="cuda")
+    x[-rows:] = one_large(rows)[:, None]
+    index = torch.arange(tokens - rows, tokens, dtype=torch.int32, device="cuda")
+    dy = torch.ones(rows, n_out, dtype=BF16, device="cuda")
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    dw = torch.empty(1, n_out, k, dtype=F32, device="cuda")
+    ws = torch.empty(B.grouped_linear_workspace_size("bf16", 1, n_out, k, rows), dtype=torch.uint8, device="cuda")
+    B.grouped_linear_weight_grad(dy, off, x, dw, row_index=index, ws=ws)
+    torch.cuda.synchronize()
+    lost = 2.0 ** 26 + rows - 1 - dw.double()
+    # the ones of the first part, of a quarter of the rows at most, and half a step of each sum of parts
+    assert lost.abs().max() <= rows / 4 + 4 * 64
+
+
+def test_parts_of_sums_over_a_wide_output(B):
+    """A sum over 2^20 output features in one tile of the input gradient."""
+    rows, n_out, k = 3, 1 << 20, 64
+    dy = one_large(n_out).expand(rows, n_out).contiguous()
+    w = torch.ones(1, n_out, k, dtype=BF16, device="cuda")
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    dx = torch.empty(rows, k, dtype=BF16, device="cuda")
+    ws = torch.empty(B.grouped_linear_workspace_size("bf16", 1, n_out, k, rows), dtype=torch.uint8, device="cuda")
+    B.grouped_linear_input_grad(dy, off, w, dx, ws=ws)
+    torch.cuda.synchronize()
+    # what is exact rounds to bf16, in steps of 2^19: 2^26 + 2^20 - 1 to 2^26 + 2^20
+    assert (dx.double() == 2.0 ** 26 + 2.0 ** 20).all()
