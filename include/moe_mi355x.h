@@ -494,7 +494,9 @@ int moe_layer_forward_few_mxfp4(const moe_config *cfg, const moe_weights_mxfp4 *
 /*
  * moe_grouped_linear — one Linear of every group's expert on its own rows:
  *   y[r] = act(x[row_index[r]] W_g^T + bias_g),   offsets[g] <= r < offsets[g+1]
- * with float32 sums, rounded once.
+ * with float32 sums, rounded once.  The SiLU and its derivative, here and in the gradients,
+ * are float32's: for MOE_F32 within 12 * 2^-24 of the terms that they are made of, for
+ * MOE_BF16 (by the hardware's exp2) within 2^-19 (1 + |z|) of them.
  *   dtype       moe_dtype of x, w, bias, y and pre
  *   x           [x_rows][k], row_index [max_rows] int32 or NULL: source row of
  *               each row (a dispatch's row_token), values in [0, x_rows); NULL:

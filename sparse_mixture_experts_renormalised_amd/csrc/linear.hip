@@ -199,12 +199,12 @@ __device__ __forceinline__ void put_sums(const Linear &a, int g, int64_t out_row
     if (a.pre) put4(static_cast<O *>(a.pre) + out_row * np + p, v);
     if (a.silu)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = silu(v[i]);
+      for (int i = 0; i < 4; ++i) v[i] = silu_f32(v[i]);   // bf16's forward is not here
   } else if (MODE == kLinInputGrad) {
     if (a.act_pre) {
       get4(static_cast<const T *>(a.act_pre) + out_row * np + p, o);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] *= silu_slope(o[i]);
+      for (int i = 0; i < 4; ++i) v[i] *= sizeof(T) == 4 ? silu_slope_f32(o[i]) : silu_slope(o[i]);
     }
   } else if (a.accumulate) {
     get4(out, o);

@@ -260,3 +260,49 @@ def test_other_streams_and_graphs(B, dtype):
         for a, b, c in zip(ref, got, side):
             assert torch.equal(a, b) and torch.equal(a, c)
         run(ref, d["ws"])
+
+
+def steps_of_z():
+    """Values before a SiLU, to where it leaves float32's normal numbers."""
+    z = torch.cat([torch.linspace(-103.0, 100.0, 4000), torch.linspace(-3.0, 3.0, 1500), torch.tensor([0.0, -0.0]),
+                   torch.logspace(-30, 30, 50), -torch.logspace(-30, 2, 42)])
+    return torch.nn.functional.pad(z, (0, -len(z) % 16)).view(-1, 16).cuda()
+
+
+def test_float32_silu_far_from_zero(B):
+    """Rows through the identity, whose sums are exact.  With u = 2^-24: e = exp(-|z|) is within
+    2.2 u, its product with z and 1 + e round by u each, the reciprocal is within 1.1 u and
+    the last product rounds by u: 6.3 u of the value, which 6 and the store's own u cover;
+    below the normal numbers e is off by 2^-149, times |z|."""
+    z = steps_of_z()
+    w = torch.eye(16, device="cuda").view(1, 16, 16).contiguous()
+    off = torch.tensor([0, len(z)], dtype=torch.int32, device="cuda")
+    n = B.grouped_linear_workspace_size("f32", 1, 16, 16, len(z))
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda") if n else None
+    y, pre = torch.empty_like(z), torch.empty_like(z)
+    B.grouped_linear(z, off, w, y, silu=True, pre=pre, ws=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(pre, z)
+    v = f64(z)
+    e = np.exp(-np.abs(v))
+    ref = v * np.where(v >= 0, 1.0, e) / (1.0 + e)
+    close(y, ref, 6 * U * np.abs(ref) + np.abs(v) * 2.0 ** -149, "y")
+
+
+def test_float32_slope_far_from_zero(B):
+    """Gradients of one through the identity.  With u = 2^-24: d = 1 / (1 + e) is within 3.2 u,
+    e d within 6 u, the bracket within 5 u of its magnitudes and the product rounds by u: 12 u
+    of s + |z| s (1 - s)."""
+    z = steps_of_z()
+    w = torch.eye(16, device="cuda").view(1, 16, 16).contiguous()
+    off = torch.tensor([0, len(z)], dtype=torch.int32, device="cuda")
+    n = B.grouped_linear_workspace_size("f32", 1, 16, 16, len(z))
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda") if n else None
+    dx = torch.empty_like(z)
+    B.grouped_linear_input_grad(torch.ones_like(z), off, w, dx, pre=z, ws=ws)
+    torch.cuda.synchronize()
+    v = f64(z)
+    e = np.exp(-np.abs(v))
+    d = 1.0 / (1.0 + e)
+    s, rest = np.where(v >= 0, d, e * d), np.where(v >= 0, e * d, d)
+    close(dx, s + v * s * rest, 12 * U * (s + np.abs(v) * s * rest) + (1 + np.abs(v)) * 2.0 ** -149, "dx")
