@@ -381,3 +381,35 @@ def test_no_tokens_with_expert_rows(B):
     for n, v in sums.items():
         assert (v == 0).all(), n
     assert (y == 5).all() and (dy == 5).all()
+
+
+@pytest.mark.parametrize("act,res", TYPES)
+@pytest.mark.parametrize("T,d", [(8201, 64), (4103, 520), (2055, 2048), (2050, 2056), (2051, 4104), (1031, 8200)])
+def test_join_of_more_tokens_than_workgroups(B, T, d, act, res):
+    """A workgroup that takes several tokens gives each the bits that it gets in a batch of
+    few."""
+    print(f"[block] {T} tokens of {d} {act}/{res}", flush=True)
+    t = make((T, d, 3, 1, "layer", "layer", True, True, 0.0), act, res, 13)
+    names = [n for n in ("residual", "slot_row", "topk_gate", "gate") if t[n] is not None]
+    case = (T, d, 3, 1, "layer", "layer", True, True, 0.0)
+    _, o = run(B, case, act, res, t, 0.7)
+    few = 500
+    for a in range(0, T, few):
+        e = min(T, a + few)
+        part = {**t, **{n: t[n][a:e].contiguous() for n in names}, "shared_out": t["shared_out"][:, a:e].contiguous()}
+        _, p = run(B, (e - a, *case[1:]), act, res, part, 0.7)
+        for n in p:
+            assert torch.equal(o[n][a:e], p[n]), (n, a)
+
+
+def test_dropout_of_more_tokens_than_workgroups(B):
+    """The same elements as moe_dropout drops, up to the last token.  Roundings: of the
+    factor, of its product and of the sum, in float32."""
+    T, d, p = 8201, 24, 0.3
+    case = (T, d, 0, 0, "none", "none", False, False, p)
+    t = make(case, "f32", "f32", 14)
+    _, o = run(B, case, "f32", "f32", t, 0.7)
+    dropped = torch.empty_like(t["branch"])
+    B.dropout(t["branch"], dropped, p, t["rng"])
+    b = 0.7 * f64(dropped)
+    close(o["out"], f64(t["residual"]) + b, 4 * 2.0 ** -24 * (np.abs(b) + np.abs(f64(t["residual"]))), "out")

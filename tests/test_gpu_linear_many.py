@@ -286,3 +286,33 @@ def test_parts_of_sums_over_a_wide_output(B):
     torch.cuda.synchronize()
     # what is exact rounds to bf16, in steps of 2^19: 2^26 + 2^20 - 1 to 2^26 + 2^20
     assert (dx.double() == 2.0 ** 26 + 2.0 ** 20).all()
+
+
+# forward calls that go through the layer's kernels: counts, n_out, k, rows of a gathered x
+LAYER = [
+    # more than 512 rows a group and many tiles: ends of 128 and of 64 rows and less, a last
+    # round in halves, and (from 4096 terms on) along the sum
+    ([600, 700, 513, 0, 900, 1025, 640, 1000], 2880, 192, 2500),
+    ([600, 700, 513, 0, 900, 1025, 640, 1000], 2880, 4096, 2500),
+    # few rows a group on average, and some groups with many
+    ([5] * 60 + [200, 300, 129, 128], 320, 256, 700),
+    ([5] * 60 + [200, 300, 129, 128], 1024, 4096, 700),
+    # few rows, a last round along the sum
+    ([20] * 290 + [0] * 10 + [40], 512, 1024, 3000),
+    # an x of more than 4 GiB
+    ([600] * 8, 2880, 8192, 262144 + 9),
+]
+
+
+@pytest.mark.parametrize("bias,silu,pre", [(False, True, True), (True, True, True), (True, True, False), (True, False, False)])
+@pytest.mark.parametrize("n,gather", [(n, g) for n in range(len(LAYER)) for g in (False, True) if g or LAYER[n][3] < 1 << 18])
+def test_forward_through_the_layers_kernels(B, n, gather, bias, silu, pre):
+    counts, n_out, k, tokens = LAYER[n]
+    print(f"[linear] layer's kernels {n} {gather} {bias} {silu} {pre}", flush=True)
+    check_forward(B, Data(B, counts, n_out, k, 110 + n, tokens if gather else 0), bias, silu, pre)
+
+
+@pytest.mark.parametrize("counts,n_out,k", [([3, 0, 2], 64, 1 << 20), ([3, 0, 2], 1 << 20, 64), ([2, 130], 1 << 20, 64)])
+def test_forward_of_wide_rows(B, counts, n_out, k):
+    print(f"[linear] forward {counts} {k}->{n_out}", flush=True)
+    check_forward(B, Data(B, counts, n_out, k, 75), True, True, True)
