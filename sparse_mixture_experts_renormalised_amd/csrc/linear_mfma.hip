@@ -123,12 +123,6 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-__device__ __forceinline__ const char *uniform_ptr(const void *p) {
-  const uint64_t u = reinterpret_cast<uint64_t>(p);
-  const uint32_t lo = uniform(static_cast<int>(u)), hi = uniform(static_cast<int>(u >> 32));
-  return reinterpret_cast<const char *>((static_cast<uint64_t>(hi) << 32) | lo);
-}
-
 // ---------------------------------------------------------------------------
 // LDS to fragments.  Operands [j][n] (n = 128 or 256 columns): rows of 2n bytes whose
 // 64-byte pieces sit at piece ^ (j & 3), so that the four rows of a transposing read
