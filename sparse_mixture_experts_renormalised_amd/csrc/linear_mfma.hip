@@ -1057,6 +1057,11 @@ __global__ __launch_bounds__(256) void linear_mfma_parts_kernel(Args a) {
     }
 }
 
+// Rows of the longest group that the choices below count on: four times the mean's.
+int64_t longest_rows(int groups, int64_t max_rows) {
+  return max_rows / groups < max_rows / 4 ? max_rows / groups * 4 + 4 : max_rows;
+}
+
 // Tiles at most, and parts of a tile at most (1: the sizes never need a split).
 template <typename S>
 int64_t tile_bound(int mode, int groups, int n_out, int k, int64_t max_rows) {
@@ -1068,7 +1073,7 @@ template <typename S>
 int part_bound(int mode, int groups, int n_out, int k, int64_t max_rows) {
   if (tile_bound<S>(mode, groups, n_out, k, max_rows) > S::SLOTS) return 1;
   // groups of several times the mean's rows are split, where all are short nothing is
-  const int64_t rows = max_rows / groups < max_rows / 4 ? max_rows / groups * 4 + 4 : max_rows;
+  const int64_t rows = longest_rows(groups, max_rows);
   const int64_t steps = mode == kLinWeightGrad ? (rows + kJ - 1) / kJ : (mode == kLinForward ? k : n_out) / kJ;
   const int64_t parts = steps / kMinSteps;
   return static_cast<int>(parts < 1 ? 1 : parts < S::SLOTS ? parts : S::SLOTS);
@@ -1119,20 +1124,38 @@ bool forward_pays(const Linear &p) {
   return rows >= 64 && (rows <= 512 || tiles <= kFewTiles);
 }
 
-
-// Gradients whose sums take a few steps and that have little to do go through the float32
-// kernel's 64 x 64 tiles: here a launch alone takes 8 to 10 us, in a prologue that fills the
-// ring and a code of many lines.  This kernel / the float32 one, us in a graph:
-//   weight gradient, rows of all groups x n_out x k: 8 x 2 x 320 x 448 10.1/4.5, 31 x 64 x
-//   320 8.3/4.7, 13 x 182 x 128 x 576 21.0/13.6, 43 x 3 x 64 x 8576 10.3/7.1; beyond, 136 x
-//   2 x 1856 x 768 10.3/10.3, 4 x 4 x 576 x 9280 18.4/28.4, 1275 x 256 x 320 17.7/45.9
-//   input gradient: 1898 rows, 64 x 64 11.4/7.0, 94 of 192 x 64 16.1/10.3, 1814 of 64 x 2048
-//   47.6/41.5; beyond, 1839 of 128 x 10496 35.0/86.4, 657 of 704 x 128 14.6/24.4
+// Gradients of short sums and few tiles go through the float32 kernel's 64 x 64 tiles.  Here a
+// launch alone takes 7 to 9 us, with a prologue that fills the ring and a code of many lines.
+//   Input gradient, in ns, against this kernel: the float32 one takes 2500 less and 40 less
+// for every group, 1100 more for each 64 of the sum, and from its 257th tile on 2 and 4 for
+// each 64 of the sum more a tile.
+//   Weight gradient: the float32 one is the faster up to about 1024 tiles of two steps, 1280
+// where they are more than a round here.
+// This kernel / the float32 one, us in a graph; groups, rows of all of them (of unequal lengths);
+// behind the semicolon the sizes that stay here:
+//   input gradient, n_out x k
+//     64 x 64      1, 1024 7.2/5.8   64, 4096 9.9/6.3   256, 16384 22/8.1
+//     64 x 1024    1, 1024 8.6/6.4   16, 1024 8.7/7.6;  64, 1024 10.7/11.8  16, 16384 17/36
+//     128 x 256    64, 1024 10.2/10.2  256, 1024 19.5/17.2;  64, 16384 12/20
+//     192 x 64     64, 1024 10.6/9.7   256, 4096 20/13;  16, 1024 8.3/10.0
+//     192 x 8192   ;  16, 16 15/37   64, 128 46/143
+//   weight gradient, n_out x k
+//     64 x 320     1, 64 8/6   64, 128 10/7   256, 128 16/13;  1, 512 13/12
+//     320 x 448    4, 64 10/5   16, 256 12/9;  64, 64 14/20
+//     2048 x 1408  1, 64 11/10;  1, 128 11/15   4, 2 16/21
 bool little(const Linear &p) {
   if (p.mode == kLinForward) return false;
-  if (p.mode == kLinWeightGrad)
-    return p.max_rows <= 128 && static_cast<int64_t>(p.groups) * p.n_out * p.k <= (1 << 24);
-  return p.n_out <= 192 && p.max_rows * p.k * p.n_out <= (1 << 28);
+  const int64_t outputs = p.n_out / 64, columns = p.k / 64;
+  if (p.mode == kLinWeightGrad) {
+    const int64_t tiles = p.groups * outputs * columns, rows = longest_rows(p.groups, p.max_rows);
+    const int64_t here = tile_bound<Tiles>(p.mode, p.groups, p.n_out, p.k, p.max_rows);
+    return p.max_rows <= 512 && rows <= 128 && tiles <= (here > Tiles::SLOTS ? 1280 : 1024) &&
+           tiles * ((rows + kJ - 1) / kJ) <= 2048;
+  }
+  if (outputs > 4) return false;         // measured up to 256 terms and 256 groups
+  const int64_t tiles = columns * (p.max_rows / 64 + (p.max_rows < p.groups ? p.max_rows : p.groups));
+  const int64_t behind = tiles > 256 ? tiles - 256 : 0;
+  return 1100 * outputs + (2 + 4 * outputs) * behind < 2500 + 40 * p.groups;
 }
 
 }  // namespace
