@@ -52,7 +52,8 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kJ = 32, kXcds = 8, kCus = 256;
 constexpr int kMaxGroups = kMaxRouted + kMaxShared;
-constexpr int kMinSteps = 8;             // steps of a part of a split sum, at least
+constexpr int kMinSteps = 8;             // as many parts as leave this many steps to each of the longest
+                                         // sum; those of a shorter group are shorter, the last ones empty
 constexpr int kTileCost = 6;             // what a tile costs beside its steps, in steps
 
 // A wave's 32 x 32 blocks along either axis of C, and the workgroup's tile of QW x 2
@@ -1107,16 +1108,25 @@ using Tiles = Shape<2, 4, 4>;
 
 // The forward goes here from 64 rows a group on, up to 512 where there are more than 256
 // tiles; below, the layer's kernels stream weights faster, above, their 256 x 256 tiles are.
-// Layer's kernels / this one, us, by rows of each group:
-//                            16        32        64       128       256       512      1024
-//   8 x 2048 x 2048        35/31     39/31     48/33     76/39     65/48     61/60   101/113
-//   64 x 2048 x 2048     115/141   130/142   178/148   196/190   232/207   353/334
-//   256 x 2048 x 1408    289/321   306/331   357/346   450/419
-//   64 x 4096 x 512        82/93     90/95   145/100   143/114   127/129   195/213
-//   8 x 4096 x 14336     199/183   211/188   253/199   318/223   345/330   531/556   903/949
-// and with few tiles 1221 rows on 2 x 6272 x 2304 172/65, 138 on 1 x 5376 x 128 113/24
-// (split sums); 28962 rows on 8 x 512 x 192 29/38 is the other way (a quarter of each tile
-// lies behind the columns).
+// Layer's kernels / this one, us in a graph over two sets of operands, by rows of each group:
+//   groups x n_out x k     16       32       64      128      256      512     1024
+//   8 x 2048 x 2048      27/27    35/27    39/27    52/31    38/47    45/58    62/63
+//   64 x 2048 x 2048    115/142  124/141  144/146  151/153  194/171  268/287  482/547
+//   64 x 512 x 4096      77/97    82/95    98/97   101/105  160/144  159/155  261/272
+//   64 x 4096 x 512      66/67    66/64    74/69    88/77   122/99   185/174  346/355
+//   8 x 14336 x 4096    183/185  217/231  231/223  286/233  279/283  438/481  769/844
+//   64 x 192 x 512       16/23    18/23    21/24    27/26    23/29    24/40    30/24
+// and of unequal lengths (shares of a Zipf law of exponent 0.8), by the mean:
+//   8 x 2048 x 2048      28/26    38/29    64/32    64/36    66/42    48/50    87/98
+//   64 x 2048 x 2048    151/148  158/179  172/179  180/178  241/202  326/318  546/560
+//   64 x 1408 x 2048    119/113  124/100  132/111  140/115  176/163  247/237  410/414
+// At 384 rows of 2048 x 2048 it is 297/248, so that groups of exactly two of the layer's tiles
+// are the exception there.  The device alone knows the lengths; the choice is by the mean.  It
+// is the wrong one where tiles fill a quarter to a half of the CUs and are split, since writing
+// and adding the parts then costs more than shorter sums save (8 x 2048 x 2048 at 256 and 512
+// rows, 8 x 4096 x 512 at 256 25/40), and where a short sum's one tile of columns is partly
+// filled (64 x 192 x 512, 28962 rows on 8 x 192 x 512 23/35).  With few tiles and long sums 1221
+// rows on 2 x 6272 x 2304 take 74/53, 138 on 1 x 5376 x 128 19/10.
 constexpr int64_t kFewTiles = 256;
 bool forward_pays(const Linear &p) {
   const int64_t tiles = tile_bound<Tiles>(kLinForward, p.groups, p.n_out, p.k, p.max_rows);
