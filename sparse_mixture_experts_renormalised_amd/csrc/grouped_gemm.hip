@@ -1891,16 +1891,31 @@ hipError_t launch_bf16_rs(const GemmArgs &a, const GemmGroups &g, Epilogue epi, 
 
 }  // namespace
 
-size_t grouped_gemm_split_bytes(const GemmGroups &g) {
+size_t grouped_gemm_split_bytes(const GemmGroups &g) { return grouped_gemm_split_bytes(g, kSplitCap); }
+
+size_t grouped_gemm_split_bytes(const GemmGroups &g, int parts) {
   // the stream kernel: its split word, the last-round piece tiles and, for
   // small products, K-split partial sums; the 256x256 kernel: one float32
   // 256x256 tile per workgroup of its split last round
   const int64_t prows = split_rows(g);
   size_t stream = 256 + static_cast<size_t>(kStreamRemBytes);
-  if (prows <= kSplitMaxRows)
-    stream += sizeof(float) * static_cast<size_t>(kSplitCap) * prows * g.Nout;
+  if (prows <= kSplitMaxRows && parts > 1)
+    stream += sizeof(float) * static_cast<size_t>(parts) * prows * g.Nout;
   const size_t rs = static_cast<size_t>(kRsMaxBlocks) * kRsPieceBytes;
   return stream > rs ? stream : rs;
+}
+
+// The stream kernel takes groups of up to kStreamRows rows, beside the 256x256 kernel where
+// there may be larger ones, and alone or not at all where the sizes say so.
+constexpr int64_t kStreamRows = 128, kNoStreamMean = 384;
+
+int grouped_gemm_parts(const GemmGroups &g) {
+  if (g.max_routed_rows / g.n_routed >= kNoStreamMean) return 1;
+  // stream_split's limits: four units for each of 256 workgroups, four chunks a part
+  const int64_t units = (g.Nout + 255) / 256;
+  int64_t parts = (4 * 256 + units - 1) / units;
+  if (parts > g.K / st::KCH / 4) parts = g.K / st::KCH / 4;
+  return static_cast<int>(parts < 1 ? 1 : parts < kSplitCap ? parts : kSplitCap);
 }
 
 hipError_t launch_grouped_gemm(bool bf16, const GemmGroups &g, Epilogue epi, hipStream_t s) {
@@ -1914,12 +1929,11 @@ hipError_t launch_grouped_gemm(bool bf16, const GemmGroups &g, Epilogue epi, hip
     // from about 130 rows on.  Each kernel takes its own size class.
     // Batches of at most 32 rows per group (decode) use the deep-ring
     // 32-row shape.
-    constexpr int64_t kStreamRows = 128;
     const int64_t groups = g.n_routed > 0 ? g.n_routed : 1;
     const int64_t mean_rows = g.max_routed_rows / groups;
     const int64_t max_rows = g.n_routed > 0 ? g.max_group_rows : 0;
     const bool any_big = max_rows > kStreamRows || (g.n_shared > 0 && g.T_sh > kStreamRows);
-    const bool any_small = (g.n_routed > 0 && mean_rows < 384) || (g.n_shared > 0 && g.T_sh <= kStreamRows);
+    const bool any_small = (g.n_routed > 0 && mean_rows < kNoStreamMean) || (g.n_shared > 0 && g.T_sh <= kStreamRows);
     if (!any_big) {
       if (max_rows <= 32) return launch_bf16_stream<1, 1, 6>(a, g, epi, 1, s);
       return launch_bf16_stream<2, 2, 3, 4>(a, g, epi, 1, s);

@@ -603,22 +603,6 @@ static int check_linear(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t 
   return MOE_OK;
 }
 
-size_t moe_grouped_linear_workspace_size(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k,
-                                         int64_t max_rows) {
-  if (check_linear(dtype, n_groups, n_out, k, max_rows) != MOE_OK) return 0;
-  const size_t f32 = moe::linear_f32_workspace_bytes(n_groups, n_out, k, max_rows);
-  if (dtype == MOE_F32) return f32;
-  // the gradients' parts of split sums, on either kernel, or the forward's
-  GemmGroups g{};
-  g.n_routed = n_groups;
-  g.max_routed_rows = max_rows;
-  g.Nout = n_out;
-  const size_t forward = moe::grouped_gemm_split_bytes(g);
-  const size_t grad = moe::linear_mfma_workspace_bytes(n_groups, n_out, k, max_rows);
-  const size_t most = forward > grad ? forward : grad;
-  return most > f32 ? most : f32;
-}
-
 static moe::Linear linear_of(moe::LinearMode mode, int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k,
                              const int32_t *offsets, int64_t max_rows) {
   moe::Linear p{};
@@ -630,6 +614,26 @@ static moe::Linear linear_of(moe::LinearMode mode, int32_t dtype, int32_t n_grou
   p.k = k;
   p.max_rows = max_rows;
   return p;
+}
+
+size_t moe_grouped_linear_workspace_size(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k,
+                                         int64_t max_rows) {
+  if (check_linear(dtype, n_groups, n_out, k, max_rows) != MOE_OK) return 0;
+  const size_t f32 = moe::linear_f32_workspace_bytes(n_groups, n_out, k, max_rows);
+  if (dtype == MOE_F32) return f32;
+  // the gradients' parts of split sums, on either kernel, or the forward's
+  GemmGroups g{};
+  g.n_routed = n_groups;
+  g.max_routed_rows = max_rows;
+  g.Nout = n_out;
+  g.K = k;
+  // (a gathered x of 4 GiB and more takes the layer's kernels where this says otherwise, and
+  // what scratch there is)
+  const bool own = moe::linear_mfma_fits(linear_of(moe::kLinForward, dtype, n_groups, n_out, k, nullptr, max_rows));
+  const size_t forward = moe::grouped_gemm_split_bytes(g, own ? 1 : moe::grouped_gemm_parts(g));
+  const size_t grad = moe::linear_mfma_workspace_bytes(n_groups, n_out, k, max_rows);
+  const size_t most = forward > grad ? forward : grad;
+  return most > f32 ? most : f32;
 }
 
 static int run_linear(const moe::Linear &p, void *ws, hipStream_t s) {

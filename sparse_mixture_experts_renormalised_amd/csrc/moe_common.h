@@ -102,6 +102,10 @@ struct GemmGroups {
 // every smaller one) as it sees fit; needs only Nout, n_routed, n_shared,
 // T_sh and max_routed_rows.
 size_t grouped_gemm_split_bytes(const GemmGroups &g);
+// The same for a split of K into that many parts at most; and the most that routed groups of
+// any lengths come to, from Nout, K, n_routed and max_routed_rows.
+size_t grouped_gemm_split_bytes(const GemmGroups &g, int parts);
+int grouped_gemm_parts(const GemmGroups &g);
 
 // kEpiBiasSiluPre: the SiLU's values to C and those before it to pre (bf16,
 // routed groups only).

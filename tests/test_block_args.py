@@ -190,3 +190,14 @@ def test_no_tokens_with_expert_rows(B):
         assert call(cfg_of(B, T=0, n_shared=-1)) == -1
         assert call(cfg_of(B, T=0, top_k=65)) == -2
         assert call(cfg_of(B, T=0, n_shared=65)) == -2
+
+
+@pytest.mark.parametrize("g,n,k,rows,most", [
+    (8, 14336, 4096, 4096, 1 << 27),        # a training step on large experts
+    (1, 1 << 20, 64, 4096, 1 << 27),        # sums too short for parts
+    (1, 1 << 20, 8192, 4096, 1 << 27),      # so many outputs that they fill the chip
+    (64, 1408, 2048, 4096, 1 << 27),
+    (64, 1408, 2048, 500, 1 << 28),         # few rows: up to eight parts of 500 rows
+])
+def test_workspace_is_what_the_kernels_can_use(B, g, n, k, rows, most):
+    assert 0 < B.grouped_linear_workspace_size("bf16", g, n, k, rows) <= most
