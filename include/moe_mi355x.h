@@ -488,7 +488,10 @@ int moe_layer_forward_few_mxfp4(const moe_config *cfg, const moe_weights_mxfp4 *
  *   moe_block_join
  * and back through moe_block_join_grad - weight and input gradient of W2 -
  * moe_dropout - weight and input gradient of W1 - moe_combine with gates of one
- * (the sum of a token's rows over its slots) - moe_block_join_grad.
+ * (the sum of a token's rows over its slots) - moe_block_join_grad.  The router's
+ * gradient is not among them: from d_topk_gate through the softmax over the kept
+ * logits to w_router and to the token's row is left to the caller, who adds the
+ * latter to moe_combine's sum before the last call.
  */
 
 /*
