@@ -413,3 +413,34 @@ def test_dropout_of_more_tokens_than_workgroups(B):
     B.dropout(t["branch"], dropped, p, t["rng"])
     b = 0.7 * f64(dropped)
     close(o["out"], f64(t["residual"]) + b, 4 * 2.0 ** -24 * (np.abs(b) + np.abs(f64(t["residual"]))), "out")
+
+
+@pytest.mark.parametrize("act,res", TYPES)
+def test_as_many_slots_and_shared_experts_as_there_may_be(B, act, res):
+    """64 slots and 64 shared experts a token, and the gradients of the slots' rows and gates
+    (no norms and no weights: sums of products alone)."""
+    T, d, K = 3, 520, 64
+    case = (T, d, K, 64, "none", "none", False, False, 0.0)
+    t = make(case, act, res, 15)
+    t["w_in"] = None
+    _, o = run(B, case, act, res, t, 0.5)
+    b, mag = branch_of(t)
+    close(o["branch_out"], b, REL * mag, "branch_out")
+    out = f64(t["residual"]) + 0.5 * b
+    bound = REL * (np.abs(f64(t["residual"])) + mag)
+    close(o["out"], out, bound, "out")
+    saved, c, e = inputs_back(case, act, res, t, 2)
+    got = run_grad(B, case, act, res, t, 0.5, saved, c, e, grads_of(case, act, res, t), None)
+    torch.cuda.synchronize()
+    dh = f64(c) + f64(e)
+    close(got["d_residual"], dh, REL * np.abs(dh), "d_residual")
+    slot, w, y = t["slot_row"].cpu().numpy(), f64(t["topk_gate"]), np.nan_to_num(f64(t["y_rows"]))
+    for i in range(T):
+        for k in range(K):
+            r = slot[i, k]
+            if r < 0:
+                assert got["d_topk_gate"][i, k] == 0
+                continue
+            close(got["d_y_rows"][r], w[i, k] * 0.5 * dh[i], REL * np.abs(dh[i]), f"row of slot {k}")
+            close(got["d_topk_gate"][i, k], np.array(0.5 * (dh[i] * y[r]).sum()), np.array(REL * np.abs(dh[i] * y[r]).sum()),
+                  f"gate of slot {k}")

@@ -316,3 +316,16 @@ def test_forward_through_the_layers_kernels(B, n, gather, bias, silu, pre):
 def test_forward_of_wide_rows(B, counts, n_out, k):
     print(f"[linear] forward {counts} {k}->{n_out}", flush=True)
     check_forward(B, Data(B, counts, n_out, k, 75), True, True, True)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("long", [3, 400])
+def test_as_many_groups_as_there_may_be(B, dtype, long):
+    """1088 groups: the last of them with rows, most of one row or none, the first one long."""
+    counts = [long] + [g % 3 % 2 for g in range(1085)] + [0, 5]
+    print(f"[linear] 1088 groups {dtype} {long}", flush=True)
+    d = Data(B, counts, 64, 128, 120, sum(counts) // 2, dtype)
+    check_weight_grad(B, d, F32)
+    check_weight_grad(B, d, dtype, True)
+    check_input_grad(B, d, True)
+    check_forward(B, d, True, True, True)
