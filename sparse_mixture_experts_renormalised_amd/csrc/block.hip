@@ -23,7 +23,8 @@
 // Bound by memory, with loads in batches (a token's own rows, then two or four to eight
 // expert rows) so that many are on their way.  4096 tokens of 7168 in bf16, eight experts
 // and a shared one: forward 188 us (0.76 GB, 4.1 TB/s), gradient 288 us (1.29 GB, 4.5
-// TB/s), where a copy of two 4 GiB halves reaches 4.8.  1001 tokens of 1408 in float32 with
+// TB/s), where a copy of two 4 GiB halves reaches 4.8; over a float32 stream 212 and 338, all
+// in float32 388 and 592 (1.53 and 2.58 GB, 3.9 and 4.4 TB/s).  1001 tokens of 1408 in float32 with
 // LayerNorms and biases: gradient 20 us, 34 MB in the caches and two launches.  16 tokens of
 // 2048: forward 5.6 us, a launch and three dependent reads.
 #include "block.h"
