@@ -329,3 +329,19 @@ def test_as_many_groups_as_there_may_be(B, dtype, long):
     check_weight_grad(B, d, dtype, True)
     check_input_grad(B, d, True)
     check_forward(B, d, True, True, True)
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("gather", [False, True])
+def test_no_rows_of_wide_weights(B, gather, out):
+    """Weight gradients without a row, of more tiles than the CUs take at once: zeros."""
+    none = torch.empty(0, 2048, dtype=BF16, device="cuda")
+    x = torch.full((3, 1408), float("nan"), dtype=BF16, device="cuda")
+    off = torch.zeros(10, dtype=torch.int32, device="cuda")
+    index = torch.empty(0, dtype=torch.int32, device="cuda") if gather else None
+    dw = torch.full((9, 2048, 1408), float("nan"), dtype=out, device="cuda")
+    db = torch.full((9, 2048), float("nan"), dtype=out, device="cuda")
+    ws = torch.empty(B.grouped_linear_workspace_size("bf16", 9, 2048, 1408, 0), dtype=torch.uint8, device="cuda")
+    B.grouped_linear_weight_grad(none, off, x, dw, row_index=index, dbias=db, ws=ws)
+    torch.cuda.synchronize()
+    assert (dw == 0).all() and (db == 0).all()
